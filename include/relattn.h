@@ -293,6 +293,118 @@ RELATTN_API relattn_status_t relattn_decode_workspace_size(int B, int H, int T, 
                                                unsigned long long *bytes);
 
 /*
+ * Paged key/value cache: requests of any length share one pool of pages, so a decoder that
+ * serves many requests reserves no row before it is written. Keys and values lie in
+ * [num_pages, Hkv, page_size, d] arrays; row b of block_table names the pages of request b's
+ * tokens 0 .. page_size - 1, page_size .. 2 page_size - 1, and so on. One step of a server:
+ * relattn_paged_plan gives the new tokens of every request their pages and slots,
+ * relattn_paged_append writes their keys and values there, relattn_paged_fwd attends. The pages
+ * that describe the method have no counterpart of the paging; the attention is the causal
+ * forward of section 3.4 ("Self-Attention with Relative Position Representations" page).
+ *
+ * relattn_paged_plan — block tables, slot map and query offsets from the requests' lengths, on
+ * the GPU. With P = page_size, request b needs need_b = ceil((cached_b + new_b) / P) -
+ * ceil(cached_b / P) pages more; with incl_b = sum of need over requests 0 .. b:
+ *
+ *   block_table[b][ceil(cached_b / P) + i] = free_pages[free_head + incl_b - need_b + i]
+ *   q_start[b] = sum of new over the requests before b;  kv_len[b] = cached_b + new_b
+ *   slots[q_start[b] + i] = block_table[b][p / P] * P + p % P,   p = cached_b + i
+ *   free_head_out = free_head + pages taken
+ *
+ *   cached_len, new_len   [B] int32: tokens in the cache, tokens of this step (0: none).
+ *   block_table           [B, max_pages] int32 with table_stride elements between rows; only the
+ *                         new entries are written.
+ *   free_pages            [num_free] int32 page numbers; free_head, free_head_out: one int32
+ *                         each, the entries already taken (may be the same address).
+ *   kv_len                [B] int32 (may be cached_len itself), q_start [B + 1] int32.
+ *   slots                 [max_tokens] int32, -1 behind the last new token.
+ * A request is left out when the free pages do not suffice for it (later ones that need pages
+ * are then left out too), when it would not fit its table row or max_tokens, or when a length is
+ * negative: its slots are -1, its kv_len is cached_len, its table row stays, and the device
+ * status word becomes RELATTN_ERR_INVALID_ARG (relattn_get_device_error). A request with a
+ * negative new_len, or one above max_tokens, has no rows in q_start and slots either.
+ * page_size: a power of two, 1 .. 1024. B <= 16384 and max_tokens <= 2^23, else
+ * RELATTN_ERR_UNSUPPORTED.
+ */
+RELATTN_API relattn_status_t relattn_paged_plan(const int *cached_len, const int *new_len, int B,
+                                    int page_size, int *block_table, long long table_stride,
+                                    int max_pages, const int *free_pages, int num_free,
+                                    const int *free_head, int max_tokens, int *kv_len,
+                                    int *q_start, int *slots, int *free_head_out,
+                                    relattn_stream_t stream);
+
+/*
+ * relattn_paged_append — the new tokens' keys and values into their slots:
+ * k_pages[s / page_size][h][s % page_size] = k[t][h] for s = slots[t], and v alike.
+ *
+ *   k, v              [tokens, Hkv, d] of `dtype` (RELATTN_BF16 or RELATTN_F32), k_stride and
+ *                     v_stride elements between tokens (slices of a joint projection).
+ *   slots             [tokens] int32. Negative: the token is skipped. A slot outside the cache is
+ *                     skipped and sets the device status word to RELATTN_ERR_INVALID_ARG. If two
+ *                     tokens name one slot, either may be the one that stays.
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d], page_stride elements between pages.
+ * Nothing else of the cache is written. num_pages * page_size < 2^31. tokens = 0 does nothing.
+ */
+RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, long long k_stride,
+                                      long long v_stride, const int *slots, int tokens,
+                                      void *k_pages, void *v_pages, long long page_stride,
+                                      int num_pages, int Hkv, int page_size, int d, int dtype,
+                                      relattn_stream_t stream);
+
+/*
+ * relattn_paged_fwd — attention of the new tokens of every request over its paged cache, with
+ * the relative terms of relattn_fwd (section 3.4, eq. 3 and eq. 4): whole prompts, chunks of
+ * prompts and single tokens alike, mixed in one call. The new tokens' own keys and values are in
+ * the cache already. Token i of request b (query row q_start[b] + i, n_b = q_start[b + 1] -
+ * q_start[b] rows) stands at position t = kv_len[b] - n_b + i and sees the keys
+ *
+ *   j <= t,  and if window > 0 only j > t - window or j < sinks:
+ *   e_j = scale * q . (k_j + aK[h'][clip(j - t, clip_k) + clip_k]),
+ *   z   = sum_j softmax_j(e)_j * (v_j + aV[h'][clip(j - t, clip_k) + clip_k]),  h' = h / (H / Hkv)
+ *
+ * window is the number of latest keys that stay visible, the token's own among them (0: all);
+ * sinks is the number of first keys that stay visible behind the window. Query heads h of one
+ * group share key/value head h', its keys, values and edge vectors.
+ *
+ *   q                 [tokens, H, d] of `dtype`, q_stride elements between tokens.
+ *   k_pages, v_pages, page_stride, num_pages, page_size, block_table, table_stride, max_pages
+ *                     the cache, as above. Entries of pages that no token sees are not read
+ *                     (those that the window has left behind may be gone); rows of a page that
+ *                     no token sees may hold anything. A page number outside 0 .. num_pages - 1
+ *                     counts as zeros and sets the status word to RELATTN_ERR_INVALID_ARG. The
+ *                     keys and values that some token of the request sees must be finite.
+ *   q_start           [B + 1] int32, ascending; rows from q_start[B] on are not written.
+ *   kv_len            [B] int32: cached tokens, the new ones among them (taken as at most
+ *                     max_pages * page_size). A token at a negative position gets zeros.
+ *   aK, aV            [Hkv|1, 2 clip_k + 1, d] of `dtype` or NULL; table_head_stride as in
+ *                     relattn_fwd. Only rows 0 .. clip_k (offsets -clip_k .. 0) are read.
+ *   max_new           the most new tokens of one request, or 0 if not known: it chooses between
+ *                     kernels and the results hold for any value.
+ *   workspace         caller-owned device scratch of relattn_paged_workspace_size bytes, 16-byte
+ *                     aligned. Contents are scratch on entry and return; calls that may overlap
+ *                     (other streams, two captured graphs) need one each.
+ *   out               [tokens, H, d] of `dtype`, contiguous; must not alias an input.
+ *
+ * The work is split over the GPU by keys, whatever the mix of lengths; pieces of one token's
+ * keys are joined in a fixed order, so equal calls give equal bits.
+ * fp32 arithmetic on the SIMT units. d <= 128, clip_k <= 256 and H / Hkv <= 128, else
+ * RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing.
+ */
+RELATTN_API relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void *k_pages,
+                                   const void *v_pages, long long page_stride, int num_pages,
+                                   int page_size, const int *block_table, long long table_stride,
+                                   int max_pages, const int *q_start, const int *kv_len,
+                                   const void *aK, const void *aV, long long table_head_stride,
+                                   int clip_k, int window, int sinks, float scale, int B,
+                                   int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                   void *workspace, unsigned long long workspace_bytes, void *out,
+                                   relattn_stream_t stream);
+
+/* relattn_paged_workspace_size — host only: the workspace bytes relattn_paged_fwd needs. */
+RELATTN_API relattn_status_t relattn_paged_workspace_size(int H, int Hkv, int d,
+                                              unsigned long long *bytes);
+
+/*
  * relattn_sinusoid_table — the fixed sinusoidal encodings of every relative offset of a
  * length-n sequence, the r of the Transformer-XL score before its projection ("Relative
  * Position Encoding in Transformer-XL" page: r_{i-j} is a sinusoid of the distance, in the
@@ -459,7 +571,8 @@ RELATTN_API relattn_status_t relattn_t5_thresholds(int num_buckets, int max_dist
  * relattn_get_device_error — synchronises `stream`, then reads and clears the device
  * status word of the current device: RELATTN_OK, RELATTN_ERR_TIMEOUT if a bounded
  * device wait ran out since the last call, or RELATTN_ERR_INVALID_ARG if relattn_labeled_fwd
- * met a label without a table row. RELATTN_ERR_CUDA if the stream reports an error.
+ * met a label without a table row, or a relattn_paged_* call a request, slot or page that does
+ * not fit. RELATTN_ERR_CUDA if the stream reports an error.
  */
 RELATTN_API relattn_status_t relattn_get_device_error(relattn_stream_t stream);
 

@@ -1,6 +1,6 @@
 """relation-aware self-attention on GB300 (sm_103a): the Shaw forward, T5 / ALiBi /
-per-offset scalar biases, labelled edges, a decode step, the Shaw gradients and those
-of labelled edges and the scalar biases.
+per-offset scalar biases, labelled edges, a decode step, a paged key/value cache with its
+attention, the Shaw gradients and those of labelled edges and the scalar biases.
 
 The compute lives in librelattn.so (C ABI, include/relattn.h); this package holds its
 ctypes binding (`_lib`), the in-tree build script (`build`) and the named workloads with
@@ -13,7 +13,9 @@ from __future__ import annotations
 _BINDING = ("relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_offset_bias_fwd", "relattn_labeled_fwd", "relattn_txl_fwd", "relattn_sinusoid_table",
             "relattn_decode_fwd",
-            "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size", "relattn_bwd",
+            "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
+            "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
+            "relattn_paged_workspace_size", "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",
             "relattn_scalar_bias_bwd_workspace_size", "relattn_labeled_bwd",
             "relattn_labeled_bwd_workspace_size", "relattn_labels",

@@ -70,6 +70,17 @@ _lib.relattn_labeled_bwd_workspace_size.argtypes = [_I, _I, _I, _I, ctypes.POINT
 _lib.relattn_labeled_bwd_workspace_size.restype = _I
 _lib.relattn_decode_workspace_size.argtypes = [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
 _lib.relattn_decode_workspace_size.restype = _I
+_L = ctypes.c_longlong
+_lib.relattn_paged_plan.argtypes = [_P, _P, _I, _I, _P, _L, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P]
+_lib.relattn_paged_plan.restype = _I
+_lib.relattn_paged_append.argtypes = [_P, _P, _L, _L, _P, _I, _P, _P, _L, _I, _I, _I, _I, _I, _P]
+_lib.relattn_paged_append.restype = _I
+_lib.relattn_paged_fwd.argtypes = [_P, _L, _P, _P, _L, _I, _I, _P, _L, _I, _P, _P, _P, _P, _L, _I,
+                                   _I, _I, ctypes.c_float, _I, _I, _I, _I, _I, _I, _I, _P,
+                                   ctypes.c_ulonglong, _P, _P]
+_lib.relattn_paged_fwd.restype = _I
+_lib.relattn_paged_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
+_lib.relattn_paged_workspace_size.restype = _I
 _lib.relattn_labels.argtypes = [_I, _I, _I, _I, _I, _I, _I, _P, _P]
 _lib.relattn_labels.restype = _I
 _lib.relattn_t5_thresholds.argtypes = [_I, _I, _I, ctypes.POINTER(_I), _I, ctypes.POINTER(_I)]
@@ -94,7 +105,9 @@ _lib.relattn_version.restype = _I
 EXPORTED = ["relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_offset_bias_fwd", "relattn_labeled_fwd", "relattn_txl_fwd", "relattn_sinusoid_table",
             "relattn_decode_fwd",
-            "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size", "relattn_bwd",
+            "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
+            "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
+            "relattn_paged_workspace_size", "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",
             "relattn_scalar_bias_bwd_workspace_size", "relattn_labeled_bwd",
             "relattn_labeled_bwd_workspace_size", "relattn_labels",
@@ -597,6 +610,207 @@ def relattn_decode_fwd(q, k_cache, v_cache, cache_len, aK=None, aV=None, clip_k=
                                  _ptr(cache_len), B, H, T, d, _ptr(workspace), ws_bytes, _ptr(out),
                                  _stream(stream))
     _check(st, "relattn_decode_fwd")
+    return out
+
+
+def _tensors(device, **named):
+    """Checks of the paged calls: every tensor on `device`."""
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+def _ints(device, **named):
+    _tensors(device, **named)
+    for name, t in named.items():
+        if t.dtype != torch.int32:
+            raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _table(device, block_table, B):
+    """block_table [B, max_pages] int32; its rows may be spaced. Returns (stride, max_pages)."""
+    _tensors(device, block_table=block_table)
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [B, max_pages]")
+    M = block_table.shape[1]
+    if (M > 1 and block_table.stride(1) != 1) or (B > 1 and block_table.stride(0) < M):
+        raise ValueError("block_table's rows must be contiguous and must not overlap")
+    return (block_table.stride(0) if B > 1 else M), M
+
+
+def _spaced(name, t, shape, dtype):
+    """t has `shape` and dtype and is contiguous but for the stride of its first dimension, which
+    is returned (no shorter than a row)."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    row = 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and st != row:
+            raise ValueError("%s must be contiguous behind its first dimension" % name)
+        row *= n
+    if t.shape[0] <= 1:
+        return row
+    if t.stride(0) < row:
+        raise ValueError("%s's first dimension overlaps" % name)
+    return t.stride(0)
+
+
+def _pages(device, k_pages, v_pages):
+    """k_pages and v_pages [num_pages, Hkv, page_size, d] with one stride between pages."""
+    _tensors(device, k_pages=k_pages, v_pages=v_pages)
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
+    stride = _spaced("k_pages", k_pages, k_pages.shape, k_pages.dtype)
+    if _spaced("v_pages", v_pages, k_pages.shape, k_pages.dtype) != stride:
+        raise ValueError("k_pages and v_pages must have one page stride")
+    return stride
+
+
+def _on_device(device, stream, call):
+    """call(stream pointer) with `device` current; the stream defaults to that device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        return call(ctypes.c_void_p(stream.cuda_stream))
+    with torch.cuda.device(device):
+        return call(ctypes.c_void_p(stream.cuda_stream))
+
+
+def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, page_size,
+                       max_tokens, kv_len=None, q_start=None, slots=None, free_head_out=None,
+                       stream=None):
+    """Pages, slots and query offsets of one step's new tokens, on the GPU (include/relattn.h has
+    the formulas). Returns (kv_len [B], q_start [B + 1], slots [max_tokens], free_head_out [1]).
+
+    cached_len, new_len: [B] int32. block_table: [B, max_pages] int32, new entries written in
+    place. free_pages: int32 page numbers, of which the first free_head ([1] int32) are taken.
+    kv_len may be cached_len and free_head_out may be free_head, which then advance in place.
+    """
+    if not isinstance(cached_len, torch.Tensor):
+        raise TypeError("cached_len must be a CUDA tensor")
+    dev = cached_len.device
+    B = cached_len.numel()
+    max_tokens = int(max_tokens)
+    i32 = dict(dtype=torch.int32, device=dev)
+    kv_len = torch.empty(B, **i32) if kv_len is None else kv_len
+    q_start = torch.empty(B + 1, **i32) if q_start is None else q_start
+    slots = torch.empty(max(0, max_tokens), **i32) if slots is None else slots
+    free_head_out = torch.empty(1, **i32) if free_head_out is None else free_head_out
+    _ints(dev, cached_len=cached_len, new_len=new_len, free_pages=free_pages, free_head=free_head,
+          kv_len=kv_len, q_start=q_start, slots=slots, free_head_out=free_head_out)
+    ts, M = _table(dev, block_table, B)
+    if new_len.numel() != B or kv_len.numel() != B or q_start.numel() != B + 1:
+        raise ValueError("new_len and kv_len must have B entries, q_start B + 1")
+    if slots.numel() != max_tokens or free_head.numel() != 1 or free_head_out.numel() != 1:
+        raise ValueError("slots must have max_tokens entries, free_head and free_head_out one")
+    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_plan(
+        cached_len.data_ptr(), new_len.data_ptr(), B, int(page_size), block_table.data_ptr(), ts, M,
+        free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), max_tokens,
+        kv_len.data_ptr(), q_start.data_ptr(), slots.data_ptr(), free_head_out.data_ptr(), s))
+    _check(st, "relattn_paged_plan")
+    return kv_len, q_start, slots, free_head_out
+
+
+def relattn_paged_append(k, v, slots, k_pages, v_pages, stream=None):
+    """Rows k[t], v[t] ([tokens, Hkv, d], bf16 or fp32, any token stride) to slot slots[t] of
+    k_pages, v_pages [num_pages, Hkv, page_size, d]; negative slots are skipped. In place."""
+    if not isinstance(k_pages, torch.Tensor):
+        raise TypeError("k_pages must be a CUDA tensor")
+    dev = k_pages.device
+    ps = _pages(dev, k_pages, v_pages)
+    N, Hkv, P, d = k_pages.shape
+    _tensors(dev, k=k, v=v)
+    _ints(dev, slots=slots)
+    T = slots.numel()
+    ks = _spaced("k", k, (T, Hkv, d), k_pages.dtype)
+    vs = _spaced("v", v, (T, Hkv, d), k_pages.dtype)
+    code = _dtype_code(k_pages)
+    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_append(
+        k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, k_pages.data_ptr(),
+        v_pages.data_ptr(), ps, N, Hkv, P, d, code, s))
+    _check(st, "relattn_paged_append")
+
+
+def relattn_paged_workspace_size(H, Hkv, d) -> int:
+    """Workspace bytes relattn_paged_fwd needs (host only)."""
+    nb = ctypes.c_ulonglong(0)
+    _check(_lib.relattn_paged_workspace_size(int(H), int(Hkv), int(d), ctypes.byref(nb)),
+           "relattn_paged_workspace_size")
+    return int(nb.value)
+
+
+def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None, aV=None,
+                      clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
+                      workspace=None, table_head_stride=None, stream=None):
+    """Attention of the new tokens of every request over its paged cache with relative terms
+    ("Self-Attention with Relative Position Representations" page, section 3.4, eqs. 3-4; causal),
+    grouped heads, a sliding window and first tokens that stay visible.
+
+    q: [tokens, H, d] bf16 or fp32 (any token stride), rows q_start[b] .. q_start[b + 1] - 1 the
+    last tokens of request b; k_pages, v_pages: [num_pages, Hkv, page_size, d] with the new
+    tokens already appended; block_table: [B, max_pages] int32; q_start: [B + 1] int32; kv_len:
+    [B] int32. aK / aV: [Hkv or 1, 2*clip_k+1, d] or None. window: latest keys that stay visible
+    (0: all), sinks: first keys that do. max_new: the most new tokens of one request if known
+    (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
+    or None to make one. Returns out [tokens, H, d].
+    """
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, H, d]")
+    T, H, d = q.shape
+    dt = _dtype_code(q)
+    ps = _pages(dev, k_pages, v_pages)
+    N, Hkv, P, dk = k_pages.shape
+    if k_pages.dtype != q.dtype or dk != d:
+        raise ValueError("k_pages and v_pages must have q's dtype and head dimension")
+    qs = _spaced("q", q, (T, H, d), q.dtype)
+    _ints(dev, q_start=q_start, kv_len=kv_len)
+    B = kv_len.numel()
+    if q_start.numel() != B + 1:
+        raise ValueError("q_start must have B + 1 entries")
+    ts, M = _table(dev, block_table, B)
+    W = 2 * int(clip_k) + 1
+    for name, t in (("aK", aK), ("aV", aV)):
+        if t is not None:
+            _dev(t, name, q.dtype)
+            _tensors(dev, **{name: t})
+            if t.dim() != 3 or t.shape[1] != W or t.shape[2] != d or t.shape[0] not in (1, Hkv):
+                raise ValueError("%s must be [Hkv or 1, 2*clip_k+1, d]" % name)
+    if aK is not None and aV is not None and aK.shape[0] != aV.shape[0]:
+        raise ValueError("aK and aV must both be per head or both shared")
+    if table_head_stride is None:
+        ref = aK if aK is not None else aV
+        table_head_stride = 0 if (ref is None or ref.shape[0] == 1) else W * d
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+    _dev(out, "out", q.dtype)
+    _tensors(dev, out=out)
+    if out.shape != q.shape:
+        raise ValueError("out must be [tokens, H, d] like q")
+    if scale is None:
+        scale = d ** -0.5
+    if workspace is None:
+        workspace = torch.empty(relattn_paged_workspace_size(H, Hkv, d), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)  # its memory is not handed out before this call is done
+    _dev(workspace, "workspace")
+    _tensors(dev, workspace=workspace)
+    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_fwd(
+        q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, P, block_table.data_ptr(),
+        ts, M, q_start.data_ptr(), kv_len.data_ptr(), _ptr(aK), _ptr(aV), int(table_head_stride),
+        int(clip_k), int(window), int(sinks), float(scale), B, T, int(max_new), H, Hkv, d, dt,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(), s))
+    _check(st, "relattn_paged_fwd")
     return out
 
 

@@ -163,6 +163,27 @@ relattn_status_t scalar_bias_fwd(const void *q, const void *k, const void *v, co
     return dispatch_bf16(a, tb, s);
 }
 
+// the device of a paged call: built for sm_103a only, with its status word
+relattn_status_t paged_device(int **err) {
+    const int cc = current_cc();
+    if (cc < 0) return RELATTN_ERR_CUDA;
+    if (cc != 103) return RELATTN_ERR_UNSUPPORTED;
+    *err = status_word_for_current_device();
+    return *err ? RELATTN_OK : RELATTN_ERR_CUDA;
+}
+
+bool page_size_ok(int page_size) {
+    return page_size >= 1 && page_size <= relattn::kPagedMaxPageSize && (page_size & (page_size - 1)) == 0;
+}
+
+// [num_pages, Hkv, page_size, d] with page_stride elements between pages; slots are 32-bit
+bool page_shape_ok(int num_pages, int Hkv, int page_size, int d, long long page_stride) {
+    if (num_pages < 1 || Hkv < 1 || d < 1 || !page_size_ok(page_size)) return false;
+    if ((long long)num_pages * page_size > (1LL << 31) - 1 || (long long)Hkv * page_size > (1LL << 31) - 1)
+        return false;
+    return num_pages == 1 || page_stride / d >= (long long)Hkv * page_size;
+}
+
 }  // namespace
 
 extern "C" {
@@ -573,6 +594,155 @@ relattn_status_t relattn_offset_bias_fwd(const void *q, const void *k, const voi
     if (table_head_stride != 0 && table_head_stride < 2LL * radius + 1) return RELATTN_ERR_INVALID_ARG;
     return scalar_bias_fwd(q, k, v, table, relattn::kBiasTable, radius, table_head_stride,
                            nullptr, causal, scale, kv_len, B, H, n, d, dtype, out, stream);
+}
+
+relattn_status_t relattn_paged_plan(const int *cached_len, const int *new_len, int B,
+                                    int page_size, int *block_table, long long table_stride,
+                                    int max_pages, const int *free_pages, int num_free,
+                                    const int *free_head, int max_tokens, int *kv_len,
+                                    int *q_start, int *slots, int *free_head_out,
+                                    relattn_stream_t stream) {
+    if (!cached_len || !new_len || !block_table || !free_head || !kv_len || !q_start || !free_head_out)
+        return RELATTN_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || num_free < 0 || max_tokens < 0) return RELATTN_ERR_INVALID_ARG;
+    if ((num_free > 0 && !free_pages) || (max_tokens > 0 && !slots)) return RELATTN_ERR_INVALID_ARG;
+    if (!page_size_ok(page_size)) return RELATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
+    const void *ints[] = {cached_len, new_len, block_table, free_pages, free_head, kv_len, q_start, slots,
+                          free_head_out};
+    for (const void *p : ints)
+        if (p && !aligned(p, 4)) return RELATTN_ERR_INVALID_ARG;
+    if (B > relattn::kPlanMaxSeqs || max_tokens > relattn::kPlanMaxTokens) return RELATTN_ERR_UNSUPPORTED;
+    relattn::PagedPlanArgs a{};
+    a.cached_len = cached_len;
+    a.new_len = new_len;
+    a.B = B;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.max_tokens = max_tokens;
+    a.num_free = num_free;
+    a.bt_stride = table_stride;
+    a.free_pages = free_pages;
+    a.free_head = free_head;
+    a.block_table = block_table;
+    a.kv_len = kv_len;
+    a.q_start = q_start;
+    a.slots = slots;
+    a.free_head_out = free_head_out;
+    const relattn_status_t st = paged_device(&a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+relattn_status_t relattn_paged_append(const void *k, const void *v, long long k_stride,
+                                      long long v_stride, const int *slots, int tokens,
+                                      void *k_pages, void *v_pages, long long page_stride,
+                                      int num_pages, int Hkv, int page_size, int d, int dtype,
+                                      relattn_stream_t stream) {
+    if (!k_pages || !v_pages || k_pages == v_pages) return RELATTN_ERR_INVALID_ARG;
+    if (tokens < 0 || (tokens > 0 && (!k || !v || !slots))) return RELATTN_ERR_INVALID_ARG;
+    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
+    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
+    const long long row = (long long)Hkv * d;
+    if (tokens > 1 && (k_stride < row || v_stride < row)) return RELATTN_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(k_pages, es) || !aligned(v_pages, es) || !aligned(slots, 4))
+        return RELATTN_ERR_INVALID_ARG;
+    if (tokens == 0) return RELATTN_OK;
+    relattn::PagedAppendArgs a{};
+    a.k = k;
+    a.v = v;
+    a.k_stride = tokens > 1 ? k_stride : row;
+    a.v_stride = tokens > 1 ? v_stride : row;
+    a.slots = slots;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = page_stride;
+    a.tokens = tokens;
+    a.num_pages = num_pages;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.d = d;
+    a.elem_bytes = (int)es;
+    const relattn_status_t st = paged_device(&a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+relattn_status_t relattn_paged_workspace_size(int H, int Hkv, int d, unsigned long long *bytes) {
+    if (!bytes || H < 1 || Hkv < 1 || H % Hkv != 0 || d < 1) return RELATTN_ERR_INVALID_ARG;
+    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup) return RELATTN_ERR_UNSUPPORTED;
+    *bytes = relattn::paged_workspace_bytes(d);
+    return RELATTN_OK;
+}
+
+relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void *k_pages,
+                                   const void *v_pages, long long page_stride, int num_pages,
+                                   int page_size, const int *block_table, long long table_stride,
+                                   int max_pages, const int *q_start, const int *kv_len,
+                                   const void *aK, const void *aV, long long table_head_stride,
+                                   int clip_k, int window, int sinks, float scale, int B,
+                                   int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                   void *workspace, unsigned long long workspace_bytes, void *out,
+                                   relattn_stream_t stream) {
+    if (!k_pages || !v_pages || !block_table || !q_start || !kv_len) return RELATTN_ERR_INVALID_ARG;
+    if (tokens < 0 || B < 1 || max_new < 0 || max_pages < 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!q || !out || !workspace)) return RELATTN_ERR_INVALID_ARG;
+    if (out && (out == q || out == k_pages || out == v_pages)) return RELATTN_ERR_INVALID_ARG;
+    if (H < 1 || Hkv < 1 || H % Hkv != 0) return RELATTN_ERR_INVALID_ARG;
+    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
+    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
+    if ((long long)tokens * H > (1LL << 31) - 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 1 && q_stride < (long long)H * d) return RELATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
+    if (clip_k < 0 || window < 0 || window > (1 << 30) || sinks < 0) return RELATTN_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
+    const void *elems[] = {q, k_pages, v_pages, aK, aV, out};
+    for (const void *p : elems)
+        if (p && !aligned(p, es)) return RELATTN_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4)) return RELATTN_ERR_INVALID_ARG;
+    if (aK || aV) {
+        if (table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
+        if (out && (out == aK || out == aV)) return RELATTN_ERR_INVALID_ARG;
+    }
+    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip)
+        return RELATTN_ERR_UNSUPPORTED;
+    if (tokens == 0) return RELATTN_OK;
+    if (!aligned(workspace, 16) || workspace_bytes < relattn::paged_workspace_bytes(d))
+        return RELATTN_ERR_INVALID_ARG;
+    relattn::PagedArgs a{};
+    a.q = q;
+    a.q_stride = tokens > 1 ? q_stride : (long long)H * d;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = num_pages > 1 ? page_stride : (long long)Hkv * page_size * d;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.bt_stride = table_stride;
+    a.max_pages = max_pages;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.aK = aK;
+    a.aV = aV;
+    a.ths = table_head_stride;
+    a.clip_k = aK || aV ? clip_k : 0;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.B = B;
+    a.tokens = tokens;
+    a.max_new = max_new;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bf16 = dtype == RELATTN_BF16 ? 1 : 0;
+    a.out = out;
+    a.workspace = workspace;
+    a.wait_limit = g_wait_limit.load();
+    const relattn_status_t st = paged_device(&a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_simt(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 relattn_status_t relattn_labels(int kind, int clip_k, int num_buckets, int max_distance,

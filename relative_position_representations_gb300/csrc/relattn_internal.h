@@ -202,4 +202,58 @@ unsigned long long bwd_tc_workspace_bytes(int B, int H, int n, int clip_k);
 bool bwd_tc_covers(const BwdArgs &a);
 cudaError_t launch_bwd_tc(const BwdArgs &a, cudaStream_t s);
 
+// ---- paged key/value cache ------------------------------------------------------------------
+constexpr int kPagedMaxClip = 256;       // clip_k of the paged attention
+constexpr int kPagedMaxGroup = 128;      // query heads per key/value head
+constexpr int kPagedMaxPageSize = 1024;  // keys per page (a power of two)
+constexpr int kPlanMaxSeqs = 16384;      // sequences of one plan (their prefix sits in shared memory)
+constexpr int kPlanMaxTokens = 1 << 23;  // new tokens of one plan
+
+struct PagedPlanArgs {
+    const int *cached_len, *new_len;  // [B]
+    int B, page_size, max_pages, max_tokens, num_free;
+    long long bt_stride;              // elements between rows of block_table
+    const int *free_pages, *free_head;
+    int *block_table, *kv_len, *q_start, *slots, *free_head_out;
+    int *err;                         // device status word
+};
+cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s);
+
+struct PagedAppendArgs {
+    const void *k, *v;                // [tokens, Hkv, d], k_stride / v_stride elements between tokens
+    long long k_stride, v_stride;
+    const int *slots;                 // [tokens]
+    void *k_pages, *v_pages;          // [num_pages, Hkv, page_size, d], page_stride between pages
+    long long page_stride;
+    int tokens, num_pages, Hkv, page_size, d;
+    int elem_bytes;                   // 2 or 4
+    int *err;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s);
+
+struct PagedArgs {
+    const void *q;                    // [tokens, H, d], q_stride elements between tokens
+    long long q_stride;
+    const void *k_pages, *v_pages;    // [num_pages, Hkv, page_size, d]
+    long long page_stride;
+    int num_pages, page_size;
+    const int *block_table;           // [B, max_pages], bt_stride between rows
+    long long bt_stride;
+    int max_pages;
+    const int *q_start, *kv_len;      // [B + 1], [B]
+    const void *aK, *aV;              // [Hkv|1, 2 clip_k + 1, d] or null
+    long long ths;                    // elements between heads' tables (0 = shared)
+    int clip_k, window, sinks;
+    float scale;
+    int B, tokens, max_new, H, Hkv, d;
+    int bf16;
+    void *out;                        // [tokens, H, d]
+    void *workspace;                  // at least paged_workspace_bytes
+    int *err;
+    long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)
+};
+unsigned long long paged_workspace_bytes(int d);
+// every type, head dimension <= 128 and page size; fp32 arithmetic on the SIMT units
+cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s);
+
 }  // namespace relattn
