@@ -742,7 +742,9 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
     a.wait_limit = g_wait_limit.load();
     const relattn_status_t st = paged_device(&a.err);
     if (st != RELATTN_OK) return st;
-    return from_cuda(relattn::launch_paged_simt(a, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (relattn::paged_decode_covers(a)) return from_cuda(relattn::launch_paged_decode(a, s));
+    return from_cuda(relattn::launch_paged_simt(a, s));
 }
 
 relattn_status_t relattn_labels(int kind, int clip_k, int num_buckets, int max_distance,

@@ -255,5 +255,9 @@ struct PagedArgs {
 unsigned long long paged_workspace_bytes(int d);
 // every type, head dimension <= 128 and page size; fp32 arithmetic on the SIMT units
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s);
+// at most 16 query rows (tokens x group) per key/value head: bf16, d = 64 or 128, pages of 8 keys
+// or more, 16-byte aligned rows
+bool paged_decode_covers(const PagedArgs &a);
+cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t s);
 
 }  // namespace relattn

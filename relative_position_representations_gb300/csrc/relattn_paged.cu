@@ -2,11 +2,54 @@
 // items; and the SIMT kernel, which covers every type, head dimension and page size.
 #include <cstdint>
 #include <cstring>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "relattn_paged.cuh"
 
 namespace relattn {
 namespace paged {
+
+DeviceInfo device_info() {
+    static DeviceInfo cache[64];
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DeviceInfo{};
+    std::lock_guard<std::mutex> lk(mu);
+    if (cache[dev].sms == 0) {
+        cudaDeviceGetAttribute(&cache[dev].sms, cudaDevAttrMultiProcessorCount, dev);
+        cudaDeviceGetAttribute(&cache[dev].smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    }
+    return cache[dev];
+}
+
+cudaError_t opt_in_smem(const void *kern, const DeviceInfo &di) {
+    static std::set<std::pair<int, const void *>> done;
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({dev, kern})) return cudaSuccess;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             di.smem_optin - (int)fa.sharedSizeBytes);
+    if (e == cudaSuccess) done.insert({dev, kern});
+    return e;
+}
+
+bool wide_rows(const PagedArgs &a) {
+    const long long es = a.bf16 ? 2 : 4;
+    const uint64_t m = (uint64_t)(a.d * es) | (uint64_t)(a.q_stride * es) | (uint64_t)(a.page_stride * es) |
+                       (uint64_t)(a.ths * es) | reinterpret_cast<uintptr_t>(a.q) |
+                       reinterpret_cast<uintptr_t>(a.k_pages) | reinterpret_cast<uintptr_t>(a.v_pages) |
+                       reinterpret_cast<uintptr_t>(a.aK) | reinterpret_cast<uintptr_t>(a.aV) |
+                       reinterpret_cast<uintptr_t>(a.out);
+    return m % 16 == 0;
+}
 
 void fill_params(const PagedArgs &a, Params *p) {
     std::memset(p, 0, sizeof(*p));
@@ -401,15 +444,11 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
                         reinterpret_cast<uintptr_t>(a.k_pages) | reinterpret_cast<uintptr_t>(a.v_pages) |
                         reinterpret_cast<uintptr_t>(a.aK) | reinterpret_cast<uintptr_t>(a.aV);
     const int vec = al % (4 * es) == 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return cudaErrorInvalidDevice;
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(paged_simt_kernel<T>), di);
     if (e != cudaSuccess) return e;
-    const int grid = 2 * sms < kMaxGrid ? 2 * sms : kMaxGrid;
+    const int grid = 2 * di.sms < kMaxGrid ? 2 * di.sms : kMaxGrid;
     paged_simt_kernel<T><<<grid, kSimtThreads, smem, s>>>(p, vec);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -332,6 +332,16 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
+struct DeviceInfo {
+    int sms = 0;
+    int smem_optin = 0;   // most dynamic shared memory of one block
+};
+// of the current device, asked once per device
+DeviceInfo device_info();
+// lets `kern` use all of it, once per kernel and device
+cudaError_t opt_in_smem(const void *kern, const DeviceInfo &di);
+// every row of q, the pages, the tables and out starts on a 16-byte boundary
+bool wide_rows(const PagedArgs &a);
 // Fills the parts of Params that do not depend on the kernel.
 void fill_params(const PagedArgs &a, Params *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent
