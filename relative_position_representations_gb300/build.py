@@ -24,6 +24,7 @@ SOURCES = ["relattn_host.cu", "relattn_simt.cu", "relattn_tc_d64.cu", "relattn_t
            "relattn_decode.cu", "relattn_bwd.cu", "relattn_labeled.cu", "relattn_labeled_tc.cu", "relattn_txl.cu",
            "relattn_short.cu", "relattn_bwd_tc.cu", "relattn_txl_tc.cu", "relattn_bias_bwd.cu",
            "relattn_paged.cu", "relattn_paged_plan.cu", "relattn_paged_decode.cu",
+           "relattn_paged_tc.cu",
            "t5_buckets.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I" + INCLUDE, "-I" + CSRC]

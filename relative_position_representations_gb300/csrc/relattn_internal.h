@@ -259,5 +259,9 @@ cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s);
 // or more, 16-byte aligned rows
 bool paged_decode_covers(const PagedArgs &a);
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t s);
+// tcgen05: bf16, d = 64 or 128, pages of 8 keys or more, clip_k <= 127, 16-byte aligned rows;
+// cudaErrorNotSupported (before any launch) when the tables leave no room for the key tiles
+bool paged_tc_covers(const PagedArgs &a);
+cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s);
 
 }  // namespace relattn

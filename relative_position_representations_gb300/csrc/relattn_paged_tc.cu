@@ -1,0 +1,995 @@
+// Paged attention on the tensor cores: chunks of prompts, whole prompts and generated tokens in
+// one launch. bf16, d = 64 or 128, pages of at least 8 keys, clip_k <= 127.
+//
+// The formulas are those of relattn_tc_kernel.cuh (section 3.4, eq. 3 and eq. 4 in split form,
+// causal): S = Q K^T, R = Q aK^T over the k + 1 table rows, O = P V + beta aV. What differs is where
+// the rows and keys come from and how the work is cut.
+//
+// Rows. The g query heads that share a key head are packed: TS = 128 / g tokens make one 128-row
+// tile, loaded by one TMA box of TS tokens x g heads. An item has up to two such tiles
+// ("slots") of one request and key head. Two full tiles share every K/V tile (the L2 traffic per
+// product halves). An item of one tile only runs its key tiles alternately in the two slots,
+// with a softmax state each, joined at its end: otherwise a generated token would leave half of
+// the CTA idle.
+// Keys. The producer looks up the pages of a tile (one lane per page, K and V share the entry) and
+// every lane issues the TMA box of its own page; pages that no row of the item sees are
+// skipped. Rows of V that no row sees may hold anything, NaN among it, and 0 * NaN is NaN: the
+// MMA warps overwrite them with zeros first (at most two tiles of a piece have such rows). K needs
+// no such care, scores of unseen keys are replaced, not added to.
+// Work is split over the CTAs by keys (relattn_paged.cuh).
+//
+// Roles (384 threads, one CTA per SM): warp 0 feeds the ring (aK, K and V tiles, aV, in the order
+// of use), warp 3 the query tiles, warps 1 and 2 issue the MMAs of slot 0 and 1, warps 4-7 and
+// 8-11 run the rows of slot 0 and 1, one thread per row. TMEM as in relattn_tc_kernel.cuh: S of
+// slot s at 128 s, O at 256 + d s, P (bf16) at 384 + 64 s (d = 64) or over the lower half of S
+// (d = 128), beta over the upper half of S.
+// The band of the last k keys needs no accumulation: each of its table rows meets one key per
+// query row, so the score (log2 domain) replaces the R entry it has just used, and beta is
+// formed from the scores at the end.
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "relattn_paged.cuh"
+#include "relattn_tc_launch.cuh"
+
+namespace relattn {
+namespace paged {
+namespace {
+
+using tc::BM;
+using tc::dup;
+using tc::max32;
+using tc::pair;
+using tc::put;
+using tc::Shared;
+using tc::slot_sync;
+using tc::wait_bar;
+using tc::wait_bar_ctrl;
+
+constexpr int kThreads = tc::kThreads;
+constexpr int kTcGrid = 160;                 // CTAs at most: one per SM
+static_assert(kTcGrid * 2 * BM <= kMaxGrid * kRecordRows, "records of the workspace");
+constexpr int KB = 32;                       // keys per softmax chunk
+constexpr int NCH = kTile / KB;
+constexpr int kMaxStages = 8;
+constexpr float kRescaleLog2 = tc::kRescaleLog2;
+
+template <int D>
+struct Tm {
+    static constexpr bool P_ALIAS = D == 128;
+    static __device__ __forceinline__ uint32_t S(int s) { return 128u * (uint32_t)s; }
+    static __device__ __forceinline__ uint32_t O(int s) { return 256u + (uint32_t)(D * s); }
+    static __device__ __forceinline__ uint32_t P(int s) { return P_ALIAS ? 128u * (uint32_t)s : 384u + 64u * (uint32_t)s; }
+    static __device__ __forceinline__ uint32_t Bn(int s) { return S(s) + 64u; }
+};
+
+enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
+enum : int { B_Q_FULL = 0, B_Q_EMPTY, B_X, B_SLOT0 = 3, B_KV0 = B_SLOT0 + 2 * kSlotBars };
+constexpr int kNumBars = B_KV0 + 2 * kMaxStages;
+
+struct TcParams {
+    Params p;
+    int TS;              // tokens per slot
+    int W, npad;         // table rows (clip_k + 1), rounded up to 16
+    int SR;              // row stride (floats) of the R rows in shared memory
+    int box;             // keys per TMA box: min(page_size, 128)
+    int stages;
+    uint32_t stage_bytes;
+    uint32_t off_q[2], off_kv, off_r[2], off_stat, off_bar;
+};
+
+// one slot's share of a piece
+struct SlotWork {
+    bool split;          // the two slots take the tiles of the same rows in turn
+    int tok0, ntok;      // tokens of the slot within the item
+    int pos_lo, pos_hi;  // their positions
+    int first;           // first key in the window of the slot's first token
+    int t_last;          // the last tile of the piece that the slot uses (t0 - 1: none)
+    __device__ __forceinline__ bool uses(const Params &p, const Segment &g, int slot, int t) const {
+        if (split) return ((t - g.t0) & 1) == slot;
+        const int j0 = g.it.tile(t) * kTile;
+        return j0 <= pos_hi && (j0 + kTile > first || j0 < p.sinks);
+    }
+};
+
+__device__ __forceinline__ SlotWork slot_work(const TcParams &tp, const Segment &g, int slot) {
+    const Params &p = tp.p;
+    SlotWork w;
+    w.split = g.it.cnt <= tp.TS;
+    w.tok0 = w.split ? 0 : slot * tp.TS;
+    w.ntok = min(tp.TS, g.it.cnt - w.tok0);
+    w.pos_lo = g.it.pos_lo + w.tok0;
+    w.pos_hi = w.pos_lo + w.ntok - 1;
+    w.first = p.window > 0 ? max(0, max(w.pos_lo, 0) - p.window + 1) : 0;
+    w.t_last = g.t1 - 1;
+    while (w.t_last >= g.t0 && !w.uses(p, g, slot, w.t_last)) --w.t_last;
+    return w;
+}
+
+__device__ __forceinline__ int item_first(const Params &p, const Item &it) {
+    return p.window > 0 ? max(0, max(it.pos_lo, 0) - p.window + 1) : 0;
+}
+
+// position in the ring
+struct Ring {
+    int st, n;
+    uint32_t ph;
+    __device__ __forceinline__ explicit Ring(int stages) : st(0), n(stages), ph(0) {}
+    __device__ __forceinline__ void next() {
+        if (++st == n) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Order of the ring entries of a piece: aK; then for i = 0, 1, ...: K_i, V_{i - lag}; aV. With P in
+// its own columns (d = 64) a slot's next scores are computed while its softmax still works, so its
+// next K comes before its V: one tile ahead, two where the slots take turns.
+template <int D>
+__device__ __forceinline__ int v_lag(bool split) {
+    return Tm<D>::P_ALIAS ? 0 : (split ? 2 : 1);
+}
+
+// ======================================================================= producers
+template <int D, bool AK, bool AV>
+__device__ void kv_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_k,
+                        const CUtensorMap *tm_v, const CUtensorMap *tm_ak, const CUtensorMap *tm_av) {
+    const Params &p = tp.p;
+    constexpr int DB = D / 64;
+    const int lane = threadIdx.x & 31;
+    const uint32_t bars = sh.base + tp.off_bar, sKV = sh.base + tp.off_kv;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        const bool r = wait_bar_ctrl(b, parity, sh, p.err);
+        return __all_sync(0xffffffffu, r ? 1 : 0) != 0;
+    };
+    const int nbox = kTile / tp.box;                 // boxes of a tile, at most 16
+    const int my_box = lane % nbox, my_blk = lane / nbox;
+    Ring ring(tp.stages);
+    uint32_t count = 0;
+    bool ok = true;
+    auto claim = [&]() -> bool { return wait(bar(B_KV0 + kMaxStages + ring.st), ring.ph ^ 1u); };
+    auto step = [&]() {
+        ring.next();
+        ++count;
+    };
+    auto table = [&](const CUtensorMap *tm, int kvh) -> bool {
+        if (!claim()) return false;
+        ptx::mbar_expect_tx_w(bar(B_KV0 + ring.st), (uint32_t)tp.npad * D * 2);
+#pragma unroll
+        for (int blk = 0; blk < DB; ++blk)
+            ptx::tma_load_3d_w(sKV + (uint32_t)ring.st * tp.stage_bytes + blk * tp.npad * 128, tm,
+                               bar(B_KV0 + ring.st), blk * 64, 0, p.ths ? kvh : 0);
+        step();
+        return true;
+    };
+    Walk walk(p, rg);
+    Segment g{};
+    while (ok && walk.next(p, g)) {
+        const int nt = g.t1 - g.t0;
+        if (nt == 0) continue;
+        const bool split = g.it.cnt <= tp.TS;
+        const int lag = v_lag<D>(split);
+        const int first = item_first(p, g.it);
+        const int *bt = p.bt + (long long)g.b * p.bt_stride;
+        if (AK && !(ok = table(tm_ak, g.kvh))) break;
+        // this lane's box of tile t: page number (or -1), and whether any row sees a key of it
+        auto lookup = [&](int t, bool &seen) -> int {
+            const int j = g.it.tile(t) * kTile + my_box * tp.box;
+            seen = t < g.t1 && j <= g.it.pos_hi && (j + tp.box > first || j < p.sinks);
+            return seen ? __ldg(bt + (j >> p.pshift)) : -1;
+        };
+        // pages of tiles i, i - 1 and i - 2 (V comes up to two tiles behind K), tile i + 1 ahead
+        bool sn, s0 = false, s1 = false, s2 = false;
+        int pn = lookup(g.t0, sn), p0 = -1, p1 = -1, p2 = -1;
+        auto load = [&](const CUtensorMap *tm, int t, int pg, bool seen) -> bool {
+            if (!claim()) return false;
+            const uint32_t full = bar(B_KV0 + ring.st);
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
+            ptx::mbar_expect_tx_w(full, (uint32_t)__popc(m) * tp.box * D * 2);
+            __syncwarp();
+            const int j = g.it.tile(t) * kTile + my_box * tp.box;
+            const int row = j & ((1 << p.pshift) - 1);
+            if (seen && my_blk < DB) {
+                const bool bad = (unsigned)pg >= (unsigned)p.num_pages;
+                if (bad) report_page(p);
+                // a page outside the cache: a box outside the tensor, which reads as zeros
+                tma_load_4d(sKV + (uint32_t)ring.st * tp.stage_bytes + my_blk * kTile * 128 + my_box * tp.box * 128, tm,
+                            full, my_blk * 64, row, g.kvh, bad ? p.num_pages : pg);
+            }
+            __syncwarp();
+            step();
+            return true;
+        };
+        for (int i = 0; i < nt + lag && ok; ++i) {
+            p2 = p1; s2 = s1;
+            p1 = p0; s1 = s0;
+            p0 = pn; s0 = sn;
+            if (i < nt) {
+                pn = lookup(g.t0 + i + 1, sn);
+                if (!(ok = load(tm_k, g.t0 + i, p0, s0))) break;
+            }
+            if (i >= lag) {
+                const int pv = lag == 0 ? p0 : lag == 1 ? p1 : p2;
+                const bool sv = lag == 0 ? s0 : lag == 1 ? s1 : s2;
+                ok = load(tm_v, g.t0 + i - lag, pv, sv);
+            }
+        }
+        if (ok && AV) ok = table(tm_av, g.kvh);
+    }
+    // the copies issued into shared memory have landed before the CTA exits
+    for (uint32_t i = count > (uint32_t)tp.stages ? count - tp.stages : 0; i < count; ++i)
+        tc::drain_bar(bar(B_KV0 + (int)(i % tp.stages)), (i / tp.stages) & 1u, sh.limit);
+}
+
+template <int D>
+__device__ void q_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_q) {
+    const Params &p = tp.p;
+    constexpr int DB = D / 64;
+    const uint32_t bars = sh.base + tp.off_bar;
+    const uint32_t full = bars + 8u * B_Q_FULL, empty = bars + 8u * B_Q_EMPTY;
+    Walk walk(p, rg);
+    Segment g{};
+    uint32_t it = 0;
+    while (walk.next(p, g)) {
+        if (g.t1 == g.t0) continue;
+        const bool r = wait_bar_ctrl(empty, (it & 1u) ^ 1u, sh, p.err);
+        if (!__all_sync(0xffffffffu, r ? 1 : 0)) break;
+        const int ns = g.it.cnt <= tp.TS ? 1 : 2;
+        ptx::mbar_expect_tx_w(full, (uint32_t)ns * tp.TS * p.g * D * 2);
+        for (int s = 0; s < ns; ++s)
+#pragma unroll
+            for (int blk = 0; blk < DB; ++blk)
+                ptx::tma_load_3d_w(sh.base + tp.off_q[s] + blk * BM * 128, tm_q, full, blk * 64, g.kvh * p.g,
+                                   g.s.q0 + g.it.i0 + s * tp.TS);
+        ++it;
+    }
+    if (it) tc::drain_bar(full, (it - 1) & 1u, sh.limit);
+}
+
+// ======================================================================= MMA issuers
+// One warp per slot; both walk every ring entry and each releases it, so the release barriers
+// count two arrivals; an entry, or Q, is released only after it was waited for.
+template <int D, bool AK, bool AV>
+__device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, uint32_t tmem, int slot_in) {
+    using T = Tm<D>;
+    const Params &p = tp.p;
+    const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
+    const int lane = threadIdx.x & 31;
+    const uint32_t bars = sh.base + tp.off_bar;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    auto sbar = [&](int which) { return bar(B_SLOT0 + kSlotBars * slot + which); };
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        const bool r = wait_bar_ctrl(b, parity, sh, p.err);
+        return __all_sync(0xffffffffu, r ? 1 : 0) != 0;
+    };
+    const uint64_t dk0 = ptx::sdesc_sw128(sh.base + tp.off_kv, 16, 1024);
+    const uint64_t dv0 = ptx::sdesc_sw128(sh.base + tp.off_kv, kTile * 128, 1024);
+    const uint64_t stage16 = tp.stage_bytes >> 4;
+    const uint32_t tS = tmem + T::S(slot), tO = tmem + T::O(slot), tP = tmem + T::P(slot), tB = tmem + T::Bn(slot);
+    constexpr uint32_t idS = ptx::idesc_bf16(BM, kTile, 0), idPV = ptx::idesc_bf16(BM, D, 1);
+    auto kstep = [](int kk, int rows) -> uint64_t {
+        return (uint64_t)(((kk >> 2) * rows * 128 + (kk & 3) * 32) >> 4);
+    };
+    Ring ring(tp.stages);
+    uint32_t q_it = 0, s_it = 0, p_it = 0, pv_it = 0, bn_it = 0, bd_it = 0;
+    bool pv_pending = false, bn_pending = false, ok = true;
+
+    // before an MMA writes the slot's S columns: the rows have read the previous scores, and the
+    // MMAs that read P (over S) or beta from those columns are done
+    auto claim_s = [&]() -> bool {
+        if (bn_pending) {
+            if (!wait(sbar(SB_BN_DONE), (bd_it - 1u) & 1u)) return false;
+            bn_pending = false;
+        }
+        if (T::P_ALIAS && pv_pending) {
+            if (!wait(sbar(SB_PV_DONE), (pv_it - 1u) & 1u)) return false;
+            pv_pending = false;
+        }
+        if (!wait(sbar(SB_S_EMPTY), (s_it & 1u) ^ 1u)) return false;
+        ++s_it;
+        ptx::tc_fence_after();
+        return true;
+    };
+    Walk walk(p, rg);
+    Segment g{};
+    while (ok && walk.next(p, g)) {
+        const int nt = g.t1 - g.t0;
+        if (nt == 0) continue;
+        const SlotWork w = slot_work(tp, g, slot);
+        const bool act = w.t_last >= g.t0;
+        const bool tables = act && (!w.split || slot == 0);   // R and beta belong to this slot
+        const int lag = v_lag<D>(w.split);
+        const uint64_t dq = ptx::sdesc_sw128(sh.base + tp.off_q[w.split ? 0 : slot], 16, 1024);
+        const int first = item_first(p, g.it);
+        if (!(ok = wait(bar(B_Q_FULL), q_it & 1u))) break;
+        ++q_it;
+        ptx::tc_fence_after();
+        if (!act) ptx::mbar_arrive_w(bar(B_Q_EMPTY));
+        if (AK) {   // R = Q aK^T into the slot's S columns
+            if (!(ok = wait(bar(B_KV0 + ring.st), ring.ph))) break;
+            const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
+            if (tables) {
+                if (!(ok = claim_s())) break;
+                const uint32_t idR = ptx::idesc_bf16(BM, (uint32_t)tp.npad, 0);
+                const uint64_t da = dk0 + (uint64_t)ring.st * stage16;
+#pragma unroll 1
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ptx::tc_mma_w(tS, dq + kstep(kk, BM), da + kstep(kk, tp.npad), idR, kk > 0 ? 1u : 0u);
+                ptx::tc_commit_w(sbar(SB_S_FULL));
+                ptx::tc_commit_w(empty);
+            } else {
+                ptx::mbar_arrive_w(empty);
+            }
+            ring.next();
+        }
+        bool started = false;
+        for (int i = 0; i < nt + lag && ok; ++i) {
+            if (i < nt) {   // S_i = Q K_i^T
+                const int t = g.t0 + i;
+                if (!(ok = wait(bar(B_KV0 + ring.st), ring.ph))) break;
+                const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
+                if (w.uses(p, g, slot, t)) {
+                    ptx::tc_fence_after();
+                    if (!(ok = claim_s())) break;
+                    const uint64_t dk = dk0 + (uint64_t)ring.st * stage16;
+                    if (D == 128) ptx::tc_mma_ss_k128(tS, dq, dk, idS, 0u);
+                    else ptx::tc_mma_ss_k64(tS, dq, dk, idS, 0u);
+                    ptx::tc_commit_w(sbar(SB_S_FULL));
+                    ptx::tc_commit_w(empty);
+                    if (t == w.t_last) ptx::tc_commit_w(bar(B_Q_EMPTY));   // last read of Q
+                } else {
+                    ptx::mbar_arrive_w(empty);
+                }
+                ring.next();
+            }
+            if (i >= lag) {   // O += P V
+                const int t = g.t0 + i - lag;
+                if (!(ok = wait(bar(B_KV0 + ring.st), ring.ph))) break;
+                const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
+                if (w.uses(p, g, slot, t)) {
+                    // rows of V that no row of the item sees
+                    const int j0 = g.it.tile(t) * kTile;
+                    const int n_seen = g.it.pos_hi + 1 - j0;                   // rows below are within the cache
+                    const int u0 = max(0, p.sinks - j0), u1 = first - j0;      // rows u0 .. u1 - 1 lie behind the window
+                    if (n_seen < kTile || u1 > u0) {
+                        const uint32_t base = sh.base + tp.off_kv + (uint32_t)ring.st * tp.stage_bytes;
+                        for (int r = lane; r < kTile; r += 32)
+                            if (r >= n_seen || (r >= u0 && r < u1)) {
+#pragma unroll
+                                for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c)
+                                        ptx::st_shared_v4(base + blk * kTile * 128 + r * 128 + c * 16, 0, 0, 0, 0);
+                            }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (!(ok = wait(sbar(SB_P_FULL), p_it & 1u))) break;
+                    ++p_it;
+                    ptx::tc_fence_after();
+                    ptx::tc_mma_ts_k128(tO, tP, dv0 + (uint64_t)ring.st * stage16, idPV, started ? 1u : 0u);
+                    started = true;
+                    ptx::tc_commit_w(sbar(SB_PV_DONE));
+                    ++pv_it;
+                    pv_pending = true;
+                    ptx::tc_commit_w(empty);
+                } else {
+                    ptx::mbar_arrive_w(empty);
+                }
+                ring.next();
+            }
+        }
+        if (!ok) break;
+        if (AV) {   // O += beta aV
+            if (!(ok = wait(bar(B_KV0 + ring.st), ring.ph))) break;
+            const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
+            if (tables) {
+                if (!(ok = wait(sbar(SB_BN_FULL), bn_it & 1u))) break;
+                ++bn_it;
+                ptx::tc_fence_after();
+                const uint64_t da = ptx::sdesc_sw128(sh.base + tp.off_kv + (uint32_t)ring.st * tp.stage_bytes,
+                                                     (uint32_t)tp.npad * 128, 1024);
+#pragma unroll 1
+                for (int kk = 0; kk < tp.npad / 16; ++kk)
+                    ptx::tc_mma_ts_w(tO, tB + (uint32_t)(kk * 8), da + (uint64_t)(kk * 16 * 128 >> 4), idPV, 1u);
+                ptx::tc_commit_w(sbar(SB_BN_DONE));
+                ++bd_it;
+                bn_pending = true;
+                ptx::tc_commit_w(empty);
+            } else {
+                ptx::mbar_arrive_w(empty);
+            }
+            ring.next();
+        }
+        if (act) ptx::tc_commit_w(sbar(SB_O_FULL));
+    }
+    // every MMA issued by this warp completes before TMEM is released
+    ptx::tc_commit_w(sbar(SB_DRAIN));
+    tc::drain_bar(sbar(SB_DRAIN), 0, sh.limit);
+}
+
+// ======================================================================= softmax / epilogue
+template <int D, bool AK, bool AV>
+__device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, uint32_t tmem, int slot_in) {
+    using T = Tm<D>;
+    const Params &p = tp.p;
+    const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const int quad = uni(warp & 3);
+    const int row = quad * 32 + lane;
+    const int tok = row / p.g, hh = row - tok * p.g;   // token within the slot, head within the group
+    const int tok_lo = (quad * 32) / p.g, tok_hi = (quad * 32 + 31) / p.g;   // of this warp's rows
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t bars = sh.base + tp.off_bar;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    auto sbar_of = [&](int s, int which) { return bar(B_SLOT0 + kSlotBars * s + which); };
+    auto sbar = [&](int which) { return sbar_of(slot, which); };
+    float2 *stat = reinterpret_cast<float2 *>(sh.ptr + tp.off_stat);   // [slot][row] {m, l}
+    const float sl2 = p.scale_log2;
+    const bool pos_scale = sl2 >= 0.f;
+    const int k = p.clip_k, W = tp.W;
+    uint32_t s_it = 0, pv_it = 0, x_it = 0, o_it[2] = {0, 0};
+    bool ok = true;
+    // one warp of the slot polls, the others meet it at the slot's named barrier
+    auto wait_w = [&](uint32_t b, uint32_t parity) -> bool {
+        bool r = true;
+        if (quad == 0) {
+            r = wait_bar(b, parity, sh, p.err);
+            r = __all_sync(0xffffffffu, r ? 1 : 0) != 0;
+        }
+        return slot_sync(slot, r);
+    };
+    auto wait_s = [&]() -> bool {
+        if (!wait_w(sbar(SB_S_FULL), s_it & 1u)) return false;
+        ++s_it;
+        ptx::tc_fence_after();
+        __syncwarp();
+        return true;
+    };
+    auto release_s = [&]() {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(sbar(SB_S_EMPTY));
+    };
+    auto wait_pv = [&](uint32_t c) -> bool {
+        if (!wait_w(sbar(SB_PV_DONE), c & 1u)) return false;
+        ptx::tc_fence_after();
+        __syncwarp();
+        return true;
+    };
+    // both slots' rows (a bounded wait like every other, so an abort reaches both)
+    auto sync_slots = [&]() -> bool {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(B_X));
+        if (!wait_w(bar(B_X), x_it & 1u)) return false;
+        ++x_it;
+        ptx::tc_fence_after();
+        __syncwarp();
+        return true;
+    };
+    auto wait_o = [&](int s) -> bool {
+        if (!wait_w(sbar_of(s, SB_O_FULL), o_it[s] & 1u)) return false;
+        ptx::tc_fence_after();
+        __syncwarp();
+        return true;
+    };
+    // O *= f (rows of this warp)
+    auto scale_o = [&](float f) {
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld32(lane_base + T::O(slot) + (uint32_t)c0, r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), dup(f));
+                r[e] = __float_as_uint(v.x);
+                r[e + 1] = __float_as_uint(v.y);
+            }
+            ptx::tmem_st32(lane_base + T::O(slot) + (uint32_t)c0, r);
+        }
+        ptx::tmem_st_wait();
+    };
+    Walk walk(p, rg);
+    Segment g{};
+    bool any = false;
+    while (ok && walk.next(p, g)) {
+        any = true;
+        const SlotWork w = slot_work(tp, g, slot);
+        const bool split = w.split;
+        const bool act = w.t_last >= g.t0;
+        const bool two = split && g.t1 - g.t0 > 1;      // the other slot works on the same rows
+        const int rows = w.ntok * p.g;                  // may be negative: no rows in this slot
+        const bool mine = quad * 32 < rows;             // this warp has rows
+        const bool valid = row < rows;
+        const int pos = valid ? w.pos_lo + tok : -1;
+        const int pmin = uni(w.pos_lo + tok_lo), pmax = uni(min(w.pos_lo + tok_hi, w.pos_hi));
+        float *Rrow = reinterpret_cast<float *>(sh.ptr + tp.off_r[split ? 0 : slot]) + row * tp.SR;
+        const bool whole = g.whole();
+        const int rrow = (split ? 0 : slot * tp.TS * p.g) + row;
+        float *rec = whole ? nullptr : record(p, blockIdx.x, g.record());
+        __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.out) +
+                              ((long long)(g.s.q0 + g.it.i0 + w.tok0 + tok) * p.H + g.kvh * p.g + hh) * D;
+        if (g.t1 == g.t0 || (!split && !act)) {   // no key in this piece for any row of the slot
+            if (valid && !(split && slot == 1)) {
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(orow)[c] = make_uint4(0, 0, 0, 0);
+                } else {
+                    rec[rrow] = -INFINITY;
+                    rec[p.rec_rows + rrow] = 0.f;
+                    for (int c = 0; c < D; c += 2)
+                        *reinterpret_cast<float2 *>(rec + 2 * p.rec_rows + (long long)rrow * D + c) = make_float2(0.f, 0.f);
+                }
+            }
+            if (split || g.t1 == g.t0) continue;
+            // (pair mode) the other slot may have tiles of its own; nothing is shared with it
+            if (slot == 1) o_it[0] += slot_work(tp, g, 0).t_last >= g.t0 ? 1 : 0;
+            else o_it[1] += slot_work(tp, g, 1).t_last >= g.t0 ? 1 : 0;
+            continue;
+        }
+        if (AK && (!split || slot == 0)) {   // R row -> shared memory (log2 domain)
+            if (!(ok = wait_s())) break;
+            if (mine)
+                for (int c0 = 0; c0 < tp.npad; c0 += 16) {
+                    uint32_t r[16];
+                    ptx::tmem_ld16(lane_base + T::S(slot) + (uint32_t)c0, r);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c0 + e < W) Rrow[c0 + e] = __uint_as_float(r[e]) * sl2;
+                }
+            release_s();
+        }
+        if (split && !(ok = sync_slots())) break;
+        const float c_left = AK && mine ? Rrow[0] : 0.f;
+        float m_ref = -INFINITY, l = 0.f;
+        uint32_t n = 0;   // tiles of the slot so far
+
+        for (int t = g.t0; t <= w.t_last; ++t) {
+            if (!w.uses(p, g, slot, t)) continue;
+            const int j0 = g.it.tile(t) * kTile;
+            if (!(ok = wait_s())) break;
+            const bool last = t == w.t_last;
+            const bool keep_s = AV && last && (!split || slot == 0);   // beta will lie there
+            float x[kTile];
+            // chunk c: seen by no row of the warp / without masks / all offsets beyond the band
+            auto dead = [&](int c) -> bool {
+                const int e0 = j0 + c * KB;
+                return e0 > pmax || (p.window > 0 && e0 + KB - 1 <= pmin - p.window && e0 >= p.sinks);
+            };
+            auto full = [&](int c) -> bool {
+                const int e0 = j0 + c * KB;
+                return e0 + KB - 1 <= pmin && (p.window == 0 || e0 > pmax - p.window || e0 + KB <= p.sinks);
+            };
+            auto far = [&](int c) -> bool { return j0 + c * KB + KB - 1 <= pmin - k; };
+            auto raw = [&](int c) -> bool { return full(c) && (!AK || far(c)) && pos_scale && (!AV || far(c)); };
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < NCH; ++c)
+                    if (!dead(c)) ptx::tmem_ld32f(lane_base + T::S(slot) + (uint32_t)(c * KB), x + c * KB);
+                ptx::tmem_ld_wait();
+            }
+            if (!keep_s) release_s();
+            float alpha = 1.f;
+            if (mine) {
+                // ---- logits in the log2 domain; raw chunks stay as they are (their scale and
+                // constant go into the exponent)
+                float rmax = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    if (dead(c)) continue;
+                    float *xc = x + c * KB;
+                    if (raw(c)) {
+                        rmax = fmaxf(rmax, fmaf(max32(xc), sl2, c_left));
+                        continue;
+                    }
+                    const int e0 = j0 + c * KB;
+                    const int rb = e0 - pos + k;   // table row of element 0, before clamping
+                    if (AK && !far(c)) {
+#pragma unroll
+                        for (int e = 0; e < KB; e += 2) {
+                            const float2 r = make_float2(Rrow[min(k, max(0, rb + e))], Rrow[min(k, max(0, rb + e + 1))]);
+                            put(xc, e, __ffma2_rn(pair(xc, e), dup(sl2), r));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < KB; e += 2) put(xc, e, __ffma2_rn(pair(xc, e), dup(sl2), dup(c_left)));
+                    }
+                    if (!full(c)) {
+                        const int hi = pos - e0;                                         // seen: e <= hi and
+                        const int lo = p.window > 0 ? pos - p.window - e0 : -1 - e0;     // (e > lo or
+                        const int sk = p.sinks - e0;                                     // e < sk)
+#pragma unroll
+                        for (int e = 0; e < KB; ++e) xc[e] = e <= hi && (e > lo || e < sk) ? xc[e] : -INFINITY;
+                    }
+                    if (AV && !far(c)) {   // the score takes the place of the table row it used
+#pragma unroll
+                        for (int e = 0; e < KB; ++e)
+                            if (rb + e > 0 && rb + e <= k) Rrow[rb + e] = xc[e];
+                    }
+                    rmax = fmaxf(rmax, max32(xc));
+                }
+                if (rmax > m_ref + kRescaleLog2) {
+                    alpha = ptx::ex2(m_ref - rmax);
+                    m_ref = rmax;
+                }
+            }
+            // P and O are free once the previous P V is done (P over S: S_j was issued after it)
+            if (!T::P_ALIAS && n > 0 && !(ok = wait_pv(pv_it + n - 1u))) break;
+            if (mine) {
+                if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    l *= alpha;
+                    __syncwarp();
+                    scale_o(alpha);
+                }
+                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+                for (int c = 0; c < NCH; ++c) {
+                    float *xc = x + c * KB;
+                    if (dead(c)) {
+#pragma unroll
+                        for (int e = 0; e < KB / 2; ++e) xc[e] = 0.f;
+                    } else {
+                        const bool rw = raw(c);
+                        const float2 a2 = dup(rw ? sl2 : 1.f), b2 = dup((rw ? c_left : 0.f) - m_use);
+                        float2 s01 = dup(0.f), s23 = dup(0.f);
+#pragma unroll
+                        for (int e = 0; e < KB; e += 4) {
+                            const float2 t0 = __ffma2_rn(pair(xc, e), a2, b2);
+                            const float2 t1 = __ffma2_rn(pair(xc, e + 2), a2, b2);
+                            xc[e] = ptx::ex2(t0.x);
+                            xc[e + 1] = ptx::ex2(t0.y);
+                            xc[e + 2] = ptx::ex2(t1.x);
+                            xc[e + 3] = ptx::ex2(t1.y);
+                            s01 = __fadd2_rn(s01, pair(xc, e));
+                            s23 = __fadd2_rn(s23, pair(xc, e + 2));
+                        }
+                        l += (s01.x + s01.y) + (s23.x + s23.y);
+                        // bf16: the tensor cores' operand; l keeps the fp32 values
+#pragma unroll
+                        for (int e = 0; e < KB / 2; ++e)
+                            xc[e] = __uint_as_float(ptx::pack_bf16x2(xc[2 * e], xc[2 * e + 1]));
+                    }
+                    __syncwarp();
+                    ptx::tmem_st16f(lane_base + T::P(slot) + (uint32_t)(c * (KB / 2)), xc);
+                }
+                ptx::tmem_st_wait();
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(sbar(SB_P_FULL));
+            ++n;
+        }
+        if (!ok) break;
+        pv_it += n;
+        // ---- the row's maximum and sum; where the slots shared the rows, of both
+        float M = m_ref, f0 = 1.f, f1 = 0.f;
+        if (two) {
+            stat[slot * BM + row] = make_float2(m_ref, l);
+            if (!(ok = sync_slots())) break;
+            const float2 other = stat[(1 - slot) * BM + row];
+            M = fmaxf(m_ref, other.x);
+            const float Mu = M == -INFINITY ? 0.f : M;
+            const float fm = ptx::ex2(m_ref - Mu), fo = ptx::ex2(other.x - Mu);
+            l = slot == 0 ? fmaf(l, fm, other.y * fo) : fmaf(other.y, fo, l * fm);
+            f0 = slot == 0 ? fm : fo;
+            f1 = slot == 0 ? fo : fm;
+        }
+        if (AV) {
+            if (!split || slot == 0) {
+                if (two) {   // beta joins O of slot 0, which takes the common maximum first
+                    if (!(ok = wait_pv(pv_it - 1u))) break;
+                    if (mine) scale_o(f0);
+                }
+                if (mine) {
+                    // weights of the band's rows from their scores; row 0 gets the rest of the sum
+                    const float Mu = M == -INFINITY ? 0.f : M;
+                    const int jb = pos - k;   // key of table row r: jb + r
+                    auto weight = [&](int r) -> float {
+                        const int j = jb + r, kt = j >> 7;
+                        const int t = kt < g.it.ns ? kt : kt - g.it.lo + g.it.ns;
+                        const bool seen = valid && r <= k && j >= 0 &&
+                                          (p.window == 0 || j > pos - p.window || j < p.sinks);
+                        const bool here = seen && t >= g.t0 && t < g.t1;   // its score is of this piece
+                        return here ? ptx::ex2(Rrow[r] - Mu) : 0.f;
+                    };
+                    float band = 0.f;
+                    for (int r = 1; r <= k; ++r) band += weight(r);
+                    const float rest = fmaxf(0.f, l - band);
+                    for (int c0 = 0; c0 < tp.npad; c0 += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int r0 = c0 + 2 * e;
+                            const float b0 = r0 == 0 ? rest : weight(r0), b1 = weight(r0 + 1);
+                            pk[e] = ptx::pack_bf16x2(b0, b1);
+                        }
+                        __syncwarp();
+                        ptx::tmem_st16(lane_base + T::Bn(slot) + (uint32_t)(c0 / 2), pk);
+                    }
+                    ptx::tmem_st_wait();
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(sbar(SB_BN_FULL));
+                ptx::mbar_arrive(sbar(SB_S_EMPTY));
+            }
+            if (two) f0 = 1.f;
+        }
+        // ---- epilogue
+        if (two || slot == 0 || !split) {
+            if (!(ok = wait_o(split ? 0 : slot))) break;
+            if (two && !(ok = wait_o(1))) break;
+            if (mine) {
+                const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                if (valid && !whole && slot == (split ? 0 : slot)) {
+                    rec[rrow] = M;
+                    rec[p.rec_rows + rrow] = l;
+                }
+                const uint32_t oA = lane_base + T::O(split ? 0 : slot), oB = lane_base + T::O(1);
+                // each slot writes half of the columns where both hold the rows
+                const int cb = two && slot == 1 ? D / 2 : 0, ce = two && slot == 0 ? D / 2 : D;
+                for (int c0 = cb; c0 < ce; c0 += 32) {
+                    float r[32];
+                    ptx::tmem_ld32f(oA + (uint32_t)c0, r);
+                    ptx::tmem_ld_wait();
+                    if (two) {
+                        float r1[32];
+                        ptx::tmem_ld32f(oB + (uint32_t)c0, r1);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            put(r, e, __ffma2_rn(pair(r1, e), dup(f1), __fmul2_rn(pair(r, e), dup(f0))));
+                    }
+                    if (valid) {
+                        if (whole) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t o4[4];
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    const float2 o = __fmul2_rn(pair(r, 8 * q + 2 * h), dup(inv));
+                                    o4[h] = ptx::pack_bf16x2(o.x, o.y);
+                                }
+                                reinterpret_cast<uint4 *>(orow)[c0 / 8 + q] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                            }
+                        } else {
+                            float *dst = rec + 2 * p.rec_rows + (long long)rrow * D + c0;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4 *>(dst + e) = make_float4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            ptx::tc_fence_before();
+        }
+        // completions of both slots' O barriers in this piece
+        if (split) {
+            ++o_it[0];
+            if (two) ++o_it[1];
+            if (!(ok = sync_slots())) break;   // O, R and the statistics go to the next piece
+        } else {
+            ++o_it[slot];
+            o_it[1 - slot] += slot_work(tp, g, 1 - slot).t_last >= g.t0 ? 1 : 0;
+        }
+    }
+    if (slot == 0 && row == 0) write_desc(p, any && ok ? &g : nullptr, rg.total);
+}
+
+// ======================================================================= kernel
+template <int D, bool AK, bool AV>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ak,
+                    const __grid_constant__ CUtensorMap tm_av, const __grid_constant__ TcParams tp) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const Params &p = tp.p;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    Shared sh;
+    sh.base = (raw + 1023u) & ~1023u;
+    sh.ptr = smem_raw + (sh.base - raw);
+    uint64_t *bar_ptr = reinterpret_cast<uint64_t *>(sh.ptr + tp.off_bar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_ptr + kNumBars);
+    sh.abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    sh.limit = p.wait_limit;
+    const int warp = threadIdx.x >> 5;
+    const uint32_t bars = sh.base + tp.off_bar;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            uint32_t cnt = 1;
+            if (i >= B_SLOT0 && i < B_KV0) {
+                const int which = (i - B_SLOT0) % kSlotBars;
+                if (which == SB_S_EMPTY || which == SB_P_FULL || which == SB_BN_FULL) cnt = 128;
+            }
+            if (i == B_Q_EMPTY || i >= B_KV0 + kMaxStages) cnt = 2;
+            if (i == B_X) cnt = 256;
+            ptx::mbar_init(bars + 8u * (uint32_t)i, cnt);
+        }
+        *sh.abort_flag = 0;
+        ptx::mbar_init_fence();
+        ptx::tma_prefetch_desc(&tm_q);
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_raw = *tmem_slot;
+    const Range rg = find_range<kThreads>(p, reinterpret_cast<long long *>(sh.ptr + tp.off_stat));
+    __syncthreads();
+    if (warp < tc::kSoftWarp0) {
+        ptx::reg_dealloc<tc::kCtrlRegs>();
+        if (warp == 0) {
+            (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
+            kv_role<D, AK, AV>(tp, rg, sh, &tm_k, &tm_v, &tm_ak, &tm_av);
+        } else if (warp == 3) {
+            (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
+            q_role<D>(tp, rg, sh, &tm_q);
+        } else {
+            const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
+            mma_role<D, AK, AV>(tp, rg, sh, tmem, warp - 1);
+        }
+        __syncwarp();
+    } else {
+        ptx::reg_alloc<tc::kSoftRegs>();
+        const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
+        row_role<D, AK, AV>(tp, rg, sh, tmem, (warp - tc::kSoftWarp0) >> 2);
+    }
+    ptx::tc_fence_before();
+    ptx::cta_barrier();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem_raw, 512);
+    }
+}
+
+// ======================================================================= host
+// Shared memory for items of two tiles (wide) or one; false when fewer than `min_stages` stages
+// of the ring fit.
+template <int D>
+bool layout(TcParams *tp, bool wide, bool tables, int smem_optin, int min_stages) {
+    uint32_t off = 0;
+    for (int s = 0; s < 2; ++s) {
+        tp->off_q[s] = off;
+        if (s == 0 || wide) off += (uint32_t)BM * D * 2;
+    }
+    tp->off_kv = off;
+    uint32_t rest = 0;
+    const uint32_t r_bytes = tables ? (uint32_t)BM * tp->SR * 4 : 0;
+    const uint32_t fixed = off + r_bytes * (wide ? 2 : 1) + 2 * BM * 8 + kNumBars * 8 + 16 + 1024;
+    tp->stage_bytes = (uint32_t)kTile * D * 2;
+    if ((int)fixed > smem_optin) return false;
+    int st = (int)((smem_optin - fixed) / tp->stage_bytes);
+    if (st > kMaxStages) st = kMaxStages;
+    if (st < min_stages) return false;
+    tp->stages = st;
+    rest = off + (uint32_t)st * tp->stage_bytes;
+    for (int s = 0; s < 2; ++s) {
+        tp->off_r[s] = rest;
+        if (s == 0 || wide) rest += r_bytes;
+    }
+    tp->off_stat = rest;
+    rest += 2 * BM * 8;
+    tp->off_bar = rest;
+    return true;
+}
+
+bool make_page_map(CUtensorMap *m, const void *ptr, const PagedArgs &a, int box) {
+    tc::EncodeTiledFn enc = tc::encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dim[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+    const cuuint64_t stride[3] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.page_size * a.d * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t bx[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dim, stride, bx, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_query_map(CUtensorMap *m, const PagedArgs &a, int g, int TS) {
+    tc::EncodeTiledFn enc = tc::encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dim[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.tokens};
+    const cuuint64_t stride[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t bx[3] = {64, (cuuint32_t)g, (cuuint32_t)TS}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dim, stride, bx, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool AK, bool AV>
+cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaStream_t s) {
+    auto kern = paged_tc_kernel<D, AK, AV>;
+    const DeviceInfo di = device_info();
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
+    if (e != cudaSuccess) return e;
+    {   // the warpgroups' register shares add up only at this count (checked once per device)
+        static bool checked[64] = {};
+        static std::mutex mu;
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lk(mu);
+        if (!checked[dev & 63]) {
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, kern);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != tc::kLaunchRegs) return cudaErrorNotSupported;
+            checked[dev & 63] = true;
+        }
+    }
+    const int grid = di.sms < kTcGrid ? di.sms : kTcGrid;
+    const uint32_t smem = tp.off_bar + kNumBars * 8 + 16 + 1024;
+    kern<<<grid, kThreads, smem, s>>>(tm[0], tm[1], tm[2], tm[3], tm[4], tp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_merge(tp.p, grid, true, s);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return cudaErrorInvalidDevice;
+    TcParams tp;
+    std::memset(&tp, 0, sizeof(tp));
+    Params &p = tp.p;
+    fill_params(a, &p);
+    tp.TS = BM / p.g;
+    tp.W = a.clip_k + 1;
+    tp.npad = (tp.W + 15) / 16 * 16;
+    tp.SR = tp.W;                     // even, so that a warp's gathers along the band (stride SR - 1) hit
+    while (tp.SR % 4 != 2) ++tp.SR;   // 32 banks; 2 mod 4, so that its column walks hit 16
+    tp.box = a.page_size < kTile ? a.page_size : kTile;
+    const bool tables = a.aK || a.aV;
+    // two tiles per item where that leaves a ring of three stages, else one
+    const bool wide = layout<D>(&tp, true, tables, di.smem_optin, 3);
+    if (!wide && !layout<D>(&tp, false, tables, di.smem_optin, 2)) return cudaErrorNotSupported;
+    p.T = wide ? 2 * tp.TS : tp.TS;
+    p.T1 = tp.TS;
+    p.c0 = 2;
+    p.wt = 1;
+    p.wt2 = 2;
+    p.rec_rows = 2 * BM;
+    CUtensorMap tm[5];
+    if (!make_query_map(&tm[0], a, p.g, tp.TS) || !make_page_map(&tm[1], a.k_pages, a, tp.box) ||
+        !make_page_map(&tm[2], a.v_pages, a, tp.box))
+        return cudaErrorInvalidValue;
+    tm[3] = tm[4] = tm[0];
+    const uint64_t Ht = a.ths ? (uint64_t)a.Hkv : 1, hs = a.ths ? (uint64_t)a.ths * 2 : (uint64_t)(2 * a.clip_k + 1) * D * 2;
+    if (a.aK && !tc::make_map(&tm[3], a.aK, D, tp.W, Ht, D * 2, hs, (uint32_t)tp.npad)) return cudaErrorInvalidValue;
+    if (a.aV && !tc::make_map(&tm[4], a.aV, D, tp.W, Ht, D * 2, hs, (uint32_t)tp.npad)) return cudaErrorInvalidValue;
+    if (a.aK && a.aV) return launch_variant<D, true, true>(tm, tp, s);
+    if (a.aK) return launch_variant<D, true, false>(tm, tp, s);
+    if (a.aV) return launch_variant<D, false, true>(tm, tp, s);
+    return launch_variant<D, false, false>(tm, tp, s);
+}
+
+}  // namespace
+}  // namespace paged
+
+bool paged_tc_covers(const PagedArgs &a) {
+    if (!a.bf16 || (a.d != 64 && a.d != 128) || a.page_size < 8 || a.clip_k > 127) return false;
+    // strides that a tensor map can hold
+    if (a.page_stride >= (1LL << 38) || a.q_stride >= (1LL << 38) || a.ths >= (1LL << 38)) return false;
+    return paged::wide_rows(a);
+}
+
+cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s) {
+    return a.d == 64 ? paged::launch_d<64>(a, s) : paged::launch_d<128>(a, s);
+}
+
+}  // namespace relattn
