@@ -293,6 +293,9 @@ struct Walk {
         }
         return false;
     }
+    // the same out of line, for a kernel that walks in several places: its loops' code should
+    // stay in the instruction cache
+    __device__ __noinline__ bool next_call(const Params &p, Segment &g) { return next(p, g); }
 };
 
 // Leaves the descriptor of the item that goes on behind the range (one thread per CTA calls it,

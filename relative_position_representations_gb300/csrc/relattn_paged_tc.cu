@@ -18,8 +18,8 @@
 // no such care, scores of unseen keys are replaced, not added to.
 // Work is split over the CTAs by keys (relattn_paged.cuh).
 //
-// Roles (384 threads, one CTA per SM): warp 0 feeds the ring (aK, K and V tiles, aV, in the order
-// of use), warp 3 the query tiles, warps 1 and 2 issue the MMAs of slot 0 and 1, warps 4-7 and
+// Roles (384 threads, one CTA per SM): warp 3 walks the CTA's range, announces the pieces and loads
+// their query tiles, warp 0 feeds the ring (aK, K and V tiles, aV, in the order of use), warps 1 and 2 issue the MMAs of slot 0 and 1, warps 4-7 and
 // 8-11 run the rows of slot 0 and 1, one thread per row. TMEM as in relattn_tc_kernel.cuh: S of
 // slot s at 128 s, O at 256 + d s, P (bf16) at 384 + 64 s (d = 64) or over the lower half of S
 // (d = 128), beta over the upper half of S.
@@ -53,6 +53,7 @@ static_assert(kTcGrid * 2 * BM <= kMaxGrid * kRecordRows, "records of the worksp
 constexpr int KB = 32;                       // keys per softmax chunk
 constexpr int NCH = kTile / KB;
 constexpr int kMaxStages = 8;
+constexpr uint32_t kStatBytes = 2 * BM * 8;
 constexpr float kRescaleLog2 = tc::kRescaleLog2;
 
 template <int D>
@@ -65,7 +66,11 @@ struct Tm {
 };
 
 enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
-enum : int { B_Q_FULL = 0, B_Q_EMPTY, B_X, B_SLOT0 = 3, B_KV0 = B_SLOT0 + 2 * kSlotBars };
+constexpr int kPieces = 4;                   // pieces announced ahead
+enum : int {
+    B_Q_FULL = 0, B_Q_EMPTY, B_X, B_PIECE_FULL, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
+    B_SLOT0 = B_PIECE_EMPTY + kPieces, B_KV0 = B_SLOT0 + 2 * kSlotBars
+};
 constexpr int kNumBars = B_KV0 + 2 * kMaxStages;
 
 struct TcParams {
@@ -76,7 +81,42 @@ struct TcParams {
     int box;             // keys per TMA box: min(page_size, 128)
     int stages;
     uint32_t stage_bytes;
-    uint32_t off_q[2], off_kv, off_r[2], off_stat, off_bar;
+    uint32_t off_q[2], off_kv, off_r[2], off_stat, off_piece, off_bar;
+};
+
+// A piece of work as warp 3, which walks the CTA's range, leaves it in shared memory for the
+// other warps (cnt 0: there is no more)
+struct Piece {
+    int row0, cnt;         // first query token, tokens of the item
+    int pos_lo, pos_hi;    // their positions
+    int ns, lo, nt;        // Item: its tiles
+    int t0, t1;            // those of this piece
+    int kvh, b, pad;
+    __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    __device__ __forceinline__ int record() const { return t0 > 0 ? 0 : 1; }
+    // first key of the window of the item's first token
+    __device__ __forceinline__ int first(const Params &p) const {
+        return p.window > 0 ? max(0, max(pos_lo, 0) - p.window + 1) : 0;
+    }
+};
+static_assert(sizeof(Piece) == 48, "piece");
+
+// the pieces in order; `wait` is the role's own bounded wait
+struct Pieces {
+    uint32_t bars;
+    const Piece *ring;
+    uint32_t it;
+    __device__ __forceinline__ Pieces(const TcParams &tp, const Shared &sh)
+        : bars(sh.base + tp.off_bar), ring(reinterpret_cast<const Piece *>(sh.ptr + tp.off_piece)), it(0) {}
+    // false: the wait ran out, or there is no more
+    template <typename Wait>
+    __device__ __forceinline__ bool next(Wait wait, Piece &g, bool &ok) {
+        if (!(ok = wait(bars + 8u * (B_PIECE_FULL + (it & (kPieces - 1))), (it / kPieces) & 1u))) return false;
+        g = ring[it & (kPieces - 1)];
+        return g.cnt > 0;
+    }
+    __device__ __forceinline__ uint32_t empty() const { return bars + 8u * (B_PIECE_EMPTY + (it & (kPieces - 1))); }
 };
 
 // one slot's share of a piece
@@ -86,29 +126,25 @@ struct SlotWork {
     int pos_lo, pos_hi;  // their positions
     int first;           // first key in the window of the slot's first token
     int t_last;          // the last tile of the piece that the slot uses (t0 - 1: none)
-    __device__ __forceinline__ bool uses(const Params &p, const Segment &g, int slot, int t) const {
+    __device__ __forceinline__ bool uses(const Params &p, const Piece &g, int slot, int t) const {
         if (split) return ((t - g.t0) & 1) == slot;
-        const int j0 = g.it.tile(t) * kTile;
+        const int j0 = g.tile(t) * kTile;
         return j0 <= pos_hi && (j0 + kTile > first || j0 < p.sinks);
     }
 };
 
-__device__ __forceinline__ SlotWork slot_work(const TcParams &tp, const Segment &g, int slot) {
+__device__ __forceinline__ SlotWork slot_work(const TcParams &tp, const Piece &g, int slot) {
     const Params &p = tp.p;
     SlotWork w;
-    w.split = g.it.cnt <= tp.TS;
+    w.split = g.cnt <= tp.TS;
     w.tok0 = w.split ? 0 : slot * tp.TS;
-    w.ntok = min(tp.TS, g.it.cnt - w.tok0);
-    w.pos_lo = g.it.pos_lo + w.tok0;
+    w.ntok = min(tp.TS, g.cnt - w.tok0);
+    w.pos_lo = g.pos_lo + w.tok0;
     w.pos_hi = w.pos_lo + w.ntok - 1;
     w.first = p.window > 0 ? max(0, max(w.pos_lo, 0) - p.window + 1) : 0;
     w.t_last = g.t1 - 1;
     while (w.t_last >= g.t0 && !w.uses(p, g, slot, w.t_last)) --w.t_last;
     return w;
-}
-
-__device__ __forceinline__ int item_first(const Params &p, const Item &it) {
-    return p.window > 0 ? max(0, max(it.pos_lo, 0) - p.window + 1) : 0;
 }
 
 // position in the ring
@@ -143,7 +179,7 @@ __device__ __forceinline__ int v_lag(bool split) {
 
 // ======================================================================= producers
 template <int D, bool AK, bool AV>
-__device__ void kv_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_k,
+__device__ void kv_role(const TcParams &tp, const Shared &sh, const CUtensorMap *tm_k,
                         const CUtensorMap *tm_v, const CUtensorMap *tm_ak, const CUtensorMap *tm_av) {
     const Params &p = tp.p;
     constexpr int DB = D / 64;
@@ -174,20 +210,20 @@ __device__ void kv_role(const TcParams &tp, const Range &rg, const Shared &sh, c
         step();
         return true;
     };
-    Walk walk(p, rg);
-    Segment g{};
-    while (ok && walk.next(p, g)) {
+    Pieces pieces(tp, sh);
+    Piece g;
+    for (; ok && pieces.next(wait, g, ok); ptx::mbar_arrive_w(pieces.empty()), ++pieces.it) {
         const int nt = g.t1 - g.t0;
         if (nt == 0) continue;
-        const bool split = g.it.cnt <= tp.TS;
+        const bool split = g.cnt <= tp.TS;
         const int lag = v_lag<D>(split);
-        const int first = item_first(p, g.it);
+        const int first = g.first(p);
         const int *bt = p.bt + (long long)g.b * p.bt_stride;
         if (AK && !(ok = table(tm_ak, g.kvh))) break;
         // this lane's box of tile t: page number (or -1), and whether any row sees a key of it
         auto lookup = [&](int t, bool &seen) -> int {
-            const int j = g.it.tile(t) * kTile + my_box * tp.box;
-            seen = t < g.t1 && j <= g.it.pos_hi && (j + tp.box > first || j < p.sinks);
+            const int j = g.tile(t) * kTile + my_box * tp.box;
+            seen = t < g.t1 && j <= g.pos_hi && (j + tp.box > first || j < p.sinks);
             return seen ? __ldg(bt + (j >> p.pshift)) : -1;
         };
         // pages of tiles i, i - 1 and i - 2 (V comes up to two tiles behind K), tile i + 1 ahead
@@ -199,7 +235,7 @@ __device__ void kv_role(const TcParams &tp, const Range &rg, const Shared &sh, c
             const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
             ptx::mbar_expect_tx_w(full, (uint32_t)__popc(m) * tp.box * D * 2);
             __syncwarp();
-            const int j = g.it.tile(t) * kTile + my_box * tp.box;
+            const int j = g.tile(t) * kTile + my_box * tp.box;
             const int row = j & ((1 << p.pshift) - 1);
             if (seen && my_blk < DB) {
                 const bool bad = (unsigned)pg >= (unsigned)p.num_pages;
@@ -233,19 +269,36 @@ __device__ void kv_role(const TcParams &tp, const Range &rg, const Shared &sh, c
         tc::drain_bar(bar(B_KV0 + (int)(i % tp.stages)), (i / tp.stages) & 1u, sh.limit);
 }
 
+// Walks the CTA's range, announces its pieces and loads their query tiles.
 template <int D>
-__device__ void q_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_q) {
+__device__ void walk_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_q) {
     const Params &p = tp.p;
     constexpr int DB = D / 64;
+    const int lane = threadIdx.x & 31;
     const uint32_t bars = sh.base + tp.off_bar;
     const uint32_t full = bars + 8u * B_Q_FULL, empty = bars + 8u * B_Q_EMPTY;
+    Piece *ring = reinterpret_cast<Piece *>(sh.ptr + tp.off_piece);
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        const bool r = wait_bar_ctrl(b, parity, sh, p.err);
+        return __all_sync(0xffffffffu, r ? 1 : 0) != 0;
+    };
     Walk walk(p, rg);
     Segment g{};
-    uint32_t it = 0;
-    while (walk.next(p, g)) {
-        if (g.t1 == g.t0) continue;
-        const bool r = wait_bar_ctrl(empty, (it & 1u) ^ 1u, sh, p.err);
-        if (!__all_sync(0xffffffffu, r ? 1 : 0)) break;
+    uint32_t it = 0, q_it = 0;
+    bool more = true, any = false;
+    while (more) {
+        more = walk.next(p, g);
+        any = any || more;
+        const int i = it & (kPieces - 1);
+        if (!wait(bars + 8u * (B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u)) break;
+        if (lane == 0)
+            ring[i] = Piece{g.s.q0 + g.it.i0, more ? g.it.cnt : 0, g.it.pos_lo, g.it.pos_hi, g.it.ns, g.it.lo,
+                            g.it.nt, g.t0, g.t1, g.kvh, g.b, 0};
+        __syncwarp();
+        ptx::mbar_arrive_w(bars + 8u * (B_PIECE_FULL + i));
+        ++it;
+        if (!more || g.t1 == g.t0) continue;
+        if (!wait(empty, (q_it & 1u) ^ 1u)) break;
         const int ns = g.it.cnt <= tp.TS ? 1 : 2;
         ptx::mbar_expect_tx_w(full, (uint32_t)ns * tp.TS * p.g * D * 2);
         for (int s = 0; s < ns; ++s)
@@ -253,16 +306,18 @@ __device__ void q_role(const TcParams &tp, const Range &rg, const Shared &sh, co
             for (int blk = 0; blk < DB; ++blk)
                 ptx::tma_load_3d_w(sh.base + tp.off_q[s] + blk * BM * 128, tm_q, full, blk * 64, g.kvh * p.g,
                                    g.s.q0 + g.it.i0 + s * tp.TS);
-        ++it;
+        ++q_it;
     }
-    if (it) tc::drain_bar(full, (it - 1) & 1u, sh.limit);
+    if (q_it) tc::drain_bar(full, (q_it - 1) & 1u, sh.limit);
+    // (after an abort the pieces' records hold anything, as does the output)
+    if (lane == 0) write_desc(p, any ? &g : nullptr, rg.total);
 }
 
 // ======================================================================= MMA issuers
 // One warp per slot; both walk every ring entry and each releases it, so the release barriers
 // count two arrivals; an entry, or Q, is released only after it was waited for.
 template <int D, bool AK, bool AV>
-__device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, uint32_t tmem, int slot_in) {
+__device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
     using T = Tm<D>;
     const Params &p = tp.p;
     const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
@@ -302,9 +357,9 @@ __device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, 
         ptx::tc_fence_after();
         return true;
     };
-    Walk walk(p, rg);
-    Segment g{};
-    while (ok && walk.next(p, g)) {
+    Pieces pieces(tp, sh);
+    Piece g;
+    for (; ok && pieces.next(wait, g, ok); ptx::mbar_arrive_w(pieces.empty()), ++pieces.it) {
         const int nt = g.t1 - g.t0;
         if (nt == 0) continue;
         const SlotWork w = slot_work(tp, g, slot);
@@ -312,7 +367,7 @@ __device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, 
         const bool tables = act && (!w.split || slot == 0);   // R and beta belong to this slot
         const int lag = v_lag<D>(w.split);
         const uint64_t dq = ptx::sdesc_sw128(sh.base + tp.off_q[w.split ? 0 : slot], 16, 1024);
-        const int first = item_first(p, g.it);
+        const int first = g.first(p);
         if (!(ok = wait(bar(B_Q_FULL), q_it & 1u))) break;
         ++q_it;
         ptx::tc_fence_after();
@@ -360,8 +415,8 @@ __device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, 
                 const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
                 if (w.uses(p, g, slot, t)) {
                     // rows of V that no row of the item sees
-                    const int j0 = g.it.tile(t) * kTile;
-                    const int n_seen = g.it.pos_hi + 1 - j0;                   // rows below are within the cache
+                    const int j0 = g.tile(t) * kTile;
+                    const int n_seen = g.pos_hi + 1 - j0;                   // rows below are within the cache
                     const int u0 = max(0, p.sinks - j0), u1 = first - j0;      // rows u0 .. u1 - 1 lie behind the window
                     if (n_seen < kTile || u1 > u0) {
                         const uint32_t base = sh.base + tp.off_kv + (uint32_t)ring.st * tp.stage_bytes;
@@ -422,7 +477,7 @@ __device__ void mma_role(const TcParams &tp, const Range &rg, const Shared &sh, 
 
 // ======================================================================= softmax / epilogue
 template <int D, bool AK, bool AV>
-__device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, uint32_t tmem, int slot_in) {
+__device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
     using T = Tm<D>;
     const Params &p = tp.p;
     const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
@@ -502,11 +557,9 @@ __device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, 
         }
         ptx::tmem_st_wait();
     };
-    Walk walk(p, rg);
-    Segment g{};
-    bool any = false;
-    while (ok && walk.next(p, g)) {
-        any = true;
+    Pieces pieces(tp, sh);
+    Piece g;
+    for (; ok && pieces.next(wait_w, g, ok); ptx::mbar_arrive(pieces.empty()), ++pieces.it) {
         const SlotWork w = slot_work(tp, g, slot);
         const bool split = w.split;
         const bool act = w.t_last >= g.t0;
@@ -521,7 +574,7 @@ __device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, 
         const int rrow = (split ? 0 : slot * tp.TS * p.g) + row;
         float *rec = whole ? nullptr : record(p, blockIdx.x, g.record());
         __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.out) +
-                              ((long long)(g.s.q0 + g.it.i0 + w.tok0 + tok) * p.H + g.kvh * p.g + hh) * D;
+                              ((long long)(g.row0 + w.tok0 + tok) * p.H + g.kvh * p.g + hh) * D;
         if (g.t1 == g.t0 || (!split && !act)) {   // no key in this piece for any row of the slot
             if (valid && !(split && slot == 1)) {
                 if (whole) {
@@ -560,7 +613,7 @@ __device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, 
 
         for (int t = g.t0; t <= w.t_last; ++t) {
             if (!w.uses(p, g, slot, t)) continue;
-            const int j0 = g.it.tile(t) * kTile;
+            const int j0 = g.tile(t) * kTile;
             if (!(ok = wait_s())) break;
             const bool last = t == w.t_last;
             const bool keep_s = AV && last && (!split || slot == 0);   // beta will lie there
@@ -699,7 +752,7 @@ __device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, 
                     const int jb = pos - k;   // key of table row r: jb + r
                     auto weight = [&](int r) -> float {
                         const int j = jb + r, kt = j >> 7;
-                        const int t = kt < g.it.ns ? kt : kt - g.it.lo + g.it.ns;
+                        const int t = kt < g.ns ? kt : kt - g.lo + g.ns;
                         const bool seen = valid && r <= k && j >= 0 &&
                                           (p.window == 0 || j > pos - p.window || j < p.sinks);
                         const bool here = seen && t >= g.t0 && t < g.t1;   // its score is of this piece
@@ -786,7 +839,6 @@ __device__ void row_role(const TcParams &tp, const Range &rg, const Shared &sh, 
             o_it[1 - slot] += slot_work(tp, g, 1 - slot).t_last >= g.t0 ? 1 : 0;
         }
     }
-    if (slot == 0 && row == 0) write_desc(p, any && ok ? &g : nullptr, rg.total);
 }
 
 // ======================================================================= kernel
@@ -798,10 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Params &p = tp.p;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t raw = ptx::smem_u32(smem_raw);
     Shared sh;
-    sh.base = (raw + 1023u) & ~1023u;
-    sh.ptr = smem_raw + (sh.base - raw);
+    sh.base = ptx::smem_u32(smem_raw);
+    sh.ptr = smem_raw;
     uint64_t *bar_ptr = reinterpret_cast<uint64_t *>(sh.ptr + tp.off_bar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_ptr + kNumBars);
     sh.abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -817,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (i == B_Q_EMPTY || i >= B_KV0 + kMaxStages) cnt = 2;
             if (i == B_X) cnt = 256;
+            if (i >= B_PIECE_EMPTY && i < B_PIECE_EMPTY + kPieces) cnt = 3 + 256;   // warps 0-2, every row
             ptx::mbar_init(bars + 8u * (uint32_t)i, cnt);
         }
         *sh.abort_flag = 0;
@@ -836,19 +888,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::reg_dealloc<tc::kCtrlRegs>();
         if (warp == 0) {
             (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
-            kv_role<D, AK, AV>(tp, rg, sh, &tm_k, &tm_v, &tm_ak, &tm_av);
+            kv_role<D, AK, AV>(tp, sh, &tm_k, &tm_v, &tm_ak, &tm_av);
         } else if (warp == 3) {
             (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
-            q_role<D>(tp, rg, sh, &tm_q);
+            walk_role<D>(tp, rg, sh, &tm_q);
         } else {
             const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
-            mma_role<D, AK, AV>(tp, rg, sh, tmem, warp - 1);
+            mma_role<D, AK, AV>(tp, sh, tmem, warp - 1);
         }
         __syncwarp();
     } else {
         ptx::reg_alloc<tc::kSoftRegs>();
         const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
-        row_role<D, AK, AV>(tp, rg, sh, tmem, (warp - tc::kSoftWarp0) >> 2);
+        row_role<D, AK, AV>(tp, sh, tmem, (warp - tc::kSoftWarp0) >> 2);
     }
     ptx::tc_fence_before();
     ptx::cta_barrier();
@@ -869,22 +921,27 @@ bool layout(TcParams *tp, bool wide, bool tables, int smem_optin, int min_stages
         if (s == 0 || wide) off += (uint32_t)BM * D * 2;
     }
     tp->off_kv = off;
-    uint32_t rest = 0;
     const uint32_t r_bytes = tables ? (uint32_t)BM * tp->SR * 4 : 0;
-    const uint32_t fixed = off + r_bytes * (wide ? 2 : 1) + 2 * BM * 8 + kNumBars * 8 + 16 + 1024;
+    // the statistics that the slots exchange lie in slot 1's R rows where there are such: slots
+    // that share their rows use slot 0's only
+    const uint32_t stat_bytes = wide && r_bytes >= kStatBytes ? 0 : kStatBytes;
+    const uint32_t fixed = off + r_bytes * (wide ? 2 : 1) + stat_bytes + kPieces * sizeof(Piece) +
+                           kNumBars * 8 + 16;
     tp->stage_bytes = (uint32_t)kTile * D * 2;
     if ((int)fixed > smem_optin) return false;
     int st = (int)((smem_optin - fixed) / tp->stage_bytes);
     if (st > kMaxStages) st = kMaxStages;
     if (st < min_stages) return false;
     tp->stages = st;
-    rest = off + (uint32_t)st * tp->stage_bytes;
+    uint32_t rest = off + (uint32_t)st * tp->stage_bytes;
     for (int s = 0; s < 2; ++s) {
         tp->off_r[s] = rest;
         if (s == 0 || wide) rest += r_bytes;
     }
-    tp->off_stat = rest;
-    rest += 2 * BM * 8;
+    tp->off_stat = stat_bytes ? rest : tp->off_r[1];
+    rest += stat_bytes;
+    tp->off_piece = rest;
+    rest += kPieces * sizeof(Piece);
     tp->off_bar = rest;
     return true;
 }
@@ -933,7 +990,7 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaS
         }
     }
     const int grid = di.sms < kTcGrid ? di.sms : kTcGrid;
-    const uint32_t smem = tp.off_bar + kNumBars * 8 + 16 + 1024;
+    const uint32_t smem = tp.off_bar + kNumBars * 8 + 16;
     kern<<<grid, kThreads, smem, s>>>(tm[0], tm[1], tm[2], tm[3], tm[4], tp);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -955,8 +1012,8 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     while (tp.SR % 4 != 2) ++tp.SR;   // 32 banks; 2 mod 4, so that its column walks hit 16
     tp.box = a.page_size < kTile ? a.page_size : kTile;
     const bool tables = a.aK || a.aV;
-    // two tiles per item where that leaves a ring of three stages, else one
-    const bool wide = layout<D>(&tp, true, tables, di.smem_optin, 3);
+    // two tiles per item where that leaves a ring of two stages, else one
+    const bool wide = layout<D>(&tp, true, tables, di.smem_optin, 2);
     if (!wide && !layout<D>(&tp, false, tables, di.smem_optin, 2)) return cudaErrorNotSupported;
     p.T = wide ? 2 * tp.TS : tp.TS;
     p.T1 = tp.TS;
