@@ -106,12 +106,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     if (!d.valid) return;
     const int rows = d.cnt * p.g;
     if ((int)blockIdx.y * kMergeWarps >= rows) return;
-    auto tile_at = [&](long long y) -> int {
-        const long long cost = d.c0 + (long long)d.wt * d.nt;
-        if (y >= cost) return d.nt;
-        if (y <= d.c0) return 0;
-        return (int)((y - d.c0 + d.wt - 1) / d.wt);
-    };
+    auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.ws, d.nt); };
     // the CTAs that hold a piece, in order (the first warp lists them)
     if (warp == 0) {
         int n = 0;
@@ -136,7 +131,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         return record(p, piece[i], piece[i] == c ? 1 : 0);
     };
     const int D = p.d, nv = (D + 31) / 32;
-    for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += kMergeSplit * kMergeWarps) {
+    for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += (int)gridDim.y * kMergeWarps) {
         float m = -INFINITY;
         for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
 #pragma unroll
@@ -174,7 +169,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, kMergeSplit);
+    const int split = p.rec_rows <= kMergeWarps ? 1 : kMergeSplit;
+    cfg.gridDim = dim3(grid, split);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -233,10 +229,15 @@ struct SimtLayout {
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_constant__ Params p, int vec) {
     extern __shared__ __align__(16) float smf[];
-    __shared__ long long scr[80];
+    __shared__ Range rg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Range rg = find_range<kSimtThreads>(p, scr);
+    if (warp == 0) {
+        const Range r = find_range(p);
+        if (lane == 0) rg_s = r;
+    }
+    __syncthreads();
+    const Range rg = rg_s;
     const SimtLayout L(p.d, p.clip_k);
     const int d = p.d, d4 = L.d4, n4 = d4 / 4, k = p.clip_k;
     const bool ak = p.aK != nullptr, av = p.aV != nullptr;
@@ -433,7 +434,7 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     p.T = p.g >= kSimtRows ? 1 : kSimtRows / p.g;
     p.T1 = p.T;
     p.c0 = 1;
-    p.wt = p.wt2 = 2;
+    p.ws = p.ws2 = 1;
     p.rec_rows = kRecordRows;
     const SimtLayout L(a.d, a.clip_k);
     const int smem = L.words * (int)sizeof(float);

@@ -6,7 +6,7 @@
 // the heads that share keys share their loads. Its keys come in tiles of kTile: the tiles that
 // hold first tokens (sinks) and the tiles from the window's start to the last token's position.
 // The requests differ in length by orders of magnitude and nothing about them is known on the
-// host, so the items' costs (c0 + wt tiles) are laid end to end in (request, key/value head,
+// host, so the items' costs (c0 + 1 or 2 per tile) are laid end to end in (request, key/value head,
 // token) order and cut into one equal range per CTA; each CTA finds its range's start by a scan
 // over the requests and walks on from there. An item that lies in several ranges is computed in
 // pieces: each piece writes its rows' maximum, sum and unnormalised output to the workspace and
@@ -35,7 +35,7 @@ struct Desc {
     int valid;         // 0: nothing
     int row0, cnt;     // first query token and tokens of the item
     int kvh, nt;       // key/value head, tiles of the item
-    int c0, wt;        // the item's cost: c0 + wt * nt
+    int c0, ws;        // the item's cost: c0 + (nt << ws)
     int pad;
     long long x;       // position of the item's start in the cost line
     long long total;   // length of the cost line
@@ -52,8 +52,8 @@ struct Params {
     float scale_log2;                        // scale * log2(e)
     int B, tokens, H, Hkv, g, d;
     int T;                                   // tokens per item
-    int c0, wt;                              // cost of an item: c0 + wt * tiles
-    int wt2, T1;                             // wt2 in place of wt for items of more than T1 tokens
+    int c0, ws;                              // cost of an item: c0 + (tiles << ws)
+    int ws2, T1;                             // ws2 in place of ws for items of more than T1 tokens
     int rec_rows;                            // rows of a record
     void *out;
     Desc *desc;                              // [gridDim.x]
@@ -79,17 +79,22 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
     return s;
 }
 
+// tiles of an item of cost c0 + (nt << ws) that begin before cost position y of it
+__device__ __forceinline__ int tiles_before(long long y, int c0, int ws, int nt) {
+    if (y >= c0 + ((long long)nt << ws)) return nt;
+    if (y <= c0) return 0;
+    return ((int)y - c0 + (1 << ws) - 1) >> ws;
+}
+
 struct Item {
     int i0, cnt;          // first token (within the request) and tokens
     int pos_lo, pos_hi;   // positions of the first and the last token
     int ns, lo, nt;       // tiles: 0 .. ns - 1, then lo .. lo + nt - ns - 1
-    int cost, wt;
+    int cost, ws;
     __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
     // tiles of the item that lie before cost position y of it
     __device__ __forceinline__ int tile_at(const Params &p, long long y) const {
-        if (y >= cost) return nt;
-        if (y <= p.c0) return 0;
-        return (int)((y - p.c0 + wt - 1) / wt);
+        return tiles_before(y, p.c0, ws, nt);
     }
 };
 
@@ -106,13 +111,18 @@ __device__ __forceinline__ Item make_item(const Params &p, const Seq &s, int qt)
         it.ns = min((min(p.sinks, first) + kTile - 1) / kTile, it.lo);
         it.nt = it.ns + it.pos_hi / kTile + 1 - it.lo;
     }
-    it.wt = it.cnt > p.T1 ? p.wt2 : p.wt;
-    it.cost = p.c0 + it.wt * it.nt;
+    it.ws = it.cnt > p.T1 ? p.ws2 : p.ws;
+    it.cost = p.c0 + (it.nt << it.ws);
     return it;
 }
 
 __device__ __forceinline__ long long range_begin(long long total, int c, int G) {
-    return total / G * c + total % G * c / G;   // floor(total * c / G) without overflow
+    // floor(total * c / G) without overflow; 32-bit divisions where they do
+    if (total < (1LL << 31)) {
+        const unsigned t = (unsigned)total, g = (unsigned)G, q = t / g, r = t - q * g;
+        return (long long)q * c + r * (unsigned)c / g;
+    }
+    return total / G * c + total % G * c / G;
 }
 
 // ------------------------------------------------------------------ a CTA's range
@@ -122,123 +132,107 @@ struct Range {
     long long x;               // where that item starts
 };
 
-// All threads of the CTA call it; `sm` is scratch of at least 80 8-byte words (freed on return
-// after the caller's next __syncthreads). Every thread returns the same range.
-template <int THREADS>
-__device__ Range find_range(const Params &p, long long *sm) {
-    constexpr int W = THREADS / 32;
-    static_assert(W <= 32, "warps");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // cost of one key/value head of request b, summed by the warp for the long requests
-    auto cost_of = [&](int b) -> long long {
-        Seq s{0, 0, 0};
-        if (b < p.B) s = load_seq(p, b);
-        const int nq = (s.n + p.T - 1) / p.T;
-        long long c = 0;
-        const bool big = nq > 4;
-        if (!big)
-            for (int i = 0; i < nq; ++i) c += make_item(p, s, i).cost;
-        unsigned todo = __ballot_sync(0xffffffffu, big);
-        while (todo) {
-            const int src = __ffs(todo) - 1;
-            todo &= todo - 1;
-            Seq t;
-            t.q0 = 0;
-            t.n = __shfl_sync(0xffffffffu, s.n, src);
-            t.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
-            const int m = (t.n + p.T - 1) / p.T;
-            long long part = 0;
-            for (int i = lane; i < m; i += 32) part += make_item(p, t, i).cost;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-            if (lane == src) c = part;
-        }
-        return c;
-    };
-    auto scan = [&](long long v) -> long long {  // inclusive over the block; the total in sm[32 + W]
+// One warp calls it; every lane returns the same range. The lanes take the requests in turn, kBatch
+// of each lane's loaded at once (their latency is most of what a small step costs), and add up the
+// items of a request with many of them together.
+__device__ __forceinline__ Range find_range(const Params &p) {
+    constexpr int kBatch = 4;
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, G = (int)gridDim.x, c = (int)blockIdx.x;
+    auto scan = [&](long long v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, v, o);
+            const long long u = __shfl_up_sync(kAll, v, o);
             if (lane >= o) v += u;
         }
-        __syncthreads();
-        if (lane == 31) sm[warp] = v;
-        __syncthreads();
-        if (tid == 0) {
-            long long a = 0;
-            for (int w = 0; w < W; ++w) {
-                sm[32 + w] = a;
-                a += sm[w];
-            }
-            sm[32 + W] = a;
+        return v;
+    };
+    // costs of one key/value head of requests b0 + 32 i + lane
+    auto costs = [&](int b0, long long (&cost)[kBatch]) {
+        Seq s[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int b = b0 + 32 * i + lane;
+            s[i] = Seq{0, 0, 0};
+            if (b < p.B) s[i] = load_seq(p, b);
         }
-        __syncthreads();
-        return v + sm[32 + warp];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            cost[i] = 0;
+            const int nq = (s[i].n + p.T - 1) / p.T;
+            if (nq > 0 && nq <= 2) {
+                cost[i] = make_item(p, s[i], 0).cost;
+                if (nq > 1) cost[i] += make_item(p, s[i], 1).cost;
+            }
+            unsigned todo = __ballot_sync(kAll, nq > 2);
+            while (todo) {
+                const int src = __ffs(todo) - 1;
+                todo &= todo - 1;
+                Seq t;
+                t.q0 = 0;
+                t.n = __shfl_sync(kAll, s[i].n, src);
+                t.pos0 = __shfl_sync(kAll, s[i].pos0, src);
+                const int m = (t.n + p.T - 1) / p.T;
+                long long part = 0;
+                for (int q = lane; q < m; q += 32) part += make_item(p, t, q).cost;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+                if (lane == src) cost[i] = part;
+            }
+        }
     };
     Range r;
-    const int G = (int)gridDim.x, c = (int)blockIdx.x;
-    long long total = 0;
-    const bool once = p.B <= THREADS;
-    long long mine = 0, incl = 0;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-        mine = cost_of(b0 + tid) * p.Hkv;
-        incl = scan(mine);
-        total += sm[32 + W];
+    long long cost[kBatch];
+    r.total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32 * kBatch) {
+        costs(b0, cost);
+        long long sum = 0;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) sum += cost[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        r.total += sum * p.Hkv;
     }
-    r.total = total;
-    r.x0 = range_begin(total, c, G);
-    r.x1 = range_begin(total, c + 1, G);
-    if (tid == 0) sm[70] = p.B;   // an empty range at the end finds no request
-    __syncthreads();
-    long long carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-        if (!once) {
-            mine = cost_of(b0 + tid) * p.Hkv;
-            incl = scan(mine);
-        }
-        const long long lo = carry + incl - mine;
-        if (mine > 0 && lo <= r.x0 && r.x0 < lo + mine) {
-            sm[70] = b0 + tid;
-            sm[71] = lo;
-            sm[72] = mine / p.Hkv;
-        }
-        if (!once) carry += sm[32 + W];
-    }
-    __syncthreads();
-    r.b = (int)sm[70];
+    r.x0 = range_begin(r.total, c, G);
+    r.x1 = range_begin(r.total, c + 1, G);
+    r.b = p.B;   // an empty range at the end finds no request
     r.kvh = r.qt = 0;
     r.x = r.x1;
-    if (r.b < p.B) {
-        const long long per = sm[72];
-        const long long y = r.x0 - sm[71];
-        r.kvh = (int)(y / per);
-        const long long base = sm[71] + per * r.kvh, z = r.x0 - base;
-        if (warp == 0) {  // the item within the head
-            const Seq s = load_seq(p, r.b);
-            const int nq = (s.n + p.T - 1) / p.T;
-            long long at = 0;
-            for (int i0 = 0; i0 < nq; i0 += 32) {
-                const int i = i0 + lane;
-                const long long cst = i < nq ? make_item(p, s, i).cost : 0;
-                long long inc = cst;
+    long long at = 0, per = 0;
+    for (int b0 = 0; b0 < p.B && r.b == p.B && r.x0 < r.x1; b0 += 32 * kBatch) {
+        if (p.B > 32 * kBatch) costs(b0, cost);
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += u;
-                }
-                const long long lo = at + inc - cst;
-                const bool hit = cst > 0 && lo <= z && z < lo + cst;
-                if (hit) {
-                    sm[73] = i;
-                    sm[74] = base + lo;
-                }
-                if (__ballot_sync(0xffffffffu, hit)) break;
-                at += __shfl_sync(0xffffffffu, inc, 31);
+        for (int i = 0; i < kBatch; ++i) {
+            const long long mine = cost[i] * p.Hkv, incl = at + scan(mine), lo = incl - mine;
+            const unsigned hit = __ballot_sync(kAll, mine > 0 && lo <= r.x0 && r.x0 < incl);
+            if (hit && r.b == p.B) {
+                const int src = __ffs(hit) - 1;
+                r.b = b0 + 32 * i + src;
+                per = __shfl_sync(kAll, cost[i], src);
+                r.x = __shfl_sync(kAll, lo, src);
             }
+            at = __shfl_sync(kAll, incl, 31);
         }
-        __syncthreads();
-        r.qt = (int)sm[73];
-        r.x = sm[74];
+    }
+    if (r.b == p.B) return r;
+    // the head, then the item within it
+    long long y = r.x0 - r.x;
+    r.kvh = y < (1LL << 31) ? (int)((unsigned)y / (unsigned)min(per, 0x7fffffffLL)) : (int)(y / per);
+    r.x += per * r.kvh;
+    const Seq s = load_seq(p, r.b);
+    const int nq = (s.n + p.T - 1) / p.T;
+    for (int i0 = 0; i0 < nq; i0 += 32) {
+        const int i = i0 + lane;
+        const long long cst = i < nq ? make_item(p, s, i).cost : 0;
+        const long long incl = r.x + scan(cst);
+        const unsigned hit = __ballot_sync(kAll, cst > 0 && incl - cst <= r.x0 && r.x0 < incl);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            r.qt = i0 + src;
+            r.x = __shfl_sync(kAll, incl - cst, src);
+            break;
+        }
+        r.x = __shfl_sync(kAll, incl, 31);
     }
     return r;
 }
@@ -293,17 +287,38 @@ struct Walk {
         }
         return false;
     }
-    // the same out of line, for a kernel that walks in several places: its loops' code should
-    // stay in the instruction cache
-    __device__ __noinline__ bool next_call(const Params &p, Segment &g) { return next(p, g); }
 };
+
+// A piece as the warp that walks the CTA's range announces it to the others in shared memory (cnt 0:
+// there is no more)
+struct Piece {
+    int row0, cnt;         // first query token, tokens of the item
+    int pos_lo, pos_hi;    // their positions
+    int ns, lo, nt;        // Item: its tiles
+    int t0, t1;            // those of this piece
+    int kvh, b, pad;
+    __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    __device__ __forceinline__ int record() const { return t0 > 0 ? 0 : 1; }
+    // first key of the window of the item's first token
+    __device__ __forceinline__ int first(const Params &p) const {
+        return p.window > 0 ? max(0, max(pos_lo, 0) - p.window + 1) : 0;
+    }
+};
+static_assert(sizeof(Piece) == 48, "piece");
+constexpr int kPieces = 4;   // announced ahead
+
+__device__ __forceinline__ Piece make_piece(const Segment &g, bool more) {
+    return Piece{g.s.q0 + g.it.i0, more ? g.it.cnt : 0, g.it.pos_lo, g.it.pos_hi, g.it.ns, g.it.lo,
+                 g.it.nt, g.t0, g.t1, g.kvh, g.b, 0};
+}
 
 // Leaves the descriptor of the item that goes on behind the range (one thread per CTA calls it,
 // once, with the last segment of the range).
 __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, long long total) {
     Desc d;
     d.valid = 0;
-    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.wt = d.pad = 0;
+    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.ws = d.pad = 0;
     d.x = d.total = d.pad2[0] = d.pad2[1] = 0;
     if (g && g->t0 == 0 && g->t1 > 0 && g->t1 < g->it.nt) {
         d.valid = 1;
@@ -312,7 +327,7 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
         d.kvh = g->kvh;
         d.nt = g->it.nt;
         d.c0 = p.c0;
-        d.wt = g->it.wt;
+        d.ws = g->it.ws;
         d.x = g->x;
         d.total = total;
     }

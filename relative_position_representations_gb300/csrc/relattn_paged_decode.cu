@@ -7,60 +7,72 @@
 // 128-row tcgen05 tile would be padding for the most part and would need the keys staged for the
 // async proxy, and at these sizes the products take a tenth of the time that the bytes take.
 //
-// A tile of 128 keys is 16 keys for each of a CTA's 8 warps; each warp keeps its own running
-// maximum, sum and output over its keys, and the warps are joined once per piece. Loads run
-// through a ring of kStages groups of 16 keys per warp by 16-byte cp.async. The ring is private
-// to each lane: the lane copies exactly the 16-byte chunks that its own fragments need and reads
-// them back itself, so the loop has no barrier, no swizzle and no transposition:
-//   S^T: the order of the contracted columns is free, so lane (key l / 4, c = l % 4) takes columns
-//     32 s + 8 c .. + 7 of its keys as the k-slots of two MMA steps, and Q alike;
-//   O^T: the lane takes columns 64 u + 8 (l / 4) .. + 7 of keys 2 c, 2 c + 1 (+ 8) and pairs two
-//     keys by byte permutes; P^T comes out of S^T's accumulators by two 8 x 8 transpositions.
-//     A lane's outputs are then 8 consecutive columns of rows 2 c, 2 c + 1.
-// The ring runs ahead over the ends of the pieces (a second walk over the CTA's range issues the
-// loads), so joining the warps costs no bandwidth while it is shorter than the ring.
+// A tile of 128 keys is 16 keys for each of a CTA's 8 row warps; each keeps its own running
+// maximum, sum and output over its keys, and the warps are joined once per piece. A ninth warp
+// walks the CTA's range, announces the pieces and loads their queries and tiles by TMA (one lane
+// per page), so the row warps' loop has no barrier and almost no addresses, and the ring runs ahead
+// over the ends of the pieces: joining the warps costs no bandwidth while it is shorter than the
+// ring. (Row warps that copied their own keys, by cp.async or by TMA boxes of their own, and walked
+// the range themselves took 470 instructions a tile and 7.5 us a piece.)
+// The fragments come out of the swizzled rows without bank conflicts and without transposing V:
+//   S^T: the order of the contracted columns is free, so lane (key slot l / 4, c = l % 4) takes
+//     columns 32 s + 8 c .. + 7 of its keys as the k-slots of two MMA steps, and Q alike;
+//   O^T: the lane takes 8 columns of the keys in slots 2 c, 2 c + 1 (+ 8) and pairs two keys by
+//     byte permutes; P^T comes out of S^T's accumulators by two 8 x 8 transpositions.
+//   Slot i of 8 keys is row perm(i) = 0 4 1 5 2 6 3 7, and dim slot i is the 16-byte chunk perm(i) of
+//     64 columns: eight lanes' 16-byte reads then fall in the eight chunks of a 128-byte line.
+// Rows of a page that no token sees may hold NaN: their V is replaced by zeros in registers.
 //
 // Relative terms: R = Q aK^T (k + 1 rows) once per piece by the same MMA; keys at most k - 1
 // back add their own R entry and leave their score in a bin; the other keys share entry 0 and
 // their weights are summed. At the end of the piece each warp adds 16 rows' beta_r aV_r at a time.
 #include <cstdint>
 
-#include "relattn_paged.cuh"
-#include "sm103_ptx.cuh"
+#include <cstring>
+
+#include "relattn_paged_tma.cuh"
 
 namespace relattn {
 namespace paged {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 8;                // row warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRowThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // keys of a warp per tile
-constexpr int kStages = 2;
+constexpr int kMaxStages = 4;
 static_assert(kWarps * kGroup == kTile, "a tile is one group per warp");
 
-// D = 64 holds half the bytes per key in a group: two CTAs share an SM (their joins overlap)
+// D = 64 has half the bytes per key: two CTAs share an SM (their joins overlap)
 template <int D>
 constexpr int kCtasPerSm = D == 64 ? 2 : 1;
 template <int D>
-constexpr int kStageBytes = 2 * kGroup * D * 2;   // one warp's group: K and V
+constexpr int kStageBytes = 2 * kTile * D * 2;    // one tile: blocks of 64 columns of K, then of V
+
+enum : int { B_FULL = 0, B_EMPTY = kMaxStages, B_PIECE_FULL = 2 * kMaxStages, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
+             kNumBars = B_PIECE_EMPTY + kPieces };
 
 struct Layout {
-    uint32_t o, ml, R, Bn, bytes;        // byte offsets behind the ring
+    uint32_t q, piece, bar, o, ml, R, Bn, bytes;   // byte offsets; the ring comes first
     int lw;
     template <int D, int NT>
-    static __host__ __device__ Layout make(int clip_k, bool tables) {
+    static __host__ __device__ Layout make(int clip_k, bool tables, int stages) {
         Layout L;
         constexpr int rows = 8 * NT;
         L.lw = tables ? (clip_k + 1) | 1 : 0;
-        uint32_t off = (uint32_t)kWarps * kStages * kStageBytes<D>;
-        L.o = off;  off += kWarps * rows * D * 4;
-        L.ml = off; off += kWarps * rows * 4 * 4;
-        L.R = off;  off += rows * L.lw * 4;
-        L.Bn = off; off += rows * L.lw * 4;
+        uint32_t off = (uint32_t)stages * kStageBytes<D>;
+        L.q = off;     off += kPieces * rows * D * 2;
+        L.piece = off; off += kPieces * sizeof(Piece);
+        L.bar = off;   off += kNumBars * 8 + 16;
+        L.o = off;     off += kWarps * rows * D * 4;
+        L.ml = off;    off += kWarps * rows * 4 * 4;
+        L.R = off;     off += rows * L.lw * 4;
+        L.Bn = off;    off += rows * L.lw * 4;
         L.bytes = off;
         return L;
     }
 };
+static_assert((kPieces * sizeof(Piece) + kNumBars * 8 + 16) % 16 == 0, "alignment of what follows");
 
 // The joined outputs: 16-byte chunk `ch` of row `row`, swizzled so that the fragments' stores of
 // neighbouring rows fall in different banks
@@ -69,14 +81,6 @@ __device__ __forceinline__ int out_at(int warp, int row, int ch) {
     return (warp * 8 * NT + row) * D + ((ch ^ (row & 6)) << 2);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -97,140 +101,153 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return r;
 }
 
-// The groups that a warp gets over the CTA's range, one per call: tile after tile of piece after
-// piece. `pg` holds the page numbers of the next group's two halves (8 keys each), loaded one
-// call ahead so that the copies do not wait for the table.
-template <int D>
-struct Feed {
-    Walk walk;
-    bool more;
-    int t, t1, ns, lo;           // next tile of the piece, its end; Item::tile
-    int pos_hi, first;           // keys that some row sees: <= pos_hi and (>= first or < sinks)
-    const int *bt;
-    long long head;              // element offset of the head within a page
-    int pg[2], j0;               // of the next group
-    __device__ __forceinline__ Feed(const Params &p, const Range &r) : walk(p, r), more(true), t(0), t1(0) {}
-    __device__ __forceinline__ bool seen(const Params &p, int j) const {
-        return j <= pos_hi && (j >= first || j < p.sinks);
-    }
-    __device__ __forceinline__ void advance(const Params &p, int warp) {
-        if (++t >= t1) {
-            Segment g;
-            do {
-                if (!walk.next_call(p, g)) {
-                    more = false;
-                    return;
-                }
-            } while (g.t0 >= g.t1);
-            t = g.t0;
-            t1 = g.t1;
-            ns = g.it.ns;
-            lo = g.it.lo - g.it.ns;
-            pos_hi = g.it.pos_hi;
-            first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
-            bt = p.bt + (long long)g.b * p.bt_stride;
-            head = ((long long)g.kvh << p.pshift) * D;
-        }
-        j0 = (t < ns ? t : lo + t) * kTile + warp * kGroup;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int j = j0 + 8 * h;
-            // -2: nothing to load; -1 (or a number past the cache): no such page
-            pg[h] = j <= pos_hi && (j + 8 > first || j < p.sinks) ? max(-1, __ldg(bt + (j >> p.pshift))) : -2;
-        }
-    }
-    // issues the copies of the next group into ring stage `dst` (this lane's address)
-    __device__ __forceinline__ void issue(const Params &p, uint32_t dst, int lane) {
-        const int pm = (1 << p.pshift) - 1;
-        const int c = lane & 3, rq = lane >> 2;
-        const char *base[2];
-        bool ok[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            ok[h] = (unsigned)pg[h] < (unsigned)p.num_pages;
-            if (!ok[h] && pg[h] != -2 && lane == 0) report_page(p);
-            const long long off = ok[h] ? pg[h] * p.page_stride + head + ((j0 + 8 * h) & pm) * D : 0;
-            base[h] = static_cast<const char *>(p.k) + 2 * off;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const bool on = ok[h] && seen(p, j0 + 8 * h + rq);
-            const char *src = base[h] + (rq * D + 8 * c) * 2;
-#pragma unroll
-            for (int s = 0; s < D / 32; ++s) cp16(dst + (h * (D / 32) + s) * 512, src + 64 * s, on);
-        }
-        dst += (D / 16) * 512;
-        const long long dv = static_cast<const char *>(p.v) - static_cast<const char *>(p.k);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const char *src = base[h] + dv + (2 * c * D + 8 * rq) * 2;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const bool on = ok[h] && seen(p, j0 + 8 * h + 2 * c + e);
-#pragma unroll
-                for (int u = 0; u < D / 64; ++u)
-                    cp16(dst + ((2 * h + e) * (D / 64) + u) * 512, src + e * D * 2 + 128 * u, on);
-            }
-        }
+// row of key slot i of 8 (and chunk of dim slot i)
+__device__ __forceinline__ int perm(int i) { return (i >> 1) | ((i & 1) << 2); }
+
+// A wait that runs out sets the status word and the CTA's abort flag; later waits then give up at
+// once.
+struct Waits {
+    volatile int *abort_flag;
+    int *err;
+    long long limit;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (ptx::mbar_try(bar, parity)) return true;
+        return tc::wait_bar_slow_call(bar, parity, abort_flag, err, limit);
     }
 };
 
+// ======================================================================= the walking warp
+template <int D, int NT>
+__device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const Waits &waits, const CUtensorMap *tm_q,
+                          const CUtensorMap *tm_k, const CUtensorMap *tm_v, int stages, int box) {
+    constexpr int DB = D / 64;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = ptx::smem_u32(smem), bars = base + L.bar;
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+    auto wait = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, waits(b, parity) ? 1 : 0) != 0; };
+    Piece *ring = reinterpret_cast<Piece *>(smem + L.piece);
+    // the boxes of a tile: 128 / box pages (at most 16) x DB blocks of columns, one per lane
+    const int nbox = kTile / box, my_box = lane % nbox, my_blk = lane / nbox;
+    const uint32_t my_dst = base + my_blk * (kTile * 128) + my_box * box * 128;
+    const Range rg = find_range(p);
+    Walk walk(p, rg);
+    Segment g{};
+    uint32_t it = 0, tiles = 0;
+    int st = 0;
+    uint32_t ph = 0;
+    bool more = true, any = false, ok = true;
+    while (more && ok) {
+        more = walk.next(p, g);
+        any = any || more;
+        const int i = it & (kPieces - 1);
+        if (!(ok = wait(bar(B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u))) break;
+        if (lane == 0) {
+            ring[i] = make_piece(g, more);
+            if (more) {
+                ptx::mbar_expect_tx(bar(B_PIECE_FULL + i), (uint32_t)(p.T * p.g) * D * 2);
+#pragma unroll
+                for (int blk = 0; blk < DB; ++blk)
+                    ptx::tma_load_3d(base + L.q + (i * DB + blk) * (8 * NT * 128), tm_q, bar(B_PIECE_FULL + i), blk * 64,
+                                     g.kvh * p.g, g.s.q0 + g.it.i0);
+            } else {
+                ptx::mbar_arrive(bar(B_PIECE_FULL + i));
+            }
+        }
+        __syncwarp();
+        ++it;
+        if (!more) break;
+        const int first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
+        const int *bt = p.bt + (long long)g.b * p.bt_stride;
+        // this lane's page of tile t, looked up one tile ahead
+        auto lookup = [&](int t, bool &seen) -> int {
+            const int j = g.it.tile(t) * kTile + my_box * box;
+            seen = t < g.t1 && j <= g.it.pos_hi && (j + box > first || j < p.sinks);
+            return seen ? __ldg(bt + (j >> p.pshift)) : -1;
+        };
+        bool seen_next;
+        int pg_next = lookup(g.t0, seen_next);
+        for (int t = g.t0; t < g.t1; ++t) {
+            const bool seen = seen_next;
+            int pg = pg_next;
+            pg_next = lookup(t + 1, seen_next);
+            if (!(ok = wait(bar(B_EMPTY + st), ph ^ 1u))) break;
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
+            if (lane == 0) ptx::mbar_expect_tx(bar(B_FULL + st), (uint32_t)__popc(m) * box * D * 2 * 2);
+            __syncwarp();
+            if (seen && my_blk < DB) {
+                if ((unsigned)pg >= (unsigned)p.num_pages) {
+                    report_page(p);
+                    pg = p.num_pages;   // outside the tensor: zeros
+                }
+                const int row = (g.it.tile(t) * kTile + my_box * box) & ((1 << p.pshift) - 1);
+                const uint32_t dst = my_dst + st * kStageBytes<D>;
+                tma_load_4d(dst, tm_k, bar(B_FULL + st), my_blk * 64, row, g.kvh, pg);
+                tma_load_4d(dst + kStageBytes<D> / 2, tm_v, bar(B_FULL + st), my_blk * 64, row, g.kvh, pg);
+            }
+            __syncwarp();
+            ++tiles;
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    // no copy is in flight when the CTA exits (they have all been consumed, except after an abort)
+    for (uint32_t i = tiles > (uint32_t)stages ? tiles - stages : 0; i < tiles; ++i)
+        tc::drain_bar(bar(B_FULL + (int)(i % stages)), (i / stages) & 1u, p.wait_limit);
+    for (uint32_t i = it > (uint32_t)kPieces ? it - kPieces : 0; i < it; ++i)
+        tc::drain_bar(bar(B_PIECE_FULL + (int)(i & (kPieces - 1))), (i / kPieces) & 1u, p.wait_limit);
+    if (lane == 0) write_desc(p, any ? &g : nullptr, rg.total);
+}
+
+// ======================================================================= the row warps
 template <int D, int NT, bool AK, bool AV>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(const __grid_constant__ Params p) {
+__device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const Waits &wait, int stages) {
     constexpr int kRows = 8 * NT;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long scr[80];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int c = lane & 3, rq = lane >> 2;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Range rg = find_range<kThreads>(p, scr);
-    const Layout L = Layout::make<D, NT>(p.clip_k, AK || AV);
-    const uint32_t ring = ptx::smem_u32(smem) + (uint32_t)warp * kStages * kStageBytes<D> + lane * 16;
+    const uint32_t base = ptx::smem_u32(smem), bars = base + L.bar;
     float *so = reinterpret_cast<float *>(smem + L.o);
     float4 *sml = reinterpret_cast<float4 *>(smem + L.ml);   // {m, l, far, -} of [warp][row]
     float *Rs = reinterpret_cast<float *>(smem + L.R), *Bs = reinterpret_cast<float *>(smem + L.Bn);
+    const Piece *pieces = reinterpret_cast<const Piece *>(smem + L.piece);
     const int k = p.clip_k, W = k + 1;
+    uint32_t stage = 0, phase = 0;
+    // this lane's chunks within a block of 64 columns: key rows perm(rq) (+ 8) for S, rows c, c + 4
+    // (+ 8) for O; the chunk's place is its number xor (row mod 8)
+    const int kr = perm(rq);
+    const uint32_t ring = base + warp * (kGroup * 128);
+    const uint32_t k_at[2] = {(uint32_t)(kr * 128 + ((c ^ kr) << 4)), (uint32_t)(kr * 128 + (((c + 4) ^ kr) << 4))};
+    const uint32_t v_at[2] = {(uint32_t)(c * 128 + ((kr ^ c) << 4)), (uint32_t)((c + 4) * 128 + ((kr ^ (c + 4)) << 4))};
+    auto sync = [&]() { ptx::named_bar_sync(1, kRowThreads); };
 
-    // ---- fill the ring
-    Feed<D> feed(p, rg);
-    feed.advance(p, warp);
-#pragma unroll 1
-    for (int s = 0; s < kStages; ++s) {
-        if (feed.more) {
-            feed.issue(p, ring + s * kStageBytes<D>, lane);
-            feed.advance(p, warp);
-        }
-        cp_commit();
-    }
-    uint32_t stage = 0;
-
-    Walk walk(p, rg);
-    Segment g{};
-    bool any = false;
-    while (walk.next_call(p, g)) {
-        any = true;
-        const int rows = g.it.cnt * p.g;
-        const int pos_lo = g.it.pos_lo, pos_hi = g.it.pos_hi;
+    for (uint32_t it = 0;; ++it) {
+        const int slot = it & (kPieces - 1);
+        // all row warps go on together, or leave together; the last piece's shared arrays are free
+        const bool ok = wait(bars + 8u * (B_PIECE_FULL + slot), (it / kPieces) & 1u);
+        if (!ptx::bar_red_and(1, kRowThreads, ok)) break;
+        const Piece g = pieces[slot];
+        if (g.cnt == 0) break;
+        const int rows = g.cnt * p.g;
+        const int pos_lo = g.pos_lo, pos_hi = g.pos_hi, first = g.first(p);
         // ---- Q fragments: lane (row rq, columns 32 s + 8 c .. + 7); positions of rows 2 c, 2 c + 1
         uint4 qf[NT][D / 32];
         int pos[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = 8 * n + rq;
-            const int tok = r / p.g, hh = r - tok * p.g;
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                     (long long)(g.s.q0 + g.it.i0 + tok) * p.q_stride +
-                                     (long long)(g.kvh * p.g + hh) * D + 8 * c;
 #pragma unroll
             for (int s = 0; s < D / 32; ++s)
-                qf[n][s] = r < rows ? __ldg(reinterpret_cast<const uint4 *>(q + 32 * s)) : make_uint4(0, 0, 0, 0);
+                qf[n][s] = lds128(base + L.q + (slot * (D / 64) + (s >> 1)) * (kRows * 128) + (8 * n + rq) * 128 +
+                                  (((c + 4 * (s & 1)) ^ rq) << 4));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rr = 8 * n + 2 * c + e;
                 pos[n][e] = pos_lo + (rr < rows ? rr / p.g : 0);
             }
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bars + 8u * (B_PIECE_EMPTY + slot));
         // products of 16 rows (chunks lo of rows 0-7, hi of rows 8-15) with all query rows
         auto scores = [&](float (&x)[NT][4], const uint4 &lo, const uint4 &hi, int s) {
 #pragma unroll
@@ -263,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
             }
         }
         if (AV)
-            for (int i = tid; i < kRows * L.lw; i += kThreads) Bs[i] = -INFINITY;
-        if (AK || AV) __syncthreads();
+            for (int i = tid; i < kRows * L.lw; i += kRowThreads) Bs[i] = -INFINITY;
+        if (AK || AV) sync();
         float r0[NT][2], m[NT][2], l[NT][2], far[NT][2];
         float o[NT][D / 16][4];
 #pragma unroll
@@ -295,14 +312,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
 
 #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t) {
-            const int j0 = g.it.tile(t) * kTile + warp * kGroup;
+            const int j0 = g.tile(t) * kTile + warp * kGroup;
             const uint32_t st = ring + stage * kStageBytes<D>;
-            stage ^= 1u;
-            static_assert(kStages == 2, "the ring's position is one bit");
-            cp_wait<kStages - 1>();
+            const uint32_t empty = bars + 8u * (B_EMPTY + stage);
+            wait(bars + 8u * (B_FULL + stage), phase);
+            if (++stage == (uint32_t)stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            __syncwarp();
             float x[NT][4] = {};
 #pragma unroll
-            for (int s = 0; s < D / 32; ++s) scores(x, lds128(st + s * 512), lds128(st + (D / 32 + s) * 512), s);
+            for (int s = 0; s < D / 32; ++s) {
+                const uint32_t a = st + (s >> 1) * (kTile * 128) + k_at[s & 1];
+                scores(x, lds128(a), lds128(a + 1024), s);
+            }
             // ---- logits in the log2 domain
             const bool near = j0 + kGroup - 1 > pos_lo - k;   // some key has a table row of its own
             const bool full = j0 + kGroup - 1 <= pos_lo &&
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int lab = min(max(j0 + rq + 8 * (e >> 1) - pos[n][e & 1], -k) + k, k);
+                        const int lab = min(max(j0 + kr + 8 * (e >> 1) - pos[n][e & 1], -k) + k, k);
                         x[n][e] = fmaf(x[n][e], p.scale_log2, Rs[(8 * n + 2 * c + (e & 1)) * L.lw + lab]);
                     }
             } else {
@@ -326,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + rq + 8 * (e >> 1), q = pos[n][e & 1];
+                        const int j = j0 + kr + 8 * (e >> 1), q = pos[n][e & 1];
                         const bool on = j <= q && (p.window == 0 || j > q - p.window || j < p.sinks);
                         x[n][e] = on ? x[n][e] : -INFINITY;
                     }
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 if (AV) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int lab = j0 + rq + 8 * (e >> 1) - pos[n][e & 1] + k;
+                        const int lab = j0 + kr + 8 * (e >> 1) - pos[n][e & 1] + k;
                         if (near && lab > 0) {
                             if (lab <= k) Bs[(8 * n + 2 * c + (e & 1)) * L.lw + lab] = x[n][e];
                         } else {
@@ -384,20 +408,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 b[n][0] = transpose8(ptx::pack_bf16x2(pr[0], pr[1]));
                 b[n][1] = transpose8(ptx::pack_bf16x2(pr[2], pr[3]));
             }
-            const uint32_t sv = st + (D / 16) * 512;
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
                 uint4 v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = lds128(sv + (e * (D / 64) + u) * 512);
+                for (int e = 0; e < 4; ++e)
+                    v[e] = lds128(st + (D / 64 + u) * (kTile * 128) + (e >> 1) * 1024 + v_at[e & 1]);
+                if (!full) {   // rows that no token sees
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + c + 4 * (e & 1) + 8 * (e >> 1);
+                        if (!(j <= pos_hi && (j >= first || j < p.sinks))) v[e] = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 outputs(v, u, b);
             }
-            // ---- the stage is free: the group kStages ahead
-            if (feed.more) {
-                feed.issue(p, st, lane);
-                feed.advance(p, warp);
-            }
-            cp_commit();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(empty);
         }
         // ---- join the warps: maxima and sums first
 #pragma unroll
@@ -411,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 }
                 if (rq == 0) sml[warp * kRows + 8 * n + 2 * c + e] = make_float4(m[n][e], l[n][e], far[n][e], 0.f);
             }
-        __syncthreads();
+        sync();
         auto row_max = [&](int row) {
             float M = -INFINITY;
 #pragma unroll
@@ -430,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 }
             }
         if (AV) {   // 16 rows of the table per warp at a time: beta from the scores in the bins
-            const __nv_bfloat16 *aV = static_cast<const __nv_bfloat16 *>(p.aV) + (long long)g.kvh * p.ths + 8 * rq;
+            const __nv_bfloat16 *aV = static_cast<const __nv_bfloat16 *>(p.aV) + (long long)g.kvh * p.ths + 8 * kr;
             for (int w0 = 16 * warp; w0 < W; w0 += 16 * kWarps) {
                 uint4 v[D / 64][4];
 #pragma unroll
@@ -476,16 +503,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                     for (int u = 0; u < D / 64; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; i += 2)
-                            *reinterpret_cast<float4 *>(so + out_at<D, NT>(warp, row, 16 * u + 2 * rq + i / 2)) =
+                            *reinterpret_cast<float4 *>(so + out_at<D, NT>(warp, row, 16 * u + 2 * kr + i / 2)) =
                                 make_float4(o[n][4 * u + i][e], o[n][4 * u + i][2 + e], o[n][4 * u + i + 1][e],
                                             o[n][4 * u + i + 1][2 + e]);
                 }
             }
-        __syncthreads();
+        sync();
         const bool whole = g.whole();
         float *rec = whole ? nullptr : record(p, blockIdx.x, g.record());
         // four columns a thread
-        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+        for (int i = tid; i < rows * (D / 4); i += kRowThreads) {
             const int row = i / (D / 4), ch = i - row * (D / 4);
             float M = -INFINITY, ls = 0.f;
 #pragma unroll
@@ -506,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 const float inv = ls > 0.f ? 1.f / ls : 0.f;
                 const int tok = row / p.g, hh = row - tok * p.g;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                     ((long long)(g.s.q0 + g.it.i0 + tok) * p.H + g.kvh * p.g + hh) * D + 4 * ch;
+                                     ((long long)(g.row0 + tok) * p.H + g.kvh * p.g + hh) * D + 4 * ch;
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(ptx::pack_bf16x2(z.x * inv, z.y * inv),
                                                              ptx::pack_bf16x2(z.z * inv, z.w * inv));
             } else {
@@ -517,23 +544,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>) paged_decode_kernel(c
                 *reinterpret_cast<float4 *>(rec + 2 * p.rec_rows + row * D + 4 * ch) = z;
             }
         }
-        __syncthreads();   // the next piece writes the shared arrays
     }
-    cp_wait<0>();
-    if (tid == 0) write_desc(p, any ? &g : nullptr, rg.total);
 }
 
 template <int D, int NT, bool AK, bool AV>
-cudaError_t launch_variant(const Params &p, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p, int stages, int box) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Layout L = Layout::make<D, NT>(p.clip_k, AK || AV, stages);
+    const uint32_t bars = ptx::smem_u32(smem) + L.bar;
+    Waits waits{reinterpret_cast<volatile int *>(smem + L.bar + kNumBars * 8), p.err, p.wait_limit};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            const bool by_rows = (i >= B_EMPTY && i < B_EMPTY + kMaxStages) || i >= B_PIECE_EMPTY;
+            ptx::mbar_init(bars + 8u * (uint32_t)i, by_rows ? kWarps : 1);
+        }
+        *waits.abort_flag = 0;
+        ptx::mbar_init_fence();
+        ptx::tma_prefetch_desc(&tm_q);
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+    }
+    __syncthreads();
+    if (threadIdx.x >= kRowThreads)
+        feed_role<D, NT>(p, L, smem, waits, &tm_q, &tm_k, &tm_v, stages, box);
+    else
+        row_role<D, NT, AK, AV>(p, L, smem, waits, stages);
+}
+
+template <int D, int NT, bool AK, bool AV>
+cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box, cudaStream_t s) {
     auto kern = paged_decode_kernel<D, NT, AK, AV>;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
-    const uint32_t smem = Layout::make<D, NT>(p.clip_k, AK || AV).bytes;
+    // as many stages as the CTA's share of the SM's shared memory holds (1 KB per CTA is the
+    // system's), two at least
+    const int share = (di.smem_optin + 1024) / kCtasPerSm<D> - 1024;
+    int stages = kMaxStages;
+    while (stages > 2 && (int)Layout::make<D, NT>(p.clip_k, AK || AV, stages).bytes > share) --stages;
+    const uint32_t smem = Layout::make<D, NT>(p.clip_k, AK || AV, stages).bytes;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;
     const int want = di.sms * kCtasPerSm<D>;
     const int grid = want < kMaxGrid ? want : kMaxGrid;
-    kern<<<grid, kThreads, smem, s>>>(p);
+    kern<<<grid, kThreads, smem, s>>>(tm[0], tm[1], tm[2], p, stages, box);
     const cudaError_t le = cudaGetLastError();
     if (le != cudaSuccess) return le;
     return launch_merge(p, grid, true, s);
@@ -546,12 +602,17 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     p.T = 8 * NT / p.g;
     p.T1 = p.T;
     p.c0 = 1;   // joining the warps costs about a tile's time
-    p.wt = p.wt2 = 1;
+    p.ws = p.ws2 = 0;
     p.rec_rows = 8 * NT;
-    if (a.aK && a.aV) return launch_variant<D, NT, true, true>(p, s);
-    if (a.aK) return launch_variant<D, NT, true, false>(p, s);
-    if (a.aV) return launch_variant<D, NT, false, true>(p, s);
-    return launch_variant<D, NT, false, false>(p, s);
+    CUtensorMap tm[3];
+    const int box = a.page_size < kTile ? a.page_size : kTile;
+    if (!make_query_map(&tm[0], a, p.g, p.T) || !make_page_map(&tm[1], a.k_pages, a, box) ||
+        !make_page_map(&tm[2], a.v_pages, a, box))
+        return cudaErrorInvalidValue;
+    if (a.aK && a.aV) return launch_variant<D, NT, true, true>(tm, p, box, s);
+    if (a.aK) return launch_variant<D, NT, true, false>(tm, p, box, s);
+    if (a.aV) return launch_variant<D, NT, false, true>(tm, p, box, s);
+    return launch_variant<D, NT, false, false>(tm, p, box, s);
 }
 
 constexpr int kMostRows = 16;
@@ -560,10 +621,8 @@ constexpr int kMostRows = 16;
 }  // namespace paged
 
 bool paged_decode_covers(const PagedArgs &a) {
-    if (!a.bf16 || (a.d != 64 && a.d != 128) || a.page_size < 8) return false;
     const int g = a.H / a.Hkv;
-    if (a.max_new < 1 || (long long)a.max_new * g > paged::kMostRows) return false;
-    return paged::wide_rows(a);
+    return a.max_new >= 1 && (long long)a.max_new * g <= paged::kMostRows && paged::pages_by_tma(a);
 }
 
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t s) {

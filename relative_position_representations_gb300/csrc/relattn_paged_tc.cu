@@ -30,8 +30,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "relattn_paged.cuh"
-#include "relattn_tc_launch.cuh"
+#include "relattn_paged_tma.cuh"
 
 namespace relattn {
 namespace paged {
@@ -66,7 +65,6 @@ struct Tm {
 };
 
 enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
-constexpr int kPieces = 4;                   // pieces announced ahead
 enum : int {
     B_Q_FULL = 0, B_Q_EMPTY, B_X, B_PIECE_FULL, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
     B_SLOT0 = B_PIECE_EMPTY + kPieces, B_KV0 = B_SLOT0 + 2 * kSlotBars
@@ -83,24 +81,6 @@ struct TcParams {
     uint32_t stage_bytes;
     uint32_t off_q[2], off_kv, off_r[2], off_stat, off_piece, off_bar;
 };
-
-// A piece of work as warp 3, which walks the CTA's range, leaves it in shared memory for the
-// other warps (cnt 0: there is no more)
-struct Piece {
-    int row0, cnt;         // first query token, tokens of the item
-    int pos_lo, pos_hi;    // their positions
-    int ns, lo, nt;        // Item: its tiles
-    int t0, t1;            // those of this piece
-    int kvh, b, pad;
-    __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
-    __device__ __forceinline__ int record() const { return t0 > 0 ? 0 : 1; }
-    // first key of the window of the item's first token
-    __device__ __forceinline__ int first(const Params &p) const {
-        return p.window > 0 ? max(0, max(pos_lo, 0) - p.window + 1) : 0;
-    }
-};
-static_assert(sizeof(Piece) == 48, "piece");
 
 // the pieces in order; `wait` is the role's own bounded wait
 struct Pieces {
@@ -159,15 +139,6 @@ struct Ring {
         }
     }
 };
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
 
 // Order of the ring entries of a piece: aK; then for i = 0, 1, ...: K_i, V_{i - lag}; aV. With P in
 // its own columns (d = 64) a slot's next scores are computed while its softmax still works, so its
@@ -292,8 +263,7 @@ __device__ void walk_role(const TcParams &tp, const Range &rg, const Shared &sh,
         const int i = it & (kPieces - 1);
         if (!wait(bars + 8u * (B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u)) break;
         if (lane == 0)
-            ring[i] = Piece{g.s.q0 + g.it.i0, more ? g.it.cnt : 0, g.it.pos_lo, g.it.pos_hi, g.it.ns, g.it.lo,
-                            g.it.nt, g.t0, g.t1, g.kvh, g.b, 0};
+            ring[i] = make_piece(g, more);
         __syncwarp();
         ptx::mbar_arrive_w(bars + 8u * (B_PIECE_FULL + i));
         ++it;
@@ -877,13 +847,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_prefetch_desc(&tm_k);
         ptx::tma_prefetch_desc(&tm_v);
     }
+    // Before the warpgroups trade registers (the scan needs more than a control warp keeps), and by
+    // every warp alike: the compiler fails to allocate a branch of one warp here.
+    Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
+    {
+        const Range r = find_range(p);
+        if (threadIdx.x == 96) *range = r;
+    }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_raw = *tmem_slot;
-    const Range rg = find_range<kThreads>(p, reinterpret_cast<long long *>(sh.ptr + tp.off_stat));
-    __syncthreads();
     if (warp < tc::kSoftWarp0) {
         ptx::reg_dealloc<tc::kCtrlRegs>();
         if (warp == 0) {
@@ -891,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             kv_role<D, AK, AV>(tp, sh, &tm_k, &tm_v, &tm_ak, &tm_av);
         } else if (warp == 3) {
             (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
-            walk_role<D>(tp, rg, sh, &tm_q);
+            walk_role<D>(tp, *range, sh, &tm_q);
         } else {
             const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
             mma_role<D, AK, AV>(tp, sh, tmem, warp - 1);
@@ -946,28 +921,6 @@ bool layout(TcParams *tp, bool wide, bool tables, int smem_optin, int min_stages
     return true;
 }
 
-bool make_page_map(CUtensorMap *m, const void *ptr, const PagedArgs &a, int box) {
-    tc::EncodeTiledFn enc = tc::encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dim[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
-    const cuuint64_t stride[3] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.page_size * a.d * 2, (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t bx[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dim, stride, bx, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_query_map(CUtensorMap *m, const PagedArgs &a, int g, int TS) {
-    tc::EncodeTiledFn enc = tc::encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dim[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.tokens};
-    const cuuint64_t stride[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.q_stride * 2};
-    const cuuint32_t bx[3] = {64, (cuuint32_t)g, (cuuint32_t)TS}, es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dim, stride, bx, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool AK, bool AV>
 cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaStream_t s) {
     auto kern = paged_tc_kernel<D, AK, AV>;
@@ -1018,8 +971,8 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     p.T = wide ? 2 * tp.TS : tp.TS;
     p.T1 = tp.TS;
     p.c0 = 2;
-    p.wt = 1;
-    p.wt2 = 2;
+    p.ws = 0;
+    p.ws2 = 1;
     p.rec_rows = 2 * BM;
     CUtensorMap tm[5];
     if (!make_query_map(&tm[0], a, p.g, tp.TS) || !make_page_map(&tm[1], a.k_pages, a, tp.box) ||
@@ -1039,10 +992,7 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
 }  // namespace paged
 
 bool paged_tc_covers(const PagedArgs &a) {
-    if (!a.bf16 || (a.d != 64 && a.d != 128) || a.page_size < 8 || a.clip_k > 127) return false;
-    // strides that a tensor map can hold
-    if (a.page_stride >= (1LL << 38) || a.q_stride >= (1LL << 38) || a.ths >= (1LL << 38)) return false;
-    return paged::wide_rows(a);
+    return a.clip_k <= 127 && paged::pages_by_tma(a);
 }
 
 cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s) {
