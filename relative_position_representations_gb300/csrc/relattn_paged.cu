@@ -91,10 +91,10 @@ void fill_params(const PagedArgs &a, Params *p) {
 // CTA (c, y): the item that goes on behind CTA c's range, rows y, y + gridDim.y, ... of kMergeWarps
 // each. A row's pieces have maxima m_i, sums l_i and unnormalised outputs O_i:
 // M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. One warp per row: the statistics
-// with one piece per lane, then the outputs, four pieces' loads in flight.
+// with one piece per lane, then the outputs, eight pieces' loads in flight.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeSplit = 4;
+constexpr int kMergeUnroll = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p, int G) {
@@ -142,10 +142,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i0 = 0; i0 < n; i0 += 4) {
-            float w[4], x[4][4];
+        for (int i0 = 0; i0 < n; i0 += kMergeUnroll) {
+            float w[kMergeUnroll], x[kMergeUnroll][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kMergeUnroll; ++u) {
                 const bool on = i0 + u < n;
                 const float *q = rec(on ? i0 + u : i0);
                 w[u] = on ? exp2f(q[r] - mu) : 0.f;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
                 for (int e = 0; e < 4; ++e) x[u][e] = e < nv && lane + 32 * e < D ? o[lane + 32 * e] : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < kMergeUnroll; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[e] = fmaf(w[u], x[u][e], acc[e]);
         }
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    const int split = p.rec_rows <= kMergeWarps ? 1 : kMergeSplit;
+    // two rows per warp (one for the few rows of generated tokens): a row is a chain of dependent loads
+    const int split = p.rec_rows <= 2 * kMergeWarps ? p.rec_rows / kMergeWarps : p.rec_rows / (2 * kMergeWarps);
     cfg.gridDim = dim3(grid, split);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;

@@ -53,6 +53,7 @@ constexpr int KB = 32;                       // keys per softmax chunk
 constexpr int NCH = kTile / KB;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kStatBytes = 2 * BM * 8;
+constexpr uint32_t kOutBytes = 32 * 64;   // staging of a warp's output rows
 constexpr float kRescaleLog2 = tc::kRescaleLog2;
 
 template <int D>
@@ -66,7 +67,7 @@ struct Tm {
 
 enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
 enum : int {
-    B_Q_FULL = 0, B_Q_EMPTY, B_X, B_PIECE_FULL, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
+    B_Q_FULL = 0, B_Q_EMPTY = 2, B_X = 4, B_PIECE_FULL, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
     B_SLOT0 = B_PIECE_EMPTY + kPieces, B_KV0 = B_SLOT0 + 2 * kSlotBars
 };
 constexpr int kNumBars = B_KV0 + 2 * kMaxStages;
@@ -93,7 +94,12 @@ struct Pieces {
     template <typename Wait>
     __device__ __forceinline__ bool next(Wait wait, Piece &g, bool &ok) {
         if (!(ok = wait(bars + 8u * (B_PIECE_FULL + (it & (kPieces - 1))), (it / kPieces) & 1u))) return false;
-        g = ring[it & (kPieces - 1)];
+        // through a broadcast of lane 0: the compiler then knows every field, and each branch on it, to
+        // be warp-uniform (tcgen05 and TMA operands stay in uniform registers)
+        const Piece &s = ring[it & (kPieces - 1)];
+        auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+        g = Piece{uni(s.row0), uni(s.cnt), uni(s.pos_lo), uni(s.pos_hi), uni(s.ns), uni(s.lo),
+                  uni(s.nt),   uni(s.t0),  uni(s.t1),     uni(s.kvh),    uni(s.b),  0};
         return g.cnt > 0;
     }
     __device__ __forceinline__ uint32_t empty() const { return bars + 8u * (B_PIECE_EMPTY + (it & (kPieces - 1))); }
@@ -255,7 +261,7 @@ __device__ void walk_role(const TcParams &tp, const Range &rg, const Shared &sh,
     };
     Walk walk(p, rg);
     Segment g{};
-    uint32_t it = 0, q_it = 0;
+    uint32_t it = 0, q_it[2] = {0, 0};
     bool more = true, any = false;
     while (more) {
         more = walk.next(p, g);
@@ -268,17 +274,22 @@ __device__ void walk_role(const TcParams &tp, const Range &rg, const Shared &sh,
         ptx::mbar_arrive_w(bars + 8u * (B_PIECE_FULL + i));
         ++it;
         if (!more || g.t1 == g.t0) continue;
-        if (!wait(empty, (q_it & 1u) ^ 1u)) break;
         const int ns = g.it.cnt <= tp.TS ? 1 : 2;
-        ptx::mbar_expect_tx_w(full, (uint32_t)ns * tp.TS * p.g * D * 2);
-        for (int s = 0; s < ns; ++s)
+        bool ok = true;
+        for (int s = 0; s < ns && ok; ++s) {
+            if (!(ok = wait(empty + 8 * s, (q_it[s] & 1u) ^ 1u))) break;
+            ptx::mbar_expect_tx_w(full + 8 * s, (uint32_t)tp.TS * p.g * D * 2);
 #pragma unroll
             for (int blk = 0; blk < DB; ++blk)
-                ptx::tma_load_3d_w(sh.base + tp.off_q[s] + blk * BM * 128, tm_q, full, blk * 64, g.kvh * p.g,
+                ptx::tma_load_3d_w(sh.base + tp.off_q[s] + blk * BM * 128, tm_q, full + 8 * s, blk * 64, g.kvh * p.g,
                                    g.s.q0 + g.it.i0 + s * tp.TS);
-        ++q_it;
+            ++q_it[s];
+        }
+        if (!ok) break;
     }
-    if (q_it) tc::drain_bar(full, (q_it - 1) & 1u, sh.limit);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        if (q_it[s]) tc::drain_bar(full + 8 * s, (q_it[s] - 1) & 1u, sh.limit);
     // (after an abort the pieces' records hold anything, as does the output)
     if (lane == 0) write_desc(p, any ? &g : nullptr, rg.total);
 }
@@ -308,7 +319,7 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         return (uint64_t)(((kk >> 2) * rows * 128 + (kk & 3) * 32) >> 4);
     };
     Ring ring(tp.stages);
-    uint32_t q_it = 0, s_it = 0, p_it = 0, pv_it = 0, bn_it = 0, bd_it = 0;
+    uint32_t q_it[2] = {0, 0}, s_it = 0, p_it = 0, pv_it = 0, bn_it = 0, bd_it = 0;
     bool pv_pending = false, bn_pending = false, ok = true;
 
     // before an MMA writes the slot's S columns: the rows have read the previous scores, and the
@@ -338,10 +349,16 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         const int lag = v_lag<D>(w.split);
         const uint64_t dq = ptx::sdesc_sw128(sh.base + tp.off_q[w.split ? 0 : slot], 16, 1024);
         const int first = g.first(p);
-        if (!(ok = wait(bar(B_Q_FULL), q_it & 1u))) break;
-        ++q_it;
+        // the query tile that this slot reads; the other one is released as soon as it is there
+        const int mine = w.split ? 0 : slot;
+        for (int b = 0; b < (w.split ? 1 : 2) && ok; ++b) {
+            if (!(ok = wait(bar(B_Q_FULL + b), q_it[b] & 1u))) break;
+            ++q_it[b];
+            if (b != mine || !act) ptx::mbar_arrive_w(bar(B_Q_EMPTY + b));
+            if (b == mine) break;
+        }
+        if (!ok) break;
         ptx::tc_fence_after();
-        if (!act) ptx::mbar_arrive_w(bar(B_Q_EMPTY));
         if (AK) {   // R = Q aK^T into the slot's S columns
             if (!(ok = wait(bar(B_KV0 + ring.st), ring.ph))) break;
             const uint32_t empty = bar(B_KV0 + kMaxStages + ring.st);
@@ -373,7 +390,7 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     else ptx::tc_mma_ss_k64(tS, dq, dk, idS, 0u);
                     ptx::tc_commit_w(sbar(SB_S_FULL));
                     ptx::tc_commit_w(empty);
-                    if (t == w.t_last) ptx::tc_commit_w(bar(B_Q_EMPTY));   // last read of Q
+                    if (t == w.t_last) ptx::tc_commit_w(bar(B_Q_EMPTY + mine));   // last read of Q
                 } else {
                     ptx::mbar_arrive_w(empty);
                 }
@@ -410,6 +427,8 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     ++pv_it;
                     pv_pending = true;
                     ptx::tc_commit_w(empty);
+                    // (the other slot may have tiles left, which this warp only passes on)
+                    if (t == w.t_last && !(AV && tables)) ptx::tc_commit_w(sbar(SB_O_FULL));
                 } else {
                     ptx::mbar_arrive_w(empty);
                 }
@@ -433,12 +452,17 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                 ++bd_it;
                 bn_pending = true;
                 ptx::tc_commit_w(empty);
+                ptx::tc_commit_w(sbar(SB_O_FULL));
             } else {
                 ptx::mbar_arrive_w(empty);
             }
             ring.next();
         }
-        if (act) ptx::tc_commit_w(sbar(SB_O_FULL));
+        if (!w.split && slot == 0) {   // slot 1's query tile
+            if (!(ok = wait(bar(B_Q_FULL + 1), q_it[1] & 1u))) break;
+            ++q_it[1];
+            ptx::mbar_arrive_w(bar(B_Q_EMPTY + 1));
+        }
     }
     // every MMA issued by this warp completes before TMEM is released
     ptx::tc_commit_w(sbar(SB_DRAIN));
@@ -484,10 +508,13 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         __syncwarp();
         return true;
     };
-    auto release_s = [&]() {
+    // the warp's arrival, after all its lanes
+    auto arrive = [&](uint32_t b) {
         ptx::tc_fence_before();
-        ptx::mbar_arrive(sbar(SB_S_EMPTY));
+        __syncwarp();
+        ptx::mbar_arrive_w(b);
     };
+    auto release_s = [&]() { arrive(sbar(SB_S_EMPTY)); };
     auto wait_pv = [&](uint32_t c) -> bool {
         if (!wait_w(sbar(SB_PV_DONE), c & 1u)) return false;
         ptx::tc_fence_after();
@@ -496,8 +523,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     };
     // both slots' rows (a bounded wait like every other, so an abort reaches both)
     auto sync_slots = [&]() -> bool {
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(B_X));
+        arrive(bar(B_X));
         if (!wait_w(bar(B_X), x_it & 1u)) return false;
         ++x_it;
         ptx::tc_fence_after();
@@ -529,7 +555,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     };
     Pieces pieces(tp, sh);
     Piece g;
-    for (; ok && pieces.next(wait_w, g, ok); ptx::mbar_arrive(pieces.empty()), ++pieces.it) {
+    for (; ok && pieces.next(wait_w, g, ok); arrive(pieces.empty()), ++pieces.it) {
         const SlotWork w = slot_work(tp, g, slot);
         const bool split = w.split;
         const bool act = w.t_last >= g.t0;
@@ -587,41 +613,39 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
             if (!(ok = wait_s())) break;
             const bool last = t == w.t_last;
             const bool keep_s = AV && last && (!split || slot == 0);   // beta will lie there
-            float x[kTile];
-            // chunk c: seen by no row of the warp / without masks / all offsets beyond the band
-            auto dead = [&](int c) -> bool {
-                const int e0 = j0 + c * KB;
+            // chunk of 32 keys from e0: seen by no row of the warp / without masks / beyond the band
+            auto dead = [&](int e0) -> bool {
                 return e0 > pmax || (p.window > 0 && e0 + KB - 1 <= pmin - p.window && e0 >= p.sinks);
             };
-            auto full = [&](int c) -> bool {
-                const int e0 = j0 + c * KB;
-                return e0 + KB - 1 <= pmin && (p.window == 0 || e0 > pmax - p.window || e0 + KB <= p.sinks);
+            auto full = [&](int e0, int len) -> bool {
+                return e0 + len - 1 <= pmin && (p.window == 0 || e0 > pmax - p.window || e0 + len <= p.sinks);
             };
-            auto far = [&](int c) -> bool { return j0 + c * KB + KB - 1 <= pmin - k; };
-            auto raw = [&](int c) -> bool { return full(c) && (!AK || far(c)) && pos_scale && (!AV || far(c)); };
-            if (mine) {
+            auto far = [&](int e0, int len) -> bool { return e0 + len - 1 <= pmin - k; };
+            // Most tiles need no mask and lie beyond the band: their scores stay raw in registers (scale
+            // and constant go into the exponent) and the code is straight-line. The others take two
+            // rolled passes over the score columns, 32 keys at a time, with the logits written back.
+            const bool plain = mine && pos_scale && full(j0, kTile) && (!(AK || AV) || far(j0, kTile));
+            float x[kTile];
+            float rmax = -INFINITY;
+            if (plain) {
 #pragma unroll
-                for (int c = 0; c < NCH; ++c)
-                    if (!dead(c)) ptx::tmem_ld32f(lane_base + T::S(slot) + (uint32_t)(c * KB), x + c * KB);
+                for (int c = 0; c < NCH; ++c) ptx::tmem_ld32f(lane_base + T::S(slot) + (uint32_t)(c * KB), x + c * KB);
                 ptx::tmem_ld_wait();
-            }
-            if (!keep_s) release_s();
-            float alpha = 1.f;
-            if (mine) {
-                // ---- logits in the log2 domain; raw chunks stay as they are (their scale and
-                // constant go into the exponent)
-                float rmax = -INFINITY;
-#pragma unroll
+                if (!keep_s) release_s();
+                rmax = fmaxf(fmaxf(max32(x), max32(x + 32)), fmaxf(max32(x + 64), max32(x + 96)));
+                rmax = fmaf(rmax, sl2, c_left);
+            } else if (mine) {
+#pragma unroll 1
                 for (int c = 0; c < NCH; ++c) {
-                    if (dead(c)) continue;
-                    float *xc = x + c * KB;
-                    if (raw(c)) {
-                        rmax = fmaxf(rmax, fmaf(max32(xc), sl2, c_left));
-                        continue;
-                    }
                     const int e0 = j0 + c * KB;
+                    if (dead(e0)) continue;
+                    const uint32_t at = lane_base + T::S(slot) + (uint32_t)(c * KB);
+                    float xc[KB];
+                    ptx::tmem_ld32f(at, xc);
+                    ptx::tmem_ld_wait();
                     const int rb = e0 - pos + k;   // table row of element 0, before clamping
-                    if (AK && !far(c)) {
+                    const bool band = (AK || AV) && !far(e0, KB);
+                    if (AK && band) {
 #pragma unroll
                         for (int e = 0; e < KB; e += 2) {
                             const float2 r = make_float2(Rrow[min(k, max(0, rb + e))], Rrow[min(k, max(0, rb + e + 1))]);
@@ -631,24 +655,28 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
 #pragma unroll
                         for (int e = 0; e < KB; e += 2) put(xc, e, __ffma2_rn(pair(xc, e), dup(sl2), dup(c_left)));
                     }
-                    if (!full(c)) {
+                    if (!full(e0, KB)) {
                         const int hi = pos - e0;                                         // seen: e <= hi and
                         const int lo = p.window > 0 ? pos - p.window - e0 : -1 - e0;     // (e > lo or
                         const int sk = p.sinks - e0;                                     // e < sk)
 #pragma unroll
                         for (int e = 0; e < KB; ++e) xc[e] = e <= hi && (e > lo || e < sk) ? xc[e] : -INFINITY;
                     }
-                    if (AV && !far(c)) {   // the score takes the place of the table row it used
+                    if (AV && band) {   // the score takes the place of the table row it used
 #pragma unroll
                         for (int e = 0; e < KB; ++e)
                             if (rb + e > 0 && rb + e <= k) Rrow[rb + e] = xc[e];
                     }
                     rmax = fmaxf(rmax, max32(xc));
+                    __syncwarp();
+                    ptx::tmem_st32f(at, xc);
                 }
-                if (rmax > m_ref + kRescaleLog2) {
-                    alpha = ptx::ex2(m_ref - rmax);
-                    m_ref = rmax;
-                }
+                ptx::tmem_st_wait();
+            }
+            float alpha = 1.f;
+            if (rmax > m_ref + kRescaleLog2) {
+                alpha = ptx::ex2(m_ref - rmax);
+                m_ref = rmax;
             }
             // P and O are free once the previous P V is done (P over S: S_j was issued after it)
             if (!T::P_ALIAS && n > 0 && !(ok = wait_pv(pv_it + n - 1u))) break;
@@ -659,40 +687,50 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     scale_o(alpha);
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                // P of 32 keys from logits a xc + b, its sum into l, bf16 pairs (the tensor cores'
+                // operand; l keeps the fp32 values) into TMEM
+                auto weights = [&](float *xc, float2 a2, float2 b2, int c) {
+                    float2 s01 = dup(0.f), s23 = dup(0.f);
 #pragma unroll
-                for (int c = 0; c < NCH; ++c) {
-                    float *xc = x + c * KB;
-                    if (dead(c)) {
-#pragma unroll
-                        for (int e = 0; e < KB / 2; ++e) xc[e] = 0.f;
-                    } else {
-                        const bool rw = raw(c);
-                        const float2 a2 = dup(rw ? sl2 : 1.f), b2 = dup((rw ? c_left : 0.f) - m_use);
-                        float2 s01 = dup(0.f), s23 = dup(0.f);
-#pragma unroll
-                        for (int e = 0; e < KB; e += 4) {
-                            const float2 t0 = __ffma2_rn(pair(xc, e), a2, b2);
-                            const float2 t1 = __ffma2_rn(pair(xc, e + 2), a2, b2);
-                            xc[e] = ptx::ex2(t0.x);
-                            xc[e + 1] = ptx::ex2(t0.y);
-                            xc[e + 2] = ptx::ex2(t1.x);
-                            xc[e + 3] = ptx::ex2(t1.y);
-                            s01 = __fadd2_rn(s01, pair(xc, e));
-                            s23 = __fadd2_rn(s23, pair(xc, e + 2));
-                        }
-                        l += (s01.x + s01.y) + (s23.x + s23.y);
-                        // bf16: the tensor cores' operand; l keeps the fp32 values
-#pragma unroll
-                        for (int e = 0; e < KB / 2; ++e)
-                            xc[e] = __uint_as_float(ptx::pack_bf16x2(xc[2 * e], xc[2 * e + 1]));
+                    for (int e = 0; e < KB; e += 4) {
+                        const float2 t0 = __ffma2_rn(pair(xc, e), a2, b2);
+                        const float2 t1 = __ffma2_rn(pair(xc, e + 2), a2, b2);
+                        xc[e] = ptx::ex2(t0.x);
+                        xc[e + 1] = ptx::ex2(t0.y);
+                        xc[e + 2] = ptx::ex2(t1.x);
+                        xc[e + 3] = ptx::ex2(t1.y);
+                        s01 = __fadd2_rn(s01, pair(xc, e));
+                        s23 = __fadd2_rn(s23, pair(xc, e + 2));
                     }
-                    __syncwarp();
+                    l += (s01.x + s01.y) + (s23.x + s23.y);
+#pragma unroll
+                    for (int e = 0; e < KB / 2; ++e)
+                        xc[e] = __uint_as_float(ptx::pack_bf16x2(xc[2 * e], xc[2 * e + 1]));
                     ptx::tmem_st16f(lane_base + T::P(slot) + (uint32_t)(c * (KB / 2)), xc);
+                };
+                if (plain) {
+                    const float2 a2 = dup(sl2), b2 = dup(c_left - m_use);
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c) weights(x + c * KB, a2, b2, c);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < NCH; ++c) {
+                        float xc[KB];
+                        if (dead(j0 + c * KB)) {
+#pragma unroll
+                            for (int e = 0; e < KB; ++e) xc[e] = -INFINITY;
+                        } else {
+                            ptx::tmem_ld32f(lane_base + T::S(slot) + (uint32_t)(c * KB), xc);
+                            ptx::tmem_ld_wait();
+                        }
+                        __syncwarp();
+                        weights(xc, dup(1.f), dup(-m_use), c);
+                    }
                 }
                 ptx::tmem_st_wait();
             }
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(sbar(SB_P_FULL));
+            if (!keep_s && !plain) release_s();
+            arrive(sbar(SB_P_FULL));
             ++n;
         }
         if (!ok) break;
@@ -744,9 +782,8 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     }
                     ptx::tmem_st_wait();
                 }
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(sbar(SB_BN_FULL));
-                ptx::mbar_arrive(sbar(SB_S_EMPTY));
+                arrive(sbar(SB_BN_FULL));
+                release_s();
             }
             if (two) f0 = 1.f;
         }
@@ -761,8 +798,37 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     rec[p.rec_rows + rrow] = l;
                 }
                 const uint32_t oA = lane_base + T::O(split ? 0 : slot), oB = lane_base + T::O(1);
+                // Rows leave through the slot's R rows (all of its warps are past them): a thread holds a row, but a store of 16
+                // bytes per lane should cover 64 bytes of each of 8 rows (one of 16 bytes of 32 rows
+                // takes twice the sectors, each half written: 5.5k cycles a tile instead of 2k).
+                const uint32_t stage = sh.base + tp.off_r[slot] + (uint32_t)quad * kOutBytes;
+                const uint32_t st_at = stage + lane * 64, sw = (lane >> 1) & 3;
+                const uint32_t my16 = whole ? (uint32_t)(((long long)tok * p.H + hh) * (D / 8)) : (uint32_t)(rrow * (D / 4));
+                char *out0 = whole ? reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                              ((long long)(g.row0 + w.tok0) * p.H + g.kvh * p.g) * D)
+                                   : reinterpret_cast<char *>(rec + 2 * p.rec_rows);
+                // 64 bytes of each row, at byte `off` of the row
+                auto put64 = [&](const uint32_t *v, int off) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        ptx::st_shared_v4(st_at + ((q ^ sw) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = 8 * q + (lane >> 2);
+                        uint4 o;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                                     : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
+                        const uint32_t at = __shfl_sync(0xffffffffu, my16, r);
+                        if (quad * 32 + r < rows)
+                            *reinterpret_cast<uint4 *>(out0 + (size_t)at * 16 + off + (lane & 3) * 16) = o;
+                    }
+                    __syncwarp();
+                };
                 // each slot writes half of the columns where both hold the rows
                 const int cb = two && slot == 1 ? D / 2 : 0, ce = two && slot == 0 ? D / 2 : D;
+#pragma unroll 1
                 for (int c0 = cb; c0 < ce; c0 += 32) {
                     float r[32];
                     ptx::tmem_ld32f(oA + (uint32_t)c0, r);
@@ -775,26 +841,20 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         for (int e = 0; e < 32; e += 2)
                             put(r, e, __ffma2_rn(pair(r1, e), dup(f1), __fmul2_rn(pair(r, e), dup(f0))));
                     }
-                    if (valid) {
-                        if (whole) {
+                    uint32_t v[32];
+                    if (whole) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t o4[4];
-#pragma unroll
-                                for (int h = 0; h < 4; ++h) {
-                                    const float2 o = __fmul2_rn(pair(r, 8 * q + 2 * h), dup(inv));
-                                    o4[h] = ptx::pack_bf16x2(o.x, o.y);
-                                }
-                                reinterpret_cast<uint4 *>(orow)[c0 / 8 + q] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                            }
-                        } else {
-                            float *dst = rec + 2 * p.rec_rows + (long long)rrow * D + c0;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(dst + e) = make_float4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 o = __fmul2_rn(pair(r, 2 * e), dup(inv));
+                            v[e] = ptx::pack_bf16x2(o.x, o.y);
                         }
+                        put64(v, 2 * c0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(r[e]);
+                        put64(v, 4 * c0);
+                        put64(v + 16, 4 * c0 + 64);
                     }
-                    __syncwarp();
                 }
             }
             ptx::tc_fence_before();
@@ -834,11 +894,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t cnt = 1;
             if (i >= B_SLOT0 && i < B_KV0) {
                 const int which = (i - B_SLOT0) % kSlotBars;
-                if (which == SB_S_EMPTY || which == SB_P_FULL || which == SB_BN_FULL) cnt = 128;
+                if (which == SB_S_EMPTY || which == SB_P_FULL || which == SB_BN_FULL) cnt = 4;   // the slot's warps
             }
-            if (i == B_Q_EMPTY || i >= B_KV0 + kMaxStages) cnt = 2;
-            if (i == B_X) cnt = 256;
-            if (i >= B_PIECE_EMPTY && i < B_PIECE_EMPTY + kPieces) cnt = 3 + 256;   // warps 0-2, every row
+            if ((i >= B_Q_EMPTY && i < B_X) || i >= B_KV0 + kMaxStages) cnt = 2;     // both MMA warps
+            if (i == B_X) cnt = 8;                                                   // both slots' warps
+            if (i >= B_PIECE_EMPTY && i < B_PIECE_EMPTY + kPieces) cnt = 3 + 8;      // all but warp 3
             ptx::mbar_init(bars + 8u * (uint32_t)i, cnt);
         }
         *sh.abort_flag = 0;
@@ -889,19 +949,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Shared memory for items of two tiles (wide) or one; false when fewer than `min_stages` stages
 // of the ring fit.
 template <int D>
-bool layout(TcParams *tp, bool wide, bool tables, int smem_optin, int min_stages) {
+bool layout(TcParams *tp, bool wide, int smem_optin, int min_stages) {
     uint32_t off = 0;
     for (int s = 0; s < 2; ++s) {
         tp->off_q[s] = off;
         if (s == 0 || wide) off += (uint32_t)BM * D * 2;
     }
     tp->off_kv = off;
-    const uint32_t r_bytes = tables ? (uint32_t)BM * tp->SR * 4 : 0;
-    // the statistics that the slots exchange lie in slot 1's R rows where there are such: slots
-    // that share their rows use slot 0's only
-    const uint32_t stat_bytes = wide && r_bytes >= kStatBytes ? 0 : kStatBytes;
-    const uint32_t fixed = off + r_bytes * (wide ? 2 : 1) + stat_bytes + kPieces * sizeof(Piece) +
-                           kNumBars * 8 + 16;
+    // R rows of each slot, through which its output rows leave too; slots that share their rows use
+    // slot 0's R, so the statistics that they exchange lie in the last of slot 1's where there is room
+    // behind the output's staging
+    const uint32_t r_bytes = (uint32_t)BM * tp->SR * 4;
+    const uint32_t r1_bytes = wide ? r_bytes : 4 * kOutBytes;
+    const bool stat_in_r = wide && r_bytes >= 4 * kOutBytes + kStatBytes;
+    const uint32_t stat_bytes = stat_in_r ? 0 : kStatBytes;
+    const uint32_t fixed = off + r_bytes + r1_bytes + stat_bytes + kPieces * sizeof(Piece) + kNumBars * 8 + 16;
     tp->stage_bytes = (uint32_t)kTile * D * 2;
     if ((int)fixed > smem_optin) return false;
     int st = (int)((smem_optin - fixed) / tp->stage_bytes);
@@ -909,11 +971,11 @@ bool layout(TcParams *tp, bool wide, bool tables, int smem_optin, int min_stages
     if (st < min_stages) return false;
     tp->stages = st;
     uint32_t rest = off + (uint32_t)st * tp->stage_bytes;
-    for (int s = 0; s < 2; ++s) {
-        tp->off_r[s] = rest;
-        if (s == 0 || wide) rest += r_bytes;
-    }
-    tp->off_stat = stat_bytes ? rest : tp->off_r[1];
+    tp->off_r[0] = rest;
+    rest += r_bytes;
+    tp->off_r[1] = rest;
+    rest += r1_bytes;
+    tp->off_stat = stat_in_r ? rest - kStatBytes : rest;
     rest += stat_bytes;
     tp->off_piece = rest;
     rest += kPieces * sizeof(Piece);
@@ -961,13 +1023,12 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     tp.TS = BM / p.g;
     tp.W = a.clip_k + 1;
     tp.npad = (tp.W + 15) / 16 * 16;
-    tp.SR = tp.W;                     // even, so that a warp's gathers along the band (stride SR - 1) hit
+    tp.SR = tp.W > 16 ? tp.W : 16;    // room for the output's staging (8 KB); even, so that a warp's gathers along the band (stride SR - 1) hit
     while (tp.SR % 4 != 2) ++tp.SR;   // 32 banks; 2 mod 4, so that its column walks hit 16
     tp.box = a.page_size < kTile ? a.page_size : kTile;
-    const bool tables = a.aK || a.aV;
     // two tiles per item where that leaves a ring of two stages, else one
-    const bool wide = layout<D>(&tp, true, tables, di.smem_optin, 2);
-    if (!wide && !layout<D>(&tp, false, tables, di.smem_optin, 2)) return cudaErrorNotSupported;
+    const bool wide = layout<D>(&tp, true, di.smem_optin, 2);
+    if (!wide && !layout<D>(&tp, false, di.smem_optin, 2)) return cudaErrorNotSupported;
     p.T = wide ? 2 * tp.TS : tp.TS;
     p.T1 = tp.TS;
     p.c0 = 2;
