@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     if (!d.valid) return;
     const int rows = d.cnt * p.g;
     if ((int)blockIdx.y * kMergeWarps >= rows) return;
-    auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.ws, d.nt); };
+    auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.wt, d.nt); };
     // the CTAs that hold a piece, in order (the first warp lists them)
     if (warp == 0) {
         int n = 0;
@@ -435,7 +435,7 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     p.T = p.g >= kSimtRows ? 1 : kSimtRows / p.g;
     p.T1 = p.T;
     p.c0 = 1;
-    p.ws = p.ws2 = 1;
+    p.wt = p.wt2 = 2;
     p.rec_rows = kRecordRows;
     const SimtLayout L(a.d, a.clip_k);
     const int smem = L.words * (int)sizeof(float);

@@ -6,7 +6,7 @@
 // the heads that share keys share their loads. Its keys come in tiles of kTile: the tiles that
 // hold first tokens (sinks) and the tiles from the window's start to the last token's position.
 // The requests differ in length by orders of magnitude and nothing about them is known on the
-// host, so the items' costs (c0 + 1 or 2 per tile) are laid end to end in (request, key/value head,
+// host, so the items' costs (c0 + wt per tile) are laid end to end in (request, key/value head,
 // token) order and cut into one equal range per CTA; each CTA finds its range's start by a scan
 // over the requests and walks on from there. An item that lies in several ranges is computed in
 // pieces: each piece writes its rows' maximum, sum and unnormalised output to the workspace and
@@ -35,7 +35,7 @@ struct Desc {
     int valid;         // 0: nothing
     int row0, cnt;     // first query token and tokens of the item
     int kvh, nt;       // key/value head, tiles of the item
-    int c0, ws;        // the item's cost: c0 + (nt << ws)
+    int c0, wt;        // the item's cost: c0 + wt * nt
     int pad;
     long long x;       // position of the item's start in the cost line
     long long total;   // length of the cost line
@@ -52,8 +52,8 @@ struct Params {
     float scale_log2;                        // scale * log2(e)
     int B, tokens, H, Hkv, g, d;
     int T;                                   // tokens per item
-    int c0, ws;                              // cost of an item: c0 + (tiles << ws)
-    int ws2, T1;                             // ws2 in place of ws for items of more than T1 tokens
+    int c0, wt;                              // cost of an item: c0 + wt * tiles
+    int wt2, T1;                             // wt2 in place of wt for items of more than T1 tokens
     int rec_rows;                            // rows of a record
     void *out;
     Desc *desc;                              // [gridDim.x]
@@ -79,22 +79,22 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
     return s;
 }
 
-// tiles of an item of cost c0 + (nt << ws) that begin before cost position y of it
-__device__ __forceinline__ int tiles_before(long long y, int c0, int ws, int nt) {
-    if (y >= c0 + ((long long)nt << ws)) return nt;
+// tiles of an item of cost c0 + wt nt that begin before cost position y of it
+__device__ __forceinline__ int tiles_before(long long y, int c0, int wt, int nt) {
+    if (y >= c0 + (long long)wt * nt) return nt;
     if (y <= c0) return 0;
-    return ((int)y - c0 + (1 << ws) - 1) >> ws;
+    return ((int)y - c0 + wt - 1) / wt;
 }
 
 struct Item {
     int i0, cnt;          // first token (within the request) and tokens
     int pos_lo, pos_hi;   // positions of the first and the last token
     int ns, lo, nt;       // tiles: 0 .. ns - 1, then lo .. lo + nt - ns - 1
-    int cost, ws;
+    int cost, wt;
     __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
     // tiles of the item that lie before cost position y of it
     __device__ __forceinline__ int tile_at(const Params &p, long long y) const {
-        return tiles_before(y, p.c0, ws, nt);
+        return tiles_before(y, p.c0, wt, nt);
     }
 };
 
@@ -111,8 +111,8 @@ __device__ __forceinline__ Item make_item(const Params &p, const Seq &s, int qt)
         it.ns = min((min(p.sinks, first) + kTile - 1) / kTile, it.lo);
         it.nt = it.ns + it.pos_hi / kTile + 1 - it.lo;
     }
-    it.ws = it.cnt > p.T1 ? p.ws2 : p.ws;
-    it.cost = p.c0 + (it.nt << it.ws);
+    it.wt = it.cnt > p.T1 ? p.wt2 : p.wt;
+    it.cost = p.c0 + it.wt * it.nt;
     return it;
 }
 
@@ -318,7 +318,7 @@ __device__ __forceinline__ Piece make_piece(const Segment &g, bool more) {
 __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, long long total) {
     Desc d;
     d.valid = 0;
-    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.ws = d.pad = 0;
+    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.wt = d.pad = 0;
     d.x = d.total = d.pad2[0] = d.pad2[1] = 0;
     if (g && g->t0 == 0 && g->t1 > 0 && g->t1 < g->it.nt) {
         d.valid = 1;
@@ -327,7 +327,7 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
         d.kvh = g->kvh;
         d.nt = g->it.nt;
         d.c0 = p.c0;
-        d.ws = g->it.ws;
+        d.wt = g->it.wt;
         d.x = g->x;
         d.total = total;
     }

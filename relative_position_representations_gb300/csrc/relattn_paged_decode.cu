@@ -602,7 +602,7 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     p.T = 8 * NT / p.g;
     p.T1 = p.T;
     p.c0 = 1;   // joining the warps costs about a tile's time
-    p.ws = p.ws2 = 0;
+    p.wt = p.wt2 = 1;
     p.rec_rows = 8 * NT;
     CUtensorMap tm[3];
     const int box = a.page_size < kTile ? a.page_size : kTile;

@@ -65,7 +65,7 @@ struct Tm {
     static __device__ __forceinline__ uint32_t Bn(int s) { return S(s) + 64u; }
 };
 
-enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
+enum : int { SB_S_FULL = 0, SB_S_EMPTY, SB_P_FULL, SB_P_HALF, SB_PV_DONE, SB_O_FULL, SB_DRAIN, SB_BN_FULL, SB_BN_DONE, kSlotBars };
 enum : int {
     B_Q_FULL = 0, B_Q_EMPTY = 2, B_X = 4, B_PIECE_FULL, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
     B_SLOT0 = B_PIECE_EMPTY + kPieces, B_KV0 = B_SLOT0 + 2 * kSlotBars
@@ -418,10 +418,15 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                     }
+                    // the first 64 keys' product runs while the rows work on the others' weights
+                    const uint64_t dv = dv0 + (uint64_t)ring.st * stage16;
+                    if (!(ok = wait(sbar(SB_P_HALF), p_it & 1u))) break;
+                    ptx::tc_fence_after();
+                    ptx::tc_mma_ts_k64(tO, tP, dv, idPV, started ? 1u : 0u);
                     if (!(ok = wait(sbar(SB_P_FULL), p_it & 1u))) break;
                     ++p_it;
                     ptx::tc_fence_after();
-                    ptx::tc_mma_ts_k128(tO, tP, dv0 + (uint64_t)ring.st * stage16, idPV, started ? 1u : 0u);
+                    ptx::tc_mma_ts_k64(tO, tP + 32u, dv + 512u, idPV, 1u);
                     started = true;
                     ptx::tc_commit_w(sbar(SB_PV_DONE));
                     ++pv_it;
@@ -708,10 +713,17 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         xc[e] = __uint_as_float(ptx::pack_bf16x2(xc[2 * e], xc[2 * e + 1]));
                     ptx::tmem_st16f(lane_base + T::P(slot) + (uint32_t)(c * (KB / 2)), xc);
                 };
+                auto half_done = [&]() {
+                    ptx::tmem_st_wait();
+                    arrive(sbar(SB_P_HALF));
+                };
                 if (plain) {
                     const float2 a2 = dup(sl2), b2 = dup(c_left - m_use);
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c) weights(x + c * KB, a2, b2, c);
+                    for (int c = 0; c < NCH; ++c) {
+                        weights(x + c * KB, a2, b2, c);
+                        if (c == NCH / 2 - 1) half_done();
+                    }
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < NCH; ++c) {
@@ -725,9 +737,12 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         }
                         __syncwarp();
                         weights(xc, dup(1.f), dup(-m_use), c);
+                        if (c == NCH / 2 - 1) half_done();
                     }
                 }
                 ptx::tmem_st_wait();
+            } else {
+                arrive(sbar(SB_P_HALF));
             }
             if (!keep_s && !plain) release_s();
             arrive(sbar(SB_P_FULL));
@@ -758,24 +773,27 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     // weights of the band's rows from their scores; row 0 gets the rest of the sum
                     const float Mu = M == -INFINITY ? 0.f : M;
                     const int jb = pos - k;   // key of table row r: jb + r
-                    auto weight = [&](int r) -> float {
-                        const int j = jb + r, kt = j >> 7;
-                        const int t = kt < g.ns ? kt : kt - g.lo + g.ns;
-                        const bool seen = valid && r <= k && j >= 0 &&
-                                          (p.window == 0 || j > pos - p.window || j < p.sinks);
-                        const bool here = seen && t >= g.t0 && t < g.t1;   // its score is of this piece
-                        return here ? ptx::ex2(Rrow[r] - Mu) : 0.f;
-                    };
+                    // keys of this piece: s0 .. s1 - 1 of the first tokens, w0 .. w1 - 1 of the window
+                    const int s0 = g.t0 * kTile, s1 = min(g.t1, g.ns) * kTile;
+                    const int w0 = (max(g.t0, g.ns) - g.ns + g.lo) * kTile, w1 = (g.t1 - g.ns + g.lo) * kTile;
+                    const int from = !valid ? 1 << 30 : p.window > 0 ? max(0, pos - p.window + 1) : 0;
                     float band = 0.f;
-                    for (int r = 1; r <= k; ++r) band += weight(r);
-                    const float rest = fmaxf(0.f, l - band);
+#pragma unroll 4
+                    for (int r = 1; r <= k; ++r) {
+                        const int j = jb + r;
+                        const bool here = ((j >= w0 && j < w1) || (j >= s0 && j < s1)) &&
+                                          (j >= from || (valid && j >= 0 && j < p.sinks));
+                        const float b = here ? ptx::ex2(Rrow[r] - Mu) : 0.f;
+                        Rrow[r] = b;
+                        band += b;
+                    }
+                    Rrow[0] = fmaxf(0.f, l - band);
                     for (int c0 = 0; c0 < tp.npad; c0 += 32) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int r0 = c0 + 2 * e;
-                            const float b0 = r0 == 0 ? rest : weight(r0), b1 = weight(r0 + 1);
-                            pk[e] = ptx::pack_bf16x2(b0, b1);
+                            pk[e] = ptx::pack_bf16x2(r0 <= k ? Rrow[r0] : 0.f, r0 < k ? Rrow[r0 + 1] : 0.f);
                         }
                         __syncwarp();
                         ptx::tmem_st16(lane_base + T::Bn(slot) + (uint32_t)(c0 / 2), pk);
@@ -894,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t cnt = 1;
             if (i >= B_SLOT0 && i < B_KV0) {
                 const int which = (i - B_SLOT0) % kSlotBars;
-                if (which == SB_S_EMPTY || which == SB_P_FULL || which == SB_BN_FULL) cnt = 4;   // the slot's warps
+                if (which == SB_S_EMPTY || which == SB_P_FULL || which == SB_P_HALF || which == SB_BN_FULL) cnt = 4;   // the slot's warps
             }
             if ((i >= B_Q_EMPTY && i < B_X) || i >= B_KV0 + kMaxStages) cnt = 2;     // both MMA warps
             if (i == B_X) cnt = 8;                                                   // both slots' warps
@@ -1031,9 +1049,10 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     if (!wide && !layout<D>(&tp, false, di.smem_optin, 2)) return cudaErrorNotSupported;
     p.T = wide ? 2 * tp.TS : tp.TS;
     p.T1 = tp.TS;
-    p.c0 = 2;
-    p.ws = 0;
-    p.ws2 = 1;
+    // measured at d = 128: 1.6 us a tile of one slot's rows, 2.35 us a tile of both, 4.5 us a piece
+    p.c0 = 5;
+    p.wt = 2;
+    p.wt2 = 3;
     p.rec_rows = 2 * BM;
     CUtensorMap tm[5];
     if (!make_query_map(&tm[0], a, p.g, tp.TS) || !make_page_map(&tm[1], a.k_pages, a, tp.box) ||
