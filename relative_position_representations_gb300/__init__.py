@@ -31,5 +31,6 @@ __all__ = list(_BINDING)
 def __getattr__(name):
     if name in _BINDING:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # later lookups find it in the module
+        return value
     raise AttributeError(name)

@@ -613,75 +613,89 @@ def relattn_decode_fwd(q, k_cache, v_cache, cache_len, aK=None, aV=None, clip_k=
     return out
 
 
-def _tensors(device, **named):
-    """Checks of the paged calls: every tensor on `device`."""
-    for name, t in named.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("%s must be a CUDA tensor" % name)
-        if t.device != device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+# ---- paged cache. These calls run once per layer and step, the smallest for two microseconds on the
+# GPU, so their checks are written to cost little: devices as indexes, shapes and strides read once.
+_INT = torch.int32
 
 
-def _ints(device, **named):
-    _tensors(device, **named)
-    for name, t in named.items():
-        if t.dtype != torch.int32:
-            raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+def _on(dev, name, t):
+    """t is a tensor on CUDA device `dev` (an index)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, not on cuda:%d" % (name, t.get_device(), dev))
 
 
-def _table(device, block_table, B):
+def _ints(dev, name, t, count):
+    """t holds `count` contiguous int32 on device `dev`; returns its address."""
+    _on(dev, name, t)
+    if t.dtype is not _INT:
+        raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
+    if t.numel() != count:
+        raise ValueError("%s must have %d entries, got %d" % (name, count, t.numel()))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _table(dev, t, B):
     """block_table [B, max_pages] int32; its rows may be spaced. Returns (stride, max_pages)."""
-    _tensors(device, block_table=block_table)
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
+    _on(dev, "block_table", t)
+    if t.dtype is not _INT:
+        raise TypeError("block_table must be torch.int32, got %s" % t.dtype)
+    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1:
         raise ValueError("block_table must be [B, max_pages]")
-    M = block_table.shape[1]
-    if (M > 1 and block_table.stride(1) != 1) or (B > 1 and block_table.stride(0) < M):
+    M = t.shape[1]
+    s0, s1 = t.stride()
+    if (M > 1 and s1 != 1) or (B > 1 and s0 < M):
         raise ValueError("block_table's rows must be contiguous and must not overlap")
-    return (block_table.stride(0) if B > 1 else M), M
+    return (s0 if B > 1 else M), M
 
 
-def _spaced(name, t, shape, dtype):
+def _spaced(dev, name, t, shape, dtype):
     """t has `shape` and dtype and is contiguous but for the stride of its first dimension, which
     is returned (no shorter than a row)."""
-    if t.dtype != dtype:
+    _on(dev, name, t)
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    stride = t.stride()
+    if shape[0] > 1 and t.is_contiguous():
+        return stride[0]
     row = 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n > 1 and st != row:
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != row and shape[i] > 1:
             raise ValueError("%s must be contiguous behind its first dimension" % name)
-        row *= n
-    if t.shape[0] <= 1:
+        row *= shape[i]
+    if shape[0] <= 1:
         return row
-    if t.stride(0) < row:
+    if stride[0] < row:
         raise ValueError("%s's first dimension overlaps" % name)
-    return t.stride(0)
+    return stride[0]
 
 
-def _pages(device, k_pages, v_pages):
-    """k_pages and v_pages [num_pages, Hkv, page_size, d] with one stride between pages."""
-    _tensors(device, k_pages=k_pages, v_pages=v_pages)
+def _pages(k_pages, v_pages):
+    """k_pages and v_pages [num_pages, Hkv, page_size, d] with one stride between pages. Returns
+    (device index, page stride)."""
+    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
+        raise TypeError("k_pages must be a CUDA tensor")
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
-    stride = _spaced("k_pages", k_pages, k_pages.shape, k_pages.dtype)
-    if _spaced("v_pages", v_pages, k_pages.shape, k_pages.dtype) != stride:
+    dev, shape, dtype = k_pages.get_device(), k_pages.shape, k_pages.dtype
+    stride = _spaced(dev, "k_pages", k_pages, shape, dtype)
+    if _spaced(dev, "v_pages", v_pages, shape, dtype) != stride:
         raise ValueError("k_pages and v_pages must have one page stride")
-    return stride
+    return dev, stride
 
 
-def _on_device(device, stream, call):
-    """call(stream pointer) with `device` current; the stream defaults to that device's current one."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        return call(ctypes.c_void_p(stream.cuda_stream))
-    with torch.cuda.device(device):
-        return call(ctypes.c_void_p(stream.cuda_stream))
+def _call_on(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current; the stream defaults to its current one."""
+    stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        return fn(*args, stream)
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
 
 
 def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, page_size,
@@ -694,27 +708,25 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
     place. free_pages: int32 page numbers, of which the first free_head ([1] int32) are taken.
     kv_len may be cached_len and free_head_out may be free_head, which then advance in place.
     """
-    if not isinstance(cached_len, torch.Tensor):
+    if not isinstance(cached_len, torch.Tensor) or not cached_len.is_cuda:
         raise TypeError("cached_len must be a CUDA tensor")
-    dev = cached_len.device
+    dev = cached_len.get_device()
     B = cached_len.numel()
     max_tokens = int(max_tokens)
-    i32 = dict(dtype=torch.int32, device=dev)
-    kv_len = torch.empty(B, **i32) if kv_len is None else kv_len
-    q_start = torch.empty(B + 1, **i32) if q_start is None else q_start
-    slots = torch.empty(max(0, max_tokens), **i32) if slots is None else slots
-    free_head_out = torch.empty(1, **i32) if free_head_out is None else free_head_out
-    _ints(dev, cached_len=cached_len, new_len=new_len, free_pages=free_pages, free_head=free_head,
-          kv_len=kv_len, q_start=q_start, slots=slots, free_head_out=free_head_out)
+    if kv_len is None or q_start is None or slots is None or free_head_out is None:
+        i32 = dict(dtype=_INT, device=cached_len.device)
+        kv_len = torch.empty(B, **i32) if kv_len is None else kv_len
+        q_start = torch.empty(B + 1, **i32) if q_start is None else q_start
+        slots = torch.empty(max(0, max_tokens), **i32) if slots is None else slots
+        free_head_out = torch.empty(1, **i32) if free_head_out is None else free_head_out
     ts, M = _table(dev, block_table, B)
-    if new_len.numel() != B or kv_len.numel() != B or q_start.numel() != B + 1:
-        raise ValueError("new_len and kv_len must have B entries, q_start B + 1")
-    if slots.numel() != max_tokens or free_head.numel() != 1 or free_head_out.numel() != 1:
-        raise ValueError("slots must have max_tokens entries, free_head and free_head_out one")
-    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_plan(
-        cached_len.data_ptr(), new_len.data_ptr(), B, int(page_size), block_table.data_ptr(), ts, M,
-        free_pages.data_ptr(), free_pages.numel(), free_head.data_ptr(), max_tokens,
-        kv_len.data_ptr(), q_start.data_ptr(), slots.data_ptr(), free_head_out.data_ptr(), s))
+    F = free_pages.numel()
+    st = _call_on(
+        dev, stream, _lib.relattn_paged_plan, _ints(dev, "cached_len", cached_len, B),
+        _ints(dev, "new_len", new_len, B), B, int(page_size), block_table.data_ptr(), ts, M,
+        _ints(dev, "free_pages", free_pages, F), F, _ints(dev, "free_head", free_head, 1), max_tokens,
+        _ints(dev, "kv_len", kv_len, B), _ints(dev, "q_start", q_start, B + 1),
+        _ints(dev, "slots", slots, max_tokens), _ints(dev, "free_head_out", free_head_out, 1))
     _check(st, "relattn_paged_plan")
     return kv_len, q_start, slots, free_head_out
 
@@ -722,20 +734,15 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
 def relattn_paged_append(k, v, slots, k_pages, v_pages, stream=None):
     """Rows k[t], v[t] ([tokens, Hkv, d], bf16 or fp32, any token stride) to slot slots[t] of
     k_pages, v_pages [num_pages, Hkv, page_size, d]; negative slots are skipped. In place."""
-    if not isinstance(k_pages, torch.Tensor):
-        raise TypeError("k_pages must be a CUDA tensor")
-    dev = k_pages.device
-    ps = _pages(dev, k_pages, v_pages)
+    dev, ps = _pages(k_pages, v_pages)
     N, Hkv, P, d = k_pages.shape
-    _tensors(dev, k=k, v=v)
-    _ints(dev, slots=slots)
     T = slots.numel()
-    ks = _spaced("k", k, (T, Hkv, d), k_pages.dtype)
-    vs = _spaced("v", v, (T, Hkv, d), k_pages.dtype)
-    code = _dtype_code(k_pages)
-    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_append(
-        k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, k_pages.data_ptr(),
-        v_pages.data_ptr(), ps, N, Hkv, P, d, code, s))
+    shape, dtype = (T, Hkv, d), k_pages.dtype
+    st = _call_on(
+        dev, stream, _lib.relattn_paged_append, k.data_ptr(), v.data_ptr(),
+        _spaced(dev, "k", k, shape, dtype), _spaced(dev, "v", v, shape, dtype),
+        _ints(dev, "slots", slots, T), T, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, Hkv, P, d,
+        _dtype_code(k_pages))
     _check(st, "relattn_paged_append")
 
 
@@ -762,54 +769,60 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
     or None to make one. Returns out [tokens, H, d].
     """
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    dev = q.device
+    dev, ps = _pages(k_pages, v_pages)
+    N, Hkv, P, d = k_pages.shape
+    _on(dev, "q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, H, d]")
-    T, H, d = q.shape
-    dt = _dtype_code(q)
-    ps = _pages(dev, k_pages, v_pages)
-    N, Hkv, P, dk = k_pages.shape
-    if k_pages.dtype != q.dtype or dk != d:
+    dtype = q.dtype
+    if k_pages.dtype is not dtype or q.shape[2] != d:
         raise ValueError("k_pages and v_pages must have q's dtype and head dimension")
-    qs = _spaced("q", q, (T, H, d), q.dtype)
-    _ints(dev, q_start=q_start, kv_len=kv_len)
+    shape = q.shape
+    T, H = shape[0], shape[1]
+    dt = _dtype_code(q)
+    qs = _spaced(dev, "q", q, shape, dtype)
     B = kv_len.numel()
-    if q_start.numel() != B + 1:
-        raise ValueError("q_start must have B + 1 entries")
     ts, M = _table(dev, block_table, B)
-    W = 2 * int(clip_k) + 1
+    clip_k = int(clip_k)
+    W = 2 * clip_k + 1
+    ths, pK, pV = 0, None, None
     for name, t in (("aK", aK), ("aV", aV)):
-        if t is not None:
-            _dev(t, name, q.dtype)
-            _tensors(dev, **{name: t})
-            if t.dim() != 3 or t.shape[1] != W or t.shape[2] != d or t.shape[0] not in (1, Hkv):
-                raise ValueError("%s must be [Hkv or 1, 2*clip_k+1, d]" % name)
-    if aK is not None and aV is not None and aK.shape[0] != aV.shape[0]:
+        if t is None:
+            continue
+        _on(dev, name, t)
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise TypeError("%s must be contiguous and of q's dtype" % name)
+        if t.dim() != 3 or t.shape[1] != W or t.shape[2] != d or t.shape[0] not in (1, Hkv):
+            raise ValueError("%s must be [Hkv or 1, 2*clip_k+1, d]" % name)
+        ths = 0 if t.shape[0] == 1 else W * d
+        if name == "aK":
+            pK = t.data_ptr()
+        else:
+            pV = t.data_ptr()
+    if pK is not None and pV is not None and aK.shape[0] != aV.shape[0]:
         raise ValueError("aK and aV must both be per head or both shared")
-    if table_head_stride is None:
-        ref = aK if aK is not None else aV
-        table_head_stride = 0 if (ref is None or ref.shape[0] == 1) else W * d
+    if table_head_stride is not None:
+        ths = int(table_head_stride)
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-    _dev(out, "out", q.dtype)
-    _tensors(dev, out=out)
-    if out.shape != q.shape:
-        raise ValueError("out must be [tokens, H, d] like q")
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif _spaced(dev, "out", out, shape, dtype) != H * d:
+        raise ValueError("out must be contiguous")
     if scale is None:
         scale = d ** -0.5
     if workspace is None:
-        workspace = torch.empty(relattn_paged_workspace_size(H, Hkv, d), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(relattn_paged_workspace_size(H, Hkv, d), dtype=torch.uint8, device=q.device)
         if stream is not None:
             workspace.record_stream(stream)  # its memory is not handed out before this call is done
-    _dev(workspace, "workspace")
-    _tensors(dev, workspace=workspace)
-    st = _on_device(dev, stream, lambda s: _lib.relattn_paged_fwd(
-        q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, P, block_table.data_ptr(),
-        ts, M, q_start.data_ptr(), kv_len.data_ptr(), _ptr(aK), _ptr(aV), int(table_head_stride),
-        int(clip_k), int(window), int(sinks), float(scale), B, T, int(max_new), H, Hkv, d, dt,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(), s))
+    else:
+        _on(dev, "workspace", workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    st = _call_on(
+        dev, stream, _lib.relattn_paged_fwd, q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
+        ps, N, P, block_table.data_ptr(), ts, M, _ints(dev, "q_start", q_start, B + 1),
+        _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, int(window), int(sinks), float(scale), B,
+        T, int(max_new), H, Hkv, d, dt, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr())
     _check(st, "relattn_paged_fwd")
     return out
 

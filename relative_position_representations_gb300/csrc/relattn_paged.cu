@@ -88,24 +88,25 @@ void fill_params(const PagedArgs &a, Params *p) {
 }
 
 // ------------------------------------------------------------------ merge
-// CTA (c, y): the item that goes on behind CTA c's range, rows y, y + gridDim.y, ... of kMergeWarps
-// each. A row's pieces have maxima m_i, sums l_i and unnormalised outputs O_i:
-// M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. One warp per row: the statistics
-// with one piece per lane, then the outputs, eight pieces' loads in flight.
+// CTA (c, y): the item that goes on behind CTA c's range. A row's pieces have maxima m_i, sums l_i
+// and unnormalised outputs O_i: M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. One warp
+// takes a row and NV groups of 32 columns: the statistics with one piece per lane, then the
+// outputs with kUnroll pieces' loads in flight (a row is a chain of dependent loads, so the work is
+// spread over many warps: for the few rows of generated tokens, NV = 1, else whole rows).
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeUnroll = 8;
 
-template <typename T>
+template <typename T, int NV>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p, int G) {
+    constexpr int kUnroll = 16 / NV;
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Desc d = p.desc[c];
     if (!d.valid) return;
-    const int rows = d.cnt * p.g;
-    if ((int)blockIdx.y * kMergeWarps >= rows) return;
+    const int D = p.d, groups = NV == 1 ? (D + 31) / 32 : 1, units = d.cnt * p.g * groups;
+    if ((int)blockIdx.y * kMergeWarps >= units) return;
     auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.wt, d.nt); };
     // the CTAs that hold a piece, in order (the first warp lists them)
     if (warp == 0) {
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     auto rec = [&](int i) -> const float * {
         return record(p, piece[i], piece[i] == c ? 1 : 0);
     };
-    const int D = p.d, nv = (D + 31) / 32;
-    for (int r = blockIdx.y * kMergeWarps + warp; r < rows; r += (int)gridDim.y * kMergeWarps) {
+    for (int u0 = blockIdx.y * kMergeWarps + warp; u0 < units; u0 += (int)gridDim.y * kMergeWarps) {
+        const int r = u0 / groups, col = (u0 - r * groups) * 32 + lane;
         float m = -INFINITY;
         for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
 #pragma unroll
@@ -141,37 +142,38 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         for (int i = lane; i < n; i += 32) l += rec(i)[p.rec_rows + r] * exp2f(rec(i)[r] - mu);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i0 = 0; i0 < n; i0 += kMergeUnroll) {
-            float w[kMergeUnroll], x[kMergeUnroll][4];
+        float acc[NV] = {};
+        for (int i0 = 0; i0 < n; i0 += kUnroll) {
+            float w[kUnroll], x[kUnroll][NV];
 #pragma unroll
-            for (int u = 0; u < kMergeUnroll; ++u) {
+            for (int u = 0; u < kUnroll; ++u) {
                 const bool on = i0 + u < n;
                 const float *q = rec(on ? i0 + u : i0);
                 w[u] = on ? exp2f(q[r] - mu) : 0.f;
                 const float *o = q + 2 * p.rec_rows + (long long)r * D;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[u][e] = e < nv && lane + 32 * e < D ? o[lane + 32 * e] : 0.f;
+                for (int e = 0; e < NV; ++e) x[u][e] = col + 32 * e < D ? o[col + 32 * e] : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < kMergeUnroll; ++u)
+            for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w[u], x[u][e], acc[e]);
+                for (int e = 0; e < NV; ++e) acc[e] = fmaf(w[u], x[u][e], acc[e]);
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const int tok = r / p.g, hh = r - tok * p.g;
         T *o = static_cast<T *>(p.out) + ((long long)(d.row0 + tok) * p.H + d.kvh * p.g + hh) * D;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (lane + 32 * e < D) o[lane + 32 * e] = from_f<T>(acc[e] * inv);
+        for (int e = 0; e < NV; ++e)
+            if (col + 32 * e < D) o[col + 32 * e] = from_f<T>(acc[e] * inv);
     }
 }
 
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
+    // a warp per row and 32 columns up to 16 rows, else a warp per two rows
+    const bool few = p.rec_rows <= 16;
+    const int warps = few ? p.rec_rows * ((p.d + 31) / 32) : p.rec_rows / 2;
     cudaLaunchConfig_t cfg{};
-    // two rows per warp (one for the few rows of generated tokens): a row is a chain of dependent loads
-    const int split = p.rec_rows <= 2 * kMergeWarps ? p.rec_rows / kMergeWarps : p.rec_rows / (2 * kMergeWarps);
-    cfg.gridDim = dim3(grid, split);
+    cfg.gridDim = dim3(grid, (warps + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -179,8 +181,9 @@ cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, p, grid)
-                : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, p, grid);
+    if (!bf16) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<float, 4>, p, grid);
+    return few ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, 1>, p, grid)
+               : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, 4>, p, grid);
 }
 
 // ------------------------------------------------------------------ SIMT kernel
