@@ -743,7 +743,10 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
     const relattn_status_t st = paged_device(&a.err);
     if (st != RELATTN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (relattn::paged_decode_covers(a)) return from_cuda(relattn::launch_paged_decode(a, s));
+    if (relattn::paged_decode_covers(a)) {
+        const cudaError_t e = relattn::launch_paged_decode(a, s);
+        if (e != cudaErrorNotSupported) return from_cuda(e);
+    }
     if (relattn::paged_tc_covers(a)) {
         const cudaError_t e = relattn::launch_paged_tc(a, s);
         if (e != cudaErrorNotSupported) return from_cuda(e);

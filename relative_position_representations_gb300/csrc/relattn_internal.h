@@ -256,11 +256,12 @@ unsigned long long paged_workspace_bytes(int d);
 // every type, head dimension <= 128 and page size; fp32 arithmetic on the SIMT units
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s);
 // at most 16 query rows (tokens x group) per key/value head: bf16, d = 64 or 128, pages of 8 keys
-// or more, 16-byte aligned rows
+// or more, 16-byte aligned rows; cudaErrorNotSupported (before any launch) when the work's measure
+// may pass 31 bits
 bool paged_decode_covers(const PagedArgs &a);
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t s);
 // tcgen05: bf16, d = 64 or 128, pages of 8 keys or more, clip_k <= 127, 16-byte aligned rows;
-// cudaErrorNotSupported (before any launch) when the tables leave no room for the key tiles
+// cudaErrorNotSupported (before any launch) also when the tables leave no room for the key tiles
 bool paged_tc_covers(const PagedArgs &a);
 cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s);
 

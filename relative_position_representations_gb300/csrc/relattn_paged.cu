@@ -440,6 +440,7 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     p.c0 = 1;
     p.wt = p.wt2 = 2;
     p.rec_rows = kRecordRows;
+    p.long_line = line_is_long(p);
     const SimtLayout L(a.d, a.clip_k);
     const int smem = L.words * (int)sizeof(float);
     // 16-byte (fp32) or 8-byte (bf16) loads where every row starts on such a boundary

@@ -54,6 +54,7 @@ struct Params {
     int T;                                   // tokens per item
     int c0, wt;                              // cost of an item: c0 + wt * tiles
     int wt2, T1;                             // wt2 in place of wt for items of more than T1 tokens
+    int long_line;                           // the cost line may pass 31 bits
     int rec_rows;                            // rows of a record
     void *out;
     Desc *desc;                              // [gridDim.x]
@@ -77,6 +78,11 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
     s.n = q1 - s.q0;
     s.pos0 = min(max(p.kv_len[b], 0), p.cap) - s.n;
     return s;
+}
+
+// items of one key/value head
+__device__ __forceinline__ int items_of(const Params &p, const Seq &s) {
+    return s.n <= p.T ? (s.n > 0 ? 1 : 0) : (s.n + p.T - 1) / p.T;
 }
 
 // tiles of an item of cost c0 + wt nt that begin before cost position y of it
@@ -116,12 +122,13 @@ __device__ __forceinline__ Item make_item(const Params &p, const Seq &s, int qt)
     return it;
 }
 
+// floor(total * c / G) without overflow
+__device__ __forceinline__ int range_begin(int total, int c, int G) {
+    const unsigned t = (unsigned)total, g = (unsigned)G, q = t / g, r = t - q * g;
+    return (int)(q * c + r * (unsigned)c / g);
+}
 __device__ __forceinline__ long long range_begin(long long total, int c, int G) {
-    // floor(total * c / G) without overflow; 32-bit divisions where they do
-    if (total < (1LL << 31)) {
-        const unsigned t = (unsigned)total, g = (unsigned)G, q = t / g, r = t - q * g;
-        return (long long)q * c + r * (unsigned)c / g;
-    }
+    if (total < (1LL << 31)) return range_begin((int)total, c, G);
     return total / G * c + total % G * c / G;
 }
 
@@ -134,37 +141,42 @@ struct Range {
 
 // One warp calls it; every lane returns the same range. The lanes take the requests in turn, kBatch
 // of each lane's loaded at once (their latency is most of what a small step costs), and add up the
-// items of a request with many of them together.
-__device__ __forceinline__ Range find_range(const Params &p) {
+// items of a request with many of them together. I: a type that holds the whole line (32 bits where
+// the host has seen that they do: this code runs once, cold, in front of everything else, so every
+// instruction of it counts).
+template <typename I>
+__device__ __forceinline__ Range find_range_t(const Params &p) {
     constexpr int kBatch = 4;
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31, G = (int)gridDim.x, c = (int)blockIdx.x;
-    auto scan = [&](long long v) {
+    auto scan = [&](I v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(kAll, v, o);
+            const I u = __shfl_up_sync(kAll, v, o);
             if (lane >= o) v += u;
         }
         return v;
     };
-    // costs of one key/value head of requests b0 + 32 i + lane
-    auto costs = [&](int b0, long long (&cost)[kBatch]) {
+    auto sum = [&](I v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+        return v;
+    };
+    // cost of one key/value head of requests b0 + 32 i + lane
+    auto costs = [&](int b0, I (&cost)[kBatch]) {
         Seq s[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int b = b0 + 32 * i + lane;
+            cost[i] = 0;
             s[i] = Seq{0, 0, 0};
             if (b < p.B) s[i] = load_seq(p, b);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            cost[i] = 0;
-            const int nq = (s[i].n + p.T - 1) / p.T;
-            if (nq > 0 && nq <= 2) {
-                cost[i] = make_item(p, s[i], 0).cost;
-                if (nq > 1) cost[i] += make_item(p, s[i], 1).cost;
-            }
-            unsigned todo = __ballot_sync(kAll, nq > 2);
+            if (b0 + 32 * i >= p.B) break;
+            if (s[i].n > 0 && s[i].n <= p.T) cost[i] = make_item(p, s[i], 0).cost;
+            unsigned todo = __ballot_sync(kAll, s[i].n > p.T);
             while (todo) {
                 const int src = __ffs(todo) - 1;
                 todo &= todo - 1;
@@ -172,69 +184,71 @@ __device__ __forceinline__ Range find_range(const Params &p) {
                 t.q0 = 0;
                 t.n = __shfl_sync(kAll, s[i].n, src);
                 t.pos0 = __shfl_sync(kAll, s[i].pos0, src);
-                const int m = (t.n + p.T - 1) / p.T;
-                long long part = 0;
+                const int m = items_of(p, t);
+                I part = 0;
                 for (int q = lane; q < m; q += 32) part += make_item(p, t, q).cost;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+                part = sum(part);
                 if (lane == src) cost[i] = part;
             }
         }
     };
-    Range r;
-    long long cost[kBatch];
-    r.total = 0;
+    I cost[kBatch], total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32 * kBatch) {
         costs(b0, cost);
-        long long sum = 0;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) sum += cost[i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        r.total += sum * p.Hkv;
+        total += sum(cost[0] + cost[1] + cost[2] + cost[3]) * p.Hkv;
     }
-    r.x0 = range_begin(r.total, c, G);
-    r.x1 = range_begin(r.total, c + 1, G);
+    Range r;
+    r.total = total;
+    r.x0 = range_begin(total, c, G);
+    r.x1 = range_begin(total, c + 1, G);
     r.b = p.B;   // an empty range at the end finds no request
     r.kvh = r.qt = 0;
     r.x = r.x1;
-    long long at = 0, per = 0;
+    const I x0 = (I)r.x0;
+    I at = 0, per = 0, x = 0;
     for (int b0 = 0; b0 < p.B && r.b == p.B && r.x0 < r.x1; b0 += 32 * kBatch) {
         if (p.B > 32 * kBatch) costs(b0, cost);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const long long mine = cost[i] * p.Hkv, incl = at + scan(mine), lo = incl - mine;
-            const unsigned hit = __ballot_sync(kAll, mine > 0 && lo <= r.x0 && r.x0 < incl);
-            if (hit && r.b == p.B) {
+            if (b0 + 32 * i >= p.B || r.b != p.B) break;
+            const I mine = cost[i] * p.Hkv, incl = at + scan(mine), lo = incl - mine;
+            const unsigned hit = __ballot_sync(kAll, lo <= x0 && x0 < incl);
+            if (hit) {
                 const int src = __ffs(hit) - 1;
                 r.b = b0 + 32 * i + src;
                 per = __shfl_sync(kAll, cost[i], src);
-                r.x = __shfl_sync(kAll, lo, src);
+                x = __shfl_sync(kAll, lo, src);
             }
             at = __shfl_sync(kAll, incl, 31);
         }
     }
     if (r.b == p.B) return r;
     // the head, then the item within it
-    long long y = r.x0 - r.x;
-    r.kvh = y < (1LL << 31) ? (int)((unsigned)y / (unsigned)min(per, 0x7fffffffLL)) : (int)(y / per);
-    r.x += per * r.kvh;
+    r.kvh = (int)((x0 - x) / per);
+    x += per * r.kvh;
     const Seq s = load_seq(p, r.b);
-    const int nq = (s.n + p.T - 1) / p.T;
-    for (int i0 = 0; i0 < nq; i0 += 32) {
-        const int i = i0 + lane;
-        const long long cst = i < nq ? make_item(p, s, i).cost : 0;
-        const long long incl = r.x + scan(cst);
-        const unsigned hit = __ballot_sync(kAll, cst > 0 && incl - cst <= r.x0 && r.x0 < incl);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            r.qt = i0 + src;
-            r.x = __shfl_sync(kAll, incl - cst, src);
-            break;
+    if (s.n > p.T) {
+        const int nq = items_of(p, s);
+        for (int i0 = 0; i0 < nq; i0 += 32) {
+            const int i = i0 + lane;
+            const I cst = i < nq ? make_item(p, s, i).cost : 0;
+            const I incl = x + scan(cst);
+            const unsigned hit = __ballot_sync(kAll, incl - cst <= x0 && x0 < incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                r.qt = i0 + src;
+                x = __shfl_sync(kAll, incl - cst, src);
+                break;
+            }
+            x = __shfl_sync(kAll, incl, 31);
         }
-        r.x = __shfl_sync(kAll, incl, 31);
     }
+    r.x = x;
     return r;
+}
+
+__device__ __forceinline__ Range find_range(const Params &p) {
+    return p.long_line ? find_range_t<long long>(p) : find_range_t<int>(p);
 }
 
 // ------------------------------------------------------------------ the walk over a range
@@ -256,7 +270,7 @@ struct Walk {
         : b(r.b), kvh(r.kvh), qt(r.qt), nq(0), x(r.x), x0(r.x0), x1(r.x1), s{0, 0, 0} {
         if (b < p.B) {
             s = load_seq(p, b);
-            nq = (s.n + p.T - 1) / p.T;
+            nq = items_of(p, s);
         }
     }
     // the next piece of work of the range; an item without any key comes as one piece with no
@@ -269,7 +283,7 @@ struct Walk {
                     kvh = 0;
                     if (++b >= p.B) return false;
                     s = load_seq(p, b);
-                    nq = (s.n + p.T - 1) / p.T;
+                    nq = items_of(p, s);
                 }
                 continue;
             }
@@ -360,6 +374,11 @@ DeviceInfo device_info();
 cudaError_t opt_in_smem(const void *kern, const DeviceInfo &di);
 // every row of q, the pages, the tables and out starts on a 16-byte boundary
 bool wide_rows(const PagedArgs &a);
+// whether the cost line of this launch may pass 31 bits (T, c0, wt, wt2 set)
+inline int line_is_long(const Params &p) {
+    const double items = ((double)p.tokens / p.T + p.B) * p.Hkv;
+    return items * (p.c0 + (double)p.wt2 * (p.cap / kTile + 1)) > 2.0e9;
+}
 // Fills the parts of Params that do not depend on the kernel.
 void fill_params(const PagedArgs &a, Params *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent

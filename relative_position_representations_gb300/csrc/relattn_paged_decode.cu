@@ -129,7 +129,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
     // the boxes of a tile: 128 / box pages (at most 16) x DB blocks of columns, one per lane
     const int nbox = kTile / box, my_box = lane % nbox, my_blk = lane / nbox;
     const uint32_t my_dst = base + my_blk * (kTile * 128) + my_box * box * 128;
-    const Range rg = find_range(p);
+    const Range rg = find_range_t<int>(p);
     Walk walk(p, rg);
     Segment g{};
     uint32_t it = 0, tiles = 0;
@@ -604,6 +604,7 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     p.c0 = 1;   // joining the warps costs about a tile's time
     p.wt = p.wt2 = 1;
     p.rec_rows = 8 * NT;
+    if (line_is_long(p)) return cudaErrorNotSupported;
     CUtensorMap tm[3];
     const int box = a.page_size < kTile ? a.page_size : kTile;
     if (!make_query_map(&tm[0], a, p.g, p.T) || !make_page_map(&tm[1], a.k_pages, a, box) ||

@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every warp alike: the compiler fails to allocate a branch of one warp here.
     Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
     {
-        const Range r = find_range(p);
+        const Range r = find_range_t<int>(p);
         if (threadIdx.x == 96) *range = r;
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -1054,6 +1054,7 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     p.wt = 2;
     p.wt2 = 3;
     p.rec_rows = 2 * BM;
+    if (line_is_long(p)) return cudaErrorNotSupported;
     CUtensorMap tm[5];
     if (!make_query_map(&tm[0], a, p.g, tp.TS) || !make_page_map(&tm[1], a.k_pages, a, tp.box) ||
         !make_page_map(&tm[2], a.v_pages, a, tp.box))
