@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every warp alike: the compiler fails to allocate a branch of one warp here.
     Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
     {
-        const Range r = find_range_t<int>(p);
+        const Range r = find_range_t<int>(p, (int)blockIdx.x, (int)gridDim.x);
         if (threadIdx.x == 96) *range = r;
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
