@@ -248,7 +248,7 @@ __device__ void kv_role(const TcParams &tp, const Shared &sh, const CUtensorMap 
 
 // Walks the CTA's range, announces its pieces and loads their query tiles.
 template <int D>
-__device__ void walk_role(const TcParams &tp, const Range &rg, const Shared &sh, const CUtensorMap *tm_q) {
+__device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, const CUtensorMap *tm_q) {
     const Params &p = tp.p;
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
@@ -937,6 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem_raw = *tmem_slot;
+    const Range rg = *range;
+    __syncthreads();   // the rows' statistics go there
     if (warp < tc::kSoftWarp0) {
         ptx::reg_dealloc<tc::kCtrlRegs>();
         if (warp == 0) {
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             kv_role<D, AK, AV>(tp, sh, &tm_k, &tm_v, &tm_ak, &tm_av);
         } else if (warp == 3) {
             (void)__shfl_sync(0xffffffffu, tmem_raw, 0);
-            walk_role<D>(tp, *range, sh, &tm_q);
+            walk_role<D>(tp, rg, sh, &tm_q);
         } else {
             const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_raw, 0);
             mma_role<D, AK, AV>(tp, sh, tmem, warp - 1);

@@ -250,6 +250,24 @@ def test_attention_matches_the_definition(case, dtype, hint):
     check(x, got, k, **kw)
 
 
+@pytest.mark.parametrize("new,kv,H,Hkv,d,k,key,value,kw", [
+    # several tiles of a request per CTA and requests that end inside a CTA's share: pieces of both
+    # kinds (the end of one request's keys, the beginning of the next's), one and two tiles of rows
+    ([24, 3], [5000, 4100], 8, 8, 128, 0, False, False, {}),
+    ([24, 3], [5000, 4100], 8, 8, 128, 64, True, False, {}),
+    ([20, 9], [6100, 3000], 8, 8, 64, 16, True, True, {}),
+    ([131], [3300], 8, 8, 128, 64, True, True, {}),
+    ([131], [3300], 8, 8, 64, 16, True, True, dict(window=2000, sinks=200)),
+    ([37], [4000], 32, 8, 128, 0, False, False, {}),
+    ([1, 1, 1], [9000, 100, 7000], 16, 8, 128, 16, True, True, {}),
+    ([1, 1, 1], [9000, 100, 7000], 8, 8, 64, 16, True, True, dict(window=3500, sinks=4))])
+def test_long_keys_in_pieces(new, kv, H, Hkv, d, k, key, value, kw):
+    x = make(new, kv, H, Hkv, d, 16, BF16, k, key, value, seed=sum(kv) + k)
+    got = call(x, k, max_new=max(new), **kw)
+    assert _rp().relattn_get_device_error() == 0
+    check(x, got, k, **kw)
+
+
 @pytest.mark.parametrize("new,kv,H,d", [([1] * 5, [700, 3, 90, 2000, 128], 4, 64), ([300, 20], [900, 40], 2, 128)])
 def test_equal_calls_give_equal_bits(new, kv, H, d):
     x = make(new, kv, H, H, d, 16, BF16, 16, True, True)
