@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
     // a warp per row and 32 columns up to 16 rows, else a warp per two rows
     const bool few = p.rec_rows <= 16;
-    const int warps = few ? p.rec_rows * ((p.d + 31) / 32) : p.rec_rows / 2;
+    const int warps = few ? p.likely_rows * ((p.d + 31) / 32) : (p.likely_rows + 1) / 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid, (warps + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(kMergeThreads);
@@ -189,8 +189,11 @@ cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
 // ------------------------------------------------------------------ SIMT kernel
 // 32 query rows at a time (an item has T = max(1, 32 / g) tokens, so more only when g > 32: then
 // the rows go in groups of 32 over the same keys), 8 warps of 4 rows. 32 keys at a time are
-// staged in shared memory as fp32; lane = key for the scores (four rows share each load of a
-// key), lane = four columns for P V. All sums and statistics fp32.
+// staged in shared memory as fp32: lane = key for the scores (four rows share each load of a key),
+// lane = N4 columns for P V. The next 32 keys are on their way into registers meanwhile, and the
+// page numbers of the ones behind them. The edge tables go the same way: R = Q aK^T takes table
+// rows for keys, beta aV takes beta for P. All sums and statistics fp32; bound by latency at the
+// sizes of a test, by the fp32 units at larger ones.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 32;
 constexpr int kSimtKeys = 32;
@@ -218,7 +221,7 @@ struct SimtLayout {
         d4 = (d + 3) & ~3;
         ld = d4 + 4;                         // 16-byte loads of 8 rows fall in distinct banks
         W = clip_k + 1;
-        lw = W | 1;
+        lw = (W + kSimtKeys - 1) / kSimtKeys * kSimtKeys + 1;
         int o = 0;
         q = o;  o += kSimtRows * d4;
         k = o;  o += kSimtKeys * ld;
@@ -230,8 +233,9 @@ struct SimtLayout {
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_constant__ Params p, int vec) {
+// N4: 16-byte chunks of a row that a thread's share of 32 rows needs, ceil(d / 4 / 8)
+template <typename T, int N4>
+__global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __grid_constant__ Params p, int vec) {
     extern __shared__ __align__(16) float smf[];
     __shared__ Range rg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -247,6 +251,67 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
     const bool ak = p.aK != nullptr, av = p.aV != nullptr;
     const int P = 1 << p.pshift;
     float *qs = smf + L.q, *Ks = smf + L.k, *Vs = smf + L.v, *ps = smf + L.pr, *Rs = smf + L.R, *Bs = smf + L.Bn;
+    // a thread stages chunks my_c, my_c + 8, ... of row my_key
+    const int my_key = tid >> 3, my_c = tid & 7;
+    const bool wide = vec != 0;
+    auto fetch = [&](float4 (&x)[N4], const T *row, bool on) {
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+            const int c = my_c + 8 * i;
+            x[i] = on && c < n4 ? load4(row, 4 * c, d, wide) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    auto put = [&](float *dst, const float4 (&x)[N4]) {
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+            const int c = my_c + 8 * i;
+            if (c < n4) *reinterpret_cast<float4 *>(dst + my_key * L.ld + 4 * c) = x[i];
+        }
+    };
+    // products of this lane's staged row with the warp's four query rows
+    auto scores = [&](float (&s)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < d4; c += 4) {
+            const float4 kx = *reinterpret_cast<const float4 *>(Ks + lane * L.ld + c);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 qx = *reinterpret_cast<const float4 *>(qs + (warp * 4 + u) * d4 + c);
+                s[u] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, s[u]))));
+            }
+        }
+    };
+    // o += weights of the warp's rows (ps) times the staged rows, N4 columns of this lane
+    auto outputs = [&](float (&o)[4][N4]) {
+        if (N4 * lane >= d4) return;
+#pragma unroll 1
+        for (int kk = 0; kk < kSimtKeys; kk += 4) {
+            float4 pr[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) pr[u] = *reinterpret_cast<const float4 *>(ps + (warp * 4 + u) * kSimtKeys + kk);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float vx[N4];
+                const float *row = Vs + (kk + e) * L.ld + N4 * lane;
+                if (N4 == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(row);
+                    vx[0] = t.x; vx[N4 - 3] = t.y; vx[N4 - 2] = t.z; vx[N4 - 1] = t.w;
+                } else if (N4 == 2) {
+                    const float2 t = *reinterpret_cast<const float2 *>(row);
+                    vx[0] = t.x; vx[N4 - 1] = t.y;
+                } else {
+                    vx[0] = row[0];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float w = e == 0 ? pr[u].x : e == 1 ? pr[u].y : e == 2 ? pr[u].z : pr[u].w;
+#pragma unroll
+                    for (int i = 0; i < N4; ++i) o[u][i] = fmaf(w, vx[i], o[u][i]);
+                }
+            }
+        }
+    };
     Walk walk(p, rg);
     Segment g{};
     bool any = false;
@@ -256,174 +321,173 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
         const T *aK = static_cast<const T *>(p.aK) + (long long)g.kvh * p.ths;
         const T *aV = static_cast<const T *>(p.aV) + (long long)g.kvh * p.ths;
         const int *bt = p.bt + (long long)g.b * p.bt_stride;
+        const int first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
+        const int pos_hi = g.it.pos_hi;
+        // the piece's runs of 32 keys that some row sees: run q of tile t0 + q / 4
+        const int runs = (g.t1 - g.t0) * (kTile / kSimtKeys);
+        auto run_key = [&](int q) { return g.it.tile(g.t0 + (q >> 2)) * kTile + (q & 3) * kSimtKeys; };
+        auto next_run = [&](int q) {
+            for (; q < runs; ++q) {
+                const int j0 = run_key(q);
+                if (j0 <= pos_hi && (j0 + kSimtKeys > first || j0 < p.sinks)) break;
+            }
+            return q;
+        };
+        // page of this thread's key of run q (-1: not seen, -2: no such page)
+        auto page_of = [&](int q) -> int {
+            if (q >= runs) return -1;
+            const int j = run_key(q) + my_key;
+            if (!(j <= pos_hi && (j >= first || j < p.sinks))) return -1;
+            const int pg = bt[j >> p.pshift];
+            return (unsigned)pg < (unsigned)p.num_pages ? pg : -2;
+        };
+        auto row_of = [&](const void *base, int q, int pg) -> const T * {
+            const long long at = (long long)pg * p.page_stride + ((long long)g.kvh * P + ((run_key(q) + my_key) & (P - 1))) * d;
+            return static_cast<const T *>(base) + (pg >= 0 ? at : 0);
+        };
         for (int r0 = 0; r0 < rows; r0 += kSimtRows) {
             const int nr = min(kSimtRows, rows - r0);
+            // the first run's keys and the second one's pages, under way during the set-up
+            int q0 = next_run(0), q1 = next_run(q0 + 1);
+            int pg0 = page_of(q0), pg1 = page_of(q1);
+            float4 kx[N4], vx[N4];
+            if (pg0 == -2 && my_c == 0) report_page(p);
+            fetch(kx, row_of(p.k, q0, pg0), pg0 >= 0);
+            fetch(vx, row_of(p.v, q0, pg0), pg0 >= 0);
             __syncthreads();   // the previous rows are done with everything
-            for (int i = tid; i < kSimtRows * n4; i += kSimtThreads) {
-                const int r = i / n4, c = (i - r * n4) * 4;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < nr) {
-                    const int tok = (r0 + r) / p.g, hh = (r0 + r) - tok * p.g;
-                    x = load4(static_cast<const T *>(p.q) + (long long)(g.s.q0 + g.it.i0 + tok) * p.q_stride +
-                                  (long long)(g.kvh * p.g + hh) * d, c, d, vec != 0);
-                }
-                *reinterpret_cast<float4 *>(qs + r * d4 + c) = x;
-            }
-            __syncthreads();
-            if (ak) {   // R = Q aK^T in the log2 domain, rows 0 .. k
-                for (int i = tid; i < nr * L.W; i += kSimtThreads) {
-                    const int r = i / L.W, w = i - r * L.W;
-                    float acc = 0.f;
-                    for (int c = 0; c < d; ++c) acc = fmaf(qs[r * d4 + c], to_f(aK[(long long)w * d + c]), acc);
-                    Rs[r * L.lw + w] = acc * p.scale_log2;
-                }
+            {
+                const int tok = (r0 + my_key) / p.g, hh = (r0 + my_key) - tok * p.g;
+                const T *q = static_cast<const T *>(p.q) + (long long)(g.s.q0 + g.it.i0 + tok) * p.q_stride +
+                             (long long)(g.kvh * p.g + hh) * d;
+                float4 x[N4];
+                fetch(x, q, my_key < nr);
+#pragma unroll
+                for (int i = 0; i < N4; ++i)
+                    if (my_c + 8 * i < n4) *reinterpret_cast<float4 *>(qs + my_key * d4 + 4 * (my_c + 8 * i)) = x[i];
             }
             if (av)
                 for (int i = tid; i < kSimtRows * L.lw; i += kSimtThreads) Bs[i] = -INFINITY;
-            __syncthreads();
+            if (ak) {   // R = Q aK^T in the log2 domain
+                for (int w0 = 0; w0 < L.W; w0 += kSimtKeys) {
+                    float4 x[N4];
+                    fetch(x, aK + (long long)min(w0 + my_key, k) * d, w0 + my_key <= k);
+                    put(Ks, x);
+                    __syncthreads();
+                    float s[4];
+                    scores(s);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) Rs[(warp * 4 + u) * L.lw + w0 + lane] = s[u] * p.scale_log2;
+                    __syncthreads();
+                }
+            }
             int pos[4];
-            bool live[4];
             float m[4], l[4], far[4];
-            float4 o[4];
+            float o[4][N4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int r = warp * 4 + u;
-                live[u] = r < nr;
-                pos[u] = g.it.pos_lo + (live[u] ? (r0 + r) / p.g : 0);
+                pos[u] = r < nr ? g.it.pos_lo + (r0 + r) / p.g : -1;
                 m[u] = -INFINITY;
                 l[u] = far[u] = 0.f;
-                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < N4; ++i) o[u][i] = 0.f;
             }
-            const int first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
-            for (int t = g.t0; t < g.t1; ++t) {
-                for (int j0 = g.it.tile(t) * kTile; j0 < g.it.tile(t) * kTile + kTile; j0 += kSimtKeys) {
-                    if (j0 > g.it.pos_hi || (j0 + kSimtKeys <= first && j0 >= p.sinks)) continue;  // seen by no row
-                    __syncthreads();
-                    for (int i = tid; i < kSimtKeys * n4; i += kSimtThreads) {
-                        const int kk = i / n4, c = (i - kk * n4) * 4, j = j0 + kk;
-                        float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-                        if (j <= g.it.pos_hi && (j >= first || j < p.sinks)) {
-                            const int pg = bt[j >> p.pshift];
-                            if ((unsigned)pg < (unsigned)p.num_pages) {
-                                const long long off = (long long)pg * p.page_stride +
-                                                      ((long long)g.kvh * P + (j & (P - 1))) * d;
-                                kx = load4(static_cast<const T *>(p.k) + off, c, d, vec != 0);
-                                vx = load4(static_cast<const T *>(p.v) + off, c, d, vec != 0);
-                            } else if (c == 0) {
-                                report_page(p);
-                            }
-                        }
-                        *reinterpret_cast<float4 *>(Ks + kk * L.ld + c) = kx;
-                        *reinterpret_cast<float4 *>(Vs + kk * L.ld + c) = vx;
-                    }
-                    __syncthreads();
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int c = 0; c < d4; c += 4) {
-                        const float4 kx = *reinterpret_cast<const float4 *>(Ks + lane * L.ld + c);
+#pragma unroll 1
+            while (q0 < runs) {
+                const int j = run_key(q0) + lane;
+                __syncthreads();   // the previous run's rows have been read
+                put(Ks, kx);
+                put(Vs, vx);
+                q0 = q1;
+                pg0 = pg1;
+                if (pg0 == -2 && my_c == 0) report_page(p);
+                fetch(kx, row_of(p.k, q0, pg0), pg0 >= 0);
+                fetch(vx, row_of(p.v, q0, pg0), pg0 >= 0);
+                q1 = next_run(q1 + 1);
+                pg1 = page_of(q1);
+                __syncthreads();
+                float s[4], mx[4];
+                scores(s);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float4 qx = *reinterpret_cast<const float4 *>(qs + (warp * 4 + u) * d4 + c);
-                            s[u] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, s[u]))));
-                        }
-                    }
-                    const int j = j0 + lane;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int r = warp * 4 + u;
-                        const int lab = max(j - pos[u], -k) + k;   // table row; > k for later keys
-                        const bool seen = live[u] && j <= pos[u] &&
-                                          (p.window == 0 || j > pos[u] - p.window || j < p.sinks);
-                        float x = s[u] * p.scale_log2;
-                        if (ak && seen) x += Rs[r * L.lw + lab];
-                        x = seen ? x : -INFINITY;
-                        float mx = x;
-#pragma unroll
-                        for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                        const float mn = fmaxf(m[u], mx);
-                        const float mu = mn == -INFINITY ? 0.f : mn;
-                        const float al = exp2f(m[u] - mu);
-                        const float e = exp2f(x - mu);
-                        m[u] = mn;
-                        l[u] = l[u] * al + e;      // per lane; summed at the end
-                        if (av) {
-                            far[u] *= al;
-                            if (seen && lab > 0) Bs[r * L.lw + lab] = x;
-                            else far[u] += e;
-                        }
-                        o[u].x *= al;
-                        o[u].y *= al;
-                        o[u].z *= al;
-                        o[u].w *= al;
-                        ps[r * kSimtKeys + lane] = e;
-                    }
-                    __syncwarp();
-                    if (4 * lane < d4) {
-#pragma unroll 2
-                        for (int kk = 0; kk < kSimtKeys; kk += 4) {
-                            float4 pr[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                pr[u] = *reinterpret_cast<const float4 *>(ps + (warp * 4 + u) * kSimtKeys + kk);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 vx = *reinterpret_cast<const float4 *>(Vs + (kk + e) * L.ld + 4 * lane);
-#pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const float w = e == 0 ? pr[u].x : e == 1 ? pr[u].y : e == 2 ? pr[u].z : pr[u].w;
-                                    o[u].x = fmaf(w, vx.x, o[u].x);
-                                    o[u].y = fmaf(w, vx.y, o[u].y);
-                                    o[u].z = fmaf(w, vx.z, o[u].z);
-                                    o[u].w = fmaf(w, vx.w, o[u].w);
-                                }
-                            }
-                        }
-                    }
-                    __syncwarp();
+                for (int u = 0; u < 4; ++u) {
+                    const int r = warp * 4 + u;
+                    const int lab = max(j - pos[u], -k) + k;   // table row; > k for later keys
+                    const bool seen = j <= pos[u] && (p.window == 0 || j > pos[u] - p.window || j < p.sinks);
+                    s[u] = s[u] * p.scale_log2 + (ak && seen ? Rs[r * L.lw + lab] : 0.f);
+                    s[u] = seen ? s[u] : -INFINITY;
+                    if (av && seen && lab > 0) Bs[r * L.lw + lab] = s[u];
+                    mx[u] = s[u];
                 }
+#pragma unroll
+                for (int sh = 16; sh > 0; sh >>= 1)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], sh));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float mn = fmaxf(m[u], mx[u]), mu = mn == -INFINITY ? 0.f : mn;
+                    const float e = exp2f(s[u] - mu);
+                    if (mn != m[u]) {   // uniform over the warp
+                        const float al = exp2f(m[u] - mu);
+                        m[u] = mn;
+                        l[u] *= al;
+                        far[u] *= al;
+#pragma unroll
+                        for (int i = 0; i < N4; ++i) o[u][i] *= al;
+                    }
+                    l[u] += e;          // per lane; summed at the end
+                    if (av && j - pos[u] + k <= 0) far[u] += e;
+                    ps[(warp * 4 + u) * kSimtKeys + lane] = e;
+                }
+                __syncwarp();
+                outputs(o);
             }
             // ---- the rows' sums, the value term, the result
+#pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    l[u] += __shfl_xor_sync(0xffffffffu, l[u], sh);
+                    far[u] += __shfl_xor_sync(0xffffffffu, far[u], sh);
+                }
+            if (av) {
+                for (int w0 = 0; w0 < L.W; w0 += kSimtKeys) {
+                    float4 x[N4];
+                    fetch(x, aV + (long long)min(w0 + my_key, k) * d, w0 + my_key <= k);
+                    __syncthreads();
+                    put(Vs, x);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int w = w0 + lane;
+                        const float mu = m[u] == -INFINITY ? 0.f : m[u];
+                        ps[(warp * 4 + u) * kSimtKeys + lane] =
+                            w == 0 ? far[u] : w <= k ? exp2f(Bs[(warp * 4 + u) * L.lw + w] - mu) : 0.f;
+                    }
+                    __syncthreads();
+                    outputs(o);
+                }
+            }
             const bool whole = g.whole();
             float *rec = whole ? nullptr : record(p, blockIdx.x, g.record());
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int r = warp * 4 + u;
-                if (!live[u]) continue;   // the whole warp's row
-                float ls = l[u], fs = far[u];
-#pragma unroll
-                for (int sh = 16; sh > 0; sh >>= 1) {
-                    ls += __shfl_xor_sync(0xffffffffu, ls, sh);
-                    fs += __shfl_xor_sync(0xffffffffu, fs, sh);
-                }
-                if (av) {
-                    const float mu = m[u] == -INFINITY ? 0.f : m[u];
-                    for (int w = 0; w < L.W; ++w) {
-                        const float pw = w == 0 ? fs : exp2f(Bs[r * L.lw + w] - mu);
-                        if (pw == 0.f || 4 * lane >= d4) continue;
-                        const float4 x = load4(aV + (long long)w * d, 4 * lane, d, vec != 0);
-                        o[u].x = fmaf(pw, x.x, o[u].x);
-                        o[u].y = fmaf(pw, x.y, o[u].y);
-                        o[u].z = fmaf(pw, x.z, o[u].z);
-                        o[u].w = fmaf(pw, x.w, o[u].w);
-                    }
-                }
-                const float os[4] = {o[u].x, o[u].y, o[u].z, o[u].w};
-                const int rr = r0 + r;
+                const int r = warp * 4 + u, rr = r0 + r;
+                if (r >= nr) continue;
                 if (whole) {
-                    const float inv = ls > 0.f ? 1.f / ls : 0.f;
+                    const float inv = l[u] > 0.f ? 1.f / l[u] : 0.f;
                     const int tok = rr / p.g, hh = rr - tok * p.g;
                     T *out = static_cast<T *>(p.out) +
                              ((long long)(g.s.q0 + g.it.i0 + tok) * p.H + g.kvh * p.g + hh) * d;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * lane + e < d) out[4 * lane + e] = from_f<T>(os[e] * inv);
+                    for (int i = 0; i < N4; ++i)
+                        if (N4 * lane + i < d) out[N4 * lane + i] = from_f<T>(o[u][i] * inv);
                 } else {
                     if (lane == 0) {
                         rec[rr] = m[u];
-                        rec[p.rec_rows + rr] = ls;
+                        rec[p.rec_rows + rr] = l[u];
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * lane + e < d) rec[2 * p.rec_rows + (long long)rr * d + 4 * lane + e] = os[e];
+                    for (int i = 0; i < N4; ++i)
+                        if (N4 * lane + i < d) rec[2 * p.rec_rows + (long long)rr * d + N4 * lane + i] = o[u][i];
                 }
             }
         }
@@ -431,7 +495,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
     if (tid == 0) write_desc(p, any ? &g : nullptr, rg.total);
 }
 
-template <typename T>
+template <typename T, int N4>
 cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     Params p;
     fill_params(a, &p);
@@ -441,6 +505,7 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     p.wt = p.wt2 = 2;
     p.rec_rows = kRecordRows;
     p.long_line = line_is_long(p);
+    p.likely_rows = likely_rows(a, p.T, p.g);
     const SimtLayout L(a.d, a.clip_k);
     const int smem = L.words * (int)sizeof(float);
     // 16-byte (fp32) or 8-byte (bf16) loads where every row starts on such a boundary
@@ -452,13 +517,18 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     const int vec = al % (4 * es) == 0;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(paged_simt_kernel<T>), di);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(paged_simt_kernel<T, N4>), di);
     if (e != cudaSuccess) return e;
     const int grid = 2 * di.sms < kMaxGrid ? 2 * di.sms : kMaxGrid;
-    paged_simt_kernel<T><<<grid, kSimtThreads, smem, s>>>(p, vec);
+    paged_simt_kernel<T, N4><<<grid, kSimtThreads, smem, s>>>(p, vec);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_merge(p, grid, sizeof(T) == 2, s);
+}
+
+template <typename T>
+cudaError_t launch_simt_d(const PagedArgs &a, cudaStream_t s) {
+    return a.d <= 32 ? launch_simt_t<T, 1>(a, s) : a.d <= 64 ? launch_simt_t<T, 2>(a, s) : launch_simt_t<T, 4>(a, s);
 }
 
 }  // namespace paged
@@ -469,7 +539,7 @@ unsigned long long paged_workspace_bytes(int d) {
 }
 
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s) {
-    return a.bf16 ? paged::launch_simt_t<__nv_bfloat16>(a, s) : paged::launch_simt_t<float>(a, s);
+    return a.bf16 ? paged::launch_simt_d<__nv_bfloat16>(a, s) : paged::launch_simt_d<float>(a, s);
 }
 
 }  // namespace relattn

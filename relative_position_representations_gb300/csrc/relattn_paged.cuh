@@ -55,6 +55,7 @@ struct Params {
     int c0, wt;                              // cost of an item: c0 + wt * tiles
     int wt2, T1;                             // wt2 in place of wt for items of more than T1 tokens
     int long_line;                           // the cost line may pass 31 bits
+    int likely_rows;                         // rows of an item at most, going by max_new
     int rec_rows;                            // rows of a record
     void *out;
     Desc *desc;                              // [gridDim.x]
@@ -380,6 +381,10 @@ bool wide_rows(const PagedArgs &a);
 inline int line_is_long(const Params &p) {
     const double items = ((double)p.tokens / p.T + p.B) * p.Hkv;
     return items * (p.c0 + (double)p.wt2 * (p.cap / kTile + 1)) > 2.0e9;
+}
+inline int likely_rows(const PagedArgs &a, int T, int g) {
+    const int n = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
+    return (n < T ? n : T) * g;
 }
 // Fills the parts of Params that do not depend on the kernel.
 void fill_params(const PagedArgs &a, Params *p);

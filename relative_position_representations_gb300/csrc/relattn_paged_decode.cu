@@ -691,6 +691,7 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     p.wt = p.wt2 = 1;
     p.rec_rows = 8 * NT;
     if (line_is_long(p)) return cudaErrorNotSupported;
+    p.likely_rows = likely_rows(a, p.T, p.g);
     CUtensorMap tm[3];
     const int box = a.page_size < kTile ? a.page_size : kTile;
     if (!make_query_map(&tm[0], a, p.g, p.T) || !make_page_map(&tm[1], a.k_pages, a, box) ||

@@ -1057,6 +1057,7 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     p.wt2 = 3;
     p.rec_rows = 2 * BM;
     if (line_is_long(p)) return cudaErrorNotSupported;
+    p.likely_rows = likely_rows(a, p.T, p.g);
     CUtensorMap tm[5];
     if (!make_query_map(&tm[0], a, p.g, tp.TS) || !make_page_map(&tm[1], a.k_pages, a, tp.box) ||
         !make_page_map(&tm[2], a.v_pages, a, tp.box))
