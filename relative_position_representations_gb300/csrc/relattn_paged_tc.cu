@@ -496,12 +496,13 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     const bool pos_scale = sl2 >= 0.f;
     const int k = p.clip_k, W = tp.W;
     uint32_t s_it = 0, pv_it = 0, x_it = 0, o_it[2] = {0, 0};
-    bool ok = true;
-    // one warp of the slot polls, the others meet it at the slot's named barrier
+    bool ok = true, bad = false;
+    // one warp of the slot polls, the others meet it at the slot's named barrier (bad: a wait of
+    // this warp's own ran out)
     auto wait_w = [&](uint32_t b, uint32_t parity) -> bool {
-        bool r = true;
+        bool r = !bad;
         if (quad == 0) {
-            r = wait_bar(b, parity, sh, p.err);
+            r = r && wait_bar(b, parity, sh, p.err);
             r = __all_sync(0xffffffffu, r ? 1 : 0) != 0;
         }
         return slot_sync(slot, r);
@@ -512,6 +513,16 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         ptx::tc_fence_after();
         __syncwarp();
         return true;
+    };
+    // Inside the tile loop each warp waits for itself (a meeting of the four takes 250 cycles more). A
+    // wait that runs out marks the warp; it goes on, and the four leave together at their next meeting.
+    auto wait_own = [&](uint32_t b, uint32_t parity) {
+        if (!bad) {
+            const bool r = wait_bar(b, parity, sh, p.err);
+            bad = __all_sync(0xffffffffu, r ? 1 : 0) == 0;
+        }
+        ptx::tc_fence_after();
+        __syncwarp();
     };
     // the warp's arrival, after all its lanes
     auto arrive = [&](uint32_t b) {
@@ -615,7 +626,8 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         for (int t = g.t0; t <= w.t_last; ++t) {
             if (!w.uses(p, g, slot, t)) continue;
             const int j0 = g.tile(t) * kTile;
-            if (!(ok = wait_s())) break;
+            wait_own(sbar(SB_S_FULL), s_it & 1u);
+            ++s_it;
             const bool last = t == w.t_last;
             const bool keep_s = AV && last && (!split || slot == 0);   // beta will lie there
             // chunk of 32 keys from e0: seen by no row of the warp / without masks / beyond the band
@@ -684,7 +696,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                 m_ref = rmax;
             }
             // P and O are free once the previous P V is done (P over S: S_j was issued after it)
-            if (!T::P_ALIAS && n > 0 && !(ok = wait_pv(pv_it + n - 1u))) break;
+            if (!T::P_ALIAS && n > 0) wait_own(sbar(SB_PV_DONE), (pv_it + n - 1u) & 1u);
             if (mine) {
                 if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     l *= alpha;
@@ -748,7 +760,6 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
             arrive(sbar(SB_P_FULL));
             ++n;
         }
-        if (!ok) break;
         pv_it += n;
         // ---- the row's maximum and sum; where the slots shared the rows, of both
         float M = m_ref, f0 = 1.f, f1 = 0.f;
