@@ -105,6 +105,25 @@ struct Pieces {
     __device__ __forceinline__ uint32_t empty() const { return bars + 8u * (B_PIECE_EMPTY + (it & (kPieces - 1))); }
 };
 
+// D += A B over 64 keys (4 k-steps), one elect for the chain: A (P, bf16 pairs) in TMEM, 8 columns per
+// step, B (V) MN-major with 128-byte swizzle, 16 rows x 128 bytes per step
+__device__ __forceinline__ void mma_ts_k64(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 t, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "add.u32 a1, %1, 16;\n\tadd.s64 b1, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "add.u32 a1, %1, 24;\n\tadd.s64 b1, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "}\n" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(1u)
+        : "memory");
+}
+
 // one slot's share of a piece
 struct SlotWork {
     bool split;          // the two slots take the tiles of the same rows in turn
@@ -422,11 +441,11 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     const uint64_t dv = dv0 + (uint64_t)ring.st * stage16;
                     if (!(ok = wait(sbar(SB_P_HALF), p_it & 1u))) break;
                     ptx::tc_fence_after();
-                    ptx::tc_mma_ts_k64(tO, tP, dv, idPV, started ? 1u : 0u);
+                    mma_ts_k64(tO, tP, dv, idPV, started ? 1u : 0u);
                     if (!(ok = wait(sbar(SB_P_FULL), p_it & 1u))) break;
                     ++p_it;
                     ptx::tc_fence_after();
-                    ptx::tc_mma_ts_k64(tO, tP + 32u, dv + 512u, idPV, 1u);
+                    mma_ts_k64(tO, tP + 32u, dv + 512u, idPV, 1u);
                     started = true;
                     ptx::tc_commit_w(sbar(SB_PV_DONE));
                     ++pv_it;

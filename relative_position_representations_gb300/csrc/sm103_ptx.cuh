@@ -244,18 +244,6 @@ __device__ __forceinline__ void tc_mma_ts_k128(uint32_t d, uint32_t a_tmem, uint
         ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(1u)
         : "memory");
 }
-// ts_k64: the same over 64 keys (4 k-steps)
-__device__ __forceinline__ void tc_mma_ts_k64(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 t, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-        RELATTN_MMA_TS_STEP(8, 128) RELATTN_MMA_TS_STEP(16, 256) RELATTN_MMA_TS_STEP(24, 384) "}\n"
-        ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(1u)
-        : "memory");
-}
 // ts_k128_2: the same over 128 keys whose A operand sits in two TMEM blocks of 32 columns:
 // keys 0..63 (k-steps 0..3) at a_lo, keys 64..127 (k-steps 4..7) at a_hi
 __device__ __forceinline__ void tc_mma_ts_k128_2(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint64_t b,
