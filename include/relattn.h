@@ -387,8 +387,13 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  *
  * The work is split over the GPU by keys, whatever the mix of lengths; pieces of one token's
  * keys are joined in a fixed order, so equal calls give equal bits.
- * fp32 arithmetic on the SIMT units. d <= 128, clip_k <= 256 and H / Hkv <= 128, else
- * RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing.
+ * bf16 with d = 64 or 128, pages of at least 8 keys and rows that start on 16-byte boundaries
+ * (base pointers and strides) runs on the tensor cores, fp32 accumulation and statistics, the
+ * weights rounded to bf16 for their product: with at most 16 query rows (max_new times H / Hkv) per
+ * key/value head on a kernel for generated tokens, else, up to clip_k = 127, on the one for chunks.
+ * Everything else runs on the SIMT units with fp32 arithmetic. d <= 128, clip_k <= 256 and
+ * H / Hkv <= 128, else RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing. Device waits are
+ * bounded as in relattn_fwd; after one that runs out the output is undefined.
  */
 RELATTN_API relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void *k_pages,
                                    const void *v_pages, long long page_stride, int num_pages,
@@ -578,8 +583,8 @@ RELATTN_API relattn_status_t relattn_get_device_error(relattn_stream_t stream);
 
 /*
  * relattn_set_wait_limit — the bound of every device-side wait of the tensor-core forward
- * kernels (relattn_fwd, relattn_t5bias_fwd, relattn_alibi_fwd, relattn_offset_bias_fwd on
- * bf16), in SM clock cycles; the default is 2e9 (about one second at 2 GHz). A wait that
+ * kernels (relattn_fwd, relattn_t5bias_fwd, relattn_alibi_fwd, relattn_offset_bias_fwd,
+ * relattn_paged_fwd on bf16), in SM clock cycles; the default is 2e9 (about one second at 2 GHz). A wait that
  * runs out makes every warp of the kernel stop, wait (again bounded) for its copies and
  * tensor-core operations in flight, release its tensor memory and exit; the call's output is
  * then undefined and relattn_get_device_error reports RELATTN_ERR_TIMEOUT. The setting is
@@ -592,8 +597,8 @@ RELATTN_API relattn_status_t relattn_set_wait_limit(long long cycles);
 /*
  * relattn_debug_withhold_first_load — test hook for the timeout path: with on = 1, each
  * producer warp of the tensor-core forward kernels announces the Q tiles of its first work
- * item to their barrier but never loads them, so the tensor-core warp's bounded wait for
- * them runs out (no fault, no trap: the kernel exits through its abort path). on = 0
+ * item to their barrier but never loads them (relattn_paged_fwd: the queries of each CTA's first piece), so the
+ * bounded wait for them runs out (no fault, no trap: the kernel exits through its abort path). on = 0
  * (the default) restores normal launches. Process-wide; never set it in production.
  */
 RELATTN_API relattn_status_t relattn_debug_withhold_first_load(int on);

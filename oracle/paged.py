@@ -20,11 +20,11 @@ def plan(cached, new, table, free, head, P, max_tokens):
         fits = c >= 0 and 0 <= n <= max_tokens and -(-(c + n) // P) <= M
         need = -(-(c + n) // P) - -(-c // P) if fits else 0
         want += need
-        placed = fits and q_start[-1] + rows <= max_tokens and (need == 0 or want <= len(free))
+        placed = fits and q_start[-1] + rows <= max_tokens and (need == 0 or (head >= 0 and want <= len(free)))
         if placed:
             for i in range(need):
                 table[b, -(-c // P) + i] = free[want - need + i]
-            at = max(at, want)
+            at = max(at, want) if need else at
             slots += [int(table[b, (c + i) // P]) * P + (c + i) % P for i in range(n)]
         else:
             ok = False

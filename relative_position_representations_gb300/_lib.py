@@ -614,21 +614,33 @@ def relattn_decode_fwd(q, k_cache, v_cache, cache_len, aK=None, aV=None, clip_k=
 
 
 # ---- paged cache. These calls run once per layer and step, the smallest for two microseconds on the
-# GPU, so their checks are written to cost little: devices as indexes, shapes and strides read once.
+# GPU, so their checks are written to cost little: each attribute of a tensor is read once, and the
+# reasons are looked for only when a check has failed.
 _INT = torch.int32
 
 
-def _on(dev, name, t):
-    """t is a tensor on CUDA device `dev` (an index)."""
+def _misplaced(dev, name, t):
+    """Raises for a t that is no tensor on CUDA device `dev` (an index)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s is on cuda:%d, not on cuda:%d" % (name, t.get_device(), dev))
+    raise ValueError("%s is on cuda:%d, not on cuda:%d" % (name, t.get_device(), dev))
+
+
+def _device_of(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _on(dev, name, t):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(dev, name, t)
 
 
 def _ints(dev, name, t, count):
     """t holds `count` contiguous int32 on device `dev`; returns its address."""
-    _on(dev, name, t)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(dev, name, t)
     if t.dtype is not _INT:
         raise TypeError("%s must be torch.int32, got %s" % (name, t.dtype))
     if t.numel() != count:
@@ -640,59 +652,68 @@ def _ints(dev, name, t, count):
 
 def _table(dev, t, B):
     """block_table [B, max_pages] int32; its rows may be spaced. Returns (stride, max_pages)."""
-    _on(dev, "block_table", t)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(dev, "block_table", t)
     if t.dtype is not _INT:
         raise TypeError("block_table must be torch.int32, got %s" % t.dtype)
-    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != B or shape[1] < 1:
         raise ValueError("block_table must be [B, max_pages]")
-    M = t.shape[1]
+    M = shape[1]
     s0, s1 = t.stride()
-    if (M > 1 and s1 != 1) or (B > 1 and s0 < M):
+    if (s1 != 1 and M > 1) or (s0 < M and B > 1):
         raise ValueError("block_table's rows must be contiguous and must not overlap")
     return (s0 if B > 1 else M), M
 
 
-def _spaced(dev, name, t, shape, dtype):
-    """t has `shape` and dtype and is contiguous but for the stride of its first dimension, which
-    is returned (no shorter than a row)."""
-    _on(dev, name, t)
+def _rows(dev, name, t, n, h, d, dtype):
+    """t is [n, h, d] of dtype with contiguous [h, d] rows; returns the stride between them (no
+    shorter than a row)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(dev, name, t)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    stride = t.stride()
-    if shape[0] > 1 and t.is_contiguous():
-        return stride[0]
-    row = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if stride[i] != row and shape[i] > 1:
-            raise ValueError("%s must be contiguous behind its first dimension" % name)
-        row *= shape[i]
-    if shape[0] <= 1:
-        return row
-    if stride[0] < row:
+    if t.shape != (n, h, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (n, h, d), tuple(t.shape)))
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError("%s must be contiguous behind its first dimension" % name)
+    if n <= 1:
+        return h * d
+    if s0 < h * d:
         raise ValueError("%s's first dimension overlaps" % name)
-    return stride[0]
+    return s0
 
 
 def _pages(k_pages, v_pages):
-    """k_pages and v_pages [num_pages, Hkv, page_size, d] with one stride between pages. Returns
-    (device index, page stride)."""
-    if not isinstance(k_pages, torch.Tensor) or not k_pages.is_cuda:
-        raise TypeError("k_pages must be a CUDA tensor")
-    if k_pages.dim() != 4:
+    """k_pages and v_pages [num_pages, Hkv, page_size, d] of one dtype and layout, pages spaced at
+    will. Returns (device index, shape, dtype, page stride)."""
+    dev = _device_of("k_pages", k_pages)
+    _on(dev, "v_pages", v_pages)
+    shape, dtype, stride = k_pages.shape, k_pages.dtype, k_pages.stride()
+    if len(shape) != 4:
         raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
-    dev, shape, dtype = k_pages.get_device(), k_pages.shape, k_pages.dtype
-    stride = _spaced(dev, "k_pages", k_pages, shape, dtype)
-    if _spaced(dev, "v_pages", v_pages, shape, dtype) != stride:
-        raise ValueError("k_pages and v_pages must have one page stride")
-    return dev, stride
+    if v_pages.dtype is not dtype:
+        raise TypeError("v_pages must be %s, got %s" % (dtype, v_pages.dtype))
+    if v_pages.shape != shape:
+        raise ValueError("v_pages must have shape %s, got %s" % (tuple(shape), tuple(v_pages.shape)))
+    N, h, P, d = shape
+    for name, (s0, s1, s2, s3) in (("k_pages", stride), ("v_pages", v_pages.stride())):
+        if (s3 != 1 and d > 1) or (s2 != d and P > 1) or (s1 != P * d and h > 1):
+            raise ValueError("%s must be contiguous behind its first dimension" % name)
+        if N > 1 and s0 != stride[0]:
+            raise ValueError("k_pages and v_pages must have one page stride")
+    if N <= 1:
+        return dev, shape, dtype, h * P * d
+    if stride[0] < h * P * d:
+        raise ValueError("k_pages's first dimension overlaps")
+    return dev, shape, dtype, stride[0]
 
 
 def _call_on(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current; the stream defaults to its current one."""
     stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return fn(*args, stream)
     with torch.cuda.device(dev):
         return fn(*args, stream)
@@ -708,9 +729,7 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
     place. free_pages: int32 page numbers, of which the first free_head ([1] int32) are taken.
     kv_len may be cached_len and free_head_out may be free_head, which then advance in place.
     """
-    if not isinstance(cached_len, torch.Tensor) or not cached_len.is_cuda:
-        raise TypeError("cached_len must be a CUDA tensor")
-    dev = cached_len.get_device()
+    dev = _device_of("cached_len", cached_len)
     B = cached_len.numel()
     max_tokens = int(max_tokens)
     if kv_len is None or q_start is None or slots is None or free_head_out is None:
@@ -727,23 +746,23 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
         _ints(dev, "free_pages", free_pages, F), F, _ints(dev, "free_head", free_head, 1), max_tokens,
         _ints(dev, "kv_len", kv_len, B), _ints(dev, "q_start", q_start, B + 1),
         _ints(dev, "slots", slots, max_tokens), _ints(dev, "free_head_out", free_head_out, 1))
-    _check(st, "relattn_paged_plan")
+    if st:
+        raise RelattnError(st, "relattn_paged_plan")
     return kv_len, q_start, slots, free_head_out
 
 
 def relattn_paged_append(k, v, slots, k_pages, v_pages, stream=None):
     """Rows k[t], v[t] ([tokens, Hkv, d], bf16 or fp32, any token stride) to slot slots[t] of
     k_pages, v_pages [num_pages, Hkv, page_size, d]; negative slots are skipped. In place."""
-    dev, ps = _pages(k_pages, v_pages)
-    N, Hkv, P, d = k_pages.shape
+    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
     T = slots.numel()
-    shape, dtype = (T, Hkv, d), k_pages.dtype
+    ks, vs = _rows(dev, "k", k, T, Hkv, d, dtype), _rows(dev, "v", v, T, Hkv, d, dtype)
     st = _call_on(
-        dev, stream, _lib.relattn_paged_append, k.data_ptr(), v.data_ptr(),
-        _spaced(dev, "k", k, shape, dtype), _spaced(dev, "v", v, shape, dtype),
+        dev, stream, _lib.relattn_paged_append, k.data_ptr(), v.data_ptr(), ks, vs,
         _ints(dev, "slots", slots, T), T, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, Hkv, P, d,
         _dtype_code(k_pages))
-    _check(st, "relattn_paged_append")
+    if st:
+        raise RelattnError(st, "relattn_paged_append")
 
 
 def relattn_paged_workspace_size(H, Hkv, d) -> int:
@@ -769,43 +788,39 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
     or None to make one. Returns out [tokens, H, d].
     """
-    dev, ps = _pages(k_pages, v_pages)
-    N, Hkv, P, d = k_pages.shape
+    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
     _on(dev, "q", q)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, H, d]")
-    dtype = q.dtype
-    if k_pages.dtype is not dtype or q.shape[2] != d:
-        raise ValueError("k_pages and v_pages must have q's dtype and head dimension")
-    shape = q.shape
-    T, H = shape[0], shape[1]
+    T, H, _ = q.shape
     dt = _dtype_code(q)
-    qs = _spaced(dev, "q", q, shape, dtype)
+    qs = _rows(dev, "q", q, T, H, d, dtype)
     B = kv_len.numel()
     ts, M = _table(dev, block_table, B)
     clip_k = int(clip_k)
-    W = 2 * clip_k + 1
-    ths, pK, pV = 0, None, None
+    ths, pK, pV, heads = 0, None, None, 0
     for name, t in (("aK", aK), ("aV", aV)):
         if t is None:
             continue
         _on(dev, name, t)
+        shape = t.shape
         if t.dtype is not dtype or not t.is_contiguous():
             raise TypeError("%s must be contiguous and of q's dtype" % name)
-        if t.dim() != 3 or t.shape[1] != W or t.shape[2] != d or t.shape[0] not in (1, Hkv):
+        if shape != (1, 2 * clip_k + 1, d) and shape != (Hkv, 2 * clip_k + 1, d):
             raise ValueError("%s must be [Hkv or 1, 2*clip_k+1, d]" % name)
-        ths = 0 if t.shape[0] == 1 else W * d
-        if name == "aK":
+        if heads and shape[0] != heads:
+            raise ValueError("aK and aV must both be per head or both shared")
+        heads = shape[0]
+        ths = 0 if heads == 1 else (2 * clip_k + 1) * d
+        if t is aK:
             pK = t.data_ptr()
-        else:
+        if t is aV:
             pV = t.data_ptr()
-    if pK is not None and pV is not None and aK.shape[0] != aV.shape[0]:
-        raise ValueError("aK and aV must both be per head or both shared")
     if table_head_stride is not None:
         ths = int(table_head_stride)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
-    elif _spaced(dev, "out", out, shape, dtype) != H * d:
+        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+    elif _rows(dev, "out", out, T, H, d, dtype) != H * d:
         raise ValueError("out must be contiguous")
     if scale is None:
         scale = d ** -0.5
@@ -823,7 +838,8 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
         _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, int(window), int(sinks), float(scale), B,
         T, int(max_new), H, Hkv, d, dt, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), out.data_ptr())
-    _check(st, "relattn_paged_fwd")
+    if st:
+        raise RelattnError(st, "relattn_paged_fwd")
     return out
 
 

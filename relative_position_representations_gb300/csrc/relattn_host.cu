@@ -740,6 +740,7 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
     a.out = out;
     a.workspace = workspace;
     a.wait_limit = g_wait_limit.load();
+    a.withhold = g_withhold_q.load();
     const relattn_status_t st = paged_device(&a.err);
     if (st != RELATTN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

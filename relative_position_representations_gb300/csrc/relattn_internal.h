@@ -251,6 +251,7 @@ struct PagedArgs {
     void *workspace;                  // at least paged_workspace_bytes
     int *err;
     long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)
+    int withhold;                     // test hook: announce the first queries, do not load them
 };
 unsigned long long paged_workspace_bytes(int d);
 // every type, head dimension <= 128 and page size; fp32 arithmetic on the SIMT units

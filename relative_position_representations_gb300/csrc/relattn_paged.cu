@@ -84,6 +84,7 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->desc = static_cast<Desc *>(a.workspace);
     p->part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + desc_bytes());
     p->err = a.err;
+    p->withhold = a.withhold;
     p->wait_limit = a.wait_limit > 0 ? a.wait_limit : 2000000000ll;
 }
 

@@ -62,6 +62,7 @@ struct Params {
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
     int *err;
     long long wait_limit;
+    int withhold;                            // test hook: a CTA's first queries are announced, not loaded
 };
 
 inline size_t desc_bytes() { return (size_t)kMaxGrid * sizeof(Desc); }

@@ -146,7 +146,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
             if (more) {
                 ptx::mbar_expect_tx(bar(B_PIECE_FULL + i), (uint32_t)(p.T * p.g) * D * 2);
 #pragma unroll
-                for (int blk = 0; blk < DB; ++blk)
+                for (int blk = 0; blk < DB && !(p.withhold && it == 0); ++blk)
                     ptx::tma_load_3d(base + L.q + (i * DB + blk) * (8 * NT * 128), tm_q, bar(B_PIECE_FULL + i), blk * 64,
                                      g.kvh * p.g, g.s.q0 + g.it.i0);
             } else {

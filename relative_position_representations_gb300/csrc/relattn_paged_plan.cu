@@ -92,11 +92,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         if (b < B) {
             const long long incl = (long long)(v >> kTokenBits);
             const long long tokens = (long long)(v & ((1ull << kTokenBits) - 1));
-            const bool placed = !bad && tokens <= a.max_tokens && (need == 0 || head + incl <= a.num_free);
+            const bool placed = !bad && tokens <= a.max_tokens && (need == 0 || (head >= 0 && head + incl <= a.num_free));
             start[b + 1] = (int)(tokens < 0x7fffffffLL ? tokens : 0x7fffffffLL);
             cached_s[b] = c;
-            page_s[b] = placed ? head + (int)incl - need : -1;
-            if (placed) atomicMax(&taken_s, (int)incl);
+            page_s[b] = placed ? (need ? head + (int)incl - need : 0) : -1;
+            if (placed && need) atomicMax(&taken_s, (int)incl);
             bad_any = bad_any || !placed;
         }
     }

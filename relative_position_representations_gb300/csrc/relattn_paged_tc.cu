@@ -299,7 +299,7 @@ __device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, 
             if (!(ok = wait(empty + 8 * s, (q_it[s] & 1u) ^ 1u))) break;
             ptx::mbar_expect_tx_w(full + 8 * s, (uint32_t)tp.TS * p.g * D * 2);
 #pragma unroll
-            for (int blk = 0; blk < DB; ++blk)
+            for (int blk = 0; blk < DB && !(p.withhold && it == 1); ++blk)
                 ptx::tma_load_3d_w(sh.base + tp.off_q[s] + blk * BM * 128, tm_q, full + 8 * s, blk * 64, g.kvh * p.g,
                                    g.s.q0 + g.it.i0 + s * tp.TS);
             ++q_it[s];

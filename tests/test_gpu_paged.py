@@ -72,6 +72,9 @@ def test_plan_leaves_out_what_does_not_fit():
     run_plan([0, 0], [8, 8], 8, 4, np.zeros(0, dtype=np.int64), 0, 16)
     run_plan([4, 9], [4, 7], 8, 4, np.zeros(0, dtype=np.int64), 0, 16)   # no page needed
     run_plan([2 ** 31 - 1, 0], [5, 5], 8, 4, free, 0, 16)
+    # a free-list head that is no index: nothing is handed out
+    run_plan([4, 8], [4, 7], 8, 4, free, -3, 16)
+    run_plan([4, 8], [4, 7], 8, 4, free, 1000, 16)
     # nothing new at all, and no slots
     run_plan([4, 9, 0], [0, 0, 0], 8, 4, free, 10, 0)
 
@@ -343,6 +346,34 @@ def test_lengths_that_lie_are_kept_in_bounds(dtype):
     x["q_start"] = np.array([0, 4, 2])
     got = call(x, 4).double().cpu().numpy()
     assert np.isnan(got[4:]).all() and np.isfinite(got[:4]).all()
+
+
+@pytest.mark.parametrize("new,kv,H,Hkv,d", [([9, 1, 40], [300, 90, 40], 8, 2, 64), ([20, 3], [900, 3], 4, 4, 128)])
+def test_max_new_is_a_hint_only(new, kv, H, Hkv, d):
+    """Requests with more new tokens than the hint says."""
+    x = make(new, kv, H, Hkv, d, 16, BF16, 8, True, True)
+    for hint in (1, 2, 5, 10 ** 6):
+        check(x, call(x, 8, max_new=hint), 8)
+
+
+@pytest.mark.parametrize("new,kv,H,d", [([1, 1], [700, 90], 4, 64), ([200, 3], [900, 40], 2, 128)])
+def test_a_wait_that_runs_out_is_reported(new, kv, H, d):
+    """The first queries are announced and never loaded, with the bound at 10^6 cycles: the kernels give
+    up in order and say so, and the next call is right."""
+    rp = _rp()
+    x = make(new, kv, H, H, d, 16, BF16, 8, True, True)
+    want = call(x, 8, max_new=max(new))
+    rp.relattn_set_wait_limit(1000000)
+    rp.relattn_debug_withhold_first_load(True)
+    try:
+        call(x, 8, max_new=max(new))
+        torch.cuda.synchronize()
+    finally:
+        rp.relattn_debug_withhold_first_load(False)
+        rp.relattn_set_wait_limit(2000000000)
+    assert rp.relattn_get_device_error() == 4
+    assert torch.equal(call(x, 8, max_new=max(new)), want)
+    assert rp.relattn_get_device_error() == 0
 
 
 # ------------------------------------------------------------------------------------ a server's steps
