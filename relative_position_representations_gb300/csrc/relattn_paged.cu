@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     constexpr int kUnroll = 16 / NV;
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Desc d = p.desc[c];
     if (!d.valid) return;
@@ -173,18 +173,10 @@ cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
     // a warp per row and 32 columns up to 16 rows, else a warp per two rows
     const bool few = p.rec_rows <= 16;
     const int warps = few ? p.likely_rows * ((p.d + 31) / 32) : (p.likely_rows + 1) / 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, (warps + kMergeWarps - 1) / kMergeWarps);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (!bf16) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<float, 4>, p, grid);
-    return few ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, 1>, p, grid)
-               : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, 4>, p, grid);
+    const dim3 g(grid, (warps + kMergeWarps - 1) / kMergeWarps);
+    if (!bf16) return launch_early(paged_merge_kernel<float, 4>, g, kMergeThreads, 0, s, p, grid);
+    return few ? launch_early(paged_merge_kernel<__nv_bfloat16, 1>, g, kMergeThreads, 0, s, p, grid)
+               : launch_early(paged_merge_kernel<__nv_bfloat16, 4>, g, kMergeThreads, 0, s, p, grid);
 }
 
 // ------------------------------------------------------------------ SIMT kernel
@@ -240,7 +232,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
     extern __shared__ __align__(16) float smf[];
     __shared__ Range rg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
+    grid_release();
     if (warp == 0) {
         const Range r = find_range(p);
         if (lane == 0) rg_s = r;
@@ -521,8 +514,7 @@ cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
     cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(paged_simt_kernel<T, N4>), di);
     if (e != cudaSuccess) return e;
     const int grid = 2 * di.sms < kMaxGrid ? 2 * di.sms : kMaxGrid;
-    paged_simt_kernel<T, N4><<<grid, kSimtThreads, smem, s>>>(p, vec);
-    e = cudaGetLastError();
+    e = launch_early(paged_simt_kernel<T, N4>, dim3(grid), kSimtThreads, smem, s, p, vec);
     if (e != cudaSuccess) return e;
     return launch_merge(p, grid, sizeof(T) == 2, s);
 }

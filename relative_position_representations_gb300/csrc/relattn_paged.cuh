@@ -16,6 +16,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -387,6 +388,28 @@ inline int likely_rows(const PagedArgs &a, int T, int g) {
     const int n = a.max_new > 0 && a.max_new < a.tokens ? a.max_new : a.tokens;
     return (n < T ? n : T) * g;
 }
+// A launch that may begin before the kernel in front of it in the stream has ended: every kernel of
+// a paged call runs grid_wait() before it touches what others write or read.
+template <typename... Args>
+cudaError_t launch_early(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         std::common_type_t<Args>... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the dependent kernel's CTAs come up beside this one's. After grid_wait(): what stands in front
+// of this kernel is then over for the dependent too.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Fills the parts of Params that do not depend on the kernel.
 void fill_params(const PagedArgs &a, Params *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent

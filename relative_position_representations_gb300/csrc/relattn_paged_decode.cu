@@ -552,7 +552,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p, int stages, int box) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Layout L = Layout::make<D, NT>(p.clip_k, AK || AV, stages);
     const uint32_t bars = ptx::smem_u32(smem) + L.bar;
     Waits waits{reinterpret_cast<volatile int *>(smem + L.bar + kNumBars * 8), p.err, p.wait_limit};
@@ -568,6 +567,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
         ptx::tma_prefetch_desc(&tm_v);
     }
     __syncthreads();
+    grid_wait();
+    grid_release();
     if (threadIdx.x >= kRowThreads)
         feed_role<D, NT>(p, L, smem, waits, &tm_q, &tm_k, &tm_v, stages, box);
     else
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(32) paged_join_kernel(const __grid_constant__ 
     const int tok = r / p.g, hh = r - tok * p.g;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
                          ((long long)(s.q0 + it.i0 + tok) * p.H + rg.kvh * p.g + hh) * D + V * lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
 #pragma unroll
@@ -665,20 +666,10 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box,
     if (e != cudaSuccess) return e;
     const int want = di.sms * kCtasPerSm<D>;
     const int grid = want < kMaxGrid ? want : kMaxGrid;
-    kern<<<grid, kThreads, smem, s>>>(tm[0], tm[1], tm[2], p, stages, box);
-    const cudaError_t le = cudaGetLastError();
+    const cudaError_t le = launch_early(kern, dim3(grid), kThreads, smem, s, tm[0], tm[1], tm[2], p, stages, box);
     if (le != cudaSuccess) return le;
     if (p.B > kScanOnce) return launch_merge(p, grid, true, s);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, p.T * p.g);
-    cfg.blockDim = dim3(32);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, grid);
+    return launch_early(paged_join_kernel<D>, dim3(grid, p.T * p.g), 32, 0, s, p, grid);
 }
 
 template <int D, int NT>

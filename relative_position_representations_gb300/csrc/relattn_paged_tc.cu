@@ -927,7 +927,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_av, const __grid_constant__ TcParams tp) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const Params &p = tp.p;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Shared sh;
     sh.base = ptx::smem_u32(smem_raw);
     sh.ptr = smem_raw;
@@ -958,6 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Before the warpgroups trade registers (the scan needs more than a control warp keeps), and by
     // every warp alike: the compiler fails to allocate a branch of one warp here.
     Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
+    grid_wait();
+    grid_release();
     {
         const Range r = find_range_t<int>(p, (int)blockIdx.x, (int)gridDim.x);
         if (threadIdx.x == 96) *range = r;
@@ -1056,8 +1057,7 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaS
     }
     const int grid = di.sms < kTcGrid ? di.sms : kTcGrid;
     const uint32_t smem = tp.off_bar + kNumBars * 8 + 16;
-    kern<<<grid, kThreads, smem, s>>>(tm[0], tm[1], tm[2], tm[3], tm[4], tp);
-    e = cudaGetLastError();
+    e = launch_early(kern, dim3(grid), kThreads, smem, s, tm[0], tm[1], tm[2], tm[3], tm[4], tp);
     if (e != cudaSuccess) return e;
     return launch_merge(tp.p, grid, true, s);
 }
