@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
 // pieces' statistics and outputs are joined as in the general merge (relattn_paged.cu), but the warp
 // finds the item by the same scan as the main kernel, before it waits for that kernel's end: as
 // single-warp CTAs these fit beside the main kernel's on every SM and have done their scan, or have
-// left, long before. What remains behind the main kernel are two dependent loads and a store. Up to
+// left, long before (the first one stays in any case: a kernel behind this one may itself have been
+// launched early and waits for this one's end alone, so that end must stand behind the main kernel's).
+// What remains behind the main kernel are two dependent loads and a store. Up to
 // kScanOnce requests, which the scan takes in one pass: at 128 requests a step takes 34.9 us, with the
 // general merge 37.1; at 512 requests of one tile each 47.0 against 37.3 the other way round.
 constexpr int kScanOnce = 128;
@@ -591,6 +593,7 @@ __global__ void __launch_bounds__(32) paged_join_kernel(const __grid_constant__ 
     __shared__ short piece[kMaxGrid];
     const int lane = threadIdx.x, c = blockIdx.x, r = blockIdx.y;
     const Range rg = find_range_t<int>(p, c, G, true);
+    if (c == 0 && r == 0) grid_wait();
     if (rg.x0 >= rg.x1 || rg.b >= p.B) return;
     const Seq s = load_seq(p, rg.b);
     const Item it = make_item(p, s, rg.qt);
@@ -657,10 +660,12 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box,
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
     // as many stages as the CTA's share of the SM's shared memory holds (1 KB per CTA is the
-    // system's), two at least
+    // system's); two, at the cost of the second CTA, where long tables leave fewer; one at d = 128
+    // with 16 rows and clip_k > 131, whose tables leave no room for two at all
     const int share = (di.smem_optin + 1024) / kCtasPerSm<D> - 1024;
+    auto bytes = [&](int n) { return (int)Layout::make<D, NT>(p.clip_k, AK || AV, n).bytes; };
     int stages = kMaxStages;
-    while (stages > 2 && (int)Layout::make<D, NT>(p.clip_k, AK || AV, stages).bytes > share) --stages;
+    while (stages > 1 && bytes(stages) > (stages > 2 ? share : di.smem_optin)) --stages;
     const uint32_t smem = Layout::make<D, NT>(p.clip_k, AK || AV, stages).bytes;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;

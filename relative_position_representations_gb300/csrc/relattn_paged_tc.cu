@@ -1106,7 +1106,8 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
 }  // namespace paged
 
 bool paged_tc_covers(const PagedArgs &a) {
-    return a.clip_k <= 127 && paged::pages_by_tma(a);
+    // (a row's place among an item's outputs is counted in 16-byte units, in 32 bits)
+    return a.clip_k <= 127 && a.H <= 1 << 20 && paged::pages_by_tma(a);
 }
 
 cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s) {
