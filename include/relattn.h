@@ -319,8 +319,8 @@ RELATTN_API relattn_status_t relattn_decode_workspace_size(int B, int H, int T, 
  *   kv_len                [B] int32 (may be cached_len itself), q_start [B + 1] int32.
  *   slots                 [max_tokens] int32, -1 behind the last new token.
  * A request is left out when the free pages do not suffice for it (later ones that need pages
- * are then left out too), when it would not fit its table row or max_tokens, or when a length is
- * negative: its slots are -1, its kv_len is cached_len, its table row stays, and the device
+ * are then left out too), when it would not fit its table row or max_tokens, when its length would
+ * pass 2^31 - 1, or when a length is negative: its slots are -1, its kv_len is cached_len, its table row stays, and the device
  * status word becomes RELATTN_ERR_INVALID_ARG (relattn_get_device_error). A request with a
  * negative new_len, or one above max_tokens, has no rows in q_start and slots either.
  * page_size: a power of two, 1 .. 1024. B <= 16384 and max_tokens <= 2^23, else
@@ -343,7 +343,8 @@ RELATTN_API relattn_status_t relattn_paged_plan(const int *cached_len, const int
  *                     skipped and sets the device status word to RELATTN_ERR_INVALID_ARG. If two
  *                     tokens name one slot, either may be the one that stays.
  *   k_pages, v_pages  [num_pages, Hkv, page_size, d], page_stride elements between pages.
- * Nothing else of the cache is written. num_pages * page_size < 2^31. tokens = 0 does nothing.
+ * Nothing else of the cache is written; k and v must not overlap the rows that are.
+ * num_pages * page_size < 2^31. tokens = 0 does nothing.
  */
 RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, long long k_stride,
                                       long long v_stride, const int *slots, int tokens,
@@ -377,7 +378,8 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  *   kv_len            [B] int32: cached tokens, the new ones among them (taken as at most
  *                     max_pages * page_size). A token at a negative position gets zeros.
  *   aK, aV            [Hkv|1, 2 clip_k + 1, d] of `dtype` or NULL; table_head_stride as in
- *                     relattn_fwd. Only rows 0 .. clip_k (offsets -clip_k .. 0) are read.
+ *                     relattn_fwd. Only rows 0 .. clip_k (offsets -clip_k .. 0) are read; they
+ *                     must be finite.
  *   max_new           the most new tokens of one request, or 0 if not known: it chooses between
  *                     kernels and the results hold for any value.
  *   workspace         caller-owned device scratch of relattn_paged_workspace_size bytes, 16-byte

@@ -17,7 +17,7 @@ def plan(cached, new, table, free, head, P, max_tokens):
     for b, (c, n) in enumerate(zip(cached, new)):
         c, n = int(c), int(n)
         rows = n if 0 <= n <= max_tokens else 0
-        fits = c >= 0 and 0 <= n <= max_tokens and -(-(c + n) // P) <= M
+        fits = c >= 0 and 0 <= n <= max_tokens and -(-(c + n) // P) <= M and c + n < 2 ** 31
         need = -(-(c + n) // P) - -(-c // P) if fits else 0
         want += need
         placed = fits and q_start[-1] + rows <= max_tokens and (need == 0 or (head >= 0 and want <= len(free)))

@@ -15,7 +15,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
-#include "relattn_internal.h"
+#include "relattn_paged.cuh"
 
 namespace relattn {
 namespace {
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
             bad = c < 0 || n < 0 || n > a.max_tokens;
             const long long tot = ((long long)c + n + P - 1) >> sh;
             const int old = (int)(((long long)c + P - 1) >> sh);
-            bad = bad || tot > a.max_pages;
+            bad = bad || tot > a.max_pages || (long long)c + n > 0x7fffffffLL;
             need = bad ? 0 : (int)tot - old;
         }
         n = n < 0 || n > a.max_tokens ? 0 : n;
@@ -217,7 +217,7 @@ template <typename V, int ROWS>
 cudaError_t append_v(const PagedAppendArgs &a, cudaStream_t s) {
     const long long vpr = (long long)a.d * a.elem_bytes / (long long)sizeof(V), vpt = a.Hkv * vpr;
     if (vpt > 0x7fffffffLL) return cudaErrorNotSupported;
-    const long long units = (long long)((a.tokens + ROWS - 1) / ROWS) * vpt;
+    const long long units = ((long long)a.tokens + ROWS - 1) / ROWS * vpt;
     const long long blocks = (units + kAppendThreads - 1) / kAppendThreads;
     if (blocks > 0x7fffffffLL) return cudaErrorNotSupported;
     paged_append_kernel<V, ROWS><<<(unsigned)blocks, kAppendThreads, 0, s>>>(a, (int)vpt, (int)vpr,
@@ -236,19 +236,16 @@ cudaError_t append_rows(const PagedAppendArgs &a, cudaStream_t s) {
 cudaError_t launch_paged_plan(const PagedPlanArgs &a, cudaStream_t s) {
     PlanParams p{a, log2_of(a.page_size)};
     const size_t smem = (size_t)(3 * a.B + 1) * sizeof(int);
-    if (a.max_tokens <= kOneBlockTokens) {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<1>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+    const bool one = a.max_tokens <= kOneBlockTokens;
+    const void *kern = one ? reinterpret_cast<const void *>(paged_plan_kernel<1>)
+                           : reinterpret_cast<const void *>(paged_plan_kernel<kPlanCluster>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = paged::opt_in_smem(kern, paged::device_info());
+        if (e != cudaSuccess) return e;
+    }
+    if (one) {
         paged_plan_kernel<1><<<1, kPlanThreads, smem, s>>>(p);
         return cudaGetLastError();
-    }
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<kPlanCluster>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(kPlanCluster);

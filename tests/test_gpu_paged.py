@@ -484,3 +484,77 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(z, want[i]) for z in got[i])
+
+
+# ------------------------------------------------------------------------------------ calls in a row
+@pytest.mark.parametrize("B,Hkv,d", [(19, 8, 128), (38, 8, 64), (2, 3, 64)])
+def test_a_chain_of_calls_reads_finished_outputs(B, Hkv, d):
+    # the first two give every block whole requests (152 or 304 equal shares): no pieces to join
+    # between one call's attention and the next one's
+    rp = _rp()
+    x = make([1] * B, [3000] * B, Hkv, Hkv, d, 16, BF16, stale=False)
+    g = lambda t: t.to(DEV)
+    kp, vp, bt = g(x["k_pages"]), g(x["v_pages"]), i32(x["table"])
+    qs, ln = i32(x["q_start"]), i32(x["kv_len"])
+    ws = torch.empty(rp.relattn_paged_workspace_size(Hkv, Hkv, d), dtype=torch.uint8, device=DEV)
+
+    def chain(sync):
+        z = [g(x["q"])] + [torch.full((B, Hkv, d), float("nan"), dtype=BF16, device=DEV) for _ in range(12)]
+        torch.cuda.synchronize()
+        for i in range(12):
+            rp.relattn_paged_fwd(z[i], kp, vp, bt, qs, ln, scale=4.0, max_new=1, out=z[i + 1], workspace=ws)
+            if sync:
+                torch.cuda.synchronize()
+        z.append(z[-1] + 0)   # a kernel that is not one of these
+        torch.cuda.synchronize()
+        return z
+
+    want = chain(True)
+    assert all(bool(torch.isfinite(t).all()) for t in want)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
+@pytest.mark.parametrize("new,H,Hkv,d,k", [([1, 1], 16, 1, 128, 256), ([1, 1], 12, 1, 128, 140), ([9, 2], 1, 1, 128, 200),
+                                           ([1, 1], 16, 1, 64, 256), ([1, 3], 4, 2, 128, 256)])
+def test_generated_tokens_with_long_tables(new, H, Hkv, d, k):
+    x = make(new, [700, 300], H, Hkv, d, 16, BF16, k, True, True, seed=k + d)
+    got = call(x, k, max_new=max(new))
+    assert _rp().relattn_get_device_error() == 0
+    check(x, got, k)
+
+
+def test_plan_refuses_a_length_past_31_bits():
+    M = 2 ** 21 + 2
+    free = np.arange(8)
+    run_plan([2 ** 31 - 3], [5], 1024, M, free, 0, 8)
+    run_plan([2 ** 31 - 3], [2], 1024, M, free, 0, 8, table=np.full((1, M), 7))
+
+
+def test_plans_of_two_sizes_at_once():
+    # both need more shared memory than a kernel has by default, and not the same amount
+    import threading
+    rp = _rp()
+    fails = []
+
+    def work(B, max_tokens):
+        try:
+            c, n = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+            bt = torch.zeros((B, 1), dtype=torch.int32, device=DEV)
+            free, head = torch.arange(B, dtype=torch.int32, device=DEV), i32([0])
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            for _ in range(200):
+                rp.relattn_paged_plan(c, n, bt, free, head, 8, max_tokens, stream=s)
+            s.synchronize()
+            assert torch.equal(bt[:, 0], free)
+        except Exception as e:   # noqa: BLE001
+            fails.append(e)
+
+    for tokens in (8000, 16384):
+        ts = [threading.Thread(target=work, args=(b, tokens)) for b in (4100 if tokens < 8192 else 16384, 7990)]
+        for t in ts:
+            t.start()
+        for t in ts:
+            t.join()
+    assert not fails and rp.relattn_get_device_error() == 0
