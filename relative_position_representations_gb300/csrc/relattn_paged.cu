@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
     grid_wait();
+    grid_release();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Desc d = p.desc[c];
     if (!d.valid) return;

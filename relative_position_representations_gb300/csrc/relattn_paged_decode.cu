@@ -593,7 +593,10 @@ __global__ void __launch_bounds__(32) paged_join_kernel(const __grid_constant__ 
     __shared__ short piece[kMaxGrid];
     const int lane = threadIdx.x, c = blockIdx.x, r = blockIdx.y;
     const Range rg = find_range_t<int>(p, c, G, true);
-    if (c == 0 && r == 0) grid_wait();
+    if (c == 0 && r == 0) {
+        grid_wait();
+        grid_release();
+    }
     if (rg.x0 >= rg.x1 || rg.b >= p.B) return;
     const Seq s = load_seq(p, rg.b);
     const Item it = make_item(p, s, rg.qt);
@@ -618,6 +621,7 @@ __global__ void __launch_bounds__(32) paged_join_kernel(const __grid_constant__ 
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
                          ((long long)(s.q0 + it.i0 + tok) * p.H + rg.kvh * p.g + hh) * D + V * lane;
     grid_wait();
+    grid_release();
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
 #pragma unroll
