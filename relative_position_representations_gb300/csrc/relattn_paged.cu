@@ -90,94 +90,122 @@ void fill_params(const PagedArgs &a, Params *p) {
 
 // ------------------------------------------------------------------ merge
 // CTA (c, y): the item that goes on behind CTA c's range. A row's pieces have maxima m_i, sums l_i
-// and unnormalised outputs O_i: M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i. One warp
-// takes a row and NV groups of 32 columns: the statistics with one piece per lane, then the
-// outputs with kUnroll pieces' loads in flight (a row is a chain of dependent loads, so the work is
-// spread over many warps: for the few rows of generated tokens, NV = 1, else whole rows).
+// and unnormalised outputs O_i: M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, taken
+// kUnroll pieces at a time under a running maximum, in the order of the keys. A thread holds V
+// columns of a row and reads the row's statistics itself, so that all the loads of a row, mostly two
+// pieces, are one latency; the records come out of the L2 that they have just gone to.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeWarps = kMergeThreads / 32;
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p, int G) {
-    constexpr int kUnroll = 16 / NV;
+// lanes: threads of a row, as a power of two
+template <typename T, int V, int kUnroll>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
     grid_wait();
     grid_release();
-    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const Desc d = p.desc[c];
     if (!d.valid) return;
-    const int D = p.d, groups = NV == 1 ? (D + 31) / 32 : 1, units = d.cnt * p.g * groups;
-    if ((int)blockIdx.y * kMergeWarps >= units) return;
-    auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.wt, d.nt); };
-    // the CTAs that hold a piece, in order (the first warp lists them)
-    if (warp == 0) {
-        int n = 0;
-        for (int e0 = c; e0 < G; e0 += 32) {
-            const int e = e0 + lane;
-            int t0 = d.nt, t1 = d.nt;
-            if (e < G) {
-                const long long x0 = range_begin(d.total, e, G) - d.x, x1 = range_begin(d.total, e + 1, G) - d.x;
-                t0 = e == c ? 0 : tile_at(x0);
-                t1 = tile_at(x1);
+    const int D = p.d, rows = d.cnt * p.g, per = kMergeThreads >> lanes;   // rows of a CTA at a time
+    const int r_first = (int)blockIdx.y * per;
+    if (r_first >= rows) return;
+    int n = d.n;
+    if (n == 0) {   // short ranges: the first warp lists the CTAs that hold a piece, in order
+        if (tid < 32) {
+            auto tile_at = [&](long long y) -> int { return tiles_before(y, d.c0, d.wt, d.nt); };
+            for (int e0 = c; e0 < G; e0 += 32) {
+                const int e = e0 + lane;
+                int t0 = d.nt, t1 = d.nt;
+                if (e < G) {
+                    const long long x0 = range_begin(d.total, e, G) - d.x, x1 = range_begin(d.total, e + 1, G) - d.x;
+                    t0 = e == c ? 0 : tile_at(x0);
+                    t1 = tile_at(x1);
+                }
+                const unsigned has = __ballot_sync(0xffffffffu, t1 > t0);
+                if (t1 > t0) piece[n + __popc(has & ((1u << lane) - 1))] = (short)e;
+                n += __popc(has);
+                if (__any_sync(0xffffffffu, e >= G || t0 >= d.nt)) break;
             }
-            const unsigned has = __ballot_sync(0xffffffffu, t1 > t0);
-            if (t1 > t0) piece[n + __popc(has & ((1u << lane) - 1))] = (short)e;
-            n += __popc(has);
-            if (__any_sync(0xffffffffu, e >= G || t0 >= d.nt)) break;
+            if (lane == 0) n_s = n;
         }
-        if (lane == 0) n_s = n;
+        __syncthreads();
+        n = n_s;
     }
-    __syncthreads();
-    const int n = n_s;
-    auto rec = [&](int i) -> const float * {
-        return record(p, piece[i], piece[i] == c ? 1 : 0);
-    };
-    for (int u0 = blockIdx.y * kMergeWarps + warp; u0 < units; u0 += (int)gridDim.y * kMergeWarps) {
-        const int r = u0 / groups, col = (u0 - r * groups) * 32 + lane;
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float mu = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-        for (int i = lane; i < n; i += 32) l += rec(i)[p.rec_rows + r] * exp2f(rec(i)[r] - mu);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float acc[NV] = {};
-        for (int i0 = 0; i0 < n; i0 += kUnroll) {
-            float w[kUnroll], x[kUnroll][NV];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const bool on = i0 + u < n;
-                const float *q = rec(on ? i0 + u : i0);
-                w[u] = on ? exp2f(q[r] - mu) : 0.f;
-                const float *o = q + 2 * p.rec_rows + (long long)r * D;
-#pragma unroll
-                for (int e = 0; e < NV; ++e) x[u][e] = col + 32 * e < D ? o[col + 32 * e] : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                for (int e = 0; e < NV; ++e) acc[e] = fmaf(w[u], x[u][e], acc[e]);
-        }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+    for (int r = r_first + (tid >> lanes); r < rows; r += (int)gridDim.y * per) {
         const int tok = r / p.g, hh = r - tok * p.g;
-        T *o = static_cast<T *>(p.out) + ((long long)(d.row0 + tok) * p.H + d.kvh * p.g + hh) * D;
+        T *out = static_cast<T *>(p.out) + ((long long)(d.row0 + tok) * p.H + d.kvh * p.g + hh) * D;
+        for (int col = (tid & ((1 << lanes) - 1)) * V; col < D; col += V << lanes) {
+            float m = -INFINITY, l = 0.f, acc[V] = {};
+            for (int i0 = 0; i0 < n; i0 += kUnroll) {
+                float mi[kUnroll], li[kUnroll], x[kUnroll][V];
 #pragma unroll
-        for (int e = 0; e < NV; ++e)
-            if (col + 32 * e < D) o[col + 32 * e] = from_f<T>(acc[e] * inv);
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int i = i0 + u;
+                    mi[u] = -INFINITY;
+                    li[u] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[u][e] = 0.f;
+                    if (i < n) {
+                        const int e = d.n ? c + i : piece[i];
+                        const float *q = record(p, e, e == c ? 1 : 0);
+                        mi[u] = q[r];
+                        li[u] = q[p.rec_rows + r];
+                        const float *o = q + 2 * p.rec_rows + (long long)r * D + col;
+                        if (V == 4) {
+                            const float4 t = *reinterpret_cast<const float4 *>(o);
+                            x[u][0] = t.x; x[u][V / 4] = t.y; x[u][V / 2] = t.z; x[u][V - 1] = t.w;
+                        } else {
+                            x[u][0] = o[0];
+                        }
+                    }
+                }
+                float mn = m;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) mn = fmaxf(mn, mi[u]);
+                const float mu = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m - mu);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] *= f;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const float w = exp2f(mi[u] - mu);
+                    l = fmaf(w, li[u], l);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, x[u][e], acc[e]);
+                }
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (V == 4 && sizeof(T) == 4) {
+                *reinterpret_cast<float4 *>(out + col) =
+                    make_float4(acc[0] * inv, acc[V / 4] * inv, acc[V / 2] * inv, acc[V - 1] * inv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) out[col + e] = from_f<T>(acc[e] * inv);
+            }
+        }
     }
 }
 
+template <typename T>
+cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
+    // four columns a thread where the output's rows are as wide (records always are)
+    const bool four = p.d % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0;
+    const int want = four ? p.d / 4 : p.d;
+    int lanes = 0;
+    while (lanes < 5 && (1 << lanes) < want) ++lanes;
+    const int per = kMergeThreads >> lanes;
+    const dim3 g(grid, (p.likely_rows + per - 1) / per);
+    // records of few rows come from generated tokens, whose keys may lie in many pieces
+    if (four && p.rec_rows <= 16)
+        return launch_early(paged_merge_kernel<T, 4, 8>, g, kMergeThreads, 0, s, p, grid, lanes);
+    return four ? launch_early(paged_merge_kernel<T, 4, 4>, g, kMergeThreads, 0, s, p, grid, lanes)
+                : launch_early(paged_merge_kernel<T, 1, 4>, g, kMergeThreads, 0, s, p, grid, lanes);
+}
+
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
-    // a warp per row and 32 columns up to 16 rows, else a warp per two rows
-    const bool few = p.rec_rows <= 16;
-    const int warps = few ? p.likely_rows * ((p.d + 31) / 32) : (p.likely_rows + 1) / 2;
-    const dim3 g(grid, (warps + kMergeWarps - 1) / kMergeWarps);
-    if (!bf16) return launch_early(paged_merge_kernel<float, 4>, g, kMergeThreads, 0, s, p, grid);
-    return few ? launch_early(paged_merge_kernel<__nv_bfloat16, 1>, g, kMergeThreads, 0, s, p, grid)
-               : launch_early(paged_merge_kernel<__nv_bfloat16, 4>, g, kMergeThreads, 0, s, p, grid);
+    return bf16 ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
 }
 
 // ------------------------------------------------------------------ SIMT kernel

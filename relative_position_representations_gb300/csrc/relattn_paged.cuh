@@ -37,7 +37,7 @@ struct Desc {
     int row0, cnt;     // first query token and tokens of the item
     int kvh, nt;       // key/value head, tiles of the item
     int c0, wt;        // the item's cost: c0 + wt * nt
-    int pad;
+    int n;             // pieces, in the CTAs c .. c + n - 1; 0: some of the CTAs from c on may have none
     long long x;       // position of the item's start in the cost line
     long long total;   // length of the cost line
     long long pad2[2];
@@ -337,7 +337,7 @@ __device__ __forceinline__ Piece make_piece(const Segment &g, bool more) {
 __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, long long total) {
     Desc d;
     d.valid = 0;
-    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.wt = d.pad = 0;
+    d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.wt = d.n = 0;
     d.x = d.total = d.pad2[0] = d.pad2[1] = 0;
     if (g && g->t0 == 0 && g->t1 > 0 && g->t1 < g->it.nt) {
         d.valid = 1;
@@ -349,6 +349,13 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
         d.wt = g->it.wt;
         d.x = g->x;
         d.total = total;
+        // A tile belongs to the range that holds its first position. Ranges as long as a tile hold
+        // one each, up to the range of the last tile; position y lies in range ((y + 1) G - 1) / total.
+        const int G = (int)gridDim.x;
+        if (total / G >= g->it.wt) {
+            const long long y = g->x + p.c0 + (long long)g->it.wt * (g->it.nt - 1);
+            d.n = (int)(((y + 1) * G - 1) / total) - (int)blockIdx.x + 1;
+        }
     }
     p.desc[blockIdx.x] = d;
 }
