@@ -98,7 +98,7 @@ constexpr int kMergeThreads = 256;
 
 // lanes: threads of a row, as a power of two
 template <typename T, int V, int kUnroll>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
+__global__ void __launch_bounds__(kMergeThreads, kUnroll == 3 ? 5 : 3) paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
     grid_wait();
@@ -200,7 +200,7 @@ cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
     // records of few rows come from generated tokens, whose keys may lie in many pieces
     if (four && p.rec_rows <= 16)
         return launch_early(paged_merge_kernel<T, 4, 8>, g, kMergeThreads, 0, s, p, grid, lanes);
-    return four ? launch_early(paged_merge_kernel<T, 4, 4>, g, kMergeThreads, 0, s, p, grid, lanes)
+    return four ? launch_early(paged_merge_kernel<T, 4, 3>, g, kMergeThreads, 0, s, p, grid, lanes)
                 : launch_early(paged_merge_kernel<T, 1, 4>, g, kMergeThreads, 0, s, p, grid, lanes);
 }
 

@@ -148,9 +148,8 @@ struct Range {
 // items of a request with many of them together. I: a type that holds the whole line (32 bits where
 // the host has seen that they do: this code runs once, cold, in front of everything else, so every
 // instruction of it counts).
-template <typename I>
+template <typename I, int kBatch = 4>
 __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G, bool last = false) {
-    constexpr int kBatch = 4;
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     auto scan = [&](I v) {
@@ -199,7 +198,10 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G, boo
     I cost[kBatch], total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32 * kBatch) {
         costs(b0, cost);
-        total += sum(cost[0] + cost[1] + cost[2] + cost[3]) * p.Hkv;
+        I all = cost[0];
+#pragma unroll
+        for (int i = 1; i < kBatch; ++i) all += cost[i];
+        total += sum(all) * p.Hkv;
     }
     Range r;
     r.total = total;

@@ -960,7 +960,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();
     grid_release();
     {
-        const Range r = find_range_t<int>(p, (int)blockIdx.x, (int)gridDim.x);
+        // (32 requests at a time: a step with more than a few chunks is long; a quarter of the cold code)
+        const Range r = find_range_t<int, 1>(p, (int)blockIdx.x, (int)gridDim.x);
         if (threadIdx.x == 96) *range = r;
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -1081,10 +1082,12 @@ cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     if (!wide && !layout<D>(&tp, false, di.smem_optin, 2)) return cudaErrorNotSupported;
     p.T = wide ? 2 * tp.TS : tp.TS;
     p.T1 = tp.TS;
-    // measured at d = 128: 1.6 us a tile of one slot's rows, 2.35 us a tile of both, 4.5 us a piece
-    p.c0 = 5;
-    p.wt = 2;
-    p.wt2 = 3;
+    // Measured (prompts, mixed steps, windows): a tile of both slots counts 4, one of a slot's rows
+    // alone 3, an item 10. With 5 : 6 : 16 a mixed step takes 117 us in place of 114, with 1 : 1 : 3 122;
+    // with 3 : 4 : 8 four prompts 298 us in place of 295.
+    p.c0 = 10;
+    p.wt = 3;
+    p.wt2 = 4;
     p.rec_rows = 2 * BM;
     if (line_is_long(p)) return cudaErrorNotSupported;
     p.likely_rows = likely_rows(a, p.T, p.g);
