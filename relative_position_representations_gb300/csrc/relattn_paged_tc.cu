@@ -494,6 +494,9 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
 }
 
 // ======================================================================= softmax / epilogue
+// the bits below n of 32
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 template <int D, bool AK, bool AV>
 __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
     using T = Tm<D>;
@@ -684,7 +687,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                     if (AK && band) {
 #pragma unroll
                         for (int e = 0; e < KB; e += 2) {
-                            const float2 r = make_float2(Rrow[min(k, max(0, rb + e))], Rrow[min(k, max(0, rb + e + 1))]);
+                            const float2 r = make_float2(Rrow[__viaddmin_s32_relu(rb, e, k)], Rrow[__viaddmin_s32_relu(rb, e + 1, k)]);
                             put(xc, e, __ffma2_rn(pair(xc, e), dup(sl2), r));
                         }
                     } else {
@@ -692,16 +695,16 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         for (int e = 0; e < KB; e += 2) put(xc, e, __ffma2_rn(pair(xc, e), dup(sl2), dup(c_left)));
                     }
                     if (!full(e0, KB)) {
-                        const int hi = pos - e0;                                         // seen: e <= hi and
-                        const int lo = p.window > 0 ? pos - p.window - e0 : -1 - e0;     // (e > lo or
-                        const int sk = p.sinks - e0;                                     // e < sk)
+                        // the keys seen as bits: up to the row's position, and inside the window or first
+                        uint32_t seen = below(pos - e0 + 1);
+                        if (p.window > 0) seen &= ~below(pos - p.window - e0 + 1) | below(p.sinks - e0);
 #pragma unroll
-                        for (int e = 0; e < KB; ++e) xc[e] = e <= hi && (e > lo || e < sk) ? xc[e] : -INFINITY;
+                        for (int e = 0; e < KB; ++e) xc[e] = seen & (1u << e) ? xc[e] : -INFINITY;
                     }
                     if (AV && band) {   // the score takes the place of the table row it used
 #pragma unroll
                         for (int e = 0; e < KB; ++e)
-                            if (rb + e > 0 && rb + e <= k) Rrow[rb + e] = xc[e];
+                            if ((unsigned)(rb + e - 1) < (unsigned)k) Rrow[rb + e] = xc[e];
                     }
                     rmax = fmaxf(rmax, max32(xc));
                     __syncwarp();
