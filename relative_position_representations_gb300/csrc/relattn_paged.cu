@@ -93,12 +93,17 @@ void fill_params(const PagedArgs &a, Params *p) {
 // and unnormalised outputs O_i: M = max m_i, z = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, taken
 // kUnroll pieces at a time under a running maximum, in the order of the keys. A thread holds V
 // columns of a row and reads the row's statistics itself, so that all the loads of a row, mostly two
-// pieces, are one latency; the records come out of the L2 that they have just gone to.
+// pieces, are one latency; the records come out of the L2 that they have just gone to. Bound by that
+// latency and the threads that an SM holds. 40 MB of records of four prompts (d = 128): 9 us with 8
+// columns and 2 pieces a thread, 12.5 with 4 columns and 3 pieces, 23 with a warp per row that first
+// joined the statistics. Few rows come from generated tokens, whose keys may lie in many pieces: 4
+// columns and 8 pieces there.
 constexpr int kMergeThreads = 256;
 
 // lanes: threads of a row, as a power of two
 template <typename T, int V, int kUnroll>
-__global__ void __launch_bounds__(kMergeThreads, kUnroll == 3 ? 5 : 3) paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
+__global__ void __launch_bounds__(kMergeThreads, V == 8 ? 4 : 3)
+    paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
     grid_wait();
@@ -151,11 +156,12 @@ __global__ void __launch_bounds__(kMergeThreads, kUnroll == 3 ? 5 : 3) paged_mer
                         mi[u] = q[r];
                         li[u] = q[p.rec_rows + r];
                         const float *o = q + 2 * p.rec_rows + (long long)r * D + col;
-                        if (V == 4) {
-                            const float4 t = *reinterpret_cast<const float4 *>(o);
-                            x[u][0] = t.x; x[u][V / 4] = t.y; x[u][V / 2] = t.z; x[u][V - 1] = t.w;
-                        } else {
+                        if (V == 1) {
                             x[u][0] = o[0];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e + 3 < V; e += 4)
+                                *reinterpret_cast<float4 *>(&x[u][e]) = *reinterpret_cast<const float4 *>(o + e);
                         }
                     }
                 }
@@ -177,30 +183,29 @@ __global__ void __launch_bounds__(kMergeThreads, kUnroll == 3 ? 5 : 3) paged_mer
                 }
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (V == 4 && sizeof(T) == 4) {
-                *reinterpret_cast<float4 *>(out + col) =
-                    make_float4(acc[0] * inv, acc[V / 4] * inv, acc[V / 2] * inv, acc[V - 1] * inv);
-            } else {
+            alignas(16) T z[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) out[col + e] = from_f<T>(acc[e] * inv);
-            }
+            for (int e = 0; e < V; ++e) z[e] = from_f<T>(acc[e] * inv);
+            using W = std::conditional_t<V * sizeof(T) >= 16, uint4, std::conditional_t<V * sizeof(T) == 8, uint2, T>>;
+#pragma unroll
+            for (int e = 0; e < V * (int)sizeof(T) / (int)sizeof(W); ++e)
+                reinterpret_cast<W *>(out + col)[e] = reinterpret_cast<const W *>(z)[e];
         }
     }
 }
 
 template <typename T>
 cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
-    // four columns a thread where the output's rows are as wide (records always are)
+    // eight or four columns a thread where rows are as wide (those of the records are, at 16 bytes)
     const bool four = p.d % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0;
-    const int want = four ? p.d / 4 : p.d;
+    const bool eight = p.d % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.rec_rows > 16;
+    const int want = eight ? p.d / 8 : four ? p.d / 4 : p.d;
     int lanes = 0;
     while (lanes < 5 && (1 << lanes) < want) ++lanes;
     const int per = kMergeThreads >> lanes;
     const dim3 g(grid, (p.likely_rows + per - 1) / per);
-    // records of few rows come from generated tokens, whose keys may lie in many pieces
-    if (four && p.rec_rows <= 16)
-        return launch_early(paged_merge_kernel<T, 4, 8>, g, kMergeThreads, 0, s, p, grid, lanes);
-    return four ? launch_early(paged_merge_kernel<T, 4, 3>, g, kMergeThreads, 0, s, p, grid, lanes)
+    if (eight) return launch_early(paged_merge_kernel<T, 8, 2>, g, kMergeThreads, 0, s, p, grid, lanes);
+    return four ? launch_early(paged_merge_kernel<T, 4, 8>, g, kMergeThreads, 0, s, p, grid, lanes)
                 : launch_early(paged_merge_kernel<T, 1, 4>, g, kMergeThreads, 0, s, p, grid, lanes);
 }
 
