@@ -138,18 +138,17 @@ __device__ __forceinline__ long long range_begin(long long total, int c, int G) 
 // ------------------------------------------------------------------ a CTA's range
 struct Range {
     long long total, x0, x1;   // the cost line and this CTA's part of it
-    int b, kvh, qt;            // the item that holds x0 (or x1 - 1)
+    int b, kvh, qt;            // the item that holds x0
     long long x;               // where that item starts
 };
 
 // One warp calls it; every lane returns the range of CTA c of G and the item that holds its first
-// position (or, with `last`, its last one). The lanes take the requests in turn, kBatch
-// of each lane's loaded at once (their latency is most of what a small step costs), and add up the
-// items of a request with many of them together. I: a type that holds the whole line (32 bits where
+// position. The lanes take the requests in turn, kBatch of each lane's loaded at once (their latency
+// is most of what a small step costs), and add up the items of a request with many of them together. I: a type that holds the whole line (32 bits where
 // the host has seen that they do: this code runs once, cold, in front of everything else, so every
 // instruction of it counts).
 template <typename I, int kBatch = 4>
-__device__ __forceinline__ Range find_range_t(const Params &p, int c, int G, bool last = false) {
+__device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     auto scan = [&](I v) {
@@ -210,7 +209,7 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G, boo
     r.b = p.B;   // an empty range at the end finds no request
     r.kvh = r.qt = 0;
     r.x = r.x1;
-    const I x0 = (I)(last ? r.x1 - 1 : r.x0);
+    const I x0 = (I)r.x0;
     I at = 0, per = 0, x = 0;
     for (int b0 = 0; b0 < p.B && r.b == p.B && r.x0 < r.x1; b0 += 32 * kBatch) {
         if (p.B > 32 * kBatch) costs(b0, cost);

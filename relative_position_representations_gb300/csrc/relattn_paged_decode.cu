@@ -575,89 +575,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
         row_role<D, NT, AK, AV>(p, L, smem, waits, stages);
 }
 
-// ======================================================================= the join of split items
-// One warp per (CTA c, query row): the item that begins in c's range and goes on behind it. Its
-// pieces' statistics and outputs are joined as in the general merge (relattn_paged.cu), but the warp
-// finds the item by the same scan as the main kernel, before it waits for that kernel's end: as
-// single-warp CTAs these fit beside the main kernel's on every SM and have done their scan, or have
-// left, long before (the first one stays in any case: a kernel behind this one may itself have been
-// launched early and waits for this one's end alone, so that end must stand behind the main kernel's).
-// What remains behind the main kernel are two dependent loads and a store. Up to
-// kScanOnce requests, which the scan takes in one pass: at 128 requests a step takes 34.9 us, with the
-// general merge 37.1; at 512 requests of one tile each 47.0 against 37.3 the other way round.
-constexpr int kScanOnce = 128;
-template <int D>
-__global__ void __launch_bounds__(32) paged_join_kernel(const __grid_constant__ Params p, int G) {
-    constexpr int V = D / 32;   // columns of a lane
-    constexpr int kUnroll = 8;
-    __shared__ short piece[kMaxGrid];
-    const int lane = threadIdx.x, c = blockIdx.x, r = blockIdx.y;
-    const Range rg = find_range_t<int>(p, c, G, true);
-    if (c == 0 && r == 0) {
-        grid_wait();
-        grid_release();
-    }
-    if (rg.x0 >= rg.x1 || rg.b >= p.B) return;
-    const Seq s = load_seq(p, rg.b);
-    const Item it = make_item(p, s, rg.qt);
-    if (r >= it.cnt * p.g) return;
-    const int x = (int)rg.x;
-    auto first_tile = [&](int e) { return e == c && rg.x >= rg.x0 ? 0 : it.tile_at(p, max(0, range_begin((int)rg.total, e, G) - x)); };
-    auto end_tile = [&](int e) { return it.tile_at(p, range_begin((int)rg.total, e + 1, G) - x); };
-    const int end0 = end_tile(c);
-    if (first_tile(c) != 0 || end0 == 0 || end0 >= it.nt) return;   // not begun here, or all here
-    int n = 0;
-    for (int e0 = c; e0 < G; e0 += 32) {
-        const int e = e0 + lane;
-        const int t0 = e < G ? first_tile(e) : it.nt, t1 = e < G ? end_tile(e) : it.nt;
-        const unsigned has = __ballot_sync(0xffffffffu, t1 > t0);
-        if (t1 > t0) piece[n + __popc(has & ((1u << lane) - 1))] = (short)e;
-        n += __popc(has);
-        if (__any_sync(0xffffffffu, e >= G || t0 >= it.nt)) break;
-    }
-    __syncwarp();
-    auto rec = [&](int i) -> const float * { return record(p, piece[i], piece[i] == c ? 1 : 0); };
-    const int tok = r / p.g, hh = r - tok * p.g;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
-                         ((long long)(s.q0 + it.i0 + tok) * p.H + rg.kvh * p.g + hh) * D + V * lane;
-    grid_wait();
-    grid_release();
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, rec(i)[r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[V] = {};
-    for (int i0 = 0; i0 < n; i0 += kUnroll) {
-        float w[kUnroll], lw[kUnroll], v[kUnroll][V];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const float *q = rec(min(i0 + u, n - 1));
-            w[u] = q[r];
-            lw[u] = q[p.rec_rows + r];
-            const float *o = q + 2 * p.rec_rows + r * D + V * lane;
-            if (V == 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(o);
-                v[u][0] = t.x; v[u][1] = t.y; v[u][V - 2] = t.z; v[u][V - 1] = t.w;
-            } else {
-                const float2 t = *reinterpret_cast<const float2 *>(o);
-                v[u][0] = t.x; v[u][1] = t.y;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const float f = i0 + u < n ? ptx::ex2(w[u] - mu) : 0.f;
-            l = fmaf(f, lw[u], l);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[u][e], acc[e]);
-        }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<uint32_t *>(out + e) = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-}
-
 template <int D, int NT, bool AK, bool AV>
 cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box, cudaStream_t s) {
     auto kern = paged_decode_kernel<D, NT, AK, AV>;
@@ -677,8 +594,7 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box,
     const int grid = want < kMaxGrid ? want : kMaxGrid;
     const cudaError_t le = launch_early(kern, dim3(grid), kThreads, smem, s, tm[0], tm[1], tm[2], p, stages, box);
     if (le != cudaSuccess) return le;
-    if (p.B > kScanOnce) return launch_merge(p, grid, true, s);
-    return launch_early(paged_join_kernel<D>, dim3(grid, p.T * p.g), 32, 0, s, p, grid);
+    return launch_merge(p, grid, true, s);
 }
 
 template <int D, int NT>
