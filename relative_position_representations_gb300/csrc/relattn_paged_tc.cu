@@ -18,9 +18,20 @@
 // no such care, scores of unseen keys are replaced, not added to.
 // Work is split over the CTAs by keys (relattn_paged.cuh).
 //
+// What bounds it. d = 128: the chain of a slot, S, softmax (1750 cycles), P V and the next S over P's
+// columns (1700 with the hand-offs), 3450 cycles per tile of both slots where the tensor cores work
+// 2048; TMEM is full, so no second S can wait. d = 64 (P beside S): the issue of the softmax, two
+// warps to a scheduler, 2550 cycles a tile. A piece costs 8 to 10 thousand cycles beside its tiles
+// (R, masks and band, write-out). Four prompts of 4096 tokens, 16 heads of 128, key term: 290 us, 961
+// TFLOP/s; a mixed step (20 generated tokens, 4 chunks of about 500, up to 8K keys): 111 us, 682;
+// chunks of 2048 under a window of 4096, d = 64, both terms: 115 us, 602. Dropped: scores in halves
+// of 64 keys with two buffers (mixed step 132 -> 137 us, prompts 318 -> 439: N = 64 products read A
+// twice as often, and every half pays the hand-offs), part of the exponentials as a polynomial (318
+// -> 343 us: the issue slots are scarcer than the unit, which does a warp's in 4 cycles).
+//
 // Roles (384 threads, one CTA per SM): warp 3 walks the CTA's range, announces the pieces and loads
-// their query tiles, warp 0 feeds the ring (aK, K and V tiles, aV, in the order of use), warps 1 and 2 issue the MMAs of slot 0 and 1, warps 4-7 and
-// 8-11 run the rows of slot 0 and 1, one thread per row. TMEM as in relattn_tc_kernel.cuh: S of
+// their query tiles, warp 0 feeds the ring (aK, K and V tiles, aV, in the order of use), warps 1 and
+// 2 issue the MMAs of slot 0 and 1, warps 4-7 and 8-11 run the rows of slot 0 and 1, one thread per row. TMEM as in relattn_tc_kernel.cuh: S of
 // slot s at 128 s, O at 256 + d s, P (bf16) at 384 + 64 s (d = 64) or over the lower half of S
 // (d = 128), beta over the upper half of S.
 // The band of the last k keys needs no accumulation: each of its table rows meets one key per

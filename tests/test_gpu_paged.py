@@ -558,3 +558,22 @@ def test_plans_of_two_sizes_at_once():
         for t in ts:
             t.join()
     assert not fails and rp.relattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,off", [(36, 0), (12, 0), (64, 1), (128, 4), (40, 2)])
+def test_joined_outputs_of_any_width_and_place(d, off, dtype):
+    # long keys of few tokens, so that every item comes in pieces; outputs that start off the boundary
+    # of the join's widest stores
+    rp = _rp()
+    new, kv, H, Hkv = [9, 1, 1], [2600, 700, 1], 4, 2
+    x = make(new, kv, H, Hkv, d, 16, dtype, 5, True, True, seed=d)
+    g = lambda t: t.to(DEV)
+    T = sum(new)
+    buf = torch.full((T * H * d + 2 * off,), float("nan"), dtype=dtype, device=DEV)
+    out = buf[off:off + T * H * d].view(T, H, d)
+    rp.relattn_paged_fwd(g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), i32(x["table"]), i32(x["q_start"]),
+                         i32(x["kv_len"]), aK=g(x["aK"]), aV=g(x["aV"]), clip_k=5, out=out)
+    assert rp.relattn_get_device_error() == 0
+    check(x, out, 5)
+    assert bool(torch.isnan(buf[:off]).all()) and bool(torch.isnan(buf[off + T * H * d:]).all())
