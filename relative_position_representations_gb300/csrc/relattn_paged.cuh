@@ -316,7 +316,8 @@ struct Piece {
     int pos_lo, pos_hi;    // their positions
     int ns, lo, nt;        // Item: its tiles
     int t0, t1;            // those of this piece
-    int kvh, b, pad;
+    int kvh, b;
+    int act;               // tcgen05 kernel: bit s: slot s uses a tile of the piece
     __device__ __forceinline__ int tile(int t) const { return t < ns ? t : lo + t - ns; }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     __device__ __forceinline__ int record() const { return t0 > 0 ? 0 : 1; }

@@ -110,7 +110,7 @@ struct Pieces {
         const Piece &s = ring[it & (kPieces - 1)];
         auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
         g = Piece{uni(s.row0), uni(s.cnt), uni(s.pos_lo), uni(s.pos_hi), uni(s.ns), uni(s.lo),
-                  uni(s.nt),   uni(s.t0),  uni(s.t1),     uni(s.kvh),    uni(s.b),  0};
+                  uni(s.nt),   uni(s.t0),  uni(s.t1),     uni(s.kvh),    uni(s.b),  uni(s.act)};
         return g.cnt > 0;
     }
     __device__ __forceinline__ uint32_t empty() const { return bars + 8u * (B_PIECE_EMPTY + (it & (kPieces - 1))); }
@@ -298,8 +298,11 @@ __device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, 
         any = any || more;
         const int i = it & (kPieces - 1);
         if (!wait(bars + 8u * (B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u)) break;
-        if (lane == 0)
-            ring[i] = make_piece(g, more);
+        Piece pc = make_piece(g, more);
+        if (more && g.t1 > g.t0)   // (here, where nothing waits for it)
+            for (int s = 0; s < 2; ++s)
+                if (slot_work(tp, pc, s).t_last >= pc.t0) pc.act |= 1 << s;
+        if (lane == 0) ring[i] = pc;
         __syncwarp();
         ptx::mbar_arrive_w(bars + 8u * (B_PIECE_FULL + i));
         ++it;
@@ -607,7 +610,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     for (; ok && pieces.next(wait_w, g, ok); arrive(pieces.empty()), ++pieces.it) {
         const SlotWork w = slot_work(tp, g, slot);
         const bool split = w.split;
-        const bool act = w.t_last >= g.t0;
+        const bool act = g.act >> slot & 1;
         const bool two = split && g.t1 - g.t0 > 1;      // the other slot works on the same rows
         const int rows = w.ntok * p.g;                  // may be negative: no rows in this slot
         const bool mine = quad * 32 < rows;             // this warp has rows
@@ -634,8 +637,8 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
             }
             if (split || g.t1 == g.t0) continue;
             // (pair mode) the other slot may have tiles of its own; nothing is shared with it
-            if (slot == 1) o_it[0] += slot_work(tp, g, 0).t_last >= g.t0 ? 1 : 0;
-            else o_it[1] += slot_work(tp, g, 1).t_last >= g.t0 ? 1 : 0;
+            if (slot == 1) o_it[0] += g.act & 1;
+            else o_it[1] += g.act >> 1;
             continue;
         }
         if (AK && (!split || slot == 0)) {   // R row -> shared memory (log2 domain)
@@ -928,7 +931,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
             if (!(ok = sync_slots())) break;   // O, R and the statistics go to the next piece
         } else {
             ++o_it[slot];
-            o_it[1 - slot] += slot_work(tp, g, 1 - slot).t_last >= g.t0 ? 1 : 0;
+            o_it[1 - slot] += g.act >> (1 - slot) & 1;
         }
     }
 }
