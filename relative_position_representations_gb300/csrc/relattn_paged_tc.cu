@@ -22,9 +22,9 @@
 // columns (1700 with the hand-offs), 3450 cycles per tile of both slots where the tensor cores work
 // 2048; TMEM is full, so no second S can wait. d = 64 (P beside S): the issue of the softmax, two
 // warps to a scheduler, 2550 cycles a tile. A piece costs 8 to 10 thousand cycles beside its tiles
-// (R, masks and band, write-out). Four prompts of 4096 tokens, 16 heads of 128, key term: 290 us, 961
-// TFLOP/s; a mixed step (20 generated tokens, 4 chunks of about 500, up to 8K keys): 111 us, 682;
-// chunks of 2048 under a window of 4096, d = 64, both terms: 115 us, 602. Dropped: scores in halves
+// (R, masks and band, write-out). Four prompts of 4096 tokens, 16 heads of 128, key term: 286 us, 976
+// TFLOP/s; a mixed step (20 generated tokens, 4 chunks of about 500, up to 8K keys): 111 us, 683;
+// chunks of 2048 under a window of 4096, d = 64, both terms: 115 us, 605. Dropped: scores in halves
 // of 64 keys with two buffers (mixed step 132 -> 137 us, prompts 318 -> 439: N = 64 products read A
 // twice as often, and every half pays the hand-offs), part of the exponentials as a polynomial (318
 // -> 343 us: the issue slots are scarcer than the unit, which does a warp's in 4 cycles).
@@ -977,8 +977,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();
     grid_release();
     {
-        // (32 requests at a time: a step with more than a few chunks is long; a quarter of the cold code)
-        const Range r = find_range_t<int, 1>(p, (int)blockIdx.x, (int)gridDim.x);
+        // (64 requests at a time: at 128 the cold code costs a short step 0.4 us, at 32 the loop costs a
+        // step of 1024 requests 4 us)
+        const Range r = find_range_t<int, 2>(p, (int)blockIdx.x, (int)gridDim.x);
         if (threadIdx.x == 96) *range = r;
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
