@@ -3,8 +3,6 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
-#include <set>
-#include <utility>
 
 #include "relattn_paged.cuh"
 
@@ -25,19 +23,26 @@ DeviceInfo device_info() {
 }
 
 cudaError_t opt_in_smem(const void *kern, const DeviceInfo &di) {
-    static std::set<std::pair<int, const void *>> done;
+    // a fixed table: nothing here may throw through the C entry points (past its end a kernel is
+    // only set again)
+    static struct { int dev; const void *kern; } done[512];
+    static int n = 0;
     static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lk(mu);
-    if (done.count({dev, kern})) return cudaSuccess;
+    for (int i = 0; i < n; ++i)
+        if (done[i].dev == dev && done[i].kern == kern) return cudaSuccess;
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              di.smem_optin - (int)fa.sharedSizeBytes);
-    if (e == cudaSuccess) done.insert({dev, kern});
+    if (e == cudaSuccess && n < 512) {
+        done[n].dev = dev;
+        done[n++].kern = kern;
+    }
     return e;
 }
 
@@ -67,7 +72,6 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->kv_len = a.kv_len;
     p->num_pages = a.num_pages;
     while ((1 << p->pshift) < a.page_size) ++p->pshift;
-    p->max_pages = a.max_pages;
     const long long cap = (long long)a.max_pages << p->pshift;
     p->cap = cap > 0x7fffff00LL ? 0x7fffff00 : (int)cap;
     p->clip_k = a.clip_k;

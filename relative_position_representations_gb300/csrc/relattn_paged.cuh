@@ -48,7 +48,7 @@ struct Params {
     const void *q, *k, *v, *aK, *aV;
     long long q_stride, page_stride, bt_stride, ths;
     const int *bt, *q_start, *kv_len;
-    int num_pages, pshift, max_pages, cap;   // cap: keys a block table row can hold
+    int num_pages, pshift, cap;   // cap: keys a block table row can hold
     int clip_k, window, sinks;
     float scale_log2;                        // scale * log2(e)
     int B, tokens, H, Hkv, g, d;
