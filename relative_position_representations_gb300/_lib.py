@@ -710,6 +710,15 @@ def _pages(k_pages, v_pages):
     return dev, shape, dtype, stride[0]
 
 
+def _made(shape, dtype, like, stream):
+    """A tensor of this call's own. It belongs to the current stream: with another one given, its
+    memory is not handed out again before the call is done there."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _call_on(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current; the stream defaults to its current one."""
     stream = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
@@ -733,11 +742,10 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
     B = cached_len.numel()
     max_tokens = int(max_tokens)
     if kv_len is None or q_start is None or slots is None or free_head_out is None:
-        i32 = dict(dtype=_INT, device=cached_len.device)
-        kv_len = torch.empty(B, **i32) if kv_len is None else kv_len
-        q_start = torch.empty(B + 1, **i32) if q_start is None else q_start
-        slots = torch.empty(max(0, max_tokens), **i32) if slots is None else slots
-        free_head_out = torch.empty(1, **i32) if free_head_out is None else free_head_out
+        kv_len = _made(B, _INT, cached_len, stream) if kv_len is None else kv_len
+        q_start = _made(B + 1, _INT, cached_len, stream) if q_start is None else q_start
+        slots = _made(max(0, max_tokens), _INT, cached_len, stream) if slots is None else slots
+        free_head_out = _made(1, _INT, cached_len, stream) if free_head_out is None else free_head_out
     ts, M = _table(dev, block_table, B)
     F = free_pages.numel()
     st = _call_on(
@@ -819,15 +827,13 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     if table_head_stride is not None:
         ths = int(table_head_stride)
     if out is None:
-        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+        out = _made((T, H, d), dtype, q, stream)
     elif _rows(dev, "out", out, T, H, d, dtype) != H * d:
         raise ValueError("out must be contiguous")
     if scale is None:
         scale = d ** -0.5
     if workspace is None:
-        workspace = torch.empty(relattn_paged_workspace_size(H, Hkv, d), dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)  # its memory is not handed out before this call is done
+        workspace = _made(relattn_paged_workspace_size(H, Hkv, d), torch.uint8, q, stream)
     else:
         _on(dev, "workspace", workspace)
         if not workspace.is_contiguous():

@@ -577,3 +577,27 @@ def test_joined_outputs_of_any_width_and_place(d, off, dtype):
     assert rp.relattn_get_device_error() == 0
     check(x, out, 5)
     assert bool(torch.isnan(buf[:off]).all()) and bool(torch.isnan(buf[off + T * H * d:]).all())
+
+
+def test_results_dropped_early_keep_their_memory_until_written():
+    # a call on a stream that is still busy; its results are dropped, and what is allocated next on
+    # the current stream must not lie where that call will write
+    rp = _rp()
+    x = make([1] * 6, [900, 33, 257, 128, 400, 1], 4, 2, 64, 16, BF16, seed=3)
+    g = lambda t: t.to(DEV)
+    args = (g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), i32(x["table"]), i32(x["q_start"]), i32(x["kv_len"]))
+    B = 5000
+    c, n = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+    bt, free, head = i32(np.zeros((B, 1))), i32(np.arange(B)), i32([0])
+    s = torch.cuda.Stream()
+    rp.relattn_paged_fwd(*args)
+    torch.cuda.synchronize()
+    for call_it, shape, dtype in (
+            (lambda: rp.relattn_paged_fwd(*args, stream=s), x["q"].shape, BF16),
+            (lambda: rp.relattn_paged_plan(c, n, bt, free, head, 8, B, stream=s), (B,), torch.int32)):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)   # some 50 ms
+        call_it()
+        kept = [torch.zeros(shape, dtype=dtype, device=DEV) for _ in range(6)]
+        torch.cuda.synchronize()
+        assert all(not bool(t.any()) for t in kept)
