@@ -710,12 +710,17 @@ def _pages(k_pages, v_pages):
     return dev, shape, dtype, stride[0]
 
 
-def _made(shape, dtype, like, stream):
-    """A tensor of this call's own. It belongs to the current stream: with another one given, its
-    memory is not handed out again before the call is done there."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
+def _made(shape, dtype, like, stream, returned=True):
+    """A tensor of this call's own. With another stream than the current one given, its memory is
+    that stream's: a block that the current stream has given back may still be used by work queued
+    there, which the call on the other stream does not wait for. What is returned is used on the
+    current stream next, so its memory is not handed out again before that use is over either."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
@@ -833,7 +838,7 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     if scale is None:
         scale = d ** -0.5
     if workspace is None:
-        workspace = _made(relattn_paged_workspace_size(H, Hkv, d), torch.uint8, q, stream)
+        workspace = _made(relattn_paged_workspace_size(H, Hkv, d), torch.uint8, q, stream, returned=False)
     else:
         _on(dev, "workspace", workspace)
         if not workspace.is_contiguous():

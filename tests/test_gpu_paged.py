@@ -601,3 +601,30 @@ def test_results_dropped_early_keep_their_memory_until_written():
         kept = [torch.zeros(shape, dtype=dtype, device=DEV) for _ in range(6)]
         torch.cuda.synchronize()
         assert all(not bool(t.any()) for t in kept)
+
+
+def test_memory_made_for_a_stream_is_not_in_use_elsewhere():
+    # the current stream is busy and will still read temporaries that the caller has dropped; a call on
+    # an idle stream must not write its results or its workspace there, nor lose them
+    rp = _rp()
+    x = make([1] * 6, [900, 33, 257, 128, 400, 1], 4, 2, 64, 16, BF16, seed=4)
+    g = lambda t: t.to(DEV)
+    args = (g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), i32(x["table"]), i32(x["q_start"]), i32(x["kv_len"]))
+    B = 5000
+    c, n = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+    bt, free, head = i32(np.zeros((B, 1))), i32(np.arange(B)), i32([0])
+    s = torch.cuda.Stream()
+    for call_it, sizes in (
+            (lambda **kw: [rp.relattn_paged_fwd(*args, **kw)],
+             [x["q"].numel() * 2, rp.relattn_paged_workspace_size(4, 2, 64)]),
+            (lambda **kw: rp.relattn_paged_plan(c, n, bt, free, head, 8, B, **kw), [4 * B] * 4)):
+        want = [t.clone() for t in call_it()]
+        torch.cuda.synchronize()
+        temporaries = [torch.full((b,), 77, dtype=torch.uint8, device=DEV) for b in sizes]
+        torch.cuda._sleep(100_000_000)   # some 50 ms
+        kept = [t.clone() for t in temporaries]
+        del temporaries
+        got = call_it(stream=s)
+        torch.cuda.synchronize()
+        assert all(bool((t == 77).all()) for t in kept)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
