@@ -829,8 +829,10 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
             pK = t.data_ptr()
         if t is aV:
             pV = t.data_ptr()
-    if table_head_stride is not None:
+    if table_head_stride is not None and heads:
         ths = int(table_head_stride)
+        if ths < 0 or (Hkv - 1) * ths + (2 * clip_k + 1) * d > heads * (2 * clip_k + 1) * d:
+            raise ValueError("table_head_stride reaches past the tables")
     if out is None:
         out = _made((T, H, d), dtype, q, stream)
     elif _rows(dev, "out", out, T, H, d, dtype) != H * d:

@@ -95,3 +95,18 @@ def test_memory_made_for_a_stream_is_that_streams(binding, op, count):
     assert [t.used_on for t, _ in binding.made] == [["current"]] * (4 if op == "plan" else 1) + \
         [[]] * (op == "fwd")
     assert len(binding.calls) == 2 and binding.current == "current"
+
+
+@pytest.mark.parametrize("heads,stride,fine", [
+    (2, None, True), (2, 7 * 64, True), (2, 0, True), (1, None, True), (1, 0, True),
+    (1, 7 * 64, False), (2, 7 * 64 + 1, False), (2, 1 << 40, False), (2, -7 * 64, False)])
+def test_a_table_stride_stays_within_the_tables(binding, heads, stride, fine):
+    # the kernels read rows of head h from h * stride on
+    tables = dict(aK=gpu(heads, 7, 64), aV=gpu(heads, 7, 64), clip_k=3, table_head_stride=stride)
+    if fine:
+        binding.lib.relattn_paged_fwd(**fwd_args(), **tables)
+        assert binding.calls[0][1][14] == (7 * 64 if heads == 2 and stride is None else stride or 0)
+    else:
+        with pytest.raises(ValueError, match="table_head_stride"):
+            binding.lib.relattn_paged_fwd(**fwd_args(), **tables)
+        assert not binding.calls
