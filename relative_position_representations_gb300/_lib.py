@@ -637,6 +637,12 @@ def _on(dev, name, t):
         _misplaced(dev, name, t)
 
 
+def _in_32_bits(*values):
+    """The library takes these as C ints, and ctypes would pass on their low 32 bits."""
+    if max(values) > 0x7fffffff or min(values) < -0x80000000:
+        raise ValueError("%d does not fit in 32 bits" % max(values, key=abs))
+
+
 def _ints(dev, name, t, count):
     """t holds `count` contiguous int32 on device `dev`; returns its address."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
@@ -745,7 +751,8 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
     """
     dev = _device_of("cached_len", cached_len)
     B = cached_len.numel()
-    max_tokens = int(max_tokens)
+    max_tokens, page_size = int(max_tokens), int(page_size)
+    _in_32_bits(max_tokens, page_size, B)
     if kv_len is None or q_start is None or slots is None or free_head_out is None:
         kv_len = _made(B, _INT, cached_len, stream) if kv_len is None else kv_len
         q_start = _made(B + 1, _INT, cached_len, stream) if q_start is None else q_start
@@ -753,9 +760,10 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
         free_head_out = _made(1, _INT, cached_len, stream) if free_head_out is None else free_head_out
     ts, M = _table(dev, block_table, B)
     F = free_pages.numel()
+    _in_32_bits(M, F)
     st = _call_on(
         dev, stream, _lib.relattn_paged_plan, _ints(dev, "cached_len", cached_len, B),
-        _ints(dev, "new_len", new_len, B), B, int(page_size), block_table.data_ptr(), ts, M,
+        _ints(dev, "new_len", new_len, B), B, page_size, block_table.data_ptr(), ts, M,
         _ints(dev, "free_pages", free_pages, F), F, _ints(dev, "free_head", free_head, 1), max_tokens,
         _ints(dev, "kv_len", kv_len, B), _ints(dev, "q_start", q_start, B + 1),
         _ints(dev, "slots", slots, max_tokens), _ints(dev, "free_head_out", free_head_out, 1))
@@ -769,6 +777,7 @@ def relattn_paged_append(k, v, slots, k_pages, v_pages, stream=None):
     k_pages, v_pages [num_pages, Hkv, page_size, d]; negative slots are skipped. In place."""
     dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
     T = slots.numel()
+    _in_32_bits(N, Hkv, P, d, T)
     ks, vs = _rows(dev, "k", k, T, Hkv, d, dtype), _rows(dev, "v", v, T, Hkv, d, dtype)
     st = _call_on(
         dev, stream, _lib.relattn_paged_append, k.data_ptr(), v.data_ptr(), ks, vs,
@@ -810,7 +819,8 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     qs = _rows(dev, "q", q, T, H, d, dtype)
     B = kv_len.numel()
     ts, M = _table(dev, block_table, B)
-    clip_k = int(clip_k)
+    clip_k, window, sinks, max_new = int(clip_k), int(window), int(sinks), int(max_new)
+    _in_32_bits(clip_k, window, sinks, max_new, N, P, T, H, B, M)
     ths, pK, pV, heads = 0, None, None, 0
     for name, t in (("aK", aK), ("aV", aV)):
         if t is None:
@@ -848,8 +858,8 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     st = _call_on(
         dev, stream, _lib.relattn_paged_fwd, q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
         ps, N, P, block_table.data_ptr(), ts, M, _ints(dev, "q_start", q_start, B + 1),
-        _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, int(window), int(sinks), float(scale), B,
-        T, int(max_new), H, Hkv, d, dt, workspace.data_ptr(),
+        _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, window, sinks, float(scale), B,
+        T, max_new, H, Hkv, d, dt, workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), out.data_ptr())
     if st:
         raise RelattnError(st, "relattn_paged_fwd")

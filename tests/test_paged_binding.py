@@ -110,3 +110,26 @@ def test_a_table_stride_stays_within_the_tables(binding, heads, stride, fine):
         with pytest.raises(ValueError, match="table_head_stride"):
             binding.lib.relattn_paged_fwd(**fwd_args(), **tables)
         assert not binding.calls
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1])
+@pytest.mark.parametrize("name", ["window", "sinks", "max_new", "clip_k", "page_size", "max_tokens"])
+def test_integers_past_32_bits_are_refused(binding, name, big):
+    # (a window of 2^32 + 5 keys would have been one of 5)
+    lib = binding.lib
+    with pytest.raises(ValueError, match="32 bits"):
+        if name in ("page_size", "max_tokens"):
+            lib.relattn_paged_plan(**dict(plan_args(), **{name: big}))
+        else:
+            lib.relattn_paged_fwd(**fwd_args(), **{name: big})
+    assert not binding.calls
+
+
+def test_shapes_past_32_bits_are_refused(binding):
+    lib = binding.lib
+    pages = lambda: torch.empty_strided(((1 << 32) + 2, 1, 1, 1), (1, 1, 1, 1), dtype=BF16, device="meta").as_subclass(OnGpu)
+    with pytest.raises(ValueError, match="32 bits"):
+        lib.relattn_paged_append(gpu(3, 1, 1), gpu(3, 1, 1), gpu(3, dtype=I32), pages(), pages())
+    with pytest.raises(ValueError, match="32 bits"):
+        lib.relattn_paged_fwd(**dict(fwd_args(H=1, Hkv=1, d=1, P=1), k_pages=pages(), v_pages=pages()))
+    assert not binding.calls
