@@ -628,3 +628,24 @@ def test_memory_made_for_a_stream_is_not_in_use_elsewhere():
         torch.cuda.synchronize()
         assert all(bool((t == 77).all()) for t in kept)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------------------------ many slots
+@pytest.mark.parametrize("path", ["generated", "chunks", "f32"])
+@pytest.mark.parametrize("B,busy,keys", [
+    (65, 0.7, 60), (129, 0.7, 60), (300, 0.5, 90), (1025, 0.3, 40),
+    # a handful of long requests far apart: a block's share goes on behind a gap of idle slots
+    (700, 0.004, 5000), (4100, 0.0008, 3000)])
+def test_steps_over_many_slots(B, busy, keys, path):
+    rng = np.random.default_rng(B)
+    on = rng.random(B) < busy
+    on[[0, B - 1]] = True
+    new = np.where(on, rng.integers(1, 3, B), 0)
+    if path != "generated":
+        new[np.flatnonzero(on)[::7]] = 20          # more than one tile of rows in the f32 kernel
+    kv = np.where(on, np.maximum(new, rng.integers(1, keys, B)), rng.integers(0, 9, B))
+    kv[np.flatnonzero(on)[:3]] = keys
+    x = make(new, kv, 4, 2, 64, 16, F32 if path == "f32" else BF16, 3, True, True, seed=B)
+    got = call(x, 3, max_new=2 if path == "generated" else 0)
+    assert _rp().relattn_get_device_error() == 0
+    check(x, got, 3)
