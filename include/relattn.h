@@ -393,8 +393,8 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  * (base pointers and strides) runs on the tensor cores, fp32 accumulation and statistics, the
  * weights rounded to bf16 for their product: with at most 16 query rows (max_new times H / Hkv) per
  * key/value head on a kernel for generated tokens, else, up to clip_k = 127, on the one for chunks.
- * Everything else runs on the SIMT units with fp32 arithmetic. d <= 128, clip_k <= 256 and
- * H / Hkv <= 128, else RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing. Device waits are
+ * Everything else runs on the SIMT units with fp32 arithmetic. d <= 128, clip_k <= 256,
+ * H / Hkv <= 128 and B <= 2^24, else RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing. Device waits are
  * bounded as in relattn_fwd; after one that runs out the output is undefined.
  */
 RELATTN_API relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void *k_pages,

@@ -705,7 +705,8 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
         if (table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
         if (out && (out == aK || out == aV)) return RELATTN_ERR_INVALID_ARG;
     }
-    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip)
+    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip ||
+        B > relattn::kPagedMaxSeqs)
         return RELATTN_ERR_UNSUPPORTED;
     if (tokens == 0) return RELATTN_OK;
     if (!aligned(workspace, 16) || workspace_bytes < relattn::paged_workspace_bytes(d))

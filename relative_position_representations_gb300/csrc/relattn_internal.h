@@ -206,6 +206,7 @@ cudaError_t launch_bwd_tc(const BwdArgs &a, cudaStream_t s);
 constexpr int kPagedMaxClip = 256;       // clip_k of the paged attention
 constexpr int kPagedMaxGroup = 128;      // query heads per key/value head
 constexpr int kPagedMaxPageSize = 1024;  // keys per page (a power of two)
+constexpr int kPagedMaxSeqs = 1 << 24;   // requests of one attention call (its scan counts past them in 32 bits)
 constexpr int kPlanMaxSeqs = 16384;      // sequences of one plan (their prefix sits in shared memory)
 constexpr int kPlanMaxTokens = 1 << 23;  // new tokens of one plan
 

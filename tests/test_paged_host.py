@@ -169,3 +169,9 @@ def test_binding_wants_cuda_tensors(lib):
         lib.relattn_paged_append(p[:, :, 0], p[:, :, 0], z, p, p.clone())
     with pytest.raises(TypeError):
         lib.relattn_paged_fwd(p[:, :, 0], p, p.clone(), z.reshape(2, 1), torch.zeros(3, dtype=torch.int32), z)
+
+
+@pytest.mark.parametrize("B,status", [((1 << 24) + 1, 2), ((1 << 31) - 1, 2), (1 << 24, 0)])
+def test_attention_refuses_more_requests_than_its_scan_counts(lib, B, status):
+    # (with no tokens, so that what is accepted ends on the host)
+    refused(lib, "relattn_paged_fwd", FWD, status, B=B, tokens=0)
