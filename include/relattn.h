@@ -374,7 +374,8 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  *                     no token sees may hold anything. A page number outside 0 .. num_pages - 1
  *                     counts as zeros and sets the status word to RELATTN_ERR_INVALID_ARG. The
  *                     keys and values that some token of the request sees must be finite.
- *   q_start           [B + 1] int32, ascending; rows from q_start[B] on are not written.
+ *   q_start           [B + 1] int32, ascending; rows from q_start[B] on are not written. (Other
+ *                     numbers stay within the arrays, but then any row may hold anything.)
  *   kv_len            [B] int32: cached tokens, the new ones among them (taken as at most
  *                     max_pages * page_size). A token at a negative position gets zeros.
  *   aK, aV            [Hkv|1, 2 clip_k + 1, d] of `dtype` or NULL; table_head_stride as in

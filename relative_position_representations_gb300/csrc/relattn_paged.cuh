@@ -229,7 +229,9 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
     }
     if (r.b == p.B) return r;
     // the head, then the item within it
-    r.kvh = (int)((x0 - x) / per);
+    // (clamped: offsets that do not ascend give rows to several requests, and the line may then pass
+    // what the host has allowed for; what follows stays within the arrays for any numbers)
+    r.kvh = min(max((int)((x0 - x) / per), 0), p.Hkv - 1);
     x += per * r.kvh;
     const Seq s = load_seq(p, r.b);
     if (s.n > p.T) {
@@ -383,7 +385,7 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
         const int G = (int)gridDim.x;
         if (total / G >= g->it.wt) {
             const long long y = g->x + p.c0 + (long long)g->it.wt * (g->it.nt - 1);
-            d.n = (int)(((y + 1) * G - 1) / total) - (int)blockIdx.x + 1;
+            d.n = (int)min(((y + 1) * G - 1) / total, (long long)G - 1) - (int)blockIdx.x + 1;   // in the grid
         }
     }
     p.desc[blockIdx.x] = d;

@@ -649,3 +649,25 @@ def test_steps_over_many_slots(B, busy, keys, path):
     got = call(x, 3, max_new=2 if path == "generated" else 0)
     assert _rp().relattn_get_device_error() == 0
     check(x, got, 3)
+
+
+@pytest.mark.parametrize("path", ["generated", "chunks", "f32"])
+def test_offsets_that_do_not_ascend_are_kept_in_bounds(path):
+    # every other request is given all the rows: any of their outputs may stay, within the array
+    rp = _rp()
+    T, B, H, Hkv, d, P = 23, 40, 4, 2, 64, 16
+    dtype = F32 if path == "f32" else BF16
+    x = make([T], [3000], H, Hkv, d, P, dtype, stale=False)
+    g = lambda t: t.to(DEV)
+    buf = torch.full((T + 16, H, d), float("nan"), dtype=dtype, device=DEV)
+    table = i32(np.repeat(x["table"], B, 0))
+    rp.relattn_paged_fwd(g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), table, i32([0, T] * (B // 2) + [0]), i32([3000] * B),
+                         max_new=2 if path == "generated" else 0, out=buf[8:8 + T])
+    # (the last request's rows end at 0: it has none, as have those that begin at T)
+    assert bool(torch.isnan(buf[:8]).all()) and bool(torch.isnan(buf[8 + T:]).all())
+    one = buf[8:8 + T].cpu()
+    want = call(dict(x, kv_len=np.array([3000])), 0, max_new=2 if path == "generated" else 0).cpu()
+    # the keys may be cut differently. sum p |v| < 1 (3000 keys): bf16 weights and outputs are each off
+    # by 2^-8 of it on both sides; sums of 3000 fp32 terms and of the weights by 3000 x 2^-24 each
+    tol = 4 * 2.0 ** -8 if dtype == BF16 else 4 * 3000 * 2.0 ** -24
+    assert float((one.float() - want.float()).abs().max()) <= tol
