@@ -391,9 +391,10 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  * The work is split over the GPU by keys, whatever the mix of lengths; pieces of one token's
  * keys are joined in a fixed order, so equal calls give equal bits.
  * bf16 with d = 64 or 128, pages of at least 8 keys and rows that start on 16-byte boundaries
- * (base pointers and strides) runs on the tensor cores, fp32 accumulation and statistics, the
- * weights rounded to bf16 for their product: with at most 16 query rows (max_new times H / Hkv) per
- * key/value head on a kernel for generated tokens, else, up to clip_k = 127, on the one for chunks.
+ * (base pointers and strides) runs on the tensor cores, fp32 accumulation and statistics: with at
+ * most 16 query rows (max_new times H / Hkv) per key/value head on a kernel for generated tokens,
+ * whose weights take part in their product with 16 bits (two bf16 numbers), else, up to clip_k =
+ * 127, on the one for chunks, whose weights are rounded to bf16 as in relattn_fwd.
  * Everything else runs on the SIMT units with fp32 arithmetic. d <= 128, clip_k <= 256,
  * H / Hkv <= 128 and B <= 2^24, else RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing. Device waits are
  * bounded as in relattn_fwd; after one that runs out the output is undefined.

@@ -22,6 +22,11 @@
 //   Slot i of 8 keys is row perm(i) = 0 4 1 5 2 6 3 7, and dim slot i is the 16-byte chunk perm(i) of
 //     64 columns: eight lanes' 16-byte reads then fall in the eight chunks of a 128-byte line.
 // Rows of a page that no token sees may hold NaN: their V is replaced by zeros in registers.
+// The weights (and the bins of the value term) go into their product in two bf16 parts, so that a
+// generated token's are within 2^-16, not within 2^-8 (relattn_decode_fwd's are fp32). The tensor pipe
+// is 8 % busy with one product each; the second costs up to 8 rows 0.1 to 0.8 us of 33 to 97 (under
+// 1 %), with 16 rows, where the warps' own latency counts, 4 to 6 % (64 requests of 2K - 16K keys, one
+// key head of 128: 59.3 -> 62.8 us; with both terms, two key heads of 64: 75.0 -> 79.3).
 //
 // 64 requests with 2K - 16K keys (8 query heads per key head, d = 128): 96 us, 6.2 TB/s; 32 requests
 // with 1K - 2K keys, both terms (16 heads of 64): 41.7 us, 4.7 TB/s; a step with a handful of keys
@@ -103,6 +108,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
+}
+
+// x, y as two pairs of bf16: the rounded values and what the rounding left out
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = ptx::pack_bf16x2(x, y);
+    lo = ptx::pack_bf16x2(x - ptx::bf16lo_to_f32(hi), y - __uint_as_float(hi & 0xffff0000u));
 }
 
 // row of key slot i of 8 (and chunk of dim slot i)
@@ -301,8 +312,8 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
         }
-        // O^T += A^T B over 16 keys (or table rows): chunks v of rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-        auto outputs = [&](const uint4 (&v)[4], int u, const uint32_t (&b)[NT][2]) {
+        // O^T += A^T (B + Bl) over 16 keys (or table rows): chunks v of rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+        auto outputs = [&](const uint4 (&v)[4], int u, const uint32_t (&b)[NT][2], const uint32_t (&bl)[NT][2]) {
             const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&v[0]), *v1 = reinterpret_cast<const uint32_t *>(&v[1]);
             const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&v[2]), *v3 = reinterpret_cast<const uint32_t *>(&v[3]);
 #pragma unroll
@@ -310,7 +321,10 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                 const uint32_t a0 = __byte_perm(v0[i], v1[i], 0x5410), a1 = __byte_perm(v0[i], v1[i], 0x7632);
                 const uint32_t a2 = __byte_perm(v2[i], v3[i], 0x5410), a3 = __byte_perm(v2[i], v3[i], 0x7632);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma(o[n][4 * u + i], a0, a1, a2, a3, b[n][0], b[n][1]);
+                for (int n = 0; n < NT; ++n) {
+                    mma(o[n][4 * u + i], a0, a1, a2, a3, b[n][0], b[n][1]);
+                    mma(o[n][4 * u + i], a0, a1, a2, a3, bl[n][0], bl[n][1]);
+                }
             }
         };
 
@@ -387,7 +401,7 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                         for (int e = 0; e < 4; ++e) o[n][i][e] *= al[e & 1];
                 }
             }
-            uint32_t b[NT][2];
+            uint32_t b[NT][2], bl[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float pr[4];
@@ -397,20 +411,27 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                     pr[e] = ptx::ex2(x[n][e] - mu[e & 1]);
                     l[n][e & 1] += pr[e];
                 }
-                if (AV) {
+                if (AV && near) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int lab = j0 + kr + 8 * (e >> 1) - pos[n][e & 1] + k;
-                        if (near && lab > 0) {
+                        if (lab > 0) {
                             if (lab <= k) Bs[(8 * n + 2 * c + (e & 1)) * L.lw + lab] = x[n][e];
                         } else {
                             far[n][e & 1] += pr[e];
                         }
                     }
+                } else if (AV) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) far[n][e & 1] += pr[e];
                 }
-                // P rounded to bf16 for the tensor cores; the sums above keep fp32
-                b[n][0] = transpose8(ptx::pack_bf16x2(pr[0], pr[1]));
-                b[n][1] = transpose8(ptx::pack_bf16x2(pr[2], pr[3]));
+                // P for the tensor cores in two bf16 parts, 16 bits in all; the sums above keep fp32
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    split2(pr[2 * h], pr[2 * h + 1], b[n][h], bl[n][h]);
+                    b[n][h] = transpose8(b[n][h]);
+                    bl[n][h] = transpose8(bl[n][h]);
+                }
             }
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
@@ -425,7 +446,7 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                         if (!(j <= pos_hi && (j >= first || j < p.sinks))) v[e] = make_uint4(0, 0, 0, 0);
                     }
                 }
-                outputs(v, u, b);
+                outputs(v, u, b, bl);
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty);
@@ -472,7 +493,7 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                         v[u][e] = w < W ? __ldg(reinterpret_cast<const uint4 *>(aV + (long long)w * D + 64 * u))
                                         : make_uint4(0, 0, 0, 0);
                 }
-                uint32_t b[NT][2];
+                uint32_t b[NT][2], bl[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int row = 8 * n + rq;
@@ -490,11 +511,11 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                             }
                         }
                     }
-                    b[n][0] = ptx::pack_bf16x2(be[0], be[1]);
-                    b[n][1] = ptx::pack_bf16x2(be[2], be[3]);
+                    split2(be[0], be[1], b[n][0], bl[n][0]);
+                    split2(be[2], be[3], b[n][1], bl[n][1]);
                 }
 #pragma unroll
-                for (int u = 0; u < D / 64; ++u) outputs(v[u], u, b);
+                for (int u = 0; u < D / 64; ++u) outputs(v[u], u, b, bl);
             }
         }
 #pragma unroll

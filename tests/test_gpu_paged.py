@@ -671,3 +671,40 @@ def test_offsets_that_do_not_ascend_are_kept_in_bounds(path):
     # by 2^-8 of it on both sides; sums of 3000 fp32 terms and of the weights by 3000 x 2^-24 each
     tol = 4 * 2.0 ** -8 if dtype == BF16 else 4 * 3000 * 2.0 ** -24
     assert float((one.float() - want.float()).abs().max()) <= tol
+
+
+# ------------------------------------------------------------------------------------ weights
+def cancelling(H, d, keys, clip_k, terms, seed):
+    """One token whose outputs nearly cancel: queries of one non-zero column, so that scores carry next
+    to no error, and first values that take back what the other keys add up to. What is left are the
+    errors of the weights."""
+    x = make([1], [keys], H, H, d, 16, BF16, clip_k, terms, terms, seed=seed, stale=False)
+    x["q"].zero_()
+    x["q"][..., 0] = 4.0
+    x["k_pages"].clamp_(-2.0, 2.0)
+    x["k_pages"][x["table"][0, 0], :, 0, 0] = 2.5
+    f = lambda t: None if t is None else t.double().numpy()
+    v0 = x["v_pages"][x["table"][0, 0], :, 0]
+    run = lambda: op.attend(f(x["q"]), f(x["k_pages"]), f(x["v_pages"]), x["table"], x["q_start"], x["kv_len"],
+                            f(x["aK"]), f(x["aV"]), clip_k, 0, 0, 0.25)
+    v0.zero_()
+    rest = run()[0][0]
+    v0.fill_(1.0)
+    v0.copy_(torch.from_numpy(-rest / (run()[0][0] - rest)))
+    return x, run()
+
+
+@pytest.mark.parametrize("hint", [1, 16], ids=["8_rows", "16_rows"])
+@pytest.mark.parametrize("terms", [False, True], ids=["plain", "terms"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_generated_tokens_keep_their_weights(d, terms, hint):
+    """The weights of generated tokens take part with 16 bits (two bf16 numbers), as do the table's
+    bins; relattn_decode_fwd's are fp32."""
+    keys, k = 40, 4
+    x, (z, mass, size) = cancelling(8, d, keys, k, terms, d + hint)
+    got = call(x, k, scale=0.25, max_new=hint)
+    # a weight in two parts is off by 2^-8 x 2^-8; one product to a score; the tensor cores' sums may
+    # drop bits where the unit rounds: twice the keys' share
+    tol = op.tolerance(z, mass, size, 2 * (keys + k + 1), 1, 2.0 ** -8, 2.0 ** -16)
+    bad = np.abs(got.double().cpu().numpy() - z) - tol
+    assert bad.max() <= 0, (bad.max(), tol.max())
