@@ -341,7 +341,7 @@ RELATTN_API relattn_status_t relattn_paged_plan(const int *cached_len, const int
  *                     v_stride elements between tokens (slices of a joint projection).
  *   slots             [tokens] int32. Negative: the token is skipped. A slot outside the cache is
  *                     skipped and sets the device status word to RELATTN_ERR_INVALID_ARG. If two
- *                     tokens name one slot, either may be the one that stays.
+ *                     tokens name one slot, its row is left with a mixture of their numbers.
  *   k_pages, v_pages  [num_pages, Hkv, page_size, d], page_stride elements between pages.
  * Nothing else of the cache is written; k and v must not overlap the rows that are.
  * num_pages * page_size < 2^31. tokens = 0 does nothing.

@@ -708,3 +708,24 @@ def test_generated_tokens_keep_their_weights(d, terms, hint):
     tol = op.tolerance(z, mass, size, 2 * (keys + k + 1), 1, 2.0 ** -8, 2.0 ** -16)
     bad = np.abs(got.double().cpu().numpy() - z) - tol
     assert bad.max() <= 0, (bad.max(), tol.max())
+
+
+# ------------------------------------------------------------------------------------ one slot twice
+@pytest.mark.parametrize("T,d", [(4, 64), (2000, 128)])
+def test_two_tokens_of_one_slot(T, d):
+    """Such a row is left with a mixture of the tokens' numbers, and every other row is right."""
+    rp = _rp()
+    rnd = torch.Generator().manual_seed(T)
+    k, v = (torch.randn((T, 2, d), generator=rnd).to(BF16) for _ in range(2))
+    N, P = T // 8 + 1, 8
+    slots = np.random.default_rng(T).permutation(N * P)[:T]
+    slots[-1] = slots[0]
+    kp, vp = (torch.zeros((N, 2, P, d), dtype=BF16, device=DEV) for _ in range(2))
+    rp.relattn_paged_append(k.to(DEV), v.to(DEV), i32(slots), kp, vp)
+    for x, pages in ((k, kp.cpu()), (v, vp.cpu())):
+        rows = pages.transpose(1, 2).reshape(-1, 2, d)
+        assert torch.equal(rows[slots[1:-1]], x[1:-1])
+        twice = rows[slots[0]]
+        assert bool(((twice == x[0]) | (twice == x[-1])).all())
+        left = np.setdiff1d(np.arange(N * P), slots)
+        assert not bool(rows[left].any())
