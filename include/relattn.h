@@ -394,7 +394,10 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  * (base pointers and strides) runs on the tensor cores, fp32 accumulation and statistics: with at
  * most 16 query rows (max_new times H / Hkv) per key/value head on a kernel for generated tokens,
  * whose weights take part in their product with 16 bits (two bf16 numbers), else, up to clip_k =
- * 127, on the one for chunks, whose weights are rounded to bf16 as in relattn_fwd.
+ * 127, on the one for chunks, whose weights are rounded to bf16 as in relattn_fwd. Both measure
+ * the work in 31 bits: where requests as long as a table row can hold (max_pages * page_size) could
+ * pass that (1024 requests with 8 key/value heads: rows of 7 million keys), the call runs on the SIMT
+ * units too, whatever the lengths are.
  * Everything else runs on the SIMT units with fp32 arithmetic. d <= 128, clip_k <= 256,
  * H / Hkv <= 128 and B <= 2^24, else RELATTN_ERR_UNSUPPORTED. tokens = 0 does nothing. Device waits are
  * bounded as in relattn_fwd; after one that runs out the output is undefined.

@@ -729,3 +729,97 @@ def test_two_tokens_of_one_slot(T, d):
         assert bool(((twice == x[0]) | (twice == x[-1])).all())
         left = np.setdiff1d(np.arange(N * P), slots)
         assert not bool(rows[left].any())
+
+
+# ------------------------------------------------------------------------------------ long tables
+@pytest.mark.parametrize("new,kv,H,Hkv,k,key,value,kw", [
+    # at d = 128 the R rows of clip_k >= 98 leave room for one query tile per item, not two
+    ([70, 3], [400, 900], 6, 2, 97, True, True, {}),
+    ([70, 3], [400, 900], 6, 2, 98, True, True, {}),
+    ([70, 3], [400, 900], 6, 2, 127, True, True, {}),
+    ([300, 1], [300, 700], 2, 2, 98, True, False, {}),
+    ([300, 1], [300, 700], 2, 2, 127, False, True, {}),
+    ([131], [3300], 8, 8, 127, True, True, {}),
+    ([131], [3300], 8, 8, 98, True, True, dict(window=2000, sinks=200)),
+    ([20, 37], [6100, 4000], 32, 8, 127, True, True, {}),
+    ([200], [260], 2, 1, 127, True, True, dict(window=60, sinks=3))])
+def test_chunks_with_long_tables(new, kv, H, Hkv, k, key, value, kw):
+    x = make(new, kv, H, Hkv, 128, 16, BF16, k, key, value, seed=sum(kv) + k, extra_rows=1)
+    got = call(x, k, max_new=max(new), **kw)
+    assert _rp().relattn_get_device_error() == 0
+    check(x, got, k, **kw)
+
+
+# ------------------------------------------------------------------------------------ long prompts
+@pytest.mark.parametrize("new,kv,H,Hkv,d,k,key,value,dtype,kw", [
+    ([2100], [2100], 2, 1, 128, 64, True, False, BF16, {}),
+    ([1900, 1], [2500, 1000], 2, 2, 64, 16, True, True, BF16, dict(window=700, sinks=20)),
+    ([1200], [1300], 2, 1, 64, 16, True, True, F32, {}),
+    ([1], [40000], 16, 4, 128, 16, True, True, BF16, {}),
+    ([40], [33000], 2, 1, 64, 0, False, False, BF16, {}),
+    ([1], [40000], 4, 2, 64, 16, True, True, F32, {})])
+def test_long_requests(new, kv, H, Hkv, d, k, key, value, dtype, kw):
+    x = make(new, kv, H, Hkv, d, 64, dtype, k, key, value, seed=sum(kv) + k)
+    got = call(x, k, max_new=max(new), **kw)
+    assert _rp().relattn_get_device_error() == 0
+    check(x, got, k, **kw)
+
+
+# ------------------------------------------------------------------------------------ which kernel
+def ran_on_tensor_cores(x, k, max_new, **kw):
+    """The tensor-core kernels heed the hook that withholds the first queries, the SIMT kernel does
+    not: its call is right and reports nothing."""
+    rp = _rp()
+    rp.relattn_set_wait_limit(1000000)
+    rp.relattn_debug_withhold_first_load(True)
+    try:
+        call(x, k, max_new=max_new, **kw)
+        torch.cuda.synchronize()
+    finally:
+        rp.relattn_debug_withhold_first_load(False)
+        rp.relattn_set_wait_limit(2000000000)
+    return rp.relattn_get_device_error() == 4
+
+
+@pytest.mark.parametrize("key,value", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,H,Hkv", [(1, 4, 4), (1, 16, 1), (60, 4, 2)])
+def test_bf16_runs_on_the_tensor_cores(new, H, Hkv, d, key, value):
+    # (a variant compiled to another register count would move to the SIMT kernel)
+    x = make([new], [200], H, Hkv, d, 16, BF16, 16, key, value)
+    assert ran_on_tensor_cores(x, 16, new)
+
+
+@pytest.mark.parametrize("new,d,P,k,tensor", [
+    (60, 128, 16, 127, True), (60, 128, 16, 128, False), (60, 80, 16, 16, False), (60, 64, 4, 16, False),
+    (60, 64, 8, 16, True), (1, 128, 16, 256, True), (1, 96, 16, 16, False)])
+def test_the_documented_shapes_run_on_the_tensor_cores(new, d, P, k, tensor):
+    x = make([new], [200], 4, 2, d, P, BF16, k, True, True)
+    assert ran_on_tensor_cores(x, k, new) == tensor
+
+
+@pytest.mark.parametrize("path", ["generated", "chunks", "f32"])
+def test_a_table_for_very_long_requests(path):
+    """A table whose rows could hold 2^31 keys: the measure of the work may pass 31 bits, so every path
+    takes the SIMT kernel's 64-bit one, whatever the lengths are."""
+    rp = _rp()
+    B, H, P, M, d = 40, 4, 1024, 1 << 21, 64
+    rng = np.random.default_rng(5)
+    new = rng.integers(1, 3 if path == "generated" else 30, B)
+    kv = new + rng.integers(0, 2000, B)
+    x = make(new, kv, H, H, d, P, F32 if path == "f32" else BF16, 8, True, True, seed=2)
+    wide = torch.full((B, M), -7, dtype=torch.int32, device=DEV)
+    wide[:, :x["table"].shape[1]] = i32(x["table"])
+    g = lambda t: t.to(DEV)
+    args = (g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), wide, i32(x["q_start"]), i32(x["kv_len"]))
+    kw = dict(aK=g(x["aK"]), aV=g(x["aV"]), clip_k=8, max_new=2 if path == "generated" else 0)
+    rp.relattn_set_wait_limit(1000000)
+    rp.relattn_debug_withhold_first_load(True)
+    try:
+        got = rp.relattn_paged_fwd(*args, **kw)
+        torch.cuda.synchronize()
+    finally:
+        rp.relattn_debug_withhold_first_load(False)
+        rp.relattn_set_wait_limit(2000000000)
+    assert rp.relattn_get_device_error() == 0
+    check(x, got, 8)
