@@ -320,9 +320,12 @@ RELATTN_API relattn_status_t relattn_decode_workspace_size(int B, int H, int T, 
  *   slots                 [max_tokens] int32, -1 behind the last new token.
  * A request is left out when the free pages do not suffice for it (later ones that need pages
  * are then left out too), when it would not fit its table row or max_tokens, when its length would
- * pass 2^31 - 1, or when a length is negative: its slots are -1, its kv_len is cached_len, its table row stays, and the device
- * status word becomes RELATTN_ERR_INVALID_ARG (relattn_get_device_error). A request with a
- * negative new_len, or one above max_tokens, has no rows in q_start and slots either.
+ * pass 2^31 - 1, or when a length is negative: its slots are -1, its kv_len is cached_len, its
+ * table row stays, and the device status word becomes RELATTN_ERR_INVALID_ARG
+ * (relattn_get_device_error). Its rows stay in q_start, so that the others' rows are where the
+ * caller has put them; relattn_paged_fwd fills them with numbers that mean nothing (it takes them
+ * for the request's last cached tokens). A request with a negative new_len, or one above
+ * max_tokens, has no rows in q_start and slots either.
  * page_size: a power of two, 1 .. 1024. B <= 16384 and max_tokens <= 2^23, else
  * RELATTN_ERR_UNSUPPORTED.
  */
@@ -376,8 +379,9 @@ RELATTN_API relattn_status_t relattn_paged_append(const void *k, const void *v, 
  *                     keys and values that some token of the request sees must be finite.
  *   q_start           [B + 1] int32, ascending; rows from q_start[B] on are not written. (Other
  *                     numbers stay within the arrays, but then any row may hold anything.)
- *   kv_len            [B] int32: cached tokens, the new ones among them (taken as at most
- *                     max_pages * page_size). A token at a negative position gets zeros.
+ *   kv_len            [B] int32: cached tokens, the new ones among them. A token at a negative
+ *                     position gets zeros. A length past max_pages * page_size is taken as that,
+ *                     without a status: the new tokens are then the last that the row can hold.
  *   aK, aV            [Hkv|1, 2 clip_k + 1, d] of `dtype` or NULL; table_head_stride as in
  *                     relattn_fwd. Only rows 0 .. clip_k (offsets -clip_k .. 0) are read; they
  *                     must be finite.

@@ -748,6 +748,8 @@ def relattn_paged_plan(cached_len, new_len, block_table, free_pages, free_head, 
     cached_len, new_len: [B] int32. block_table: [B, max_pages] int32, new entries written in
     place. free_pages: int32 page numbers, of which the first free_head ([1] int32) are taken.
     kv_len may be cached_len and free_head_out may be free_head, which then advance in place.
+    A request that finds no pages or slots is left out: relattn_get_device_error says so, its
+    slots are -1, and its rows of a later relattn_paged_fwd mean nothing.
     """
     dev = _device_of("cached_len", cached_len)
     B = cached_len.numel()

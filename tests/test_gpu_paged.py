@@ -823,3 +823,24 @@ def test_a_table_for_very_long_requests(path):
         rp.relattn_set_wait_limit(2000000000)
     assert rp.relattn_get_device_error() == 0
     check(x, got, 8)
+
+
+def test_a_step_in_which_a_request_is_left_out():
+    """The status says so, and the others' outputs are right."""
+    rp = _rp()
+    H, Hkv, d, P = 4, 2, 64, 16
+    new, cached = np.array([5, 40, 3]), np.array([20, 0, 31])
+    x = make(new, cached + new, H, Hkv, d, P, BF16, 8, True, True, stale=False)
+    table = x["table"].copy()
+    g = lambda t: t.to(DEV)
+    bt, lens, head = i32(table), i32(cached), i32([0])
+    # the first request's page has room (20 + 5 of 32), the others want three pages and one: none is free
+    kv, qs, slots, _ = rp.relattn_paged_plan(lens, i32(new), bt, i32([]), head, P, int(new.sum()))
+    assert rp.relattn_get_device_error() == 1
+    assert kv.tolist() == [25, 0, 31] and qs.tolist() == [0, 5, 45, 48]
+    assert (slots[5:] == -1).all() and (slots[:5] >= 0).all()
+    z = rp.relattn_paged_fwd(g(x["q"]), g(x["k_pages"]), g(x["v_pages"]), bt, qs, kv, aK=g(x["aK"]), aV=g(x["aV"]),
+                             clip_k=8)
+    assert rp.relattn_get_device_error() == 0
+    one = dict(x, q=x["q"][:5], table=table[:1], q_start=np.array([0, 5]), kv_len=np.array([25]))
+    check(one, z[:5], 8)
