@@ -224,9 +224,11 @@ cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
 // lane = N4 columns for P V. The next 32 keys are on their way into registers meanwhile, and the
 // page numbers of the ones behind them. The edge tables go the same way: R = Q aK^T takes table
 // rows for keys, beta aV takes beta for P. All sums and statistics fp32. Bound by
-// shared memory (a lane's 16 products of scores take 5 loads of 16 bytes, its 32 of outputs 8) and, at
-// the sizes of a test, by latency: three chunks of 61 - 127 tokens over 100 - 700 keys (8 heads of 64,
-// both terms, fp32) take 47 us, 6 TFLOP/s.
+// shared memory (a lane's 16 products of scores take 5 loads of 16 bytes, its 32 of outputs 8: 1800
+// cycles of its wavefronts for a run of 32 keys at d = 64, two CTAs to an SM) and by latency: a run
+// takes a CTA on its own 2 us. Three chunks of 61 - 127 tokens over 100 - 700 keys (8 heads of 64, both
+// terms, fp32) take 47 us, 6 TFLOP/s: 10 are a step's fixed cost, 5 the two terms, the rest one or two
+// tiles (four runs each) of every CTA, cut into pieces, and their merge.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 32;
 constexpr int kSimtKeys = 32;

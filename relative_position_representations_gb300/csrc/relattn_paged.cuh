@@ -144,9 +144,10 @@ struct Range {
 
 // One warp calls it; every lane returns the range of CTA c of G and the item that holds its first
 // position. The lanes take the requests in turn, kBatch of each lane's loaded at once (their latency
-// is most of what a small step costs), and add up the items of a request with many of them together. I: a type that holds the whole line (32 bits where
-// the host has seen that they do: this code runs once, cold, in front of everything else, so every
-// instruction of it counts).
+// is most of what a small step costs), and add up the items of a request with many of them
+// together. I: a type that holds the whole line (32 bits where the host has seen that they do: this
+// code runs once, cold, in front of everything else, so every instruction of it counts). Every CTA
+// looks at all requests, twice where a batch does not hold them: 13 to 17 us for each 1000 of them.
 template <typename I, int kBatch = 4>
 __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
     constexpr unsigned kAll = 0xffffffffu;

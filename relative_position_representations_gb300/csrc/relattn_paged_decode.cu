@@ -30,7 +30,7 @@
 //
 // 64 requests with 2K - 16K keys (8 query heads per key head, d = 128): 96 us, 6.2 TB/s; 32 requests
 // with 1K - 2K keys, both terms (16 heads of 64): 41.7 us, 4.7 TB/s; a step with a handful of keys
-// takes 5.9 us (scan of the lengths, first loads, two launches), which is what the latter lacks.
+// takes 6.0 us (scan of the lengths, first loads, two launches), which is what the latter lacks.
 //
 // Relative terms: R = Q aK^T (k + 1 rows) once per piece by the same MMA; keys at most k - 1
 // back add their own R entry and leave their score in a bin; the other keys share entry 0 and

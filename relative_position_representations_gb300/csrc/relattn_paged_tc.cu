@@ -22,8 +22,10 @@
 // columns (1700 with the hand-offs), 3450 cycles per tile of both slots where the tensor cores work
 // 2048; TMEM is full, so no second S can wait. d = 64 (P beside S): the issue of the softmax, two
 // warps to a scheduler, 2550 cycles a tile. A piece costs 8 to 10 thousand cycles beside its tiles
-// (R, masks and band, write-out). Four prompts of 4096 tokens, 16 heads of 128, key term: 286 us, 976
-// TFLOP/s; a mixed step (20 generated tokens, 4 chunks of about 500, up to 8K keys): 111 us, 683;
+// (R, masks and band, write-out). A generated token fills g of the 128 rows of its tiles. Four prompts
+// of 4096 tokens, 16 heads of 128, key term: 285 us, 982 TFLOP/s; a mixed step (20 generated tokens, 4
+// chunks of about 500, up to 8K keys): 110 us, 685, where the generated tokens are 20 of 1989 tokens,
+// 2156 of 7092 tiles and by the measured costs 26 % of the work;
 // chunks of 2048 under a window of 4096, d = 64, both terms: 115 us, 605. Dropped: scores in halves
 // of 64 keys with two buffers (mixed step 132 -> 137 us, prompts 318 -> 439: N = 64 products read A
 // twice as often, and every half pays the hand-offs), part of the exponentials as a polynomial (318
