@@ -421,6 +421,55 @@ RELATTN_API relattn_status_t relattn_paged_workspace_size(int H, int Hkv, int d,
                                               unsigned long long *bytes);
 
 /*
+ * relattn_paged_evict — cuts requests back to their most attended keys, in place. Of every request
+ * with more than `limit` cached keys, each key/value head keeps `budget` keys: the first `sinks`,
+ * the last `recent`, and of the others the budget - sinks - recent with the largest mass, ties to
+ * the lower position (a NaN counts as the largest mass). The r-th kept key of a head, in the order
+ * of the positions, moves to position r with its value and its mass; the request then has `budget`
+ * keys, and the pages behind them go back to the free list. Positions of later calls (and so the
+ * offsets of the relative terms) count the kept keys. Requests with at most `limit` keys stay as
+ * they are.
+ *
+ *   kv_len            [B] int32: cached keys (a length past max_pages * page_size is taken as that).
+ *   block_table, table_stride, max_pages, num_pages, page_size, k_pages, v_pages, page_stride
+ *                     the cache, as in relattn_paged_append. The table is only read; rows of the
+ *                     pages behind the budget keep what they hold.
+ *   mass              [num_pages, Hkv, page_size] fp32, mass_stride elements between pages: what
+ *                     relattn_paged_weights has gathered.
+ *   budget, limit, sinks, recent   budget >= 1, limit >= budget, sinks + recent <= budget. A limit
+ *                     some way above the budget saves work: a cut moves most of a request's keys,
+ *                     whether it drops one key or a thousand.
+ *   free_pages, num_free, free_head, free_head_out
+ *                     the list that relattn_paged_plan takes pages from, or NULL, 0 and NULLs. The n
+ *                     pages that become free, request after request, are written to
+ *                     free_pages[free_head - n .. free_head - 1]; free_head_out = free_head - n (may
+ *                     be the same address). With free_head < n or > num_free nothing is given back
+ *                     and the status word becomes RELATTN_ERR_INVALID_ARG.
+ *   kv_len_out        [B] int32: budget where a request was cut, else kv_len (may be kv_len itself).
+ *   workspace         caller-owned device scratch of relattn_paged_evict_workspace_size bytes (with
+ *                     max_keys = max_pages * page_size), 16-byte aligned; calls that may overlap need
+ *                     one each.
+ *
+ * Keys that keep their position are not written, so a page that several requests share is safe if
+ * all of its keys lie below `sinks`; no other page may be shared. A page number outside the cache
+ * sets the status word to RELATTN_ERR_INVALID_ARG: its masses count least, and rows from or to it
+ * are not copied. bf16 or fp32, d <= 128, B <= 16384, else RELATTN_ERR_UNSUPPORTED. Waits between
+ * the CTAs (for a row to be read before it is overwritten) are bounded as in relattn_fwd.
+ */
+RELATTN_API relattn_status_t relattn_paged_evict(const int *kv_len, const int *block_table,
+                                     long long table_stride, int max_pages, void *k_pages,
+                                     void *v_pages, long long page_stride, float *mass,
+                                     long long mass_stride, int num_pages, int page_size, int budget,
+                                     int limit, int sinks, int recent, int *free_pages, int num_free,
+                                     const int *free_head, int B, int Hkv, int d, int dtype,
+                                     void *workspace, unsigned long long workspace_bytes,
+                                     int *kv_len_out, int *free_head_out, relattn_stream_t stream);
+
+/* relattn_paged_evict_workspace_size — host only: the workspace bytes relattn_paged_evict needs. */
+RELATTN_API relattn_status_t relattn_paged_evict_workspace_size(int B, int Hkv, long long max_keys,
+                                                    unsigned long long *bytes);
+
+/*
  * relattn_sinusoid_table — the fixed sinusoidal encodings of every relative offset of a
  * length-n sequence, the r of the Transformer-XL score before its projection ("Relative
  * Position Encoding in Transformer-XL" page: r_{i-j} is a sinusoid of the distance, in the

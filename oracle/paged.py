@@ -46,6 +46,39 @@ def append(k, v, slots, k_pages, v_pages):
     return k_pages, v_pages
 
 
+def evict(kv_len, table, k_pages, v_pages, mass, budget, limit, sinks, recent, free=None, head=0):
+    """Returns (kv_len, k_pages, v_pages, mass, free, head): every request past `limit` keys cut to
+    `budget` head by head, key by key; its pages behind the budget put back in front of `head`."""
+    k_pages, v_pages, mass = k_pages.copy(), v_pages.copy(), mass.copy()
+    free = None if free is None else np.array(free)
+    P, cap = mass.shape[2], table.shape[1] * mass.shape[2]
+    out, gone = [], []
+    for b, n in enumerate(kv_len):
+        n = min(max(int(n), 0), cap)
+        if n <= limit:
+            out.append(int(kv_len[b]))
+            continue
+        out.append(budget)
+        gone += [int(x) for x in table[b, -(-budget // P):-(-n // P)]]
+        at = lambda j: (table[b, j // P], j % P)
+        for h in range(mass.shape[1]):
+            rest = range(sinks, n - recent)
+            w = [mass[at(j)[0], h, at(j)[1]] for j in rest]
+            w = [np.inf if np.isnan(x) else x for x in w]
+            nan = [np.isnan(mass[at(j)[0], h, at(j)[1]]) for j in rest]
+            heavy = sorted(range(len(w)), key=lambda i: (not nan[i], -w[i], i))[:budget - sinks - recent]
+            kept = list(range(sinks)) + sorted(sinks + i for i in heavy) + list(range(n - recent, n))
+            assert len(kept) == budget
+            for x in (k_pages, v_pages, mass):
+                rows = [x[at(j)[0], h, at(j)[1]].copy() for j in kept]
+                for r, row in enumerate(rows):
+                    x[at(r)[0], h, at(r)[1]] = row
+    if free is not None:
+        head -= len(gone)
+        free[head:head + len(gone)] = gone
+    return np.array(out), k_pages, v_pages, mass, free, head
+
+
 def attend(q, k_pages, v_pages, table, q_start, kv_len, aK, aV, clip_k, window, sinks, scale):
     """q [T, H, d], pages [N, Hkv, P, d], tables [Hkv|1, 2k+1, d] or None, all float64.
 

@@ -81,6 +81,11 @@ _lib.relattn_paged_fwd.argtypes = [_P, _L, _P, _P, _L, _I, _I, _P, _L, _I, _P, _
 _lib.relattn_paged_fwd.restype = _I
 _lib.relattn_paged_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
 _lib.relattn_paged_workspace_size.restype = _I
+_lib.relattn_paged_evict.argtypes = [_P, _P, _L, _I, _P, _P, _L, _P, _L, _I, _I, _I, _I, _I, _I, _P, _I, _P,
+                                     _I, _I, _I, _I, _P, ctypes.c_ulonglong, _P, _P, _P]
+_lib.relattn_paged_evict.restype = _I
+_lib.relattn_paged_evict_workspace_size.argtypes = [_I, _I, _L, ctypes.POINTER(ctypes.c_ulonglong)]
+_lib.relattn_paged_evict_workspace_size.restype = _I
 _lib.relattn_labels.argtypes = [_I, _I, _I, _I, _I, _I, _I, _P, _P]
 _lib.relattn_labels.restype = _I
 _lib.relattn_t5_thresholds.argtypes = [_I, _I, _I, ctypes.POINTER(_I), _I, ctypes.POINTER(_I)]
@@ -107,7 +112,8 @@ EXPORTED = ["relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_decode_fwd",
             "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
             "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
-            "relattn_paged_workspace_size", "relattn_bwd",
+            "relattn_paged_workspace_size", "relattn_paged_evict", "relattn_paged_evict_workspace_size",
+            "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",
             "relattn_scalar_bias_bwd_workspace_size", "relattn_labeled_bwd",
             "relattn_labeled_bwd_workspace_size", "relattn_labels",
@@ -866,6 +872,89 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
     if st:
         raise RelattnError(st, "relattn_paged_fwd")
     return out
+
+
+def _mass(dev, t, N, Hkv, P):
+    """t is [num_pages, Hkv, page_size] fp32, pages spaced at will; returns the stride between them."""
+    _on(dev, "mass", t)
+    if t.dtype is not torch.float32:
+        raise TypeError("mass must be torch.float32, got %s" % t.dtype)
+    if t.shape != (N, Hkv, P):
+        raise ValueError("mass must have shape %s, got %s" % ((N, Hkv, P), tuple(t.shape)))
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and P > 1) or (s1 != P and Hkv > 1):
+        raise ValueError("mass must be contiguous behind its first dimension")
+    if N <= 1:
+        return Hkv * P
+    if s0 < Hkv * P:
+        raise ValueError("mass's first dimension overlaps")
+    return s0
+
+
+def _scratch(workspace, size, like, stream):
+    """The caller's workspace, or one of `size()` bytes."""
+    if workspace is None:
+        return _made(size(), torch.uint8, like, stream, returned=False)
+    _on(like.get_device(), "workspace", workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def relattn_paged_evict_workspace_size(B, Hkv, max_keys) -> int:
+    """Workspace bytes relattn_paged_evict needs for tables of max_keys = max_pages * page_size
+    keys a row (host only)."""
+    B, Hkv, max_keys = int(B), int(Hkv), int(max_keys)
+    _in_32_bits(B, Hkv, max_keys)
+    nb = ctypes.c_ulonglong(0)
+    _check(_lib.relattn_paged_evict_workspace_size(B, Hkv, max_keys, ctypes.byref(nb)),
+           "relattn_paged_evict_workspace_size")
+    return int(nb.value)
+
+
+def relattn_paged_evict(kv_len, block_table, k_pages, v_pages, mass, budget, limit=None, sinks=0,
+                        recent=0, free_pages=None, free_head=None, kv_len_out=None,
+                        free_head_out=None, workspace=None, stream=None):
+    """Cuts every request with more than `limit` (default: budget) cached keys back to `budget`, in
+    place: each key/value head keeps its first `sinks`, its last `recent` and the heaviest of the
+    others, closed up in their order (include/relattn.h has the details). Returns (kv_len_out [B],
+    free_head_out [1] or None).
+
+    kv_len: [B] int32; block_table: [B, max_pages] int32; k_pages, v_pages: [num_pages, Hkv,
+    page_size, d]; mass: [num_pages, Hkv, page_size] fp32, the keys' accumulated weights, which move
+    along. free_pages, free_head: the list that relattn_paged_plan takes pages from; the pages that
+    become free go back onto it. kv_len_out may be kv_len, free_head_out may be free_head.
+    """
+    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
+    ms = _mass(dev, mass, N, Hkv, P)
+    B = kv_len.numel()
+    ts, M = _table(dev, block_table, B)
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    limit = budget if limit is None else int(limit)
+    F, pF, pH, pO = 0, None, None, None
+    if (free_pages is None) != (free_head is None):
+        raise ValueError("free_pages and free_head go together")
+    if free_pages is not None:
+        F = free_pages.numel()
+        pF, pH = _ints(dev, "free_pages", free_pages, F), _ints(dev, "free_head", free_head, 1)
+        if free_head_out is None:
+            free_head_out = _made(1, _INT, kv_len, stream)
+        pO = _ints(dev, "free_head_out", free_head_out, 1)
+    elif free_head_out is not None:
+        raise ValueError("free_head_out needs free_pages and free_head")
+    _in_32_bits(N, Hkv, P, d, B, M, F, budget, limit, sinks, recent)
+    kv = _ints(dev, "kv_len", kv_len, B)
+    if kv_len_out is None:
+        kv_len_out = _made(B, _INT, kv_len, stream)
+    workspace = _scratch(workspace, lambda: relattn_paged_evict_workspace_size(B, Hkv, M * P), kv_len, stream)
+    st = _call_on(
+        dev, stream, _lib.relattn_paged_evict, kv, block_table.data_ptr(), ts, M, k_pages.data_ptr(),
+        v_pages.data_ptr(), ps, mass.data_ptr(), ms, N, P, budget, limit, sinks, recent, pF, F, pH, B, Hkv, d,
+        _dtype_code(k_pages), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ints(dev, "kv_len_out", kv_len_out, B), pO)
+    if st:
+        raise RelattnError(st, "relattn_paged_evict")
+    return kv_len_out, free_head_out
 
 
 def relattn_labels(kind, n_q, n_k, clip_k=0, num_buckets=32, max_distance=128,

@@ -669,6 +669,74 @@ relattn_status_t relattn_paged_append(const void *k, const void *v, long long k_
     return from_cuda(relattn::launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+relattn_status_t relattn_paged_evict_workspace_size(int B, int Hkv, long long max_keys,
+                                                    unsigned long long *bytes) {
+    if (!bytes || B < 1 || Hkv < 1 || max_keys < 1) return RELATTN_ERR_INVALID_ARG;
+    if (B > relattn::kPlanMaxSeqs || max_keys > 0x7fffffffLL - 128) return RELATTN_ERR_UNSUPPORTED;
+    if ((long long)B * Hkv > 0x7fffffffLL / ((max_keys + 127) / 128 * 8)) return RELATTN_ERR_UNSUPPORTED;
+    *bytes = relattn::paged_evict_workspace_bytes(B, Hkv, max_keys);
+    return RELATTN_OK;
+}
+
+relattn_status_t relattn_paged_evict(const int *kv_len, const int *block_table, long long table_stride,
+                                     int max_pages, void *k_pages, void *v_pages, long long page_stride,
+                                     float *mass, long long mass_stride, int num_pages, int page_size,
+                                     int budget, int limit, int sinks, int recent, int *free_pages,
+                                     int num_free, const int *free_head, int B, int Hkv, int d, int dtype,
+                                     void *workspace, unsigned long long workspace_bytes, int *kv_len_out,
+                                     int *free_head_out, relattn_stream_t stream) {
+    if (!kv_len || !block_table || !k_pages || !v_pages || !mass || !workspace || !kv_len_out)
+        return RELATTN_ERR_INVALID_ARG;
+    if (k_pages == v_pages || mass == k_pages || mass == v_pages) return RELATTN_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || num_free < 0) return RELATTN_ERR_INVALID_ARG;
+    if (free_pages ? !free_head || !free_head_out : num_free > 0) return RELATTN_ERR_INVALID_ARG;
+    if (budget < 1 || limit < budget || sinks < 0 || recent < 0 || (long long)sinks + recent > budget)
+        return RELATTN_ERR_INVALID_ARG;
+    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
+    if (num_pages > 1 && mass_stride < (long long)Hkv * page_size) return RELATTN_ERR_INVALID_ARG;
+    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
+    if (!aligned(k_pages, es) || !aligned(v_pages, es) || !aligned(workspace, 16)) return RELATTN_ERR_INVALID_ARG;
+    const void *words[] = {kv_len, block_table, mass, free_pages, free_head, kv_len_out, free_head_out};
+    for (const void *p : words)
+        if (p && !aligned(p, 4)) return RELATTN_ERR_INVALID_ARG;
+    if (d > relattn::kEvictMaxDim) return RELATTN_ERR_UNSUPPORTED;
+    unsigned long long need = 0;
+    const relattn_status_t sz = relattn_paged_evict_workspace_size(B, Hkv, (long long)max_pages * page_size, &need);
+    if (sz != RELATTN_OK) return sz;
+    if (workspace_bytes < need) return RELATTN_ERR_INVALID_ARG;
+    relattn::PagedEvictArgs a{};
+    a.kv_len = kv_len;
+    a.kv_len_out = kv_len_out;
+    a.block_table = block_table;
+    a.bt_stride = table_stride;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.budget = budget;
+    a.limit = limit;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.row_bytes = (long long)d * (long long)es;
+    a.page_bytes = (num_pages > 1 ? page_stride : (long long)Hkv * page_size * d) * (long long)es;
+    a.mass = mass;
+    a.mass_stride = num_pages > 1 ? mass_stride : (long long)Hkv * page_size;
+    a.free_pages = free_pages;
+    a.num_free = num_free;
+    a.free_head = free_head;
+    a.free_head_out = free_head_out;
+    a.workspace = workspace;
+    a.wait_limit = g_wait_limit.load();
+    const relattn_status_t st = paged_device(&a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_evict(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 relattn_status_t relattn_paged_workspace_size(int H, int Hkv, int d, unsigned long long *bytes) {
     if (!bytes || H < 1 || Hkv < 1 || H % Hkv != 0 || d < 1) return RELATTN_ERR_INVALID_ARG;
     if (d > 128 || H / Hkv > relattn::kPagedMaxGroup) return RELATTN_ERR_UNSUPPORTED;

@@ -232,6 +232,29 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs &a, cudaStream_t s);
 
+constexpr int kEvictMaxDim = 128;        // elements of a row that eviction moves
+
+struct PagedEvictArgs {
+    const int *kv_len, *block_table;  // [B], [B, max_pages] (bt_stride between rows)
+    int *kv_len_out;                  // may be kv_len
+    long long bt_stride;
+    int B, Hkv, page_size, max_pages, num_pages;
+    int budget, limit, sinks, recent;
+    void *k_pages, *v_pages;          // [num_pages, Hkv, page_size] rows of row_bytes
+    long long page_bytes, row_bytes;
+    float *mass;                      // [num_pages, Hkv, page_size], mass_stride elements between pages
+    long long mass_stride;
+    int *free_pages;                  // may be null: pages are not given back
+    int num_free;
+    const int *free_head;
+    int *free_head_out;               // may be free_head
+    void *workspace;
+    int *err;
+    long long wait_limit;
+};
+unsigned long long paged_evict_workspace_bytes(int B, int Hkv, long long max_keys);
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s);
+
 struct PagedArgs {
     const void *q;                    // [tokens, H, d], q_stride elements between tokens
     long long q_stride;
