@@ -421,6 +421,64 @@ RELATTN_API relattn_status_t relattn_paged_workspace_size(int H, int Hkv, int d,
                                               unsigned long long *bytes);
 
 /*
+ * relattn_paged_fwd_lse — relattn_paged_fwd that also leaves each row's log-sum-exp: lse [tokens, H]
+ * fp32, contiguous, lse = ln sum_j exp(e_j) over the keys that the row sees, -infinity where it sees
+ * none; or NULL. Rows from q_start[B] on are not written.
+ */
+RELATTN_API relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_stride, const void *k_pages,
+                                       const void *v_pages, long long page_stride, int num_pages,
+                                       int page_size, const int *block_table, long long table_stride,
+                                       int max_pages, const int *q_start, const int *kv_len,
+                                       const void *aK, const void *aV, long long table_head_stride,
+                                       int clip_k, int window, int sinks, float scale, int B,
+                                       int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                       void *workspace, unsigned long long workspace_bytes, void *out,
+                                       float *lse, relattn_stream_t stream);
+
+/*
+ * relattn_paged_weights — the attention weight that every cached key gets from the new tokens:
+ *
+ *   mass[page][h'][row] (+)= sum over new tokens i of the request and query heads h of group h' that see
+ *                            key j of exp(e_ij - lse_ih),   page, row: those of position j,
+ *
+ * with e_ij, the positions and what a token sees as in relattn_paged_fwd (the tables of the values play
+ * no part). It follows relattn_paged_fwd_lse in a step; relattn_paged_evict goes by what it gathers.
+ *
+ *   q, q_stride, k_pages, page_stride, num_pages, page_size, block_table, table_stride, max_pages,
+ *   q_start, kv_len, aK, table_head_stride, clip_k, window, sinks, scale, B, tokens, max_new, H, Hkv,
+ *   d, dtype          as in relattn_paged_fwd. The rows may also be only the last tokens of a prompt,
+ *                     whose weights stand for those of what follows.
+ *   lse               [tokens, H] fp32, contiguous.
+ *   mass              [num_pages, Hkv, page_size] fp32, mass_stride elements between pages. Written
+ *                     are the entries of keys that some row of the request sees, no others.
+ *   accumulate        1: keys in front of the new tokens keep what they have and get the sum added, the
+ *                     new tokens' own entries are set; 0: every entry that is written is set.
+ *   workspace         caller-owned device scratch of relattn_paged_weights_workspace_size bytes, 16-byte
+ *                     aligned; calls that may overlap need one each.
+ *
+ * Each entry is summed in one place and in a fixed order, in fp32, so equal calls give equal bits. Entries of
+ * a page that several requests of the call share hold no defined number afterwards. A page number
+ * outside the cache counts nothing and sets the status word to RELATTN_ERR_INVALID_ARG. bf16 with d =
+ * 64 or 128, pages of at least 8 keys and rows that start on 16-byte boundaries runs on the tensor
+ * cores (with at most 16 query rows, max_new times H / Hkv, per key/value head on a kernel for
+ * generated tokens, else up to clip_k = 127), everything else on the SIMT units. Limits and refusals as in
+ * relattn_paged_fwd; tokens = 0 does nothing.
+ */
+RELATTN_API relattn_status_t relattn_paged_weights(const void *q, long long q_stride, const void *k_pages,
+                                       long long page_stride, int num_pages, int page_size,
+                                       const int *block_table, long long table_stride, int max_pages,
+                                       const int *q_start, const int *kv_len, const void *aK,
+                                       long long table_head_stride, int clip_k, int window, int sinks,
+                                       float scale, const float *lse, int accumulate, int B, int tokens,
+                                       int max_new, int H, int Hkv, int d, int dtype, void *workspace,
+                                       unsigned long long workspace_bytes, float *mass,
+                                       long long mass_stride, relattn_stream_t stream);
+
+/* relattn_paged_weights_workspace_size — host only: the workspace bytes relattn_paged_weights needs. */
+RELATTN_API relattn_status_t relattn_paged_weights_workspace_size(int tokens, int H,
+                                                      unsigned long long *bytes);
+
+/*
  * relattn_paged_evict — cuts requests back to their most attended keys, in place. Of every request
  * with more than `limit` cached keys, each key/value head keeps `budget` keys: the first `sinks`,
  * the last `recent`, and of the others the budget - sinks - recent with the largest mass, ties to

@@ -127,6 +127,79 @@ def attend(q, k_pages, v_pages, table, q_start, kv_len, aK, aV, clip_k, window, 
     return z, mass, size
 
 
+def _rows(q_start, kv_len, cap, window, sinks):
+    """(request, query row, position, keys that it sees) of every new token."""
+    for b in range(len(kv_len)):
+        n = int(q_start[b + 1] - q_start[b])
+        kv = min(max(int(kv_len[b]), 0), cap)
+        for i in range(n):
+            pos = kv - n + i
+            j = np.arange(pos + 1) if pos >= 0 else np.zeros(0, dtype=np.int64)
+            if window > 0:
+                j = j[(j > pos - window) | (j < sinks)]
+            yield b, int(q_start[b]) + i, pos, j
+
+
+def _scores(q, k_pages, table, b, t, h, pos, j, aK, clip_k, scale):
+    N, Hkv, P, _ = k_pages.shape
+    hk = h // (q.shape[1] // Hkv)
+    page = table[b, j // P]
+    good = (page >= 0) & (page < N)
+    K = np.where(good[:, None], k_pages[np.where(good, page, 0), hk, j % P], 0.0)
+    A = np.abs(K)
+    if aK is not None:
+        rel = aK[hk if aK.shape[0] > 1 else 0][np.clip(j - pos, -clip_k, clip_k) + clip_k]
+        K, A = K + rel, A + np.abs(rel)
+    return scale * (K @ q[t, h]), abs(scale) * (A @ np.abs(q[t, h]))
+
+
+def log_sum(q, k_pages, table, q_start, kv_len, aK, clip_k, window, sinks, scale):
+    """lse [T, H] (-inf without keys) and the size of the sums behind a row's scores, [T, H]."""
+    T, H, _ = q.shape
+    lse, size = np.full((T, H), -np.inf), np.zeros((T, H))
+    for b, t, pos, j in _rows(q_start, kv_len, table.shape[1] * k_pages.shape[2], window, sinks):
+        for h in range(H if len(j) else 0):
+            e, a = _scores(q, k_pages, table, b, t, h, pos, j, aK, clip_k, scale)
+            lse[t, h] = e.max() + np.log(np.exp(e - e.max()).sum())
+            size[t, h] = a.max()
+    return lse, size
+
+
+def weights(q, k_pages, table, q_start, kv_len, aK, clip_k, window, sinks, scale, lse, mass, accumulate):
+    """Returns (mass, bound): the masses after the new tokens, and how far fp32 arithmetic may be from
+    them. A weight's exponent is the difference of two numbers of at most `size` (a sum of 2 (d + 6)
+    rounded terms) and |lse|, its exponential is within 2 x 2^-22, and a key's sum has as many terms
+    as rows see it."""
+    u = 2.0 ** -24
+    Hkv, P, d = k_pages.shape[1], k_pages.shape[2], q.shape[2]
+    g = q.shape[1] // Hkv
+    mass = mass.copy()
+    bound = np.zeros_like(mass)
+    got, err, new = {}, {}, {}
+    for b, t, pos, j in _rows(q_start, kv_len, table.shape[1] * P, window, sinks):
+        first_new = min(max(int(kv_len[b]), 0), table.shape[1] * P) - int(q_start[b + 1] - q_start[b])
+        for h in range(q.shape[1]):
+            if not len(j):
+                continue
+            e, a = _scores(q, k_pages, table, b, t, h, pos, j, aK, clip_k, scale)
+            w = np.exp(e - lse[t, h])
+            delta = 4.0 * (d + 6) * u * a + 8.0 * u * (a + abs(lse[t, h])) + 2.0 ** -21
+            for x, p, s in zip(j, w, w * delta):
+                at = (b, int(x), h // g)
+                got[at] = got.get(at, 0.0) + p
+                err[at] = err.get(at, 0.0) + s
+                new[at] = x >= first_new
+    rows = int(max(np.diff(q_start), default=0)) * g
+    for (b, j, h), s in got.items():
+        page = table[b, j // P]
+        if not 0 <= page < mass.shape[0]:
+            continue
+        old = mass[page, h, j % P] if accumulate and not new[b, j, h] else 0.0
+        mass[page, h, j % P] = old + s
+        bound[page, h, j % P] = err[b, j, h] + 2.0 * rows * u * s + 2.0 * u * abs(old + s) + 1e-36
+    return mass, bound
+
+
 def tolerance(z, mass, size, keys, d, half_step, weight_step):
     """How far a kernel may be from z, element by element.
 

@@ -79,6 +79,14 @@ _lib.relattn_paged_fwd.argtypes = [_P, _L, _P, _P, _L, _I, _I, _P, _L, _I, _P, _
                                    _I, _I, ctypes.c_float, _I, _I, _I, _I, _I, _I, _I, _P,
                                    ctypes.c_ulonglong, _P, _P]
 _lib.relattn_paged_fwd.restype = _I
+_lib.relattn_paged_fwd_lse.argtypes = _lib.relattn_paged_fwd.argtypes[:-1] + [_P, _P]
+_lib.relattn_paged_fwd_lse.restype = _I
+_lib.relattn_paged_weights.argtypes = [_P, _L, _P, _L, _I, _I, _P, _L, _I, _P, _P, _P, _L, _I, _I, _I,
+                                       ctypes.c_float, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
+                                       ctypes.c_ulonglong, _P, _L, _P]
+_lib.relattn_paged_weights.restype = _I
+_lib.relattn_paged_weights_workspace_size.argtypes = [_I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
+_lib.relattn_paged_weights_workspace_size.restype = _I
 _lib.relattn_paged_workspace_size.argtypes = [_I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
 _lib.relattn_paged_workspace_size.restype = _I
 _lib.relattn_paged_evict.argtypes = [_P, _P, _L, _I, _P, _P, _L, _P, _L, _I, _I, _I, _I, _I, _I, _P, _I, _P,
@@ -112,7 +120,8 @@ EXPORTED = ["relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_decode_fwd",
             "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
             "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
-            "relattn_paged_workspace_size", "relattn_paged_evict", "relattn_paged_evict_workspace_size",
+            "relattn_paged_workspace_size", "relattn_paged_fwd_lse", "relattn_paged_weights",
+            "relattn_paged_weights_workspace_size", "relattn_paged_evict", "relattn_paged_evict_workspace_size",
             "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",
             "relattn_scalar_bias_bwd_workspace_size", "relattn_labeled_bwd",
@@ -803,32 +812,8 @@ def relattn_paged_workspace_size(H, Hkv, d) -> int:
     return int(nb.value)
 
 
-def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None, aV=None,
-                      clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
-                      workspace=None, table_head_stride=None, stream=None):
-    """Attention of the new tokens of every request over its paged cache with relative terms
-    ("Self-Attention with Relative Position Representations" page, section 3.4, eqs. 3-4; causal),
-    grouped heads, a sliding window and first tokens that stay visible.
-
-    q: [tokens, H, d] bf16 or fp32 (any token stride), rows q_start[b] .. q_start[b + 1] - 1 the
-    last tokens of request b; k_pages, v_pages: [num_pages, Hkv, page_size, d] with the new
-    tokens already appended; block_table: [B, max_pages] int32; q_start: [B + 1] int32; kv_len:
-    [B] int32. aK / aV: [Hkv or 1, 2*clip_k+1, d] or None. window: latest keys that stay visible
-    (0: all), sinks: first keys that do. max_new: the most new tokens of one request if known
-    (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
-    or None to make one. Returns out [tokens, H, d].
-    """
-    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
-    _on(dev, "q", q)
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, H, d]")
-    T, H, _ = q.shape
-    dt = _dtype_code(q)
-    qs = _rows(dev, "q", q, T, H, d, dtype)
-    B = kv_len.numel()
-    ts, M = _table(dev, block_table, B)
-    clip_k, window, sinks, max_new = int(clip_k), int(window), int(sinks), int(max_new)
-    _in_32_bits(clip_k, window, sinks, max_new, N, P, T, H, B, M)
+def _edge_tables(dev, aK, aV, Hkv, clip_k, d, dtype, table_head_stride):
+    """aK and aV [Hkv or 1, 2*clip_k+1, d] or None; returns (head stride, address, address)."""
     ths, pK, pV, heads = 0, None, None, 0
     for name, t in (("aK", aK), ("aV", aV)):
         if t is None:
@@ -851,6 +836,37 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
         ths = int(table_head_stride)
         if ths < 0 or (Hkv - 1) * ths + (2 * clip_k + 1) * d > heads * (2 * clip_k + 1) * d:
             raise ValueError("table_head_stride reaches past the tables")
+    return ths, pK, pV
+
+
+def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None, aV=None,
+                      clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
+                      workspace=None, table_head_stride=None, stream=None, lse=None):
+    """Attention of the new tokens of every request over its paged cache with relative terms
+    ("Self-Attention with Relative Position Representations" page, section 3.4, eqs. 3-4; causal),
+    grouped heads, a sliding window and first tokens that stay visible.
+
+    q: [tokens, H, d] bf16 or fp32 (any token stride), rows q_start[b] .. q_start[b + 1] - 1 the
+    last tokens of request b; k_pages, v_pages: [num_pages, Hkv, page_size, d] with the new
+    tokens already appended; block_table: [B, max_pages] int32; q_start: [B + 1] int32; kv_len:
+    [B] int32. aK / aV: [Hkv or 1, 2*clip_k+1, d] or None. window: latest keys that stay visible
+    (0: all), sinks: first keys that do. max_new: the most new tokens of one request if known
+    (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
+    or None to make one. lse: a [tokens, H] fp32 tensor for the rows' log-sum-exp
+    (relattn_paged_fwd_lse), or None. Returns out [tokens, H, d].
+    """
+    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
+    _on(dev, "q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, H, d]")
+    T, H, _ = q.shape
+    dt = _dtype_code(q)
+    qs = _rows(dev, "q", q, T, H, d, dtype)
+    B = kv_len.numel()
+    ts, M = _table(dev, block_table, B)
+    clip_k, window, sinks, max_new = int(clip_k), int(window), int(sinks), int(max_new)
+    _in_32_bits(clip_k, window, sinks, max_new, N, P, T, H, B, M)
+    ths, pK, pV = _edge_tables(dev, aK, aV, Hkv, clip_k, d, dtype, table_head_stride)
     if out is None:
         out = _made((T, H, d), dtype, q, stream)
     elif _rows(dev, "out", out, T, H, d, dtype) != H * d:
@@ -863,15 +879,27 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
         _on(dev, "workspace", workspace)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    st = _call_on(
-        dev, stream, _lib.relattn_paged_fwd, q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(),
-        ps, N, P, block_table.data_ptr(), ts, M, _ints(dev, "q_start", q_start, B + 1),
-        _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, window, sinks, float(scale), B,
-        T, max_new, H, Hkv, d, dt, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), out.data_ptr())
+    args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, P, block_table.data_ptr(), ts, M,
+            _ints(dev, "q_start", q_start, B + 1), _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, window,
+            sinks, float(scale), B, T, max_new, H, Hkv, d, dt, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), out.data_ptr())
+    if lse is None:
+        st = _call_on(dev, stream, _lib.relattn_paged_fwd, *args)
+    else:
+        st = _call_on(dev, stream, _lib.relattn_paged_fwd_lse, *args, _lse(dev, lse, T, H))
     if st:
         raise RelattnError(st, "relattn_paged_fwd")
     return out
+
+
+def _lse(dev, t, T, H):
+    """t is [tokens, H] contiguous fp32; returns its address."""
+    _on(dev, "lse", t)
+    if t.dtype is not torch.float32:
+        raise TypeError("lse must be torch.float32, got %s" % t.dtype)
+    if t.shape != (T, H) or not t.is_contiguous():
+        raise ValueError("lse must be contiguous and have shape %s, got %s" % ((T, H), tuple(t.shape)))
+    return t.data_ptr()
 
 
 def _mass(dev, t, N, Hkv, P):
@@ -899,6 +927,60 @@ def _scratch(workspace, size, like, stream):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
+
+
+def relattn_paged_fwd_lse(q, k_pages, v_pages, block_table, q_start, kv_len, **kw):
+    """relattn_paged_fwd (which takes the same arguments) that returns (out, lse [tokens, H] fp32)."""
+    if kw.get("lse") is None:
+        _on(_device_of("k_pages", k_pages), "q", q)
+        kw["lse"] = _made(tuple(q.shape[:2]), torch.float32, q, kw.get("stream"))
+    return relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, **kw), kw["lse"]
+
+
+def relattn_paged_weights_workspace_size(tokens, H) -> int:
+    """Workspace bytes relattn_paged_weights needs (host only)."""
+    tokens, H = int(tokens), int(H)
+    _in_32_bits(tokens, H)
+    nb = ctypes.c_ulonglong(0)
+    _check(_lib.relattn_paged_weights_workspace_size(tokens, H, ctypes.byref(nb)),
+           "relattn_paged_weights_workspace_size")
+    return int(nb.value)
+
+
+def relattn_paged_weights(q, k_pages, block_table, q_start, kv_len, lse, mass, aK=None, clip_k=0,
+                          window=0, sinks=0, scale=None, accumulate=True, max_new=0, workspace=None,
+                          table_head_stride=None, stream=None):
+    """The attention weight that every cached key gets from the new tokens, summed over them and over
+    the query heads of its group, added to mass (accumulate) or put in its place; in either case the new
+    tokens' own entries are set. In place; returns mass.
+
+    lse: [tokens, H] fp32, what relattn_paged_fwd has left for the same rows. mass: [num_pages, Hkv,
+    page_size] fp32. The other arguments are those of relattn_paged_fwd.
+    """
+    dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, k_pages)
+    _on(dev, "q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, H, d]")
+    T, H, _ = q.shape
+    qs = _rows(dev, "q", q, T, H, d, dtype)
+    ms = _mass(dev, mass, N, Hkv, P)
+    B = kv_len.numel()
+    ts, M = _table(dev, block_table, B)
+    clip_k, window, sinks, max_new = int(clip_k), int(window), int(sinks), int(max_new)
+    _in_32_bits(clip_k, window, sinks, max_new, N, P, T, H, B, M)
+    ths, pK, _ = _edge_tables(dev, aK, None, Hkv, clip_k, d, dtype, table_head_stride)
+    if scale is None:
+        scale = d ** -0.5
+    workspace = _scratch(workspace, lambda: relattn_paged_weights_workspace_size(T, H), q, stream)
+    st = _call_on(
+        dev, stream, _lib.relattn_paged_weights, q.data_ptr(), qs, k_pages.data_ptr(), ps, N, P,
+        block_table.data_ptr(), ts, M, _ints(dev, "q_start", q_start, B + 1), _ints(dev, "kv_len", kv_len, B),
+        pK, ths, clip_k, window, sinks, float(scale), _lse(dev, lse, T, H), 1 if accumulate else 0, B, T,
+        max_new, H, Hkv, d, _dtype_code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        mass.data_ptr(), ms)
+    if st:
+        raise RelattnError(st, "relattn_paged_weights")
+    return mass
 
 
 def relattn_paged_evict_workspace_size(B, Hkv, max_keys) -> int:

@@ -669,6 +669,85 @@ relattn_status_t relattn_paged_append(const void *k, const void *v, long long k_
     return from_cuda(relattn::launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+relattn_status_t relattn_paged_weights_workspace_size(int tokens, int H, unsigned long long *bytes) {
+    if (!bytes || tokens < 0 || H < 1 || (long long)tokens * H > (1LL << 31) - 1) return RELATTN_ERR_INVALID_ARG;
+    *bytes = relattn::paged_weights_workspace_bytes(tokens, H);
+    return RELATTN_OK;
+}
+
+relattn_status_t relattn_paged_weights(const void *q, long long q_stride, const void *k_pages,
+                                       long long page_stride, int num_pages, int page_size,
+                                       const int *block_table, long long table_stride, int max_pages,
+                                       const int *q_start, const int *kv_len, const void *aK,
+                                       long long table_head_stride, int clip_k, int window, int sinks,
+                                       float scale, const float *lse, int accumulate, int B, int tokens,
+                                       int max_new, int H, int Hkv, int d, int dtype, void *workspace,
+                                       unsigned long long workspace_bytes, float *mass,
+                                       long long mass_stride, relattn_stream_t stream) {
+    if (!k_pages || !block_table || !q_start || !kv_len || !mass) return RELATTN_ERR_INVALID_ARG;
+    if (tokens < 0 || B < 1 || max_new < 0 || max_pages < 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!q || !lse || !workspace)) return RELATTN_ERR_INVALID_ARG;
+    if (mass == k_pages || mass == q || mass == lse || mass == aK) return RELATTN_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return RELATTN_ERR_INVALID_ARG;
+    if (H < 1 || Hkv < 1 || H % Hkv != 0) return RELATTN_ERR_INVALID_ARG;
+    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
+    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
+    if (num_pages > 1 && mass_stride < (long long)Hkv * page_size) return RELATTN_ERR_INVALID_ARG;
+    if ((long long)tokens * H > (1LL << 31) - 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 1 && q_stride < (long long)H * d) return RELATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
+    if (clip_k < 0 || window < 0 || window > (1 << 30) || sinks < 0) return RELATTN_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
+    const void *elems[] = {q, k_pages, aK}, *words[] = {block_table, q_start, kv_len, lse, mass};
+    for (const void *p : elems)
+        if (p && !aligned(p, es)) return RELATTN_ERR_INVALID_ARG;
+    for (const void *p : words)
+        if (p && !aligned(p, 4)) return RELATTN_ERR_INVALID_ARG;
+    if (aK && table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
+    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip ||
+        B > relattn::kPagedMaxSeqs)
+        return RELATTN_ERR_UNSUPPORTED;
+    if (tokens == 0) return RELATTN_OK;
+    if (!aligned(workspace, 16) || workspace_bytes < relattn::paged_weights_workspace_bytes(tokens, H))
+        return RELATTN_ERR_INVALID_ARG;
+    relattn::PagedWeightsArgs w{};
+    relattn::PagedArgs &a = w.a;
+    a.q = q;
+    a.q_stride = tokens > 1 ? q_stride : (long long)H * d;
+    a.k_pages = a.v_pages = k_pages;
+    a.page_stride = num_pages > 1 ? page_stride : (long long)Hkv * page_size * d;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.bt_stride = table_stride;
+    a.max_pages = max_pages;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.aK = aK;
+    a.ths = aK ? table_head_stride : 0;
+    a.clip_k = aK ? clip_k : 0;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.B = B;
+    a.tokens = tokens;
+    a.max_new = max_new;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bf16 = dtype == RELATTN_BF16 ? 1 : 0;
+    a.wait_limit = g_wait_limit.load();
+    a.withhold = g_withhold_q.load();
+    w.lse = lse;
+    w.accumulate = accumulate;
+    w.mass = mass;
+    w.mass_stride = num_pages > 1 ? mass_stride : (long long)Hkv * page_size;
+    w.workspace = workspace;
+    const relattn_status_t st = paged_device(&a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_weights(w, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 relattn_status_t relattn_paged_evict_workspace_size(int B, int Hkv, long long max_keys,
                                                     unsigned long long *bytes) {
     if (!bytes || B < 1 || Hkv < 1 || max_keys < 1) return RELATTN_ERR_INVALID_ARG;
@@ -753,6 +832,21 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
                                    int tokens, int max_new, int H, int Hkv, int d, int dtype,
                                    void *workspace, unsigned long long workspace_bytes, void *out,
                                    relattn_stream_t stream) {
+    return relattn_paged_fwd_lse(q, q_stride, k_pages, v_pages, page_stride, num_pages, page_size, block_table,
+                                 table_stride, max_pages, q_start, kv_len, aK, aV, table_head_stride, clip_k,
+                                 window, sinks, scale, B, tokens, max_new, H, Hkv, d, dtype, workspace,
+                                 workspace_bytes, out, nullptr, stream);
+}
+
+relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_stride, const void *k_pages,
+                                       const void *v_pages, long long page_stride, int num_pages,
+                                       int page_size, const int *block_table, long long table_stride,
+                                       int max_pages, const int *q_start, const int *kv_len,
+                                       const void *aK, const void *aV, long long table_head_stride,
+                                       int clip_k, int window, int sinks, float scale, int B,
+                                       int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                       void *workspace, unsigned long long workspace_bytes, void *out,
+                                       float *lse, relattn_stream_t stream) {
     if (!k_pages || !v_pages || !block_table || !q_start || !kv_len) return RELATTN_ERR_INVALID_ARG;
     if (tokens < 0 || B < 1 || max_new < 0 || max_pages < 1) return RELATTN_ERR_INVALID_ARG;
     if (tokens > 0 && (!q || !out || !workspace)) return RELATTN_ERR_INVALID_ARG;
@@ -768,7 +862,9 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
     const void *elems[] = {q, k_pages, v_pages, aK, aV, out};
     for (const void *p : elems)
         if (p && !aligned(p, es)) return RELATTN_ERR_INVALID_ARG;
-    if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4)) return RELATTN_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
+        return RELATTN_ERR_INVALID_ARG;
+    if (lse && (lse == out || lse == q || lse == k_pages || lse == v_pages)) return RELATTN_ERR_INVALID_ARG;
     if (aK || aV) {
         if (table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
         if (out && (out == aK || out == aV)) return RELATTN_ERR_INVALID_ARG;
@@ -807,6 +903,7 @@ relattn_status_t relattn_paged_fwd(const void *q, long long q_stride, const void
     a.d = d;
     a.bf16 = dtype == RELATTN_BF16 ? 1 : 0;
     a.out = out;
+    a.lse = lse;
     a.workspace = workspace;
     a.wait_limit = g_wait_limit.load();
     a.withhold = g_withhold_q.load();

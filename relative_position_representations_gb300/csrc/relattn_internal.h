@@ -272,11 +272,23 @@ struct PagedArgs {
     int B, tokens, max_new, H, Hkv, d;
     int bf16;
     void *out;                        // [tokens, H, d]
+    float *lse;                       // [tokens, H] or null: the rows' log-sum-exp
     void *workspace;                  // at least paged_workspace_bytes
     int *err;
     long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)
     int withhold;                     // test hook: announce the first queries, do not load them
 };
+struct PagedWeightsArgs {
+    PagedArgs a;                      // (v_pages, out, lse and workspace unused)
+    const float *lse;                 // [tokens, H]
+    int accumulate;
+    float *mass;                      // [num_pages, Hkv, page_size], mass_stride elements between pages
+    long long mass_stride;
+    void *workspace;
+};
+unsigned long long paged_weights_workspace_bytes(int tokens, int H);
+cudaError_t launch_paged_weights(const PagedWeightsArgs &a, cudaStream_t s);
+
 unsigned long long paged_workspace_bytes(int d);
 // every type, head dimension <= 128 and page size; fp32 arithmetic on the SIMT units
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s);

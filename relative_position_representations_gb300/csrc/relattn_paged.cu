@@ -85,6 +85,7 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->g = a.H / a.Hkv;
     p->d = a.d;
     p->out = a.out;
+    p->lse = a.lse;
     p->desc = static_cast<Desc *>(a.workspace);
     p->part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + desc_bytes());
     p->err = a.err;
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kMergeThreads, V == 8 ? 4 : 3)
                 }
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (p.lse && col == 0) p.lse[(long long)(d.row0 + tok) * p.H + d.kvh * p.g + hh] = row_lse(m, l);
             alignas(16) T z[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) z[e] = from_f<T>(acc[e] * inv);
@@ -511,8 +513,9 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
                 if (whole) {
                     const float inv = l[u] > 0.f ? 1.f / l[u] : 0.f;
                     const int tok = rr / p.g, hh = rr - tok * p.g;
-                    T *out = static_cast<T *>(p.out) +
-                             ((long long)(g.s.q0 + g.it.i0 + tok) * p.H + g.kvh * p.g + hh) * d;
+                    const long long at = (long long)(g.s.q0 + g.it.i0 + tok) * p.H + g.kvh * p.g + hh;
+                    T *out = static_cast<T *>(p.out) + at * d;
+                    if (p.lse && lane == 0) p.lse[at] = row_lse(m[u], l[u]);
 #pragma unroll
                     for (int i = 0; i < N4; ++i)
                         if (N4 * lane + i < d) out[N4 * lane + i] = from_f<T>(o[u][i] * inv);

@@ -59,6 +59,7 @@ struct Params {
     int likely_rows;                         // rows of an item at most, going by max_new
     int rec_rows;                            // rows of a record
     void *out;
+    float *lse;                              // [tokens][H] or null
     Desc *desc;                              // [gridDim.x]
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
     int *err;
@@ -394,6 +395,11 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
 
 __device__ __forceinline__ float *record(const Params &p, int c, int which) {
     return p.part + ((long long)c * 2 + which) * p.rec_rows * (p.d + 2);
+}
+
+// log-sum-exp of a row from its maximum (log2 domain) and sum
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // one status for a page entry outside the cache: its keys and values count as zeros

@@ -557,8 +557,9 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
             if (whole) {
                 const float inv = ls > 0.f ? 1.f / ls : 0.f;
                 const int tok = row / p.g, hh = row - tok * p.g;
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                     ((long long)(g.row0 + tok) * p.H + g.kvh * p.g + hh) * D + 4 * ch;
+                const long long at = (long long)(g.row0 + tok) * p.H + g.kvh * p.g + hh;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at * D + 4 * ch;
+                if (p.lse && ch == 0) p.lse[at] = row_lse(M, ls);
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(ptx::pack_bf16x2(z.x * inv, z.y * inv),
                                                              ptx::pack_bf16x2(z.z * inv, z.w * inv));
             } else {

@@ -628,6 +628,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         if (g.t1 == g.t0 || (!split && !act)) {   // no key in this piece for any row of the slot
             if (valid && !(split && slot == 1)) {
                 if (whole) {
+                    if (p.lse) p.lse[(orow - static_cast<__nv_bfloat16 *>(p.out)) / D] = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(orow)[c] = make_uint4(0, 0, 0, 0);
                 } else {
@@ -860,9 +861,13 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
             if (two && !(ok = wait_o(1))) break;
             if (mine) {
                 const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-                if (valid && !whole && slot == (split ? 0 : slot)) {
-                    rec[rrow] = M;
-                    rec[p.rec_rows + rrow] = l;
+                if (valid && slot == (split ? 0 : slot)) {
+                    if (!whole) {
+                        rec[rrow] = M;
+                        rec[p.rec_rows + rrow] = l;
+                    } else if (p.lse) {
+                        p.lse[(orow - static_cast<__nv_bfloat16 *>(p.out)) / D] = row_lse(M, l);
+                    }
                 }
                 const uint32_t oA = lane_base + T::O(split ? 0 : slot), oB = lane_base + T::O(1);
                 // Rows leave through the slot's R rows (all of its warps are past them): a thread holds a row, but a store of 16
