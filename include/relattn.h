@@ -436,6 +436,42 @@ RELATTN_API relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_st
                                        float *lse, relattn_stream_t stream);
 
 /*
+ * relattn_paged_shared_fwd — relattn_paged_fwd for requests that share long prefixes (one instruction
+ * text, one document, samples of one prompt): the same results, with a group's shared keys read and
+ * multiplied once for all of its rows.
+ *
+ *   group_start       [groups + 1] int32, ascending: requests group_start[g] .. group_start[g + 1] - 1
+ *                     are group g; requests in front of the first and behind the last share nothing.
+ *   prefix_len        [groups] int32: the rows of the block table of a group's requests name the same
+ *                     pages (or pages of the same contents) for the keys below prefix_len[g]. The new
+ *                     tokens may lie within them. Less than 128 keys, or one request with new tokens, is
+ *                     no prefix worth sharing and is treated as none.
+ *   lse               [tokens, H] fp32 or NULL, as in relattn_paged_fwd_lse.
+ *   workspace         of relattn_paged_shared_workspace_size bytes.
+ *   All other arguments, limits and refusals as in relattn_paged_fwd.
+ *
+ * Which of a group's rows a shared key is read through is not defined, nor how much of the prefix is shared: up
+ * to a multiple of 128, and up to clip_k - 1 keys less where new tokens follow closely. With window > 0 the call
+ * does what relattn_paged_fwd does. group_start and prefix_len are device memory like the
+ * lengths, so a captured step can be replayed; other numbers than allowed stay within the arrays, but then any
+ * row may hold anything. groups <= 2^24, else RELATTN_ERR_UNSUPPORTED.
+ */
+RELATTN_API relattn_status_t relattn_paged_shared_fwd(const void *q, long long q_stride, const void *k_pages,
+                                          const void *v_pages, long long page_stride, int num_pages,
+                                          int page_size, const int *block_table, long long table_stride,
+                                          int max_pages, const int *q_start, const int *kv_len,
+                                          const int *group_start, const int *prefix_len, int groups,
+                                          const void *aK, const void *aV, long long table_head_stride,
+                                          int clip_k, int window, int sinks, float scale, int B,
+                                          int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                          void *workspace, unsigned long long workspace_bytes, void *out,
+                                          float *lse, relattn_stream_t stream);
+
+/* relattn_paged_shared_workspace_size — host only: the workspace bytes relattn_paged_shared_fwd needs. */
+RELATTN_API relattn_status_t relattn_paged_shared_workspace_size(int tokens, int H, int Hkv, int d,
+                                                     unsigned long long *bytes);
+
+/*
  * relattn_paged_weights — the attention weight that every cached key gets from the new tokens:
  *
  *   mass[page][h'][row] (+)= sum over new tokens i of the request and query heads h of group h' that see

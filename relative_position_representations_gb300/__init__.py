@@ -15,7 +15,8 @@ _BINDING = ("relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_decode_fwd",
             "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
             "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
-            "relattn_paged_workspace_size", "relattn_paged_fwd_lse", "relattn_paged_weights",
+            "relattn_paged_workspace_size", "relattn_paged_fwd_lse", "relattn_paged_shared_fwd",
+            "relattn_paged_shared_workspace_size", "relattn_paged_weights",
             "relattn_paged_weights_workspace_size", "relattn_paged_evict", "relattn_paged_evict_workspace_size",
             "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",

@@ -81,6 +81,11 @@ _lib.relattn_paged_fwd.argtypes = [_P, _L, _P, _P, _L, _I, _I, _P, _L, _I, _P, _
 _lib.relattn_paged_fwd.restype = _I
 _lib.relattn_paged_fwd_lse.argtypes = _lib.relattn_paged_fwd.argtypes[:-1] + [_P, _P]
 _lib.relattn_paged_fwd_lse.restype = _I
+_lib.relattn_paged_shared_fwd.argtypes = _lib.relattn_paged_fwd.argtypes[:12] + [_P, _P, _I] + \
+    _lib.relattn_paged_fwd.argtypes[12:-1] + [_P, _P]
+_lib.relattn_paged_shared_fwd.restype = _I
+_lib.relattn_paged_shared_workspace_size.argtypes = [_I, _I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]
+_lib.relattn_paged_shared_workspace_size.restype = _I
 _lib.relattn_paged_weights.argtypes = [_P, _L, _P, _L, _I, _I, _P, _L, _I, _P, _P, _P, _L, _I, _I, _I,
                                        ctypes.c_float, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
                                        ctypes.c_ulonglong, _P, _L, _P]
@@ -120,7 +125,8 @@ EXPORTED = ["relattn_fwd", "relattn_t5bias_fwd", "relattn_alibi_fwd",
             "relattn_decode_fwd",
             "relattn_decode_fwd_noalloc", "relattn_decode_workspace_size",
             "relattn_paged_plan", "relattn_paged_append", "relattn_paged_fwd",
-            "relattn_paged_workspace_size", "relattn_paged_fwd_lse", "relattn_paged_weights",
+            "relattn_paged_workspace_size", "relattn_paged_fwd_lse", "relattn_paged_shared_fwd",
+            "relattn_paged_shared_workspace_size", "relattn_paged_weights",
             "relattn_paged_weights_workspace_size", "relattn_paged_evict", "relattn_paged_evict_workspace_size",
             "relattn_bwd",
             "relattn_bwd_workspace_size", "relattn_scalar_bias_bwd",
@@ -839,22 +845,9 @@ def _edge_tables(dev, aK, aV, Hkv, clip_k, d, dtype, table_head_stride):
     return ths, pK, pV
 
 
-def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None, aV=None,
-                      clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
-                      workspace=None, table_head_stride=None, stream=None, lse=None):
-    """Attention of the new tokens of every request over its paged cache with relative terms
-    ("Self-Attention with Relative Position Representations" page, section 3.4, eqs. 3-4; causal),
-    grouped heads, a sliding window and first tokens that stay visible.
-
-    q: [tokens, H, d] bf16 or fp32 (any token stride), rows q_start[b] .. q_start[b + 1] - 1 the
-    last tokens of request b; k_pages, v_pages: [num_pages, Hkv, page_size, d] with the new
-    tokens already appended; block_table: [B, max_pages] int32; q_start: [B + 1] int32; kv_len:
-    [B] int32. aK / aV: [Hkv or 1, 2*clip_k+1, d] or None. window: latest keys that stay visible
-    (0: all), sinks: first keys that do. max_new: the most new tokens of one request if known
-    (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
-    or None to make one. lse: a [tokens, H] fp32 tensor for the rows' log-sum-exp
-    (relattn_paged_fwd_lse), or None. Returns out [tokens, H, d].
-    """
+def _paged_fwd(where, groups, q, k_pages, v_pages, block_table, q_start, kv_len, aK, aV, clip_k, window, sinks,
+               scale, max_new, out, workspace, table_head_stride, stream, lse):
+    """relattn_paged_fwd and relattn_paged_shared_fwd (groups: (group_start, prefix_len), else None)."""
     dev, (N, Hkv, P, d), dtype, ps = _pages(k_pages, v_pages)
     _on(dev, "q", q)
     if q.dim() != 3:
@@ -873,23 +866,48 @@ def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None
         raise ValueError("out must be contiguous")
     if scale is None:
         scale = d ** -0.5
-    if workspace is None:
-        workspace = _made(relattn_paged_workspace_size(H, Hkv, d), torch.uint8, q, stream, returned=False)
+    if groups is None:
+        size = lambda: relattn_paged_workspace_size(H, Hkv, d)
     else:
-        _on(dev, "workspace", workspace)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    args = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, P, block_table.data_ptr(), ts, M,
-            _ints(dev, "q_start", q_start, B + 1), _ints(dev, "kv_len", kv_len, B), pK, pV, ths, clip_k, window,
-            sinks, float(scale), B, T, max_new, H, Hkv, d, dt, workspace.data_ptr(),
+        size = lambda: relattn_paged_shared_workspace_size(T, H, Hkv, d)
+    workspace = _scratch(workspace, size, q, stream)
+    pL = None if lse is None else _lse(dev, lse, T, H)
+    cache = (q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), ps, N, P, block_table.data_ptr(), ts, M,
+             _ints(dev, "q_start", q_start, B + 1), _ints(dev, "kv_len", kv_len, B))
+    rest = (pK, pV, ths, clip_k, window, sinks, float(scale), B, T, max_new, H, Hkv, d, dt, workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), out.data_ptr())
-    if lse is None:
-        st = _call_on(dev, stream, _lib.relattn_paged_fwd, *args)
+    if groups is not None:
+        G = groups[1].numel()
+        _in_32_bits(G)
+        st = _call_on(dev, stream, _lib.relattn_paged_shared_fwd, *cache, _ints(dev, "group_start", groups[0], G + 1),
+                      _ints(dev, "prefix_len", groups[1], G), G, *rest, pL)
+    elif lse is not None:
+        st = _call_on(dev, stream, _lib.relattn_paged_fwd_lse, *cache, *rest, pL)
     else:
-        st = _call_on(dev, stream, _lib.relattn_paged_fwd_lse, *args, _lse(dev, lse, T, H))
+        st = _call_on(dev, stream, _lib.relattn_paged_fwd, *cache, *rest)
     if st:
-        raise RelattnError(st, "relattn_paged_fwd")
+        raise RelattnError(st, where)
     return out
+
+
+def relattn_paged_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, aK=None, aV=None,
+                      clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
+                      workspace=None, table_head_stride=None, stream=None, lse=None):
+    """Attention of the new tokens of every request over its paged cache with relative terms
+    ("Self-Attention with Relative Position Representations" page, section 3.4, eqs. 3-4; causal),
+    grouped heads, a sliding window and first tokens that stay visible.
+
+    q: [tokens, H, d] bf16 or fp32 (any token stride), rows q_start[b] .. q_start[b + 1] - 1 the
+    last tokens of request b; k_pages, v_pages: [num_pages, Hkv, page_size, d] with the new
+    tokens already appended; block_table: [B, max_pages] int32; q_start: [B + 1] int32; kv_len:
+    [B] int32. aK / aV: [Hkv or 1, 2*clip_k+1, d] or None. window: latest keys that stay visible
+    (0: all), sinks: first keys that do. max_new: the most new tokens of one request if known
+    (any value is right). workspace: a CUDA tensor of at least relattn_paged_workspace_size bytes,
+    or None to make one. lse: a [tokens, H] fp32 tensor for the rows' log-sum-exp
+    (relattn_paged_fwd_lse), or None. Returns out [tokens, H, d].
+    """
+    return _paged_fwd("relattn_paged_fwd", None, q, k_pages, v_pages, block_table, q_start, kv_len, aK, aV, clip_k,
+                      window, sinks, scale, max_new, out, workspace, table_head_stride, stream, lse)
 
 
 def _lse(dev, t, T, H):
@@ -927,6 +945,32 @@ def _scratch(workspace, size, like, stream):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
+
+
+def relattn_paged_shared_workspace_size(tokens, H, Hkv, d) -> int:
+    """Workspace bytes relattn_paged_shared_fwd needs (host only)."""
+    tokens, H, Hkv, d = int(tokens), int(H), int(Hkv), int(d)
+    _in_32_bits(tokens, H, Hkv, d)
+    nb = ctypes.c_ulonglong(0)
+    _check(_lib.relattn_paged_shared_workspace_size(tokens, H, Hkv, d, ctypes.byref(nb)),
+           "relattn_paged_shared_workspace_size")
+    return int(nb.value)
+
+
+def relattn_paged_shared_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, group_start, prefix_len, aK=None,
+                             aV=None, clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
+                             workspace=None, table_head_stride=None, stream=None, lse=None):
+    """relattn_paged_fwd for requests that share long prefixes: the same results, with the shared keys of a
+    group read and multiplied once for all of its rows.
+
+    group_start: [groups + 1] int32, ascending: requests group_start[g] .. group_start[g + 1] - 1 are group g
+    (the others share nothing). prefix_len: [groups] int32: the table rows of a group name the same pages
+    for the keys below it. workspace: at least relattn_paged_shared_workspace_size bytes, or None. The
+    other arguments are those of relattn_paged_fwd.
+    """
+    return _paged_fwd("relattn_paged_shared_fwd", (group_start, prefix_len), q, k_pages, v_pages, block_table, q_start,
+                      kv_len, aK, aV, clip_k, window, sinks, scale, max_new, out, workspace, table_head_stride,
+                      stream, lse)
 
 
 def relattn_paged_fwd_lse(q, k_pages, v_pages, block_table, q_start, kv_len, **kw):

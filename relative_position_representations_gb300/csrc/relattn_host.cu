@@ -184,6 +184,73 @@ bool page_shape_ok(int num_pages, int Hkv, int page_size, int d, long long page_
     return num_pages == 1 || page_stride / d >= (long long)Hkv * page_size;
 }
 
+// the arguments that relattn_paged_fwd's calls share, checked and taken over (all but the workspace's size)
+relattn_status_t paged_args(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
+                            long long page_stride, int num_pages, int page_size, const int *block_table,
+                            long long table_stride, int max_pages, const int *q_start, const int *kv_len,
+                            const void *aK, const void *aV, long long table_head_stride, int clip_k, int window,
+                            int sinks, float scale, int B, int tokens, int max_new, int H, int Hkv, int d,
+                            int dtype, void *workspace, void *out, float *lse, relattn::PagedArgs &a) {
+    if (!k_pages || !v_pages || !block_table || !q_start || !kv_len) return RELATTN_ERR_INVALID_ARG;
+    if (tokens < 0 || B < 1 || max_new < 0 || max_pages < 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 0 && (!q || !out || !workspace)) return RELATTN_ERR_INVALID_ARG;
+    if (out && (out == q || out == k_pages || out == v_pages)) return RELATTN_ERR_INVALID_ARG;
+    if (H < 1 || Hkv < 1 || H % Hkv != 0) return RELATTN_ERR_INVALID_ARG;
+    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
+    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
+    if ((long long)tokens * H > (1LL << 31) - 1) return RELATTN_ERR_INVALID_ARG;
+    if (tokens > 1 && q_stride < (long long)H * d) return RELATTN_ERR_INVALID_ARG;
+    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
+    if (clip_k < 0 || window < 0 || window > (1 << 30) || sinks < 0) return RELATTN_ERR_INVALID_ARG;
+    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
+    const void *elems[] = {q, k_pages, v_pages, aK, aV, out};
+    for (const void *p : elems)
+        if (p && !aligned(p, es)) return RELATTN_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
+        return RELATTN_ERR_INVALID_ARG;
+    if (lse && (lse == out || lse == q || lse == k_pages || lse == v_pages)) return RELATTN_ERR_INVALID_ARG;
+    if (aK || aV) {
+        if (table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
+        if (out && (out == aK || out == aV)) return RELATTN_ERR_INVALID_ARG;
+    }
+    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip ||
+        B > relattn::kPagedMaxSeqs)
+        return RELATTN_ERR_UNSUPPORTED;
+    if (tokens > 0 && !aligned(workspace, 16)) return RELATTN_ERR_INVALID_ARG;
+    a.q = q;
+    a.q_stride = tokens > 1 ? q_stride : (long long)H * d;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = num_pages > 1 ? page_stride : (long long)Hkv * page_size * d;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.block_table = block_table;
+    a.bt_stride = table_stride;
+    a.max_pages = max_pages;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.aK = aK;
+    a.aV = aV;
+    a.ths = table_head_stride;
+    a.clip_k = aK || aV ? clip_k : 0;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.B = B;
+    a.tokens = tokens;
+    a.max_new = max_new;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bf16 = dtype == RELATTN_BF16 ? 1 : 0;
+    a.out = out;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.wait_limit = g_wait_limit.load();
+    a.withhold = g_withhold_q.load();
+    return RELATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -847,78 +914,51 @@ relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_stride, const 
                                        int tokens, int max_new, int H, int Hkv, int d, int dtype,
                                        void *workspace, unsigned long long workspace_bytes, void *out,
                                        float *lse, relattn_stream_t stream) {
-    if (!k_pages || !v_pages || !block_table || !q_start || !kv_len) return RELATTN_ERR_INVALID_ARG;
-    if (tokens < 0 || B < 1 || max_new < 0 || max_pages < 1) return RELATTN_ERR_INVALID_ARG;
-    if (tokens > 0 && (!q || !out || !workspace)) return RELATTN_ERR_INVALID_ARG;
-    if (out && (out == q || out == k_pages || out == v_pages)) return RELATTN_ERR_INVALID_ARG;
-    if (H < 1 || Hkv < 1 || H % Hkv != 0) return RELATTN_ERR_INVALID_ARG;
-    if (dtype != RELATTN_BF16 && dtype != RELATTN_F32) return RELATTN_ERR_INVALID_ARG;
-    if (!page_shape_ok(num_pages, Hkv, page_size, d, page_stride)) return RELATTN_ERR_INVALID_ARG;
-    if ((long long)tokens * H > (1LL << 31) - 1) return RELATTN_ERR_INVALID_ARG;
-    if (tokens > 1 && q_stride < (long long)H * d) return RELATTN_ERR_INVALID_ARG;
-    if (B > 1 && table_stride < max_pages) return RELATTN_ERR_INVALID_ARG;
-    if (clip_k < 0 || window < 0 || window > (1 << 30) || sinks < 0) return RELATTN_ERR_INVALID_ARG;
-    const uintptr_t es = dtype == RELATTN_BF16 ? 2 : 4;
-    const void *elems[] = {q, k_pages, v_pages, aK, aV, out};
-    for (const void *p : elems)
-        if (p && !aligned(p, es)) return RELATTN_ERR_INVALID_ARG;
-    if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || (lse && !aligned(lse, 4)))
-        return RELATTN_ERR_INVALID_ARG;
-    if (lse && (lse == out || lse == q || lse == k_pages || lse == v_pages)) return RELATTN_ERR_INVALID_ARG;
-    if (aK || aV) {
-        if (table_head_stride != 0 && table_head_stride < (2LL * clip_k + 1) * d) return RELATTN_ERR_INVALID_ARG;
-        if (out && (out == aK || out == aV)) return RELATTN_ERR_INVALID_ARG;
-    }
-    if (d > 128 || H / Hkv > relattn::kPagedMaxGroup || clip_k > relattn::kPagedMaxClip ||
-        B > relattn::kPagedMaxSeqs)
-        return RELATTN_ERR_UNSUPPORTED;
-    if (tokens == 0) return RELATTN_OK;
-    if (!aligned(workspace, 16) || workspace_bytes < relattn::paged_workspace_bytes(d))
-        return RELATTN_ERR_INVALID_ARG;
     relattn::PagedArgs a{};
-    a.q = q;
-    a.q_stride = tokens > 1 ? q_stride : (long long)H * d;
-    a.k_pages = k_pages;
-    a.v_pages = v_pages;
-    a.page_stride = num_pages > 1 ? page_stride : (long long)Hkv * page_size * d;
-    a.num_pages = num_pages;
-    a.page_size = page_size;
-    a.block_table = block_table;
-    a.bt_stride = table_stride;
-    a.max_pages = max_pages;
-    a.q_start = q_start;
-    a.kv_len = kv_len;
-    a.aK = aK;
-    a.aV = aV;
-    a.ths = table_head_stride;
-    a.clip_k = aK || aV ? clip_k : 0;
-    a.window = window;
-    a.sinks = sinks;
-    a.scale = scale;
-    a.B = B;
-    a.tokens = tokens;
-    a.max_new = max_new;
-    a.H = H;
-    a.Hkv = Hkv;
-    a.d = d;
-    a.bf16 = dtype == RELATTN_BF16 ? 1 : 0;
-    a.out = out;
-    a.lse = lse;
-    a.workspace = workspace;
-    a.wait_limit = g_wait_limit.load();
-    a.withhold = g_withhold_q.load();
-    const relattn_status_t st = paged_device(&a.err);
+    relattn_status_t st = paged_args(q, q_stride, k_pages, v_pages, page_stride, num_pages, page_size, block_table,
+                                     table_stride, max_pages, q_start, kv_len, aK, aV, table_head_stride, clip_k,
+                                     window, sinks, scale, B, tokens, max_new, H, Hkv, d, dtype, workspace, out, lse, a);
+    if (st != RELATTN_OK || tokens == 0) return st;
+    if (workspace_bytes < relattn::paged_workspace_bytes(d)) return RELATTN_ERR_INVALID_ARG;
+    st = paged_device(&a.err);
     if (st != RELATTN_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (relattn::paged_decode_covers(a)) {
-        const cudaError_t e = relattn::launch_paged_decode(a, s);
-        if (e != cudaErrorNotSupported) return from_cuda(e);
-    }
-    if (relattn::paged_tc_covers(a)) {
-        const cudaError_t e = relattn::launch_paged_tc(a, s);
-        if (e != cudaErrorNotSupported) return from_cuda(e);
-    }
-    return from_cuda(relattn::launch_paged_simt(a, s));
+    return from_cuda(relattn::launch_paged(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+relattn_status_t relattn_paged_shared_workspace_size(int tokens, int H, int Hkv, int d,
+                                                     unsigned long long *bytes) {
+    if (tokens < 0 || (H > 0 && tokens > ((1LL << 31) - 1) / H)) return RELATTN_ERR_INVALID_ARG;
+    const relattn_status_t st = relattn_paged_workspace_size(H, Hkv, d, bytes);
+    if (st == RELATTN_OK) *bytes = relattn::paged_shared_workspace_bytes(tokens, H, d);
+    return st;
+}
+
+relattn_status_t relattn_paged_shared_fwd(const void *q, long long q_stride, const void *k_pages,
+                                          const void *v_pages, long long page_stride, int num_pages,
+                                          int page_size, const int *block_table, long long table_stride,
+                                          int max_pages, const int *q_start, const int *kv_len,
+                                          const int *group_start, const int *prefix_len, int groups,
+                                          const void *aK, const void *aV, long long table_head_stride,
+                                          int clip_k, int window, int sinks, float scale, int B,
+                                          int tokens, int max_new, int H, int Hkv, int d, int dtype,
+                                          void *workspace, unsigned long long workspace_bytes, void *out,
+                                          float *lse, relattn_stream_t stream) {
+    relattn::PagedSharedArgs sa{};
+    if (groups < 0 || (groups > 0 && (!group_start || !prefix_len))) return RELATTN_ERR_INVALID_ARG;
+    if ((group_start && !aligned(group_start, 4)) || (prefix_len && !aligned(prefix_len, 4))) return RELATTN_ERR_INVALID_ARG;
+    relattn_status_t st = paged_args(q, q_stride, k_pages, v_pages, page_stride, num_pages, page_size, block_table,
+                                     table_stride, max_pages, q_start, kv_len, aK, aV, table_head_stride, clip_k,
+                                     window, sinks, scale, B, tokens, max_new, H, Hkv, d, dtype, workspace, out, lse, sa.a);
+    if (st != RELATTN_OK) return st;
+    if (groups > relattn::kPagedMaxSeqs) return RELATTN_ERR_UNSUPPORTED;
+    if (tokens == 0) return RELATTN_OK;
+    if (workspace_bytes < relattn::paged_shared_workspace_bytes(tokens, H, d)) return RELATTN_ERR_INVALID_ARG;
+    sa.group_start = group_start;
+    sa.prefix_len = prefix_len;
+    sa.groups = groups;
+    st = paged_device(&sa.a.err);
+    if (st != RELATTN_OK) return st;
+    return from_cuda(relattn::launch_paged_shared(sa, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 relattn_status_t relattn_labels(int kind, int clip_k, int num_buckets, int max_distance,

@@ -273,11 +273,25 @@ struct PagedArgs {
     int bf16;
     void *out;                        // [tokens, H, d]
     float *lse;                       // [tokens, H] or null: the rows' log-sum-exp
+    // parts of a call with shared prefixes (Params has what they mean); 0 and null otherwise
+    int flat, f32_out;
+    const int *first_key, *row_of;
     void *workspace;                  // at least paged_workspace_bytes
     int *err;
     long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)
     int withhold;                     // test hook: announce the first queries, do not load them
 };
+// attention over prefixes that groups of requests share, then over each request's own keys, joined
+struct PagedSharedArgs {
+    PagedArgs a;
+    const int *group_start, *prefix_len;  // [groups + 1], [groups]
+    int groups;
+};
+unsigned long long paged_shared_workspace_bytes(int tokens, int H, int d);
+cudaError_t launch_paged_shared(const PagedSharedArgs &a, cudaStream_t s);
+// the kernel that covers the call
+cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s);
+
 struct PagedWeightsArgs {
     PagedArgs a;                      // (v_pages, out, lse and workspace unused)
     const float *lse;                 // [tokens, H]

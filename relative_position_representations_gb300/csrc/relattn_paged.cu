@@ -86,6 +86,10 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->d = a.d;
     p->out = a.out;
     p->lse = a.lse;
+    p->step = a.flat ? 0 : 1;
+    p->f32_out = a.f32_out;
+    p->first_key = a.first_key;
+    p->row_of = a.row_of;
     p->desc = static_cast<Desc *>(a.workspace);
     p->part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + desc_bytes());
     p->err = a.err;
@@ -216,7 +220,7 @@ cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
 }
 
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
+    return bf16 && !p.f32_out ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
 }
 
 // ------------------------------------------------------------------ SIMT kernel
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
         const int rows = g.it.cnt * p.g;
         const T *aK = static_cast<const T *>(p.aK) + (long long)g.kvh * p.ths;
         const T *aV = static_cast<const T *>(p.aV) + (long long)g.kvh * p.ths;
-        const int *bt = p.bt + (long long)g.b * p.bt_stride;
+        const int *bt = p.bt + (long long)table_row(p, g.b) * p.bt_stride;
         const int first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
         const int pos_hi = g.it.pos_hi;
         // the piece's runs of 32 keys that some row sees: run q of tile t0 + q / 4
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int r = warp * 4 + u;
-                pos[u] = r < nr ? g.it.pos_lo + (r0 + r) / p.g : -1;
+                pos[u] = r < nr ? g.it.pos_lo + (r0 + r) / p.g * p.step : -1;
                 m[u] = -INFINITY;
                 l[u] = far[u] = 0.f;
 #pragma unroll
@@ -518,7 +522,10 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
                     if (p.lse && lane == 0) p.lse[at] = row_lse(m[u], l[u]);
 #pragma unroll
                     for (int i = 0; i < N4; ++i)
-                        if (N4 * lane + i < d) out[N4 * lane + i] = from_f<T>(o[u][i] * inv);
+                        if (N4 * lane + i < d) {
+                            if (p.f32_out) static_cast<float *>(p.out)[at * d + N4 * lane + i] = o[u][i] * inv;
+                            else out[N4 * lane + i] = from_f<T>(o[u][i] * inv);
+                        }
                 } else {
                     if (lane == 0) {
                         rec[rr] = m[u];
@@ -574,6 +581,18 @@ cudaError_t launch_simt_d(const PagedArgs &a, cudaStream_t s) {
 unsigned long long paged_workspace_bytes(int d) {
     return (unsigned long long)paged::desc_bytes() +
            (unsigned long long)paged::kMaxGrid * 2 * paged::kRecordRows * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s) {
+    if (paged_decode_covers(a)) {
+        const cudaError_t e = launch_paged_decode(a, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    if (paged_tc_covers(a)) {
+        const cudaError_t e = launch_paged_tc(a, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    return launch_paged_simt(a, s);
 }
 
 cudaError_t launch_paged_simt(const PagedArgs &a, cudaStream_t s) {

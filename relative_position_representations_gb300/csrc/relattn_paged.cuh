@@ -60,6 +60,11 @@ struct Params {
     int rec_rows;                            // rows of a record
     void *out;
     float *lse;                              // [tokens][H] or null
+    // a call whose requests share prefixes (relattn_paged_shared.cu) runs in two parts
+    int step;                                // 1; 0: all tokens of a request stand at its last position
+    int f32_out;                             // out is fp32 whatever the inputs are
+    const int *first_key;                    // [tokens] or null: first key of the token's request (whole tiles)
+    const int *row_of;                       // [B] or null: the request's row of the block table
     Desc *desc;                              // [gridDim.x]
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
     int *err;
@@ -73,6 +78,7 @@ inline size_t desc_bytes() { return (size_t)kMaxGrid * sizeof(Desc); }
 struct Seq {
     int q0, n;      // first query row and new tokens
     int pos0;       // position of the first new token (negative: fewer keys than new tokens)
+    int lo;         // first tile of its keys
 };
 
 __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
@@ -81,6 +87,7 @@ __device__ __forceinline__ Seq load_seq(const Params &p, int b) {
     const int q1 = min(max(p.q_start[b + 1], s.q0), p.tokens);
     s.n = q1 - s.q0;
     s.pos0 = min(max(p.kv_len[b], 0), p.cap) - s.n;
+    s.lo = p.first_key && s.n > 0 ? p.first_key[s.q0] / kTile : 0;
     return s;
 }
 
@@ -112,14 +119,14 @@ __device__ __forceinline__ Item make_item(const Params &p, const Seq &s, int qt)
     Item it;
     it.i0 = qt * p.T;
     it.cnt = min(p.T, s.n - it.i0);
-    it.pos_lo = s.pos0 + it.i0;
-    it.pos_hi = it.pos_lo + it.cnt - 1;
+    it.pos_lo = p.step ? s.pos0 + it.i0 : s.pos0 + s.n - 1;
+    it.pos_hi = p.step ? it.pos_lo + it.cnt - 1 : it.pos_lo;
     it.ns = it.lo = it.nt = 0;
     if (it.pos_hi >= 0) {
         const int first = p.window > 0 ? max(0, max(it.pos_lo, 0) - p.window + 1) : 0;  // first key in the window
-        it.lo = first / kTile;
+        it.lo = max(first / kTile, s.lo);
         it.ns = min((min(p.sinks, first) + kTile - 1) / kTile, it.lo);
-        it.nt = it.ns + it.pos_hi / kTile + 1 - it.lo;
+        it.nt = max(it.ns + it.pos_hi / kTile + 1 - it.lo, 0);
     }
     it.wt = it.cnt > p.T1 ? p.wt2 : p.wt;
     it.cost = p.c0 + it.wt * it.nt;
@@ -173,7 +180,7 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
         for (int i = 0; i < kBatch; ++i) {
             const int b = b0 + 32 * i + lane;
             cost[i] = 0;
-            s[i] = Seq{0, 0, 0};
+            s[i] = Seq{0, 0, 0, 0};
             if (b < p.B) s[i] = load_seq(p, b);
         }
 #pragma unroll
@@ -188,6 +195,7 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
                 t.q0 = 0;
                 t.n = __shfl_sync(kAll, s[i].n, src);
                 t.pos0 = __shfl_sync(kAll, s[i].pos0, src);
+                t.lo = __shfl_sync(kAll, s[i].lo, src);
                 const int m = items_of(p, t);
                 I part = 0;
                 for (int q = lane; q < m; q += 32) part += make_item(p, t, q).cost;
@@ -300,7 +308,7 @@ struct Walk {
     long long x, x0, x1;
     Seq s;
     __device__ __forceinline__ Walk(const Params &p, const Range &r)
-        : b(r.b), kvh(r.kvh), qt(r.qt), nq(0), x(r.x), x0(r.x0), x1(r.x1), s{0, 0, 0} {
+        : b(r.b), kvh(r.kvh), qt(r.qt), nq(0), x(r.x), x0(r.x0), x1(r.x1), s{0, 0, 0, 0} {
         if (b < p.B) {
             s = load_seq(p, b);
             nq = items_of(p, s);
@@ -360,9 +368,11 @@ struct Piece {
 static_assert(sizeof(Piece) == 48, "piece");
 constexpr int kPieces = 4;   // announced ahead
 
-__device__ __forceinline__ Piece make_piece(const Segment &g, bool more) {
+__device__ __forceinline__ int table_row(const Params &p, int b) { return p.row_of && b < p.B ? p.row_of[b] : b; }
+
+__device__ __forceinline__ Piece make_piece(const Params &p, const Segment &g, bool more) {
     return Piece{g.s.q0 + g.it.i0, more ? g.it.cnt : 0, g.it.pos_lo, g.it.pos_hi, g.it.ns, g.it.lo,
-                 g.it.nt, g.t0, g.t1, g.kvh, g.b, 0};
+                 g.it.nt, g.t0, g.t1, g.kvh, table_row(p, g.b), 0};
 }
 
 // Leaves the descriptor of the item that goes on behind the range (one thread per CTA calls it,

@@ -157,7 +157,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
         const int i = it & (kPieces - 1);
         if (!(ok = wait(bar(B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u))) break;
         if (lane == 0) {
-            ring[i] = make_piece(g, more);
+            ring[i] = make_piece(p, g, more);
             if (more) {
                 ptx::mbar_expect_tx(bar(B_PIECE_FULL + i), (uint32_t)(p.T * p.g) * D * 2);
 #pragma unroll
@@ -172,7 +172,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
         ++it;
         if (!more) break;
         const int first = p.window > 0 ? max(0, max(g.it.pos_lo, 0) - p.window + 1) : 0;
-        const int *bt = p.bt + (long long)g.b * p.bt_stride;
+        const int *bt = p.bt + (long long)table_row(p, g.b) * p.bt_stride;
         // this lane's page of tile t, looked up one tile ahead
         auto lookup = [&](int t, bool &seen) -> int {
             const int j = g.it.tile(t) * kTile + my_box * box;
@@ -258,7 +258,7 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rr = 8 * n + 2 * c + e;
-                pos[n][e] = pos_lo + (rr < rows ? rr / p.g : 0);
+                pos[n][e] = pos_lo + (rr < rows ? rr / p.g * p.step : 0);
             }
         }
         __syncwarp();
@@ -560,8 +560,12 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
                 const long long at = (long long)(g.row0 + tok) * p.H + g.kvh * p.g + hh;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at * D + 4 * ch;
                 if (p.lse && ch == 0) p.lse[at] = row_lse(M, ls);
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(ptx::pack_bf16x2(z.x * inv, z.y * inv),
-                                                             ptx::pack_bf16x2(z.z * inv, z.w * inv));
+                if (p.f32_out)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + 4 * ch) =
+                        make_float4(z.x * inv, z.y * inv, z.z * inv, z.w * inv);
+                else
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(ptx::pack_bf16x2(z.x * inv, z.y * inv),
+                                                                 ptx::pack_bf16x2(z.z * inv, z.w * inv));
             } else {
                 if (ch == 0) {
                     rec[row] = M;

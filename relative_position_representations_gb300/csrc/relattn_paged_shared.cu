@@ -1,0 +1,229 @@
+// Attention of requests that share prefixes: groups of requests whose first keys lie in the same pages.
+//
+// In two parts, whose softmaxes are joined: over the shared keys, where the rows of all requests of
+// a group go through the same products (so each shared key is read once for a group and meets full tiles of
+// rows), and over each request's own keys. With L the shared part's length, chosen on a tile's border and
+// so that every row of the group stands at least clip_k - 1 behind its last key, all of its keys have
+// the first table row in common:
+//   e_ij = scale q_i . (k_j + aK_0),  sum_j p_ij (v_j + aV_0) = sum_j p_ij v_j + aV_0 sum_j p_ij,
+// so the part needs neither positions nor masks nor tables: it is plain attention, and the two constants
+// enter where the parts are joined. Both parts run on the kernels of relattn_paged_fwd, which leave
+// fp32 outputs and log-sum-exps: the first with a group for a request and all of its tokens at the
+// shared part's end, the second from the shared part's end on.
+#include <cstdint>
+#include <cstring>
+
+#include "relattn_paged.cuh"
+
+namespace relattn {
+namespace paged {
+namespace {
+
+constexpr int kSplitThreads = 1024;
+constexpr int kSplitWarps = kSplitThreads / 32;
+constexpr int kJoinThreads = 256;
+
+struct SplitParams {
+    Params p;                         // q_start, kv_len, B, tokens, cap, clip_k
+    const int *group_start, *prefix_len;
+    int groups, most;                 // entries of the lists below
+    int *first_key;                   // [tokens]: where the own keys of the token's request begin
+    int *q_start, *kv_len, *row_of;   // [most + 1], [most], [most]: the shared parts as requests
+};
+
+// Which groups share what. Entry 2 i is the i-th group that shares keys, entry 2 i + 1 the rows up to the
+// next one (without keys). A warp per group.
+__global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __grid_constant__ SplitParams sp) {
+    __shared__ int on_s[kSplitWarps], end_s;
+    const Params &p = sp.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_wait();
+    grid_release();
+    for (int t = tid; t < p.tokens; t += kSplitThreads) sp.first_key[t] = 0;
+    if (tid == 0) end_s = 0;
+    int done = 0;
+    for (int g0 = 0; g0 < sp.groups; g0 += kSplitWarps) {
+        const int g = g0 + warp;
+        int keys = 0, q0 = 0, q1 = 0, row = 0;
+        if (g < sp.groups) {
+            const int b0 = min(max(sp.group_start[g], 0), p.B), b1 = min(max(sp.group_start[g + 1], b0), p.B);
+            int least = 0x7fffffff, busy = 0, first = p.B;
+            for (int b = b0 + lane; b < b1; b += 32) {
+                const Seq s = load_seq(p, b);
+                if (s.n == 0) continue;
+                least = min(least, s.pos0);
+                first = min(first, b);
+                ++busy;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+                first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+                busy += __shfl_xor_sync(0xffffffffu, busy, o);
+            }
+            if (busy > 1) {
+                keys = max(min(sp.prefix_len[g], least - p.clip_k + 1), 0) / kTile * kTile;
+                q0 = min(max(p.q_start[b0], 0), p.tokens);
+                q1 = min(max(p.q_start[b1], q0), p.tokens);
+                row = first;
+            }
+        }
+        const bool on = keys > 0 && q1 > q0;
+        if (lane == 0) on_s[warp] = on;
+        __syncthreads();
+        const unsigned all = __ballot_sync(0xffffffffu, on_s[lane] != 0);
+        const int i = done + __popc(all & ((1u << warp) - 1));
+        if (on && 2 * i + 1 < sp.most + 1) {
+            for (int t = q0 + lane; t < q1; t += 32) sp.first_key[t] = keys;
+            if (lane == 0) {
+                sp.q_start[2 * i] = q0;
+                sp.q_start[2 * i + 1] = q1;
+                sp.kv_len[2 * i] = keys;
+                sp.row_of[2 * i] = row;
+                if (2 * i + 1 < sp.most) {
+                    sp.kv_len[2 * i + 1] = 0;
+                    sp.row_of[2 * i + 1] = 0;
+                }
+                atomicMax(&end_s, q1);
+            }
+        }
+        done += __popc(all);
+        __syncthreads();
+    }
+    for (int i = 2 * done + tid; i <= sp.most; i += kSplitThreads) {
+        sp.q_start[i] = end_s;
+        if (i < sp.most) sp.kv_len[i] = sp.row_of[i] = 0;
+    }
+}
+
+struct JoinParams {
+    const void *q, *aK, *aV;
+    long long q_stride, ths;
+    int tokens, H, g, d;
+    float scale_log2;
+    const int *first_key;
+    const float *o_a, *o_b, *lse_a, *lse_b;   // shared part, own keys
+    void *out;
+    float *lse;
+};
+
+// A warp per row: z = (w_a (z_a + aV_0) + w_b z_b) / (w_a + w_b), w = 2^(log-sum-exp - their maximum).
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ JoinParams p) {
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    grid_wait();
+    grid_release();
+    if (row >= (long long)p.tokens * p.H) return;
+    const int t = (int)(row / p.H), h = (int)(row - (long long)t * p.H);
+    const long long table = (long long)(h / p.g) * p.ths;
+    const bool shared = p.first_key[t] > 0;
+    float a = -INFINITY, b = p.lse_b[row] * kLog2e;
+    if (shared) {
+        float r = 0.f;
+        if (p.aK) {
+            const T *q = static_cast<const T *>(p.q) + (long long)t * p.q_stride + (long long)h * p.d;
+            const T *k0 = static_cast<const T *>(p.aK) + table;
+            for (int c = lane; c < p.d; c += 32) r = fmaf(to_f(q[c]), to_f(k0[c]), r);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        }
+        a = fmaf(r, p.scale_log2, p.lse_a[row] * kLog2e);
+    }
+    const float m = fmaxf(a, b), mu = m == -INFINITY ? 0.f : m;
+    const float wa = exp2f(a - mu), wb = exp2f(b - mu), l = wa + wb, inv = l > 0.f ? 1.f / l : 0.f;
+    const T *v0 = p.aV ? static_cast<const T *>(p.aV) + table : nullptr;
+    for (int c = lane; c < p.d; c += 32) {
+        float z = wb * p.o_b[row * p.d + c];
+        if (shared) z = fmaf(wa, p.o_a[row * p.d + c] + (v0 ? to_f(v0[c]) : 0.f), z);
+        static_cast<T *>(p.out)[row * p.d + c] = from_f<T>(z * inv);
+    }
+    if (p.lse && lane == 0) p.lse[row] = row_lse(mu, l);
+}
+
+size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }
+
+}  // namespace
+}  // namespace paged
+
+// workspace: that of the parts, their outputs and log-sum-exps, first keys, the shared parts' list
+unsigned long long paged_shared_workspace_bytes(int tokens, int H, int d) {
+    const size_t rows = (size_t)tokens * H;
+    return paged_workspace_bytes(d) + 2 * paged::round16(rows * d * 4) + 2 * paged::round16(rows * 4) +
+           4 * paged::round16(((size_t)tokens + 2) * 4);
+}
+
+cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
+    using namespace paged;
+    const PagedArgs &a = sa.a;
+    // Under a window a token sees little of a prefix; one token shares with nobody. The requests' own rows of
+    // the table hold the prefix too.
+    if (a.window > 0 || sa.groups == 0 || a.tokens < 2) return launch_paged(a, s);
+    const size_t rows = (size_t)a.tokens * a.H, ints = round16(((size_t)a.tokens + 2) * 4);
+    char *w = static_cast<char *>(a.workspace) + paged_workspace_bytes(a.d);
+    auto take = [&](size_t bytes) {
+        char *at = w;
+        w += bytes;
+        return at;
+    };
+    float *o_a = reinterpret_cast<float *>(take(round16(rows * a.d * 4)));
+    float *o_b = reinterpret_cast<float *>(take(round16(rows * a.d * 4)));
+    float *lse_a = reinterpret_cast<float *>(take(round16(rows * 4)));
+    float *lse_b = reinterpret_cast<float *>(take(round16(rows * 4)));
+    SplitParams sp;
+    std::memset(&sp, 0, sizeof(sp));
+    fill_params(a, &sp.p);
+    sp.group_start = sa.group_start;
+    sp.prefix_len = sa.prefix_len;
+    sp.groups = sa.groups;
+    sp.most = 2LL * sa.groups < a.tokens ? 2 * sa.groups : a.tokens;   // (a group that shares has two tokens)
+    sp.first_key = reinterpret_cast<int *>(take(ints));
+    sp.q_start = reinterpret_cast<int *>(take(ints));
+    sp.kv_len = reinterpret_cast<int *>(take(ints));
+    sp.row_of = reinterpret_cast<int *>(take(ints));
+    cudaError_t e = launch_early(shared_split_kernel, dim3(1), kSplitThreads, 0, s, sp);
+    if (e != cudaSuccess) return e;
+    PagedArgs part = a;      // the shared keys
+    part.aK = part.aV = nullptr;
+    part.ths = 0;
+    part.clip_k = 0;
+    part.q_start = sp.q_start;
+    part.kv_len = sp.kv_len;
+    part.row_of = sp.row_of;
+    part.B = sp.most;
+    part.max_new = a.tokens;
+    part.flat = part.f32_out = 1;
+    part.out = o_a;
+    part.lse = lse_a;
+    if ((e = launch_paged(part, s)) != cudaSuccess) return e;
+    part = a;                // each request's own
+    part.first_key = sp.first_key;
+    part.f32_out = 1;
+    part.out = o_b;
+    part.lse = lse_b;
+    if ((e = launch_paged(part, s)) != cudaSuccess) return e;
+    JoinParams j;
+    std::memset(&j, 0, sizeof(j));
+    j.q = a.q;
+    j.aK = a.aK;
+    j.aV = a.aV;
+    j.q_stride = a.q_stride;
+    j.ths = a.ths;
+    j.tokens = a.tokens;
+    j.H = a.H;
+    j.g = a.H / a.Hkv;
+    j.d = a.d;
+    j.scale_log2 = sp.p.scale_log2;
+    j.first_key = sp.first_key;
+    j.o_a = o_a;
+    j.o_b = o_b;
+    j.lse_a = lse_a;
+    j.lse_b = lse_b;
+    j.out = a.out;
+    j.lse = a.lse;
+    const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    return a.bf16 ? launch_early(shared_join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, j)
+                  : launch_early(shared_join_kernel<float>, grid, kJoinThreads, 0, s, j);
+}
+
+}  // namespace relattn

@@ -157,8 +157,8 @@ __device__ __forceinline__ SlotWork slot_work(const TcParams &tp, const Piece &g
     w.split = g.cnt <= tp.TS;
     w.tok0 = w.split ? 0 : slot * tp.TS;
     w.ntok = min(tp.TS, g.cnt - w.tok0);
-    w.pos_lo = g.pos_lo + w.tok0;
-    w.pos_hi = w.pos_lo + w.ntok - 1;
+    w.pos_lo = g.pos_lo + w.tok0 * p.step;
+    w.pos_hi = w.pos_lo + (w.ntok - 1) * p.step;
     w.first = p.window > 0 ? max(0, max(w.pos_lo, 0) - p.window + 1) : 0;
     w.t_last = g.t1 - 1;
     while (w.t_last >= g.t0 && !w.uses(p, g, slot, w.t_last)) --w.t_last;
@@ -300,7 +300,7 @@ __device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, 
         any = any || more;
         const int i = it & (kPieces - 1);
         if (!wait(bars + 8u * (B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u)) break;
-        Piece pc = make_piece(g, more);
+        Piece pc = make_piece(p, g, more);
         if (more && g.t1 > g.t0)   // (here, where nothing waits for it)
             for (int s = 0; s < 2; ++s)
                 if (slot_work(tp, pc, s).t_last >= pc.t0) pc.act |= 1 << s;
@@ -523,7 +523,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     const int quad = uni(warp & 3);
     const int row = quad * 32 + lane;
     const int tok = row / p.g, hh = row - tok * p.g;   // token within the slot, head within the group
-    const int tok_lo = (quad * 32) / p.g, tok_hi = (quad * 32 + 31) / p.g;   // of this warp's rows
+    const int tok_lo = (quad * 32) / p.g * p.step, tok_hi = (quad * 32 + 31) / p.g * p.step;   // of this warp's rows
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t bars = sh.base + tp.off_bar;
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
@@ -617,20 +617,19 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         const int rows = w.ntok * p.g;                  // may be negative: no rows in this slot
         const bool mine = quad * 32 < rows;             // this warp has rows
         const bool valid = row < rows;
-        const int pos = valid ? w.pos_lo + tok : -1;
+        const int pos = valid ? w.pos_lo + tok * p.step : -1;
         const int pmin = uni(w.pos_lo + tok_lo), pmax = uni(min(w.pos_lo + tok_hi, w.pos_hi));
         float *Rrow = reinterpret_cast<float *>(sh.ptr + tp.off_r[split ? 0 : slot]) + row * tp.SR;
         const bool whole = g.whole();
         const int rrow = (split ? 0 : slot * tp.TS * p.g) + row;
         float *rec = whole ? nullptr : record(p, blockIdx.x, g.record());
-        __nv_bfloat16 *orow = static_cast<__nv_bfloat16 *>(p.out) +
-                              ((long long)(g.row0 + w.tok0 + tok) * p.H + g.kvh * p.g + hh) * D;
+        const long long orow = (long long)(g.row0 + w.tok0 + tok) * p.H + g.kvh * p.g + hh;   // of the outputs
         if (g.t1 == g.t0 || (!split && !act)) {   // no key in this piece for any row of the slot
             if (valid && !(split && slot == 1)) {
                 if (whole) {
-                    if (p.lse) p.lse[(orow - static_cast<__nv_bfloat16 *>(p.out)) / D] = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(orow)[c] = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[orow] = -INFINITY;
+                    const int wide = p.f32_out ? D / 4 : D / 8;
+                    for (int c = 0; c < wide; ++c) static_cast<uint4 *>(p.out)[orow * wide + c] = make_uint4(0, 0, 0, 0);
                 } else {
                     rec[rrow] = -INFINITY;
                     rec[p.rec_rows + rrow] = 0.f;
@@ -866,7 +865,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         rec[rrow] = M;
                         rec[p.rec_rows + rrow] = l;
                     } else if (p.lse) {
-                        p.lse[(orow - static_cast<__nv_bfloat16 *>(p.out)) / D] = row_lse(M, l);
+                        p.lse[orow] = row_lse(M, l);
                     }
                 }
                 const uint32_t oA = lane_base + T::O(split ? 0 : slot), oB = lane_base + T::O(1);
@@ -875,9 +874,10 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                 // takes twice the sectors, each half written: 5.5k cycles a tile instead of 2k).
                 const uint32_t stage = sh.base + tp.off_r[slot] + (uint32_t)quad * kOutBytes;
                 const uint32_t st_at = stage + lane * 64, sw = (lane >> 1) & 3;
-                const uint32_t my16 = whole ? (uint32_t)(((long long)tok * p.H + hh) * (D / 8)) : (uint32_t)(rrow * (D / 4));
-                char *out0 = whole ? reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                              ((long long)(g.row0 + w.tok0) * p.H + g.kvh * p.g) * D)
+                const bool half = whole && !p.f32_out;   // rows of bf16
+                const uint32_t my16 = whole ? (uint32_t)(((long long)tok * p.H + hh) * (half ? D / 8 : D / 4)) : (uint32_t)(rrow * (D / 4));
+                char *out0 = whole ? static_cast<char *>(p.out) +
+                                         ((long long)(g.row0 + w.tok0) * p.H + g.kvh * p.g) * (half ? D * 2 : D * 4)
                                    : reinterpret_cast<char *>(rec + 2 * p.rec_rows);
                 // 64 bytes of each row, at byte `off` of the row
                 auto put64 = [&](const uint32_t *v, int off) {
@@ -914,7 +914,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                             put(r, e, __ffma2_rn(pair(r1, e), dup(f1), __fmul2_rn(pair(r, e), dup(f0))));
                     }
                     uint32_t v[32];
-                    if (whole) {
+                    if (half) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float2 o = __fmul2_rn(pair(r, 2 * e), dup(inv));
@@ -923,7 +923,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         put64(v, 2 * c0);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(r[e]);
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(r[e] * inv);
                         put64(v, 4 * c0);
                         put64(v + 16, 4 * c0 + 64);
                     }

@@ -385,7 +385,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
         const int i = it & (kPieces - 1);
         if (!(ok = wait(bar(B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u))) break;
         if (lane == 0) {
-            ring[i] = make_piece(g, more);
+            ring[i] = make_piece(p, g, more);
             ptx::mbar_arrive(bar(B_PIECE_FULL + i));
         }
         __syncwarp();
