@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
             if (b < p.B) {
                 const Seq s = load_seq(p, b);
                 if (s.n > 0) {
-                    u = (long long)p.Hkv * units_of(make_item(p, s, 0).nt, w.per_tile);
+                    u = (long long)p.Hkv * units_of(w, make_item(p, s, 0).nt, s.n);
                     c = u > 0;
                 }
             }
@@ -101,17 +101,18 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
         return;
     }
     const int l16 = tid & 15, g16 = tid >> 4;
-    const long long rows = (long long)p.tokens * p.H, r0 = (long long)blockIdx.x * kPrepRows + g16;
+    const uint32_t rows = (uint32_t)p.tokens * (uint32_t)p.H, r0 = blockIdx.x * kPrepRows + g16;   // below 2^31
     const T *q = static_cast<const T *>(p.q), *aK = static_cast<const T *>(p.aK);
     float s[4] = {};
+    const uint32_t mine = r0 + 16 * (l16 & 3);
+    const float e = l16 < 4 && mine < rows ? w.lse[mine] : 0.f;
     if (aK) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const long long r = r0 + 16 * u;
+            const uint32_t r = r0 + 16 * u;
             if (r >= rows) continue;
-            const long long t = r / p.H;
-            const int h = (int)(r - t * p.H);
-            const T *x = q + t * p.q_stride + (long long)h * p.d, *y = aK + (long long)(h / p.g) * p.ths;
+            const uint32_t t = r / (uint32_t)p.H, h = r - t * (uint32_t)p.H;
+            const T *x = q + (long long)t * p.q_stride + h * (uint32_t)p.d, *y = aK + (long long)(h / (uint32_t)p.g) * p.ths;
             for (int c = l16 * E; c < p.d; c += 16 * E) s[u] += dot<T, E>(x + c, y + c);
         }
 #pragma unroll
@@ -119,13 +120,9 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const long long r = r0 + 16 * u;
-        if (l16 == u && r < rows) {
-            const float e = w.lse[r];
-            w.nl[r] = e == -INFINITY ? -INFINITY : fmaf(s[u], p.scale_log2, -e * kLog2e);
-        }
+    if (l16 < 4 && mine < rows) {
+        const float x = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
+        w.nl[mine] = e == -INFINITY ? -INFINITY : fmaf(x, p.scale_log2, -e * kLog2e);
     }
 }
 
@@ -208,8 +205,8 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
         const int b = w.busy[entry_s];
         const Seq s = load_seq(p, b);
         const Item it = make_item(p, s, 0);
-        const int per = it.nt * kRunsPerTile, kvh = min((int)(rest_s / per), p.Hkv - 1);
-        const int run = (int)(rest_s - (long long)kvh * per);
+        const int run = min((int)(rest_s / p.Hkv), it.nt * kRunsPerTile - 1);
+        const int kvh = (int)(rest_s % p.Hkv);
         const int j0 = it.tile(run / kRunsPerTile) * kTile + (run % kRunsPerTile) * kRun;
         const int first = p.window > 0 ? max(0, max(it.pos_lo, 0) - p.window + 1) : 0;
         auto seen = [&](int j) { return j <= it.pos_hi && (j >= first || j < p.sinks); };
@@ -305,13 +302,14 @@ cudaError_t launch_simt(WeightParams w, cudaStream_t s) {
 // At most 16 query rows per key head (bf16, d = 64 or 128, pages of at least 8 keys): keys are the wide
 // side of m16n8k16 products, as in the attention of generated tokens, whose staging this has: a ninth
 // warp walks the CTA's share of the tiles and feeds a ring by TMA, eight row warps take 16 keys of a tile
-// each. A key's weights of all rows come together in one warp, so nothing is joined; the mass that is there and the
-// page numbers are fetched a tile ahead. HBM bounds it: a key is 2 d bytes and 8 of mass.
+// each. A key's weights of all rows come together in one warp, so nothing is joined; the masses that are there
+// and the page numbers come with the keys. HBM bounds it: a key is 2 d bytes and 8 of mass.
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRowThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // keys of a warp per tile
 constexpr int kMaxStages = 6;
+constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
 
 template <int D>
 constexpr int kStageBytes = kTile * D * 2;
@@ -322,7 +320,7 @@ enum : int { B_FULL = 0, B_EMPTY = kMaxStages, B_PIECE_FULL = 2 * kMaxStages, B_
              kNumBars = B_PIECE_EMPTY + kPieces };
 
 struct Layout {
-    uint32_t piece, bar, R, bytes;
+    uint32_t piece, bar, side, R, bytes;
     int lw;
     template <int D, int NT>
     static __host__ __device__ Layout make(int clip_k, bool ak, int stages) {
@@ -331,11 +329,13 @@ struct Layout {
         uint32_t off = (uint32_t)stages * kStageBytes<D>;
         L.piece = off; off += kPieces * sizeof(Piece);
         L.bar = off;   off += kNumBars * 8 + 16;
+        L.side = off;  off += (uint32_t)stages * kSideBytes;
         L.R = off;     off += 8 * NT * L.lw * 4;
         L.bytes = off;
         return L;
     }
 };
+static_assert((kPieces * sizeof(Piece) + kNumBars * 8 + 16) % 16 == 0, "alignment of the masses");
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -363,8 +363,9 @@ struct Waits {
 };
 
 template <int D>
-__device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const Waits &waits, const CUtensorMap *tm_k,
-                          int stages, int box) {
+__device__ void feed_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &waits,
+                          const CUtensorMap *tm_k, int stages, int box, int old_by_tma) {
+    const Params &p = w.p;
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_u32(smem), bars = base + L.bar;
@@ -405,17 +406,23 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
             int pg = pg_next;
             pg_next = lookup(t + 1, seen_next);
             if (!(ok = wait(bar(B_EMPTY + st), ph ^ 1u))) break;
-            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
-            if (lane == 0) ptx::mbar_expect_tx(bar(B_FULL + st), (uint32_t)__popc(m) * box * D * 2);
+            const int j = g.it.tile(t) * kTile + my_box * box, row = j & ((1 << p.pshift) - 1);
+            const bool bad = seen && (unsigned)pg >= (unsigned)p.num_pages;
+            if (bad) report_page(p);
+            const bool old = old_by_tma && seen && !bad && my_blk == 0 && j < g.it.pos_lo;   // some key is not new
+            if (my_blk == 0) reinterpret_cast<int *>(smem + L.side + st * kSideBytes)[my_box] = bad ? -1 : pg;
             __syncwarp();
-            if (seen && my_blk < DB && !(p.withhold && tiles == 0)) {
-                if ((unsigned)pg >= (unsigned)p.num_pages) {
-                    report_page(p);
-                    pg = p.num_pages;   // outside the tensor: zeros
-                }
-                const int row = (g.it.tile(t) * kTile + my_box * box) & ((1 << p.pshift) - 1);
-                tma_load_4d(my_dst + st * kStageBytes<D>, tm_k, bar(B_FULL + st), my_blk * 64, row, g.kvh, pg);
-            }
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0), mo = __ballot_sync(0xffffffffu, old);
+            if (lane == 0)
+                ptx::mbar_expect_tx(bar(B_FULL + st), (uint32_t)(__popc(m) * box * D * 2 + __popc(mo) * box * 4));
+            __syncwarp();
+            if (seen && my_blk < DB && !(p.withhold && tiles == 0))   // a page outside the cache: zeros
+                tma_load_4d(my_dst + st * kStageBytes<D>, tm_k, bar(B_FULL + st), my_blk * 64, row, g.kvh,
+                            bad ? p.num_pages : pg);
+            if (old)
+                bulk_load(base + L.side + st * kSideBytes + 64 + my_box * box * 4,
+                          w.mass + (long long)pg * w.mass_stride + (((long long)g.kvh << p.pshift) + row), box * 4,
+                          bar(B_FULL + st));
             __syncwarp();
             ++tiles;
             if (++st == stages) {
@@ -430,7 +437,8 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
 }
 
 template <int D, int NT, bool AK>
-__device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &wait, int stages) {
+__device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &wait, int stages, int box,
+                         int old_by_tma) {
     constexpr int kRows = 8 * NT;
     const Params &p = w.p;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -514,33 +522,14 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
 #pragma unroll
                 for (int e = 0; e < 2; ++e) r0[n][e] = nl[n][e] + (AK ? Rs[(8 * n + 2 * c + e) * L.lw] : 0.f);
         };
-        // this lane's key of a tile: slot kr (lanes with c = 0) or kr + 8 (c = 1)
-        const int *bt = p.bt + (long long)g.b * p.bt_stride;
-        const int mine = warp * kGroup + kr + 8 * c;
-        auto page_of = [&](int t) -> int {
-            if (c > 1 || t >= g.t1) return -1;
-            const int j = g.tile(t) * kTile + mine;
-            if (!(j <= g.pos_hi && (j >= first || j < p.sinks))) return -1;
-            const int pg = __ldg(bt + (j >> p.pshift));
-            return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
-        };
-        auto mass_at = [&](int t, int pg) {
-            return w.mass + (long long)pg * w.mass_stride +
-                   (((long long)g.kvh << p.pshift) + ((g.tile(t) * kTile + mine) & ((1 << p.pshift) - 1)));
-        };
-        auto old_of = [&](int t, int pg) {
-            return pg >= 0 && w.accumulate && g.tile(t) * kTile + mine < g.pos_lo ? *mass_at(t, pg) : 0.f;
-        };
-        int pg0 = page_of(g.t0), pg1 = page_of(g.t0 + 1);
+        const int mine = warp * kGroup + kr + 8 * c;   // this lane's key of a tile, where c < 2
         if (!many) set_rows(0);
-        float old0 = old_of(g.t0, pg0);
 #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t) {
             const int j0 = g.tile(t) * kTile + warp * kGroup;
             const uint32_t st = ring + stage * kStageBytes<D>;
             const uint32_t empty = bars + 8u * (B_EMPTY + stage);
-            const int pg2 = page_of(t + 2);
-            const float old1 = t + 1 < g.t1 ? old_of(t + 1, pg1) : 0.f;
+            const uint8_t *side = smem + L.side + stage * kSideBytes;
             wait(bars + 8u * (B_FULL + stage), phase);
             if (++stage == (uint32_t)stages) {
                 stage = 0;
@@ -589,6 +578,13 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) sum[e >> 1] += ptx::ex2(x[n][e]);
             }
+            const int j = g.tile(t) * kTile + mine;
+            int pg = -1;
+            float old = 0.f;
+            if (c < 2 && j <= g.pos_hi && (j >= first || j < p.sinks)) {
+                pg = reinterpret_cast<const int *>(side)[mine / box];
+                if (old_by_tma && j < g.pos_lo) old = reinterpret_cast<const float *>(side + 64)[mine];
+            }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty);
 #pragma unroll
@@ -596,10 +592,12 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
             }
-            if (pg0 >= 0) *mass_at(t, pg0) = old0 + (c == 0 ? sum[0] : sum[1]);
-            pg0 = pg1;
-            pg1 = pg2;
-            old0 = old1;
+            if (pg >= 0) {
+                float *at = w.mass + (long long)pg * w.mass_stride +
+                            (((long long)g.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
+                if (!old_by_tma && w.accumulate && j < g.pos_lo) old = *at;
+                *at = old + (c == 0 ? sum[0] : sum[1]);
+            }
         }
     }
 }
@@ -607,7 +605,7 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
 template <int D, int NT, bool AK>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     weights_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightParams w, int stages,
-                          int box) {
+                          int box, int old_by_tma) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const Params &p = w.p;
     const Layout L = Layout::make<D, NT>(p.clip_k, AK, stages);
@@ -626,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     grid_wait();
     grid_release();
     if (threadIdx.x >= kRowThreads)
-        feed_role<D>(p, L, smem, waits, &tm_k, stages, box);
+        feed_role<D>(w, L, smem, waits, &tm_k, stages, box, old_by_tma);
     else
-        row_role<D, NT, AK>(w, L, smem, waits, stages);
+        row_role<D, NT, AK>(w, L, smem, waits, stages, box, old_by_tma);
 }
 
 template <int D, int NT, bool AK>
@@ -645,7 +643,7 @@ cudaError_t launch_decode(const PagedWeightsArgs &a, const WeightParams &w, cuda
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(di.sms * kCtasPerSm<D>), kThreads, Layout::make<D, NT>(w.p.clip_k, AK, stages).bytes, s,
-                        tm, w, stages, box);
+                        tm, w, stages, box, masses_by_tma(w));
 }
 
 template <int D, int NT>

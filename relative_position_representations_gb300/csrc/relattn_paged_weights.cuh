@@ -18,7 +18,10 @@ struct WeightParams {
     float *mass;
     long long mass_stride;
     int accumulate;
-    int per_tile;                // units: 0: pairs of tiles; else units of one tile
+    int per_tile;                // units: 0: pairs of tiles (below); else units of one tile
+    int tile_tokens;             // tokens of a query tile
+    // pairs of tiles in a unit: the rows of one query tile stay while four pairs of key tiles pass by
+    __host__ __device__ int pairs(int n) const { return n <= tile_tokens ? 4 : 1; }
     unsigned long long *ticket;  // the next unit
     int *count;                  // requests with new tokens ...
     int *busy;                   // ... their numbers ...
@@ -41,7 +44,20 @@ __device__ __forceinline__ int find_unit(const WeightParams &w, int count, long 
     return lo;
 }
 
-__host__ __device__ __forceinline__ int units_of(int nt, int per_tile) { return per_tile ? nt * per_tile : (nt + 1) / 2; }
+__device__ __forceinline__ int units_of(const WeightParams &w, int nt, int n) {
+    const int step = 2 * w.pairs(n);
+    return w.per_tile ? nt * w.per_tile : (nt + step - 1) / step;
+}
+// masses of a tile are copied as 16-byte aligned runs
+inline int masses_by_tma(const WeightParams &w) {
+    return w.accumulate && w.mass_stride % 4 == 0 && reinterpret_cast<uintptr_t>(w.mass) % 16 == 0;
+}
+// `bytes` (a multiple of 16) from 16-byte aligned memory
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // tokens of a request that see some key of j0 .. j0 + len - 1 (window and sinks taken into account)
 __device__ __forceinline__ int first_token(int j0, int pos0) { return max(0, j0 - pos0); }

@@ -4,16 +4,20 @@
 // S^T = K Q^T on tcgen05 with the keys as the 128 rows of the accumulator: a thread has one key and adds
 // up its weights over the columns, the query rows, so nothing crosses threads and nothing but the sums
 // leaves the SM. A unit is two tiles of keys of one head, which stay in shared memory while the
-// request's query tiles pass by; each of them meets both. Units are taken by ticket, longest first
-// within a head (the first keys of a prompt are seen by every row).
+// request's query tiles pass by; each of them meets both. Units are taken by ticket, the heads of a
+// request together and its first keys first: every row of a prompt sees those, so the long units come first.
 // A row's constant nl (the table term of far keys less the log-sum-exp) is formed in front and
 // lies in shared memory beside its query tile, so a weight is one FMA and one exponential. Where some key of
 // a unit is less than clip_k back, R = Q aK^T is one product more of the query tile, its accumulator
 // drained into shared memory by the first tile's threads (a row each).
 //
 // Roles (384 threads, one CTA per SM): warp 3 takes tickets and announces units, warp 0 loads keys, tables and
-// query tiles, warp 2 the rows' constants, warp 1 issues the MMAs, warps 4-7 and 8-11 sum the unit's
-// first and second tile. TMEM: two accumulators of 128 columns for each tile.
+// query tiles, warp 2 the rows' constants, warp 1 issues the MMAs, warps 4-7 and 8-11 sum a pair's first and
+// second tile. A warp takes all of its scores into registers and gives the accumulator back before it works on
+// them. (Sixteen warps with half of the columns each: the instructions around a tile count twice, 1.30 us a
+// pair of tiles and a query tile in place of 1.11.)
+// TMEM: three accumulators of 128 columns, and the unit's keys, copied there where more than one query
+// tile passes by: a 128 x 128 product with both operands in shared memory reads as much as that can give.
 #include <cstdint>
 #include <cstring>
 
@@ -32,27 +36,36 @@ using tc::Shared;
 using tc::wait_bar;
 using tc::wait_bar_ctrl;
 
-constexpr int kThreads = 384;
-constexpr int kRowThreads = 256;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = 128 + 32 * kSumWarps;
 constexpr int KB = 32;               // columns read from an accumulator at a time
 constexpr int kUnits = 4;            // announced ahead
 constexpr int kMaxK = 4, kMaxQ = 4;  // stages
+constexpr int kAccs = 3;             // accumulators
+constexpr int kSides = 4;            // tiles whose page numbers and masses are held
+constexpr int kBatch = 4;            // query tiles whose constants come together ...
+constexpr int kBatches = 2;          // ... and how often
+constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
 
 enum : int {
     B_K_FULL = 0, B_K_EMPTY = B_K_FULL + kMaxK, B_Q_FULL = B_K_EMPTY + kMaxK, B_Q_EMPTY = B_Q_FULL + kMaxQ,
     B_AK_FULL = B_Q_EMPTY + kMaxQ, B_AK_EMPTY, B_UNIT_FULL, B_UNIT_EMPTY = B_UNIT_FULL + kUnits,
-    B_ACC_FULL = B_UNIT_EMPTY + kUnits, B_ACC_EMPTY = B_ACC_FULL + 4, B_DRAIN = B_ACC_EMPTY + 4, kNumBars
+    B_ACC_FULL = B_UNIT_EMPTY + kUnits, B_ACC_EMPTY = B_ACC_FULL + kAccs, B_SIDE_FULL = B_ACC_EMPTY + kAccs,
+    B_SIDE_EMPTY = B_SIDE_FULL + kSides, B_NL_FULL = B_SIDE_EMPTY + kSides, B_NL_EMPTY = B_NL_FULL + kBatches,
+    B_R_FULL = B_NL_EMPTY + kBatches, B_R_EMPTY, B_KEYS_FREE, B_DRAIN, kNumBars
 };
 
 struct Unit {
     int row0, n, pos0;   // first query token of the request, its new tokens, position of the first
-    int b, kvh;
-    int j0, j1;          // first keys of the tiles (j1 < 0: one tile only)
-    int qa, qb;          // query tiles
+    int row, kvh;        // of the block table; key head
+    int t0, t1;          // tiles, in pairs
+    int ns, lo;          // Item: where they lie
+    int qa, qb;          // query tiles (one, where there are several pairs)
     int band;            // some row may be less than clip_k past some key
-    int more, pad;
+    int more, pad[3];
+    __device__ __forceinline__ int key(int t) const { return t < t1 ? (t < ns ? t : lo + t - ns) * kTile : -1; }
 };
-static_assert(sizeof(Unit) == 48, "unit");
+static_assert(sizeof(Unit) == 64, "unit");
 
 struct TcParams {
     WeightParams w;
@@ -60,22 +73,23 @@ struct TcParams {
     int npad, SR;        // table rows rounded up to 16; row stride (floats) of R in shared memory
     int box;             // keys per TMA box
     int nk, nq;          // stages of keys and of query tiles
-    uint32_t tile_bytes, off_q, off_ak, off_r, off_nl, off_unit, off_bar;
+    int old_by_tma;      // masses are fetched with the keys
+    uint32_t tile_bytes, off_q, off_ak, off_r, off_nl, off_side, off_unit, off_bar;
 };
 
 // what a query tile is to a unit, the same for every role
 struct QueryTile {
     int tok0, ntok, pos_lo, pos_hi;
-    bool band;
+    bool band;           // with the tiles at j0 and j1
 };
-__device__ __forceinline__ QueryTile query_tile(const TcParams &tp, const Unit &u, int q) {
+__device__ __forceinline__ QueryTile query_tile(const TcParams &tp, const Unit &u, int q, int j0, int j1) {
     QueryTile t;
     t.tok0 = q * tp.TS;
     t.ntok = min(tp.TS, u.n - t.tok0);
     t.pos_lo = u.pos0 + t.tok0;
     t.pos_hi = t.pos_lo + t.ntok - 1;
     auto near = [&](int j) { return j >= 0 && j + kTile - 1 > t.pos_lo - tp.w.p.clip_k && j <= t.pos_hi; };
-    t.band = u.band && (near(u.j0) || near(u.j1));
+    t.band = u.band && (near(j0) || near(j1));
     return t;
 }
 
@@ -92,8 +106,8 @@ struct Units {
     __device__ __forceinline__ Unit get() const {
         const Unit &s = ring[it & (kUnits - 1)];
         auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-        return Unit{uni(s.row0), uni(s.n),  uni(s.pos0), uni(s.b),    uni(s.kvh),  uni(s.j0),
-                    uni(s.j1),   uni(s.qa), uni(s.qb),   uni(s.band), uni(s.more), 0};
+        return Unit{uni(s.row0), uni(s.n),  uni(s.pos0), uni(s.row), uni(s.kvh),  uni(s.t0),  uni(s.t1),
+                    uni(s.ns),   uni(s.lo), uni(s.qa),   uni(s.qb),  uni(s.band), uni(s.more), {}};
     }
 };
 
@@ -125,25 +139,26 @@ __device__ void ticket_role(const TcParams &tp, const Shared &sh) {
         Unit u{};
         if ((long long)t < total) {
             long long rest;
-            u.b = tp.w.busy[find_unit(tp.w, count, (long long)t, rest)];
-            const Seq s = load_seq(p, u.b);
+            u.row = tp.w.busy[find_unit(tp.w, count, (long long)t, rest)];
+            const Seq s = load_seq(p, u.row);
             const Item it = make_item(p, s, 0);
-            const int per = (it.nt + 1) / 2;
-            u.kvh = min((int)(rest / per), p.Hkv - 1);
-            const int a = 2 * (int)(rest - (long long)u.kvh * per);
+            const int step = 2 * tp.w.pairs(s.n), i = (int)(rest / p.Hkv);
+            u.kvh = (int)(rest - (long long)i * p.Hkv);
             u.row0 = s.q0;
             u.n = s.n;
             u.pos0 = s.pos0;
-            u.j0 = it.tile(a) * kTile;
-            u.j1 = a + 1 < it.nt ? it.tile(a + 1) * kTile : -1;
-            int lo = first_token(u.j0, s.pos0), hi = end_token(p, u.j0, kTile, s.pos0, s.n);
-            if (u.j1 >= 0) {
-                lo = min(lo, first_token(u.j1, s.pos0));
-                hi = max(hi, end_token(p, u.j1, kTile, s.pos0, s.n));
+            u.t0 = i * step;
+            u.t1 = min(u.t0 + step, it.nt);
+            u.ns = it.ns;
+            u.lo = it.lo;
+            int lo = s.n, hi = 0;
+            for (int q = u.t0; q < u.t1; ++q) {
+                lo = min(lo, first_token(u.key(q), s.pos0));
+                hi = max(hi, end_token(p, u.key(q), kTile, s.pos0, s.n));
             }
             u.qa = lo / tp.TS;
             u.qb = (hi + tp.TS - 1) / tp.TS;
-            u.band = AK && p.clip_k > 0 && max(u.j0, u.j1) + kTile - 1 > s.pos0 + u.qa * tp.TS - p.clip_k;
+            u.band = AK && p.clip_k > 0 && u.key(u.t1 - 1) + kTile - 1 > s.pos0 + u.qa * tp.TS - p.clip_k;
             u.more = 1;
         }
         bool ok = wait_bar_ctrl(units.empty(), units.parity() ^ 1u, sh, p.err);
@@ -172,38 +187,55 @@ __device__ void load_role(const TcParams &tp, const Shared &sh, const CUtensorMa
     };
     const int nbox = kTile / tp.box, my_box = lane % nbox, my_blk = lane / nbox;
     Units units(tp, sh);
-    Ring kr(tp.nk), qr(tp.nq);
+    Ring kr(tp.nk), qr(tp.nq), sr(kSides);
     uint32_t ak_it = 0, k_count = 0, q_count = 0;
     bool ok = true;
     for (; ok; ++units.it) {
         if (!(ok = wait(units.full(), units.parity()))) break;
         const Unit u = units.get();
         if (!u.more) break;
-        const int *bt = p.bt + (long long)u.b * p.bt_stride;
+        const int *bt = p.bt + (long long)u.row * p.bt_stride;
         const int pos_hi = u.pos0 + u.n - 1;
         const int first = p.window > 0 ? max(0, max(u.pos0, 0) - p.window + 1) : 0;
-        for (int s = 0; s < 2 && ok; ++s) {
-            const int j0 = s ? u.j1 : u.j0;
-            if (j0 < 0) break;
-            const int j = j0 + my_box * tp.box;
-            const bool seen = j <= pos_hi && (j + tp.box > first || j < p.sinks);
-            int pg = seen ? __ldg(bt + (j >> p.pshift)) : -1;
-            if (!(ok = wait(bar(B_K_EMPTY + kr.st), kr.ph ^ 1u))) break;
-            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
-            ptx::mbar_expect_tx_w(bar(B_K_FULL + kr.st), (uint32_t)__popc(m) * tp.box * D * 2);
+        // the tile's pages, one a lane, looked up a tile ahead; their numbers and the masses that are there come along
+        auto lookup = [&](int t, bool &seen) -> int {
+            const int j = u.key(t) + my_box * tp.box;
+            seen = t < u.t1 && j <= pos_hi && (j + tp.box > first || j < p.sinks);
+            return seen ? __ldg(bt + (j >> p.pshift)) : -1;
+        };
+        bool seen_next;
+        int pg_next = lookup(u.t0, seen_next);
+        auto load_keys = [&](int t) -> bool {
+            const bool seen = seen_next;
+            int pg = pg_next;
+            pg_next = lookup(t + 1, seen_next);
+            if (!wait(bar(B_SIDE_EMPTY + sr.st), sr.ph ^ 1u) || !wait(bar(B_K_EMPTY + kr.st), kr.ph ^ 1u)) return false;
+            const int j = u.key(t) + my_box * tp.box, row = j & ((1 << p.pshift) - 1);
+            const bool bad = seen && (unsigned)pg >= (unsigned)p.num_pages;
+            if (bad) report_page(p);
+            // (masses of the tile's new keys count for nothing, so where all are new none are fetched)
+            const bool old = tp.old_by_tma && seen && !bad && my_blk == 0 && j < u.pos0;
+            uint8_t *side = sh.ptr + tp.off_side + sr.st * kSideBytes;
+            if (my_blk == 0) reinterpret_cast<int *>(side)[my_box] = bad ? -1 : pg;
             __syncwarp();
-            if (seen && my_blk < DB) {
-                if ((unsigned)pg >= (unsigned)p.num_pages) {
-                    report_page(p);
-                    pg = p.num_pages;   // a box outside the tensor: zeros
-                }
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0), mo = __ballot_sync(0xffffffffu, old);
+            ptx::mbar_expect_tx_w(bar(B_SIDE_FULL + sr.st), (uint32_t)(__popc(mo) * tp.box * 4));
+            ptx::mbar_expect_tx_w(bar(B_K_FULL + kr.st), (uint32_t)(__popc(m) * tp.box * D * 2));
+            __syncwarp();
+            if (seen && my_blk < DB)   // a page outside the cache: a box outside the tensor, which reads as zeros
                 tma_load_4d(sh.base + (uint32_t)kr.st * tp.tile_bytes + my_blk * kTile * 128 + my_box * tp.box * 128, tm_k,
-                            bar(B_K_FULL + kr.st), my_blk * 64, j & ((1 << p.pshift) - 1), u.kvh, pg);
-            }
+                            bar(B_K_FULL + kr.st), my_blk * 64, row, u.kvh, bad ? p.num_pages : pg);
+            if (old)
+                bulk_load(sh.base + tp.off_side + sr.st * kSideBytes + 64 + my_box * tp.box * 4,
+                          tp.w.mass + (long long)pg * tp.w.mass_stride + (((long long)u.kvh << p.pshift) + row), tp.box * 4,
+                          bar(B_SIDE_FULL + sr.st));
             __syncwarp();
             kr.next();
+            sr.next();
             ++k_count;
-        }
+            return true;
+        };
+        for (int t = u.t0; t < u.t1 && t < u.t0 + 2 && ok; ++t) ok = load_keys(t);
         if (!ok) break;
         if (AK && u.band) {
             if (!(ok = wait(bar(B_AK_EMPTY), (ak_it & 1u) ^ 1u))) break;
@@ -224,11 +256,14 @@ __device__ void load_role(const TcParams &tp, const Shared &sh, const CUtensorMa
             qr.next();
             ++q_count;
         }
+        for (int t = u.t0 + 2; t < u.t1 && ok; ++t) ok = load_keys(t);
         if (ok) ptx::mbar_arrive_w(units.empty());
     }
     // no copy is in flight when the CTA exits
     for (uint32_t i = k_count > (uint32_t)tp.nk ? k_count - tp.nk : 0; i < k_count; ++i)
         tc::drain_bar(bar(B_K_FULL + (int)(i % tp.nk)), (i / tp.nk) & 1u, sh.limit);
+    for (uint32_t i = k_count > (uint32_t)kSides ? k_count - kSides : 0; i < k_count; ++i)
+        tc::drain_bar(bar(B_SIDE_FULL + (int)(i % kSides)), (i / kSides) & 1u, sh.limit);
     for (uint32_t i = q_count > (uint32_t)tp.nq ? q_count - tp.nq : 0; i < q_count; ++i)
         tc::drain_bar(bar(B_Q_FULL + (int)(i % tp.nq)), (i / tp.nq) & 1u, sh.limit);
     if (AK && ak_it) tc::drain_bar(bar(B_AK_FULL), (ak_it - 1) & 1u, sh.limit);
@@ -252,30 +287,69 @@ __device__ void const_role(const TcParams &tp, const Shared &sh) {
         head[e] = i - i / p.g * p.g;
     }
     Units units(tp, sh);
-    Ring qr(tp.nq);
+    Ring nr(kBatches);
     for (bool ok = true; ok; ++units.it) {
         if (!(ok = wait(units.full(), units.parity()))) break;
         const Unit u = units.get();
         if (!u.more) break;
-        for (int q = u.qa; q < u.qb; ++q) {
-            float v[4];
+        for (int q0 = u.qa; q0 < u.qb; q0 += kBatch) {
+            float v[kBatch][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = tok[e] < u.n - q * tp.TS
-                           ? __ldg(tp.w.nl + (long long)(u.row0 + q * tp.TS + tok[e]) * p.H + u.kvh * p.g + head[e])
-                           : -INFINITY;
-            if (!(ok = wait(bar(B_Q_EMPTY + qr.st), qr.ph ^ 1u))) break;
-            float4 *dst = reinterpret_cast<float4 *>(sh.ptr + tp.off_nl + qr.st * BM * 4);
-            dst[lane] = make_float4(v[0], v[1], v[2], v[3]);
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[i][e] = q0 + i < u.qb && tok[e] < u.n - (q0 + i) * tp.TS
+                                  ? __ldg(tp.w.nl + (long long)(u.row0 + (q0 + i) * tp.TS + tok[e]) * p.H + u.kvh * p.g + head[e])
+                                  : -INFINITY;
+            if (!(ok = wait(bar(B_NL_EMPTY + nr.st), nr.ph ^ 1u))) break;
+            float4 *dst = reinterpret_cast<float4 *>(sh.ptr + tp.off_nl + nr.st * kBatch * BM * 4);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) dst[i * 32 + lane] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
             __syncwarp();
-            ptx::mbar_arrive_w(bar(B_Q_FULL + qr.st));
-            qr.next();
+            ptx::mbar_arrive_w(bar(B_NL_FULL + nr.st));
+            nr.next();
         }
         if (ok) ptx::mbar_arrive_w(units.empty());
     }
 }
 
 // ======================================================================= MMAs
+constexpr uint32_t kAccCol = 128;    // first accumulator; the keys of tile s lie at D / 2 * s
+
+// D = A B over D / 16 k-steps, one elect for the chain: A in TMEM, 8 columns a step, B K-major with 128-byte
+// swizzle and 128 rows
+#define RELATTN_STEP(A, B) \
+    "add.u32 a1, %1, " #A ";\n\tadd.s64 b1, %2, " #B ";\n\t" \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+template <int D>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+    if (D == 64)
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 t, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+            RELATTN_STEP(8, 2) RELATTN_STEP(16, 4) RELATTN_STEP(24, 6) "}\n" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(0u), "r"(1u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 t, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+            RELATTN_STEP(8, 2) RELATTN_STEP(16, 4) RELATTN_STEP(24, 6) RELATTN_STEP(32, 1024) RELATTN_STEP(40, 1026)
+            RELATTN_STEP(48, 1028) RELATTN_STEP(56, 1030) "}\n" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(0u), "r"(1u)
+            : "memory");
+}
+#undef RELATTN_STEP
+// 128 rows x 16 elements of a K-major tile with 128-byte swizzle to 8 columns, a row per lane: an A operand
+__device__ __forceinline__ void copy_keys(uint32_t cols, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.128x256b [%0], %1;\n\t}\n" ::"r"(cols), "l"(desc)
+        : "memory");
+}
+
 template <int D, bool AK>
 __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem) {
     const Params &p = tp.w.p;
@@ -293,60 +367,92 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem) {
     const uint32_t idR = ptx::idesc_bf16(BM, (uint32_t)tp.npad, 0);
     Units units(tp, sh);
     Ring kr(tp.nk), qr(tp.nq);
-    uint32_t cnt[2] = {0, 0}, ak_it = 0;
+    uint32_t ak_it = 0, keys_it = 0;
+    int acc_i = 0;
+    uint32_t acc_ph = 0;
     bool ok = true;
-    // the next accumulator of tile s
-    auto claim = [&](int s) -> bool {
-        const uint32_t c = cnt[s];
-        if (!wait(bar(B_ACC_EMPTY + 2 * s + (int)(c & 1u)), ((c >> 1) & 1u) ^ 1u)) return false;
+    // the accumulators in turn
+    auto claim = [&]() -> bool {
+        if (!wait(bar(B_ACC_EMPTY + acc_i), acc_ph ^ 1u)) return false;
         ptx::tc_fence_after();
         return true;
+    };
+    auto acc_at = [&]() { return tmem + kAccCol + (uint32_t)acc_i * kTile; };
+    auto acc_done = [&]() {
+        ptx::tc_commit_w(bar(B_ACC_FULL + acc_i));
+        if (++acc_i == kAccs) {
+            acc_i = 0;
+            acc_ph ^= 1u;
+        }
     };
     for (; ok; ++units.it) {
         if (!(ok = wait(units.full(), units.parity()))) break;
         const Unit u = units.get();
         if (!u.more) break;
-        const int tiles = u.j1 >= 0 ? 2 : 1;
-        int kst[2];
-        for (int s = 0; s < tiles && ok; ++s) {
-            kst[s] = kr.st;
-            ok = wait(bar(B_K_FULL + kr.st), kr.ph);
-            kr.next();
-        }
-        if (ok && AK && u.band) ok = wait(bar(B_AK_FULL), ak_it++ & 1u);
-        for (int q = u.qa; q < u.qb && ok; ++q) {
-            if (!(ok = wait(bar(B_Q_FULL + qr.st), qr.ph))) break;
-            ptx::tc_fence_after();
-            const uint64_t dq = dq0 + (uint64_t)qr.st * tile16;
-            if (AK && query_tile(tp, u, q).band) {
-                if (!(ok = claim(0))) break;
-                const uint32_t acc = tmem + (cnt[0] & 1u) * kTile;
-#pragma unroll 1
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t at_q = (uint64_t)(((kk >> 2) * BM * 128 + (kk & 3) * 32) >> 4);
-                    const uint64_t at_a = (uint64_t)(((kk >> 2) * tp.npad * 128 + (kk & 3) * 32) >> 4);
-                    ptx::tc_mma_w(acc, dq + at_q, da + at_a, idR, kk > 0 ? 1u : 0u);
-                }
-                ptx::tc_commit_w(bar(B_ACC_FULL + (int)(cnt[0] & 1u)));
-                ++cnt[0];
-            }
+        if (AK && u.band) ok = wait(bar(B_AK_FULL), ak_it++ & 1u);
+        for (int t = u.t0; t < u.t1 && ok; t += 2) {
+            const int tiles = min(2, u.t1 - t);
+            int kst[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                if (s >= tiles) break;
-                if (!(ok = claim(s))) break;
-                const uint32_t acc = tmem + (2 * s + (cnt[s] & 1u)) * kTile;
-                const uint64_t dk = dk0 + (uint64_t)kst[s] * tile16;
-                if (D == 128) ptx::tc_mma_ss_k128(acc, dk, dq, idS, 0u);
-                else ptx::tc_mma_ss_k64(acc, dk, dq, idS, 0u);
-                ptx::tc_commit_w(bar(B_ACC_FULL + 2 * s + (int)(cnt[s] & 1u)));
-                ++cnt[s];
+                if (s >= tiles || !ok) break;
+                kst[s] = kr.st;
+                ok = wait(bar(B_K_FULL + kr.st), kr.ph);
+                kr.next();
+            }
+            const bool ts = u.qb - u.qa > 1;   // the keys meet more than one query tile: into TMEM, once their
+            if (ok && ts) {                    // predecessors there have been multiplied for the last time
+                if (keys_it && !(ok = wait(bar(B_KEYS_FREE), (keys_it - 1) & 1u))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s >= tiles) break;
+#pragma unroll 1
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        copy_keys(tmem + (uint32_t)(s * (D / 2) + 8 * kk),
+                                  dk0 + (uint64_t)kst[s] * tile16 + (uint64_t)(((kk >> 2) * BM * 128 + (kk & 3) * 32) >> 4));
+                    ptx::tc_commit_w(bar(B_K_EMPTY + kst[s]));
+                }
+            }
+            for (int q = u.qa; q < u.qb && ok; ++q) {
+                if (t == u.t0 && !(ok = wait(bar(B_Q_FULL + qr.st), qr.ph))) break;
+                ptx::tc_fence_after();
+                const uint64_t dq = dq0 + (uint64_t)qr.st * tile16;
+                if (AK && query_tile(tp, u, q, u.key(t), u.key(t + 1)).band) {
+                    if (!(ok = claim())) break;
+#pragma unroll 1
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t at_q = (uint64_t)(((kk >> 2) * BM * 128 + (kk & 3) * 32) >> 4);
+                        const uint64_t at_a = (uint64_t)(((kk >> 2) * tp.npad * 128 + (kk & 3) * 32) >> 4);
+                        ptx::tc_mma_w(acc_at(), dq + at_q, da + at_a, idR, kk > 0 ? 1u : 0u);
+                    }
+                    acc_done();
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s >= tiles) break;
+                    if (!(ok = claim())) break;
+                    const uint64_t dk = dk0 + (uint64_t)kst[s] * tile16;
+                    if (ts) mma_ts<D>(acc_at(), tmem + (uint32_t)(s * (D / 2)), dq, idS);
+                    else if (D == 128) ptx::tc_mma_ss_k128(acc_at(), dk, dq, idS, 0u);
+                    else ptx::tc_mma_ss_k64(acc_at(), dk, dq, idS, 0u);
+                    acc_done();
+                }
+                if (!ok) break;
+                if (t + 2 >= u.t1) {   // (the query tile of a unit of several pairs stays)
+                    ptx::tc_commit_w(bar(B_Q_EMPTY + qr.st));
+                    qr.next();
+                }
             }
             if (!ok) break;
-            ptx::tc_commit_w(bar(B_Q_EMPTY + qr.st));
-            qr.next();
+            if (ts) {
+                ptx::tc_commit_w(bar(B_KEYS_FREE));
+                ++keys_it;
+            } else {
+                for (int s = 0; s < tiles; ++s) ptx::tc_commit_w(bar(B_K_EMPTY + kst[s]));
+            }
         }
         if (!ok) break;
-        for (int s = 0; s < tiles; ++s) ptx::tc_commit_w(bar(B_K_EMPTY + kst[s]));
         if (AK && u.band) ptx::tc_commit_w(bar(B_AK_EMPTY));
         ptx::mbar_arrive_w(units.empty());
     }
@@ -356,6 +462,7 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem) {
 }
 
 // ======================================================================= sums
+// the bits below n of 32
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 template <int D, bool AK>
@@ -370,89 +477,68 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
     const float sl2 = p.scale_log2;
     const int k = p.clip_k;
     float *Rs = reinterpret_cast<float *>(sh.ptr + tp.off_r);
-    uint32_t cnt = 0;
+    uint32_t r_it = 0;
+    int acc_i = 0;
+    uint32_t acc_ph = 0;
     bool bad = false;
-    // a wait that runs out marks the warp; it goes on, and all leave together at the next unit
+    // a wait that runs out marks the lane, whose warp leaves at the next unit (the flag that it has set ends
+    // the others' waits; there is no barrier that they would miss it at)
     auto wait_own = [&](uint32_t b, uint32_t parity) {
-        if (!bad) {
-            const bool r = wait_bar(b, parity, sh, p.err);
-            bad = __all_sync(0xffffffffu, r ? 1 : 0) == 0;
-        }
+        bad = !wait_bar(b, parity, sh, p.err) || bad;
         __syncwarp();
     };
+    auto arrive = [&](uint32_t b) {
+        __syncwarp();
+        ptx::mbar_arrive_w(b);
+    };
+    // the accumulators in turn: R's, the first tile's, the second's; a warp passes over those that are not its own
     auto wait_acc = [&]() {
-        wait_own(bar(B_ACC_FULL + 2 * slot + (int)(cnt & 1u)), (cnt >> 1) & 1u);
+        wait_own(bar(B_ACC_FULL + acc_i), acc_ph);
         ptx::tc_fence_after();
+    };
+    auto next_acc = [&]() {
+        if (++acc_i == kAccs) {
+            acc_i = 0;
+            acc_ph ^= 1u;
+        }
     };
     auto release_acc = [&]() {
         ptx::tc_fence_before();
-        __syncwarp();
-        ptx::mbar_arrive_w(bar(B_ACC_EMPTY + 2 * slot + (int)(cnt & 1u)));
-        ++cnt;
+        arrive(bar(B_ACC_EMPTY + acc_i));
     };
+    auto acc_at = [&]() { return lanes + kAccCol + (uint32_t)acc_i * kTile; };
     Units units(tp, sh);
-    Ring qr(tp.nq);
+    Ring nr(kBatches), sr(kSides);
     for (;; ++units.it) {
         wait_own(units.full(), units.parity());
-        if (!ptx::bar_red_and(1, kRowThreads, !bad)) break;
+        if (__any_sync(0xffffffffu, bad)) break;
         const Unit u = units.get();
-        __syncwarp();
-        ptx::mbar_arrive_w(units.empty());
+        arrive(units.empty());
         if (!u.more) break;
-        const int j0 = slot ? u.j1 : u.j0;
-        const bool have = j0 >= 0;
-        const int j = j0 + quad * 32 + lane, j_lo = j0 + quad * 32, j_hi = j_lo + 31;
-        // where the key's mass is, and what it holds
-        float *at = nullptr;
-        float old = 0.f;
-        {
-            const int pos_hi = u.pos0 + u.n - 1, first = p.window > 0 ? max(0, max(u.pos0, 0) - p.window + 1) : 0;
-            if (have && j <= pos_hi && (j >= first || j < p.sinks)) {
-                const int pg = __ldg(p.bt + (long long)u.b * p.bt_stride + (j >> p.pshift));
-                if ((unsigned)pg < (unsigned)p.num_pages) {
-                    at = tp.w.mass + (long long)pg * tp.w.mass_stride +
-                         (((long long)u.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
-                    if (tp.w.accumulate && j < u.pos0) old = *at;
-                }
+        const int last = u.pos0 + u.n - 1, first = p.window > 0 ? max(0, max(u.pos0, 0) - p.window + 1) : 0;
+        for (int t0 = u.t0; t0 < u.t1; t0 += 2) {
+            const bool two = t0 + 1 < u.t1, have = !slot || two;
+            const int j0 = u.key(t0 + slot);
+            const int j = j0 + quad * 32 + lane, j_lo = j0 + quad * 32, j_hi = j_lo + 31;
+            // Query tiles plain0 .. plain1 - 1 are whole, see all of the warp's keys and lie past the band (of either
+            // tile): no masks, no tables. They come after the first one or two, but for windows.
+            int plain0, plain1 = min(u.n / tp.TS, u.qb);
+            {
+                const int past = max(AK ? max(j_hi, max(j0, u.key(t0 + 1 - slot)) + kTile - 1) + k : j_hi, u.pos0);
+                plain0 = (past - u.pos0 + tp.TS - 1) / tp.TS;
+                if (p.window > 0 && j_hi >= p.sinks)
+                    plain1 = (int)max(0LL, min((long long)plain1, ((long long)j_lo + p.window - u.pos0) / tp.TS));
+                if (u.pos0 < 0) plain1 = 0;
             }
-        }
-        float2 s01 = dup(0.f), s23 = dup(0.f);
-        for (int q = u.qa; q < u.qb; ++q) {
-            const QueryTile t = query_tile(tp, u, q);
-            wait_own(bar(B_Q_FULL + qr.st), qr.ph);   // the constants
-            const float *nl = reinterpret_cast<const float *>(sh.ptr + tp.off_nl + qr.st * BM * 4);
-            if (AK && t.band) {
-                ptx::named_bar_sync(2, kRowThreads);   // the last R has been read
-                if (slot == 0) {
-                    wait_acc();
-                    float *row = Rs + (quad * 32 + lane) * tp.SR;
-                    float r0 = 0.f;
-                    for (int c0 = 0; c0 < tp.npad; c0 += 16) {
-                        uint32_t r[16];
-                        ptx::tmem_ld16(lanes + (cnt & 1u) * kTile + (uint32_t)c0, r);
-                        ptx::tmem_ld_wait();
-                        if (c0 == 0) r0 = __uint_as_float(r[0]);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c0 + e <= k) row[c0 + e] = (__uint_as_float(r[e]) - r0) * sl2;
-                    }
-                    release_acc();
-                }
-                ptx::named_bar_sync(2, kRowThreads);
-            }
-            if (have) {
-                wait_acc();
-                const uint32_t acc = lanes + (uint32_t)(2 * slot + (cnt & 1u)) * kTile;
-                const bool far = !AK || k == 0 || j_hi <= t.pos_lo - k;   // else the tile is a band tile: R is there
-                const bool full = t.ntok == tp.TS && j_hi <= t.pos_lo &&
-                                  (p.window == 0 || j_lo > t.pos_hi - p.window || j_hi < p.sinks);
-                const bool dead = j_lo > t.pos_hi || (p.window > 0 && j_hi <= t.pos_lo - p.window && j_lo >= p.sinks);
-                // weights of 32 columns, their logits a x + nl
-                auto weights = [&](float *x, int c) {
-                    const float4 *n4 = reinterpret_cast<const float4 *>(nl + c);
+            float2 s01 = dup(0.f), s23 = dup(0.f);
+            for (int q = u.qa; q < u.qb; ++q) {
+                const int in = (q - u.qa) & (kBatch - 1);
+                if (in == 0 && t0 == u.t0) wait_own(bar(B_NL_FULL + nr.st), nr.ph);
+                const float *nl = reinterpret_cast<const float *>(sh.ptr + tp.off_nl + (nr.st * kBatch + in) * BM * 4);
+                auto weights = [&](float *x, int c) {   // of 32 columns, with their constants
 #pragma unroll
                     for (int e = 0; e < KB; e += 4) {
-                        const float4 n = n4[e / 4];
+                        const float4 n = *reinterpret_cast<const float4 *>(nl + c + e);
                         const float2 a = __ffma2_rn(pair(x, e), dup(sl2), make_float2(n.x, n.y));
                         const float2 b = __ffma2_rn(pair(x, e + 2), dup(sl2), make_float2(n.z, n.w));
                         x[e] = ptx::ex2(a.x);
@@ -468,60 +554,118 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         s23 = __fadd2_rn(s23, make_float2(x[e + 2], x[e + 3]));
                     }
                 };
-                if (full && far) {
-                    float x[2][KB];
-                    ptx::tmem_ld32f(acc, x[0]);
+                if (q >= plain0 && q < plain1) {
+                    if (slot) next_acc();
+                    if (have) {
+                        wait_acc();
+                        float x[kTile];
 #pragma unroll
-                    for (int c = 0; c < kTile / KB; ++c) {
+                        for (int c = 0; c < kTile; c += KB) ptx::tmem_ld32f(acc_at() + (uint32_t)c, x + c);
                         ptx::tmem_ld_wait();
-                        if (c + 1 < kTile / KB) ptx::tmem_ld32f(acc + (uint32_t)((c + 1) * KB), x[(c + 1) & 1]);
-                        else release_acc();
-                        weights(x[c & 1], c * KB);
-                        add(x[c & 1]);
-                    }
-                } else if (!dead) {
-                    // the columns that see this key: tokens from its own on, as far as the window reaches
-                    const int rows = t.ntok * p.g, c_lo = max(0, j - t.pos_lo) * p.g;
-                    int c_hi = rows;
-                    if (p.window > 0 && j >= p.sinks)
-                        c_hi = (int)max(0LL, min((long long)rows, ((long long)j + p.window - t.pos_lo) * p.g));
-#pragma unroll 1
-                    for (int c = 0; c < kTile; c += KB) {
-                        float x[KB];
-                        ptx::tmem_ld32f(acc + (uint32_t)c, x);
-                        ptx::tmem_ld_wait();
-                        if (!far) {
-                            int tok = c / p.g, hh = c - tok * p.g;
+                        release_acc();
+                        next_acc();
 #pragma unroll
-                            for (int e = 0; e < KB; ++e) {
-                                const int lab = min(max(j - t.pos_lo - tok + k, 0), k);
-                                x[e] = fmaf(x[e], sl2, nl[c + e] + Rs[(c + e) * tp.SR + lab]);
-                                if (++hh == p.g) {
-                                    hh = 0;
-                                    ++tok;
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < KB; ++e) x[e] = ptx::ex2(x[e]);
-                        } else {
-                            weights(x, c);
+                        for (int c = 0; c < kTile; c += KB) {
+                            weights(x + c, c);
+                            add(x + c);
                         }
-                        const uint32_t on = below(c_hi - c) & ~below(c_lo - c);
-#pragma unroll
-                        for (int e = 0; e < KB; ++e) x[e] = on & (1u << e) ? x[e] : 0.f;
-                        add(x);
-                        __syncwarp();
                     }
-                    release_acc();
+                    if (!slot && two) next_acc();
                 } else {
-                    release_acc();
+                    const QueryTile t = query_tile(tp, u, q, u.key(t0), u.key(t0 + 1));
+                    if (AK && t.band) {
+                        if (slot == 0) {   // R, a row each
+                            wait_acc();
+                            wait_own(bar(B_R_EMPTY), (r_it & 1u) ^ 1u);   // the last one has been read
+                            float *row = Rs + (quad * 32 + lane) * tp.SR;
+                            float r0 = 0.f;
+                            for (int c0 = 0; c0 < tp.npad; c0 += 16) {
+                                uint32_t r[16];
+                                ptx::tmem_ld16(acc_at() + (uint32_t)c0, r);
+                                ptx::tmem_ld_wait();
+                                if (c0 == 0) r0 = __uint_as_float(r[0]);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (c0 + e <= k) row[c0 + e] = (__uint_as_float(r[e]) - r0) * sl2;
+                            }
+                            release_acc();
+                            ptx::mbar_arrive_w(bar(B_R_FULL));
+                        }
+                        next_acc();
+                        wait_own(bar(B_R_FULL), r_it & 1u);
+                        ++r_it;
+                    }
+                    if (slot) next_acc();
+                    if (have) {
+                        wait_acc();
+                        const bool far = !AK || k == 0 || j_hi <= t.pos_lo - k;   // else R is there
+                        const bool full = t.ntok == tp.TS && j_hi <= t.pos_lo &&
+                                          (p.window == 0 || j_lo > t.pos_hi - p.window || j_hi < p.sinks);
+                        const bool dead = j_lo > t.pos_hi || (p.window > 0 && j_hi <= t.pos_lo - p.window && j_lo >= p.sinks);
+                        if (!dead) {
+                            // the columns that see this key: tokens from its own on, as far as the window reaches
+                            int c_lo = 0, c_hi = kTile;
+                            if (!full) {
+                                c_lo = max(0, j - t.pos_lo) * p.g;
+                                c_hi = t.ntok * p.g;
+                                if (p.window > 0 && j >= p.sinks)
+                                    c_hi = (int)max(0LL, min((long long)c_hi, ((long long)j + p.window - t.pos_lo) * p.g));
+                            }
+                            int hh = 0, lab = j - t.pos_lo + k;
+                            const float *row = Rs;
+#pragma unroll 1
+                            for (int c = 0; c < kTile; c += KB) {
+                                float x[KB];
+                                ptx::tmem_ld32f(acc_at() + (uint32_t)c, x);
+                                ptx::tmem_ld_wait();
+                                if (far) {
+                                    weights(x, c);
+                                } else {   // R of token i: its entry for key j, one further back with every token
+#pragma unroll
+                                    for (int e = 0; e < KB; ++e) {
+                                        x[e] = ptx::ex2(fmaf(x[e], sl2, nl[c + e] + row[min(max(lab, 0), k)]));
+                                        row += tp.SR;
+                                        if (++hh == p.g) {
+                                            hh = 0;
+                                            --lab;
+                                        }
+                                    }
+                                }
+                                const uint32_t on = below(c_hi - c) & ~below(c_lo - c);
+#pragma unroll
+                                for (int e = 0; e < KB; ++e) x[e] = on >> e & 1 ? x[e] : 0.f;
+                                add(x);
+                                __syncwarp();
+                            }
+                        }
+                        release_acc();
+                        next_acc();
+                    }
+                    if (!slot && two) next_acc();
+                    if (AK && t.band) arrive(bar(B_R_EMPTY));
+                }
+                if ((in == kBatch - 1 || q + 1 == u.qb) && t0 + 2 >= u.t1) {
+                    arrive(bar(B_NL_EMPTY + nr.st));
+                    nr.next();
                 }
             }
-            __syncwarp();
-            ptx::mbar_arrive_w(bar(B_Q_EMPTY + qr.st));
-            qr.next();
+            if (slot) sr.next();   // (the pair's first tile is the other warps')
+            if (have) {
+                wait_own(bar(B_SIDE_FULL + sr.st), sr.ph);
+                const uint8_t *side = sh.ptr + tp.off_side + sr.st * kSideBytes;
+                const int pg = reinterpret_cast<const int *>(side)[(j - j0) / tp.box];
+                const bool mine = pg >= 0 && j <= last && (j >= first || j < p.sinks);
+                float *at = tp.w.mass + (long long)pg * tp.w.mass_stride +
+                            (((long long)u.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
+                float old = 0.f;
+                if (tp.w.accumulate && mine && j < u.pos0)
+                    old = tp.old_by_tma ? reinterpret_cast<const float *>(side + 64)[j - j0] : *at;
+                arrive(bar(B_SIDE_EMPTY + sr.st));
+                if (mine && !bad) *at = old + ((s01.x + s01.y) + (s23.x + s23.y));
+                sr.next();
+            }
+            if (!slot && two) sr.next();
         }
-        if (at) *at = old + ((s01.x + s01.y) + (s23.x + s23.y));
     }
 }
 
@@ -543,10 +687,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
-            if (i >= B_Q_FULL && i < B_Q_EMPTY) n = 2;                         // the copy and the constants
-            if (i >= B_Q_EMPTY && i < B_AK_FULL) n = 1 + kRowThreads / 32;     // the MMAs and the sums
-            if (i >= B_UNIT_EMPTY && i < B_ACC_FULL) n = 3 + kRowThreads / 32;
-            if (i >= B_ACC_EMPTY && i < B_DRAIN) n = 4;
+            if (i >= B_UNIT_EMPTY && i < B_ACC_FULL) n = 3 + kSumWarps;
+            if (i >= B_ACC_EMPTY && i < B_SIDE_FULL) n = kSumWarps / 2;        // a tile's warps
+            if (i >= B_SIDE_EMPTY && i < B_NL_FULL) n = 4;                     // a tile's warps
+            if (i >= B_NL_EMPTY && i < B_R_FULL) n = kSumWarps;
+            if (i == B_R_FULL) n = kSumWarps / 2;
+            if (i == B_R_EMPTY) n = kSumWarps;
             ptx::mbar_init(bars + 8u * (uint32_t)i, n);
         }
         *sh.abort_flag = 0;
@@ -565,11 +711,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     grid_wait();
     grid_release();
-    if (warp == 0) load_role<D, AK>(tp, sh, &tm_q, &tm_k, &tm_ak);
-    else if (warp == 1) mma_role<D, AK>(tp, sh, tmem);
-    else if (warp == 2) const_role(tp, sh);
-    else if (warp == 3) ticket_role<AK>(tp, sh);
-    else sum_role<D, AK>(tp, sh, tmem, (warp - 4) >> 2);
+    if (warp < 4) {
+        if (warp == 0) load_role<D, AK>(tp, sh, &tm_q, &tm_k, &tm_ak);
+        else if (warp == 1) mma_role<D, AK>(tp, sh, tmem);
+        else if (warp == 2) const_role(tp, sh);
+        else ticket_role<AK>(tp, sh);
+    } else {
+        sum_role<D, AK>(tp, sh, tmem, (warp - 4) >> 2);
+    }
     __syncwarp();
     ptx::tc_fence_before();
     ptx::cta_barrier();
@@ -598,22 +747,26 @@ cudaError_t launch_d(const PagedWeightsArgs &wa, const WeightParams &w, cudaStre
     const Params &p = w.p;
     const bool ak = a.aK != nullptr;
     tp.TS = BM / p.g;
+    tp.w.tile_tokens = tp.TS;
     tp.npad = (p.clip_k + 1 + 15) / 16 * 16;
     tp.SR = (p.clip_k + 1) | 1;   // a column walk of R hits 32 banks
     tp.box = a.page_size < kTile ? a.page_size : kTile;
     tp.tile_bytes = (uint32_t)kTile * D * 2;
     const uint32_t ak_bytes = ak && p.clip_k ? (uint32_t)tp.npad * D * 2 : 0, r_bytes = ak && p.clip_k ? BM * tp.SR * 4 : 0;
-    const uint32_t rest = (r_bytes + 15) / 16 * 16 + kMaxQ * BM * 4 + kUnits * sizeof(Unit) + kNumBars * 8 + 16;
-    // two tiles of keys at least, more query tiles than key tiles
+    const uint32_t rest = r_bytes + kBatches * kBatch * BM * 4 + kSides * kSideBytes + kUnits * sizeof(Unit) + kNumBars * 8 + 16;
     int stages = (int)(((uint32_t)di.smem_optin - rest - ak_bytes) / tp.tile_bytes);
     if (stages > kMaxK + kMaxQ) stages = kMaxK + kMaxQ;
     if (stages < 4) return cudaErrorNotSupported;
-    tp.nk = stages / 2;
-    tp.nq = stages - tp.nk;
+    // Two tiles of keys are enough where they move on to TMEM. One query tile to a request: the keys stream
+    // by and the query tile stays, so more keys are on their way
+    const long long rows = (long long)(a.max_new > 0 ? a.max_new : a.tokens / a.B) * p.g;
+    tp.nk = rows <= BM ? (stages - 2 < kMaxK ? stages - 2 : kMaxK) : 2;
+    tp.nq = stages - tp.nk < kMaxQ ? stages - tp.nk : kMaxQ;
     tp.off_q = tp.nk * tp.tile_bytes;
     tp.off_ak = tp.off_q + tp.nq * tp.tile_bytes;
     tp.off_nl = tp.off_ak + ak_bytes;
-    tp.off_unit = tp.off_nl + kMaxQ * BM * 4;
+    tp.off_side = tp.off_nl + kBatches * kBatch * BM * 4;
+    tp.off_unit = tp.off_side + kSides * kSideBytes;
     tp.off_bar = tp.off_unit + kUnits * sizeof(Unit);
     tp.off_r = tp.off_bar + kNumBars * 8 + 16;
     uint32_t smem = tp.off_r + r_bytes;
@@ -624,7 +777,8 @@ cudaError_t launch_d(const PagedWeightsArgs &wa, const WeightParams &w, cudaStre
     tm[2] = tm[0];
     const uint64_t Ht = a.ths ? (uint64_t)a.Hkv : 1, hs = a.ths ? (uint64_t)a.ths * 2 : (uint64_t)(2 * a.clip_k + 1) * D * 2;
     if (ak && !tc::make_map(&tm[2], a.aK, D, p.clip_k + 1, Ht, D * 2, hs, (uint32_t)tp.npad)) return cudaErrorInvalidValue;
-    cudaError_t e = launch_weights_prep(w, true, s);
+    tp.old_by_tma = masses_by_tma(w);
+    cudaError_t e = launch_weights_prep(tp.w, true, s);
     if (e != cudaSuccess) return e;
     return ak ? launch_variant<D, true>(tm, tp, smem, di.sms, s) : launch_variant<D, false>(tm, tp, smem, di.sms, s);
 }
