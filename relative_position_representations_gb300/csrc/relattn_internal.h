@@ -274,8 +274,9 @@ struct PagedArgs {
     void *out;                        // [tokens, H, d]
     float *lse;                       // [tokens, H] or null: the rows' log-sum-exp
     // parts of a call with shared prefixes (Params has what they mean); 0 and null otherwise
-    int flat, f32_out;
-    const int *first_key, *row_of;
+    int flat, f32_out, overlap;
+    const int *first_key, *row_of, *ctas;
+    struct PagedMerge *merge;         // where to leave the merge that is to follow; null: it is launched
     void *workspace;                  // at least paged_workspace_bytes
     int *err;
     long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)

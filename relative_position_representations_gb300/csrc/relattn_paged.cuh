@@ -23,6 +23,9 @@
 #include "relattn_internal.h"
 
 namespace relattn {
+
+struct PagedMerge;
+
 namespace paged {
 
 constexpr int kTile = 128;               // keys per tile
@@ -65,8 +68,11 @@ struct Params {
     int f32_out;                             // out is fp32 whatever the inputs are
     const int *first_key;                    // [tokens] or null: first key of the token's request (whole tiles)
     const int *row_of;                       // [B] or null: the request's row of the block table
+    const int *ctas;                         // CTAs that share the work (the others have none); null: all
+    int overlap;                             // runs beside the kernel in front of it, and ends after it
     Desc *desc;                              // [gridDim.x]
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
+    PagedMerge *merge;                       // host: PagedArgs has what it means
     int *err;
     long long wait_limit;
     int withhold;                            // test hook: a CTA's first queries are announced, not loaded
@@ -141,6 +147,10 @@ __device__ __forceinline__ int range_begin(int total, int c, int G) {
 __device__ __forceinline__ long long range_begin(long long total, int c, int G) {
     if (total < (1LL << 31)) return range_begin((int)total, c, G);
     return total / G * c + total % G * c / G;
+}
+// CTAs of the launch that take part
+__device__ __forceinline__ int grid_of(const Params &p, int launched) {
+    return p.ctas ? min(max(*p.ctas, 1), launched) : launched;
 }
 
 // ------------------------------------------------------------------ a CTA's range
@@ -265,7 +275,7 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
 }
 
 __device__ __forceinline__ Range find_range(const Params &p) {
-    const int c = (int)blockIdx.x, G = (int)gridDim.x;
+    const int c = (int)blockIdx.x, G = grid_of(p, (int)gridDim.x);
     return p.long_line ? find_range_t<long long>(p, c, G) : find_range_t<int>(p, c, G);
 }
 
@@ -394,13 +404,20 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
         d.total = total;
         // A tile belongs to the range that holds its first position. Ranges as long as a tile hold
         // one each, up to the range of the last tile; position y lies in range ((y + 1) G - 1) / total.
-        const int G = (int)gridDim.x;
+        const int G = grid_of(p, (int)gridDim.x);
         if (total / G >= g->it.wt) {
             const long long y = g->x + p.c0 + (long long)g->it.wt * (g->it.nt - 1);
             d.n = (int)min(((y + 1) * G - 1) / total, (long long)G - 1) - (int)blockIdx.x + 1;   // in the grid
         }
     }
     p.desc[blockIdx.x] = d;
+}
+
+// a CTA of the launch without a part in the work
+__device__ __forceinline__ bool idle_cta(const Params &p) {
+    if (!p.ctas || (int)blockIdx.x < grid_of(p, (int)gridDim.x)) return false;
+    if (threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
+    return true;
 }
 
 __device__ __forceinline__ float *record(const Params &p, int c, int which) {
@@ -460,6 +477,8 @@ cudaError_t launch_early(void (*kern)(Args...), dim3 grid, int threads, size_t s
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
+// (with p.overlap a kernel starts when the one in front of it has passed this wait itself, so that what
+// stands in front of that one is over; it waits for it at its own end)
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the dependent kernel's CTAs come up beside this one's. After grid_wait(): what stands in front
 // of this kernel is then over for the dependent too.
@@ -469,6 +488,14 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 void fill_params(const PagedArgs &a, Params *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s);
+// the merges that two calls with f32_out have left (rows of 16 bytes' multiples), in one launch
+cudaError_t launch_merges(const PagedMerge &a, const PagedMerge &b, cudaStream_t s);
 
 }  // namespace paged
+
+struct PagedMerge {
+    paged::Params p;
+    int grid = 0;   // 0: nothing to merge
+};
+
 }  // namespace relattn

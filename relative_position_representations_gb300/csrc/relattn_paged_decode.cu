@@ -144,7 +144,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
     // the boxes of a tile: 128 / box pages (at most 16) x DB blocks of columns, one per lane
     const int nbox = kTile / box, my_box = lane % nbox, my_blk = lane / nbox;
     const uint32_t my_dst = base + my_blk * (kTile * 128) + my_box * box * 128;
-    const Range rg = find_range_t<int>(p, (int)blockIdx.x, (int)gridDim.x);
+    const Range rg = find_range_t<int>(p, (int)blockIdx.x, grid_of(p, (int)gridDim.x));
     Walk walk(p, rg);
     Segment g{};
     uint32_t it = 0, tiles = 0;
@@ -597,12 +597,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
         ptx::tma_prefetch_desc(&tm_v);
     }
     __syncthreads();
-    grid_wait();
+    if (!p.overlap) grid_wait();
     grid_release();
-    if (threadIdx.x >= kRowThreads)
-        feed_role<D, NT>(p, L, smem, waits, &tm_q, &tm_k, &tm_v, stages, box);
-    else
-        row_role<D, NT, AK, AV>(p, L, smem, waits, stages);
+    if (!idle_cta(p)) {
+        if (threadIdx.x >= kRowThreads)
+            feed_role<D, NT>(p, L, smem, waits, &tm_q, &tm_k, &tm_v, stages, box);
+        else
+            row_role<D, NT, AK, AV>(p, L, smem, waits, stages);
+    }
+    if (p.overlap) grid_wait();
 }
 
 template <int D, int NT, bool AK, bool AV>

@@ -9,7 +9,10 @@
 // so the part needs neither positions nor masks nor tables: it is plain attention, and the two constants
 // enter where the parts are joined. Both parts run on the kernels of relattn_paged_fwd, which leave
 // fp32 outputs and log-sum-exps: the first with a group for a request and all of its tokens at the
-// shared part's end, the second from the shared part's end on.
+// shared part's end, the second from the shared part's end on. They run side by side: the first is bound by
+// its chain of products and softmax, the second by HBM, and neither needs the other, so a kernel in front
+// measures their work and gives each as many SMs that both end together; the second's CTAs come up where
+// the first's have nothing to do.
 #include <cstdint>
 #include <cstring>
 
@@ -23,18 +26,30 @@ constexpr int kSplitThreads = 1024;
 constexpr int kSplitWarps = kSplitThreads / 32;
 constexpr int kJoinThreads = 256;
 
+// What the parts take, in SM cycles: an item, a tile of keys of an item of at most one query tile (of the
+// first part; the only kind of the second), one of two; and what a CTA takes beside its work.
+struct Costs {
+    float item, tile, tile2, fixed;
+};
+
 struct SplitParams {
     Params p;                         // q_start, kv_len, B, tokens, cap, clip_k
     const int *group_start, *prefix_len;
     int groups, most;                 // entries of the lists below
     int *first_key;                   // [tokens]: where the own keys of the token's request begin
     int *q_start, *kv_len, *row_of;   // [most + 1], [most], [most]: the shared parts as requests
+    int *ctas;                        // [2]: CTAs of the two parts, which run side by side
+    int sms, own_per_sm;              // SMs; CTAs of the second part that an SM holds
+    int tile_tokens;                  // tokens of a query tile of the first part
+    int own_tokens;                   // tokens of an item of the second part
+    Costs shared, own;
 };
 
 // Which groups share what. Entry 2 i is the i-th group that shares keys, entry 2 i + 1 the rows up to the
 // next one (without keys). A warp per group.
 __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __grid_constant__ SplitParams sp) {
     __shared__ int on_s[kSplitWarps], end_s;
+    __shared__ float work_s[2][kSplitWarps];
     const Params &p = sp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_wait();
@@ -42,6 +57,7 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
     for (int t = tid; t < p.tokens; t += kSplitThreads) sp.first_key[t] = 0;
     if (tid == 0) end_s = 0;
     int done = 0;
+    float work = 0.f;
     for (int g0 = 0; g0 < sp.groups; g0 += kSplitWarps) {
         const int g = g0 + warp;
         int keys = 0, q0 = 0, q1 = 0, row = 0;
@@ -74,6 +90,10 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
         const unsigned all = __ballot_sync(0xffffffffu, on_s[lane] != 0);
         const int i = done + __popc(all & ((1u << warp) - 1));
         if (on && 2 * i + 1 < sp.most + 1) {
+            const int n = q1 - q0, pairs = n / (2 * sp.tile_tokens), rest = n - pairs * 2 * sp.tile_tokens;
+            if (lane == 0)
+                work += (float)p.Hkv * (pairs * (sp.shared.item + sp.shared.tile2 * (keys / kTile)) +
+                                        (rest ? sp.shared.item + (rest > sp.tile_tokens ? sp.shared.tile2 : sp.shared.tile) * (keys / kTile) : 0.f));
             for (int t = q0 + lane; t < q1; t += 32) sp.first_key[t] = keys;
             if (lane == 0) {
                 sp.q_start[2 * i] = q0;
@@ -93,6 +113,57 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
     for (int i = 2 * done + tid; i <= sp.most; i += kSplitThreads) {
         sp.q_start[i] = end_s;
         if (i < sp.most) sp.kv_len[i] = sp.row_of[i] = 0;
+    }
+    // the own keys' work, and the SMs of either part: as many that both end together
+    float own = 0.f;
+    for (int b = tid; b < p.B; b += kSplitThreads) {
+        const Seq s = load_seq(p, b);
+        const int last = s.pos0 + s.n - 1;
+        if (s.n == 0 || last < 0) continue;
+        const int tiles = max(last / kTile + 1 - sp.first_key[s.q0] / kTile, 0);
+        own += (float)p.Hkv * ((s.n + sp.own_tokens - 1) / sp.own_tokens) * (sp.own.item + sp.own.tile * tiles);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        own += __shfl_xor_sync(0xffffffffu, own, o);
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+    }
+    if (lane == 0) {
+        work_s[0][warp] = work;
+        work_s[1][warp] = own;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        work = work_s[0][lane];
+        own = work_s[1][lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            work += __shfl_xor_sync(0xffffffffu, work, o);
+            own += __shfl_xor_sync(0xffffffffu, own, o);
+        }
+        float best = INFINITY;
+        int at = 1;
+        for (int n = 1 + lane; n < sp.sms; n += 32) {
+            const float t = fmaxf(work / n + sp.shared.fixed, own / (sp.sms - n) + sp.own.fixed);
+            if (t < best) {
+                best = t;
+                at = n;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float t = __shfl_xor_sync(0xffffffffu, best, o);
+            const int n = __shfl_xor_sync(0xffffffffu, at, o);
+            if (t < best || (t == best && n < at)) {
+                best = t;
+                at = n;
+            }
+        }
+        if (work == 0.f) at = 1;
+        if (lane == 0) {
+            sp.ctas[0] = at;
+            sp.ctas[1] = max(sp.sms - at, 1) * sp.own_per_sm;
+        }
     }
 }
 
@@ -141,15 +212,20 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_
     if (p.lse && lane == 0) p.lse[row] = row_lse(mu, l);
 }
 
+// [d > 64] as measured: tiles of the kernel for chunks with one and two query tiles; tiles of the one for generated
+// tokens, which HBM bounds
+constexpr Costs kChunkCosts[2] = {{6400.f, 1900.f, 2550.f, 6400.f}, {8600.f, 2600.f, 3450.f, 8600.f}};
+constexpr Costs kTokenCosts[2] = {{1100.f, 1100.f, 1100.f, 2200.f}, {2200.f, 2200.f, 2200.f, 4400.f}};
+
 size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 }  // namespace
 }  // namespace paged
 
-// workspace: that of the parts, their outputs and log-sum-exps, first keys, the shared parts' list
+// workspace: that of either part, their outputs and log-sum-exps, first keys, the shared parts' list, CTAs
 unsigned long long paged_shared_workspace_bytes(int tokens, int H, int d) {
     const size_t rows = (size_t)tokens * H;
-    return paged_workspace_bytes(d) + 2 * paged::round16(rows * d * 4) + 2 * paged::round16(rows * 4) +
+    return 2 * paged_workspace_bytes(d) + 16 + 2 * paged::round16(rows * d * 4) + 2 * paged::round16(rows * 4) +
            4 * paged::round16(((size_t)tokens + 2) * 4);
 }
 
@@ -160,7 +236,7 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     // the table hold the prefix too.
     if (a.window > 0 || sa.groups == 0 || a.tokens < 2) return launch_paged(a, s);
     const size_t rows = (size_t)a.tokens * a.H, ints = round16(((size_t)a.tokens + 2) * 4);
-    char *w = static_cast<char *>(a.workspace) + paged_workspace_bytes(a.d);
+    char *w = static_cast<char *>(a.workspace) + 2 * paged_workspace_bytes(a.d);
     auto take = [&](size_t bytes) {
         char *at = w;
         w += bytes;
@@ -181,6 +257,18 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     sp.q_start = reinterpret_cast<int *>(take(ints));
     sp.kv_len = reinterpret_cast<int *>(take(ints));
     sp.row_of = reinterpret_cast<int *>(take(ints));
+    sp.ctas = reinterpret_cast<int *>(take(16));
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return cudaErrorInvalidDevice;
+    const int g = sp.p.g;
+    sp.sms = di.sms;
+    sp.tile_tokens = 128 / g;
+    sp.shared = kChunkCosts[a.d > 64];
+    // (a.max_new is a hint; the split of the SMs follows it, the results do not)
+    const bool few = paged_decode_covers(a);
+    sp.own_tokens = few ? 16 / g : 2 * sp.tile_tokens;
+    sp.own = few ? kTokenCosts[a.d > 64] : kChunkCosts[a.d > 64];
+    sp.own_per_sm = few && a.d <= 64 ? 2 : 1;
     cudaError_t e = launch_early(shared_split_kernel, dim3(1), kSplitThreads, 0, s, sp);
     if (e != cudaSuccess) return e;
     PagedArgs part = a;      // the shared keys
@@ -195,13 +283,29 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     part.flat = part.f32_out = 1;
     part.out = o_a;
     part.lse = lse_a;
+    PagedMerge merges[2];
+    part.merge = &merges[0];
+    part.ctas = sp.ctas;
     if ((e = launch_paged(part, s)) != cudaSuccess) return e;
     part = a;                // each request's own
     part.first_key = sp.first_key;
     part.f32_out = 1;
     part.out = o_b;
     part.lse = lse_b;
+    part.workspace = static_cast<char *>(a.workspace) + paged_workspace_bytes(a.d);
+    part.merge = &merges[1];
+    part.ctas = sp.ctas + 1;
+    part.overlap = 1;
     if ((e = launch_paged(part, s)) != cudaSuccess) return e;
+    if (merges[0].grid && merges[1].grid) {
+        if ((e = launch_merges(merges[0], merges[1], s)) != cudaSuccess) return e;
+    } else {   // (what ran on the SIMT units has been merged)
+        for (PagedMerge &m : merges)
+            if (m.grid) {
+                m.p.merge = nullptr;
+                if ((e = launch_merge(m.p, m.grid, true, s)) != cudaSuccess) return e;
+            }
+    }
     JoinParams j;
     std::memset(&j, 0, sizeof(j));
     j.q = a.q;

@@ -981,12 +981,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Before the warpgroups trade registers (the scan needs more than a control warp keeps), and by
     // every warp alike: the compiler fails to allocate a branch of one warp here.
     Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
-    grid_wait();
+    if (!p.overlap) grid_wait();
     grid_release();
+    if (idle_cta(p)) {
+        if (p.overlap) grid_wait();
+        return;
+    }
     {
         // (64 requests at a time: at 128 the cold code costs a short step 0.4 us, at 32 the loop costs a
         // step of 1024 requests 4 us)
-        const Range r = find_range_t<int, 2>(p, (int)blockIdx.x, (int)gridDim.x);
+        const Range r = find_range_t<int, 2>(p, (int)blockIdx.x, grid_of(p, (int)gridDim.x));
         if (threadIdx.x == 96) *range = r;
     }
     if (warp == 1) ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
@@ -1020,6 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem_raw, 512);
     }
+    if (p.overlap) grid_wait();
 }
 
 // ======================================================================= host
