@@ -3,7 +3,7 @@
 // accumulated weight, ties to the earlier key. The kept keys close up in place, in their order.
 //
 // Selection. A unit is one head of one such request, taken by a cluster of 1, 2, 4 or 8 CTAs (as many
-// as the longest row of the table can use, 16384 keys each). The CTAs hold their keys' weights in
+// as the longest row of the table can use, 16384 keys each; shorter tables have smaller CTAs). The CTAs hold their keys' weights in
 // registers, as integers in the same order, and find the budget's last weight by three histograms
 // (11, 11 and 10 bits) that they add up over distributed shared memory: the weights are read once. A
 // unit past the cluster's registers reads them again (out of L2) in each pass. What comes out is
@@ -30,10 +30,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kRun = 128;                    // keys of a run
 constexpr int kLeastBlock = 16;              // places of a block at least
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kRunsHeld = 4 * kSelWarps;     // runs whose weights a CTA holds: four of each warp
+constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
+// runs whose weights a selecting CTA holds: four of each warp
+__host__ __device__ constexpr int runs_held(int threads) { return threads / 8; }
 constexpr int kMoveThreads = 256;
 constexpr int kInFlight = 16;                // vectors of a thread on their way
 constexpr int kTimeout = 4;                  // RELATTN_ERR_TIMEOUT in the status word
@@ -62,8 +62,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 
 __device__ __forceinline__ int length_of(const EvictParams &p, int b) { return min(max(p.a.kv_len[b], 0), p.cap); }
 
-template <bool VEC>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p, int C) {
+template <bool VEC, int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
+    evict_select_kernel(const __grid_constant__ EvictParams p, int C) {
+    constexpr int kSelWarps = kSelThreads / 32, kRunsHeld = runs_held(kSelThreads), kMine = kBins / kSelThreads;
+    constexpr int kSums = kRunsHeld / 32;    // runs of a lane where a warp adds them all up
     __shared__ uint32_t hist[2][kBins];
     __shared__ uint32_t bits[kBitWords];
     __shared__ int before[kBitWords];        // requests to cut in front of each word
@@ -114,12 +117,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     for (int u = (int)blockIdx.x / C; u < units; u += groups) {
         const int r = u / a.Hkv, h = u - r * a.Hkv;
         __syncthreads();
-        if (tid < words) {
-            const int i = r - before[tid];
-            if (i >= 0 && i < __popc(bits[tid])) {   // the i-th bit of the word
-                uint32_t w = bits[tid];
+        for (int at = tid; at < words; at += kSelThreads) {
+            const int i = r - before[at];
+            if (i >= 0 && i < __popc(bits[at])) {   // the i-th bit of the word
+                uint32_t w = bits[at];
                 for (int q = 0; q < i; ++q) w &= w - 1;
-                unit_b = 32 * tid + __ffs(w) - 1;
+                unit_b = 32 * at + __ffs(w) - 1;
             }
         }
         if (tid < 2) totals[tid] = 0;
@@ -191,15 +194,34 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
                 }
                 cluster.sync();
                 for (int i = tid; i < kBins; i += kSelThreads) hist[(pass + 1) & 1][i] = 0;
-                // bins from the top, two a thread, over the cluster
-                const int d0 = kBins - 1 - 2 * tid;
-                int n0 = 0, n1 = 0;
-                for (int q = 0; q < C; ++q) {
-                    const uint32_t *rh = C == 1 ? hs : cluster.map_shared_rank(hs, q);
-                    n0 += (int)rh[d0];
-                    n1 += (int)rh[d0 - 1];
+                // bins from the top, kMine a thread, over the cluster
+                const int d0 = kBins - kMine * (tid + 1);   // the thread's lowest
+                int n[kMine];
+#pragma unroll
+                for (int e = 0; e < kMine; ++e) n[e] = 0;
+                if (C == 1) {
+#pragma unroll
+                    for (int e = 0; e < kMine; ++e) n[e] = (int)hs[d0 + e];
+                } else {
+                    uint2 v[kMaxCluster][kMine / 2];   // (all on their way together)
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q)
+#pragma unroll
+                        for (int e = 0; e < kMine; e += 2)
+                            v[q][e / 2] = q < C ? *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(hs, q) + d0 + e)
+                                                : make_uint2(0, 0);
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q)
+#pragma unroll
+                        for (int e = 0; e < kMine; e += 2) {
+                            n[e] += (int)v[q][e / 2].x;
+                            n[e + 1] += (int)v[q][e / 2].y;
+                        }
                 }
-                int v = n0 + n1;
+                int mine = 0;
+#pragma unroll
+                for (int e = 0; e < kMine; ++e) mine += n[e];
+                int v = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int x = __shfl_up_sync(0xffffffffu, v, o);
@@ -210,13 +232,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
                 int s = lane < warp ? warp_sum[lane] : 0;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const int above = s + v - n0 - n1;   // keys in higher bins
-                if (above < rest && rest <= above + n0) {
-                    pick_bin = d0;
-                    pick_rest = rest - above;
-                } else if (above + n0 < rest && rest <= above + n0 + n1) {
-                    pick_bin = d0 - 1;
-                    pick_rest = rest - above - n0;
+                int above = s + v - mine;   // keys in higher bins
+#pragma unroll
+                for (int e = kMine - 1; e >= 0; --e) {
+                    if (above < rest && rest <= above + n[e]) {
+                        pick_bin = d0 + e;
+                        pick_rest = rest - above;
+                    }
+                    above += n[e];
                 }
                 __syncthreads();
                 T |= (uint32_t)pick_bin << sh;
@@ -274,11 +297,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
                 if (lane == 0) count[i * kSelWarps + warp] = both;
             }
             __syncthreads();
-            // sums in front of every run: lane l of each warp has runs 4 l .. 4 l + 3
-            int q[4], x_all = 0, y_all = 0;
+            // sums in front of every run: lane l of each warp has runs kSums l .. kSums l + kSums - 1
+            int q[kSums], x_all = 0, y_all = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                q[e] = count[4 * lane + e];
+            for (int e = 0; e < kSums; ++e) {
+                q[e] = count[kSums * lane + e];
                 x_all += q[e] & 0xffff;
                 y_all += q[e] >> 16;
             }
@@ -298,16 +321,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
                 {
                     int xa = xi - x_all, ya = yi - y_all;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (e == (w & 3)) {
+                    for (int e = 0; e < kSums; ++e) {
+                        if (e == w % kSums) {
                             xs = xa;
                             ys = ya;
                         }
                         xa += q[e] & 0xffff;
                         ya += q[e] >> 16;
                     }
-                    xs = __shfl_sync(0xffffffffu, xs, w >> 2) + at_above;
-                    ys = __shfl_sync(0xffffffffu, ys, w >> 2) + at_even;
+                    xs = __shfl_sync(0xffffffffu, xs, w / kSums) + at_above;
+                    ys = __shfl_sync(0xffffffffu, ys, w / kSums) + at_even;
                 }
                 if (c >= c1) continue;       // the whole warp alike
                 unsigned x, y;
@@ -420,9 +443,12 @@ __device__ __forceinline__ void store_release(int *p, int v) {
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// vpr: vectors of a row of d elements
-template <typename V>
+// vpr: vectors of a row of d elements. EVEN: a key's vectors (2 vpr) divide the threads, so that a thread's are
+// all of one place in their rows (what goes for every row of a power of two; the addresses of a block take
+// four times its loads otherwise)
+template <typename V, bool EVEN>
 __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictParams p, int vpr) {
+    __shared__ long long from_at[kRun], to_at[kRun];   // where the rows are: bytes behind k_pages or v_pages
     __shared__ int from[kRun], to[kRun];     // slots; -1: the row stays where it is
     __shared__ int item_s, ok_s;
     const PagedEvictArgs &a = p.a;
@@ -436,14 +462,18 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
     const int units = p.state[1] * a.Hkv, blocks = (a.budget + p.block - 1) / p.block;
     const long long items = (long long)units * blocks;
     const int row_vecs = 2 * vpr;            // a block's fit the CTA's registers
+    const int my_rem = tid % row_vecs, my_row = tid / row_vecs, row_step = kMoveThreads / row_vecs;   // EVEN
     const int P = a.page_size;
     auto base = [&](bool v) { return static_cast<char *>(v ? a.v_pages : a.k_pages); };
+    int ahead = 0;                           // the next ticket, taken while this one's block is moved
+    if (tid == 0) ahead = atomicAdd(&p.state[0], 1);
     for (;;) {
-        if (tid == 0) item_s = atomicAdd(&p.state[0], 1);
+        if (tid == 0) item_s = ahead;
         if (tid < kRun) from[tid] = -1;
         __syncthreads();
         const int item = item_s;
         if (item < 0 || item >= items) break;
+        if (tid == 0) ahead = atomicAdd(&p.state[0], 1);
         const int t = item / units, u = item - t * units, r = u / a.Hkv, h = u - r * a.Hkv;
         const int2 req = p.list[r];
         const int runs = (req.y + kRun - 1) / kRun;
@@ -481,20 +511,34 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
         }
         if (tid < cnt) to[tid] = slot_of(i0 + tid);
         __syncthreads();
+        auto place = [&](int slot) { return (long long)(slot >> p.shift) * a.page_bytes + ((long long)h * P + (slot & (P - 1))) * a.row_bytes; };
+        if (tid < cnt) {
+            const bool moves = from[tid] >= 0 && to[tid] >= 0;
+            from_at[tid] = moves ? place(from[tid]) : -1;
+            to_at[tid] = moves ? place(to[tid]) : -1;
+        }
+        __syncthreads();
         // ---- rows into registers
-        const int nv = cnt * row_vecs;
         V x[kInFlight];
         float w = 0.f;
+        // the k-th of this thread's vectors: its row (no less than cnt: none), and where in the row
+        auto vector = [&](int k, int &row, char *&at) {
+            int rem = my_rem;
+            row = my_row + k * row_step;
+            if (!EVEN) {
+                const int i = tid + k * kMoveThreads;
+                row = i / row_vecs;
+                rem = i - row * row_vecs;
+            }
+            const bool kv = rem >= vpr;
+            at = base(kv) + (long long)(rem - (kv ? vpr : 0)) * sizeof(V);
+        };
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {
-            const int i = tid + k * kMoveThreads;
-            if (i >= nv) continue;
-            const int row = i / row_vecs, rem = i - row * row_vecs, kv = rem >= vpr, c = rem - kv * vpr;
-            const int s = from[row];
-            if (s < 0 || to[row] < 0) continue;
-            x[k] = *reinterpret_cast<const V *>(base(kv) + (long long)(s >> p.shift) * a.page_bytes +
-                                                ((long long)h * P + (s & (P - 1))) * a.row_bytes +
-                                                (long long)c * sizeof(V));
+            int row;
+            char *at;
+            vector(k, row, at);
+            if (row < cnt && from_at[row] >= 0) x[k] = *reinterpret_cast<const V *>(at + from_at[row]);
         }
         const int mine = tid < cnt && to[tid] >= 0 ? from[tid] : -1;
         if (mine >= 0) w = a.mass[(long long)(mine >> p.shift) * a.mass_stride + (long long)h * P + (mine & (P - 1))];
@@ -517,13 +561,10 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
         if (ok_s) {
 #pragma unroll
             for (int k = 0; k < kInFlight; ++k) {
-                const int i = tid + k * kMoveThreads;
-                if (i >= nv) continue;
-                const int row = i / row_vecs, rem = i - row * row_vecs, kv = rem >= vpr, c = rem - kv * vpr;
-                const int s = to[row];
-                if (s < 0 || from[row] < 0) continue;
-                *reinterpret_cast<V *>(base(kv) + (long long)(s >> p.shift) * a.page_bytes +
-                                       ((long long)h * P + (s & (P - 1))) * a.row_bytes + (long long)c * sizeof(V)) = x[k];
+                int row;
+                char *at;
+                vector(k, row, at);
+                if (row < cnt && to_at[row] >= 0) *reinterpret_cast<V *>(at + to_at[row]) = x[k];
             }
             if (mine >= 0) {
                 const int s = to[tid];
@@ -573,13 +614,15 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s) {
     p.blocks = p.runs * (kRun / p.block);
     const paged::DeviceInfo di = paged::device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
+    // the smallest CTAs that hold a row of the table, then clusters of the largest
+    const int threads = p.runs <= runs_held(256) ? 256 : p.runs <= runs_held(512) ? 512 : 1024;
     int C = 1;
-    while (C < 8 && (long long)C * kRunsHeld < p.runs) C *= 2;
-    const size_t most = (size_t)(2 * di.sms / C);
+    while (C < kMaxCluster && (long long)C * runs_held(threads) < p.runs) C *= 2;
+    const size_t most = (size_t)(2 * di.sms * (1024 / threads) / C);
     const int groups = (int)(units < most ? units : most);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(groups * C);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -591,9 +634,13 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s) {
     cfg.attrs = at;
     cfg.numAttrs = 2;
     const bool vec = a.page_size % 4 == 0 && a.mass_stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.mass) % 16 == 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? evict_select_kernel<true> : evict_select_kernel<false>, p, C);
+    auto select = threads == 256 ? (vec ? evict_select_kernel<true, 256> : evict_select_kernel<false, 256>)
+                  : threads == 512 ? (vec ? evict_select_kernel<true, 512> : evict_select_kernel<false, 512>)
+                                   : (vec ? evict_select_kernel<true, 1024> : evict_select_kernel<false, 1024>);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, select, p, C);
     if (e != cudaSuccess) return e;
-    auto move = wide == 16 ? evict_move_kernel<uint4> : wide == 4 ? evict_move_kernel<uint32_t> : evict_move_kernel<uint16_t>;
+    auto move = wide == 16 ? evict_move_kernel<uint4, false> : wide == 4 ? evict_move_kernel<uint32_t, false> : evict_move_kernel<uint16_t, false>;
+    if (wide == 16 && kMoveThreads % (2 * vpr) == 0) move = evict_move_kernel<uint4, true>;
     return paged::launch_early(move, dim3(2 * di.sms + 1), kMoveThreads, 0, s, p, vpr);
 }
 
