@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
                 }
                 const int each = kRun / p.block, t = (off + p.block - 1) / p.block + lane;
                 if (lane < each) p.done[(long long)u * p.blocks + c * each + lane] = 0;
-                if (t * p.block < off + kept) p.start[(long long)u * p.blocks + t] = c;
+                if (t < p.blocks && t * p.block < off + kept) p.start[(long long)u * p.blocks + t] = c;
             }
             at_above += __shfl_sync(0xffffffffu, xi, 31);
             at_even += __shfl_sync(0xffffffffu, yi, 31);
@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
 // One block: kv_len_out, and the pages behind the budget back onto the list, request by request.
 __device__ void evict_lengths(const EvictParams &p) {
     const PagedEvictArgs &a = p.a;
-    __shared__ int warp_sum[kMoveThreads / 32];
+    __shared__ int warp_sum[kMoveThreads / 32], count_s[kMoveThreads], to_s[kMoveThreads];
+    constexpr int kManyPages = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int first = (int)(((long long)a.budget + a.page_size - 1) >> p.shift);
     const int requests = p.state[1];
@@ -423,13 +424,25 @@ __device__ void evict_lengths(const EvictParams &p) {
         int sum;
         const int mine = at + block_scan(n, sum) - n;
         at += sum;
-        // a warp per request writes its pages
-        for (int q = 0; q < 32; ++q) {
-            const int nn = __shfl_sync(0xffffffffu, n, q), to = __shfl_sync(0xffffffffu, mine, q);
-            if (nn == 0) continue;
-            const int *row = a.block_table + (long long)p.list[i0 + 32 * warp + q].x * a.bt_stride + first;
-            for (int e = lane; e < nn; e += 32) dst[to + e] = row[e];
+        // a warp per request writes its pages, or the block where they are many
+        __syncthreads();
+        count_s[tid] = n;
+        to_s[tid] = mine;
+        __syncthreads();
+        for (int q = warp; q < kMoveThreads; q += kMoveThreads / 32) {
+            const int nn = count_s[q];
+            if (nn > kManyPages) continue;
+            const int *row = a.block_table + (long long)(nn ? p.list[i0 + q].x : 0) * a.bt_stride + first;
+            for (int e = lane; e < nn; e += 32) dst[to_s[q] + e] = row[e];
         }
+        for (int q = 0; q < min(kMoveThreads, requests - i0); ++q) {
+            const int nn = count_s[q];
+            if (nn <= kManyPages) continue;
+            const int *row = a.block_table + (long long)p.list[i0 + q].x * a.bt_stride + first;
+#pragma unroll 4
+            for (int e = tid; e < nn; e += kMoveThreads) dst[to_s[q] + e] = row[e];
+        }
+        __syncthreads();
     }
 }
 
@@ -455,10 +468,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     paged::grid_wait();
     paged::grid_release();
-    if (blockIdx.x == gridDim.x - 1) {
-        evict_lengths(p);
-        return;
-    }
+    if (blockIdx.x == 0) evict_lengths(p);
     const int units = p.state[1] * a.Hkv, blocks = (a.budget + p.block - 1) / p.block;
     const long long items = (long long)units * blocks;
     const int row_vecs = 2 * vpr;            // a block's fit the CTA's registers
@@ -641,7 +651,7 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     auto move = wide == 16 ? evict_move_kernel<uint4, false> : wide == 4 ? evict_move_kernel<uint32_t, false> : evict_move_kernel<uint16_t, false>;
     if (wide == 16 && kMoveThreads % (2 * vpr) == 0) move = evict_move_kernel<uint4, true>;
-    return paged::launch_early(move, dim3(2 * di.sms + 1), kMoveThreads, 0, s, p, vpr);
+    return paged::launch_early(move, dim3(2 * di.sms), kMoveThreads, 0, s, p, vpr);
 }
 
 }  // namespace relattn
