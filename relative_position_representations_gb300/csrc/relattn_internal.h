@@ -276,13 +276,18 @@ struct PagedArgs {
     // parts of a call with shared prefixes (Params has what they mean); 0 and null otherwise
     int flat, f32_out, overlap;
     const int *first_key, *row_of, *ctas;
-    struct PagedMerge *merge;         // where to leave the merge that is to follow; null: it is launched
+    int *owner;                       // not null: split items are left in their pieces ...
+    struct PagedLeft *left;           // ... and the launch says here how
     void *workspace;                  // at least paged_workspace_bytes
     int *err;
     long long wait_limit;             // bound of every device wait (cycles, <= 0: 2e9)
     int withhold;                     // test hook: announce the first queries, do not load them
 };
 // attention over prefixes that groups of requests share, then over each request's own keys, joined
+struct PagedLeft {
+    int rec_rows, grid;               // rows of a record, CTAs of the launch
+    const int *ctas;                  // Params::ctas of the launch
+};
 struct PagedSharedArgs {
     PagedArgs a;
     const int *group_start, *prefix_len;  // [groups + 1], [groups]

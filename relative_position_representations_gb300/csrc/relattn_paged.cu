@@ -92,7 +92,8 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->row_of = a.row_of;
     p->ctas = a.ctas;
     p->overlap = a.overlap;
-    p->merge = a.merge;
+    p->owner = a.owner;
+    p->left = a.left;
     p->desc = static_cast<Desc *>(a.workspace);
     p->part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + desc_bytes());
     p->err = a.err;
@@ -114,10 +115,12 @@ constexpr int kMergeThreads = 256;
 
 // lanes: threads of a row, as a power of two
 template <typename T, int V, int kUnroll>
-__device__ __forceinline__ void merge_rows(const Params &p, int launched, int lanes, int blocks_y) {
+__global__ void __launch_bounds__(kMergeThreads, V == 8 ? 4 : 3)
+    paged_merge_kernel(const __grid_constant__ Params p, int G, int lanes) {
     __shared__ short piece[kMaxGrid];
     __shared__ int n_s;
-    const int G = grid_of(p, launched);
+    grid_wait();
+    grid_release();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const Desc d = p.desc[c];
     if (!d.valid) return;
@@ -146,7 +149,7 @@ __device__ __forceinline__ void merge_rows(const Params &p, int launched, int la
         __syncthreads();
         n = n_s;
     }
-    for (int r = r_first + (tid >> lanes); r < rows; r += blocks_y * per) {
+    for (int r = r_first + (tid >> lanes); r < rows; r += (int)gridDim.y * per) {
         const int tok = r / p.g, hh = r - tok * p.g;
         T *out = static_cast<T *>(p.out) + ((long long)(d.row0 + tok) * p.H + d.kvh * p.g + hh) * D;
         for (int col = (tid & ((1 << lanes) - 1)) * V; col < D; col += V << lanes) {
@@ -205,40 +208,14 @@ __device__ __forceinline__ void merge_rows(const Params &p, int launched, int la
     }
 }
 
-template <typename T, int V, int kUnroll>
-__global__ void __launch_bounds__(kMergeThreads, V == 8 ? 4 : 3)
-    paged_merge_kernel(const __grid_constant__ Params p, int launched, int lanes) {
-    grid_wait();
-    grid_release();
-    merge_rows<T, V, kUnroll>(p, launched, lanes, (int)gridDim.y);
-}
-
-struct TwoMerges {
-    Params p[2];
-    int launched[2], lanes[2], y[2];   // y: blocks of an item
-};
-__global__ void __launch_bounds__(kMergeThreads, 3) paged_merges_kernel(const __grid_constant__ TwoMerges m) {
-    grid_wait();
-    grid_release();
-    const int z = blockIdx.z;
-    if ((int)blockIdx.x >= m.launched[z] || (int)blockIdx.y >= m.y[z]) return;
-    if (m.p[z].rec_rows > 16) merge_rows<float, 8, 2>(m.p[z], m.launched[z], m.lanes[z], m.y[z]);
-    else merge_rows<float, 4, 8>(m.p[z], m.launched[z], m.lanes[z], m.y[z]);
-}
-
-// threads of a row of `want` vectors, as a power of two
-int row_lanes(int want) {
-    int lanes = 0;
-    while (lanes < 5 && (1 << lanes) < want) ++lanes;
-    return lanes;
-}
-
 template <typename T>
 cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
     // eight or four columns a thread where rows are as wide (those of the records are, at 16 bytes)
     const bool four = p.d % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0;
     const bool eight = p.d % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.rec_rows > 16;
-    const int lanes = row_lanes(eight ? p.d / 8 : four ? p.d / 4 : p.d);
+    const int want = eight ? p.d / 8 : four ? p.d / 4 : p.d;
+    int lanes = 0;
+    while (lanes < 5 && (1 << lanes) < want) ++lanes;
     const int per = kMergeThreads >> lanes;
     const dim3 g(grid, (p.likely_rows + per - 1) / per);
     if (eight) return launch_early(paged_merge_kernel<T, 8, 2>, g, kMergeThreads, 0, s, p, grid, lanes);
@@ -246,27 +223,9 @@ cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
                 : launch_early(paged_merge_kernel<T, 1, 4>, g, kMergeThreads, 0, s, p, grid, lanes);
 }
 
-cudaError_t launch_merges(const PagedMerge &a, const PagedMerge &b, cudaStream_t s) {
-    const PagedMerge *two[2] = {&a, &b};
-    TwoMerges m;
-    int x = 0, y = 0;
-    for (int z = 0; z < 2; ++z) {
-        const Params &p = two[z]->p;
-        m.p[z] = p;
-        m.launched[z] = two[z]->grid;
-        m.lanes[z] = row_lanes(p.d / (p.rec_rows > 16 ? 8 : 4));
-        const int per = kMergeThreads >> m.lanes[z];
-        m.y[z] = (p.likely_rows + per - 1) / per;
-        x = x > m.launched[z] ? x : m.launched[z];
-        y = y > m.y[z] ? y : m.y[z];
-    }
-    return launch_early(paged_merges_kernel, dim3(x, y, 2), kMergeThreads, 0, s, m);
-}
-
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
-    if (p.merge) {
-        p.merge->p = p;
-        p.merge->grid = grid;
+    if (p.owner) {   // the caller joins the pieces
+        *p.left = PagedLeft{p.rec_rows, grid, p.ctas};
         return cudaSuccess;
     }
     return bf16 && !p.f32_out ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
@@ -408,6 +367,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
     bool any = false;
     while (walk.next(p, g)) {
         any = true;
+        if (warp == 0) write_owner(p, g);
         const int rows = g.it.cnt * p.g;
         const T *aK = static_cast<const T *>(p.aK) + (long long)g.kvh * p.ths;
         const T *aV = static_cast<const T *>(p.aV) + (long long)g.kvh * p.ths;
@@ -644,7 +604,6 @@ cudaError_t launch_paged(const PagedArgs &a, cudaStream_t s) {
     PagedArgs all = a;   // the whole grid, in its turn
     all.ctas = nullptr;
     all.overlap = 0;
-    all.merge = nullptr;
     return launch_paged_simt(all, s);
 }
 

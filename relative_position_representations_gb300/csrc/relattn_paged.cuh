@@ -23,9 +23,6 @@
 #include "relattn_internal.h"
 
 namespace relattn {
-
-struct PagedMerge;
-
 namespace paged {
 
 constexpr int kTile = 128;               // keys per tile
@@ -72,7 +69,9 @@ struct Params {
     int overlap;                             // runs beside the kernel in front of it, and ends after it
     Desc *desc;                              // [gridDim.x]
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
-    PagedMerge *merge;                       // host: PagedArgs has what it means
+    int *owner;                              // [tokens][Hkv] or null: the CTA that begins a token's item, where
+                                             // the item goes on behind its range; else -1 (out has its rows)
+    PagedLeft *left;                         // host
     int *err;
     long long wait_limit;
     int withhold;                            // test hook: a CTA's first queries are announced, not loaded
@@ -385,6 +384,13 @@ __device__ __forceinline__ Piece make_piece(const Params &p, const Segment &g, b
                  g.it.nt, g.t0, g.t1, g.kvh, table_row(p, g.b), 0};
 }
 
+// Says where the rows of the segment's item are, if it is the item's first (a warp calls it).
+__device__ __forceinline__ void write_owner(const Params &p, const Segment &g) {
+    if (!p.owner || g.t0 > 0) return;
+    for (int i = threadIdx.x & 31; i < g.it.cnt; i += 32)
+        p.owner[(long long)(g.s.q0 + g.it.i0 + i) * p.Hkv + g.kvh] = g.whole() ? -1 : (int)blockIdx.x;
+}
+
 // Leaves the descriptor of the item that goes on behind the range (one thread per CTA calls it,
 // once, with the last segment of the range).
 __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, long long total) {
@@ -488,14 +494,7 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 void fill_params(const PagedArgs &a, Params *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s);
-// the merges that two calls with f32_out have left (rows of 16 bytes' multiples), in one launch
-cudaError_t launch_merges(const PagedMerge &a, const PagedMerge &b, cudaStream_t s);
 
 }  // namespace paged
-
-struct PagedMerge {
-    paged::Params p;
-    int grid = 0;   // 0: nothing to merge
-};
 
 }  // namespace relattn

@@ -156,6 +156,7 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
         any = any || more;
         const int i = it & (kPieces - 1);
         if (!(ok = wait(bar(B_PIECE_EMPTY + i), ((it / kPieces) & 1u) ^ 1u))) break;
+        if (more) write_owner(p, g);
         if (lane == 0) {
             ring[i] = make_piece(p, g, more);
             if (more) {

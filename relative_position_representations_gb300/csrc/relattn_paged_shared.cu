@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
         int keys = 0, q0 = 0, q1 = 0, row = 0;
         if (g < sp.groups) {
             const int b0 = min(max(sp.group_start[g], 0), p.B), b1 = min(max(sp.group_start[g + 1], b0), p.B);
+            const int most = sp.prefix_len[g];
             int least = 0x7fffffff, busy = 0, first = p.B;
             for (int b = b0 + lane; b < b1; b += 32) {
                 const Seq s = load_seq(p, b);
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
                 busy += __shfl_xor_sync(0xffffffffu, busy, o);
             }
             if (busy > 1) {
-                keys = max(min(sp.prefix_len[g], least - p.clip_k + 1), 0) / kTile * kTile;
+                keys = max(min(most, least - p.clip_k + 1), 0) / kTile * kTile;
                 q0 = min(max(p.q_start[b0], 0), p.tokens);
                 q1 = min(max(p.q_start[b1], q0), p.tokens);
                 row = first;
@@ -167,65 +168,167 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
     }
 }
 
+// What a part has left: rows of whole items in o (normalised, with their log-sum-exps in lse), the others in
+// the records of the CTAs that hold a piece.
+struct Part {
+    const float *o, *lse, *rec;
+    const int *owner, *ctas;
+    const Desc *desc;
+    int rec_rows, launched;
+};
+
 struct JoinParams {
     const void *q, *aK, *aV;
     long long q_stride, ths;
-    int tokens, H, g, d;
+    int tokens, H, Hkv, g, d;
     float scale_log2;
-    const int *first_key;
-    const float *o_a, *o_b, *lse_a, *lse_b;   // shared part, own keys
+    const int *first_key, *q_start;
+    int B;
+    Part part[2];                     // shared keys, own keys
     void *out;
     float *lse;
 };
 
-// A warp per row: z = (w_a (z_a + aV_0) + w_b z_b) / (w_a + w_b), w = 2^(log-sum-exp - their maximum).
-template <typename T>
+// A warp per row, N columns from lane + 32 i: joins the pieces of either part in the order of their keys, under a
+// running maximum: z = sum f_i (acc_i + l_i aV_0) / sum f_i l_i, f_i = 2^(m_i - M), aV_0 and the constant of aK_0 in m_i for
+// the shared keys alone. Both parts go through one loop: the code runs once and cold, and its fetching took longer
+// than its loads when each part had a copy (17 us a step in place of 9).
+template <typename T, int N>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const __grid_constant__ JoinParams p) {
+    constexpr int kBatch = 4;                // pieces on their way together
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
     grid_wait();
     grid_release();
     if (row >= (long long)p.tokens * p.H) return;
-    const int t = (int)(row / p.H), h = (int)(row - (long long)t * p.H);
-    const long long table = (long long)(h / p.g) * p.ths;
-    const bool shared = p.first_key[t] > 0;
-    float a = -INFINITY, b = p.lse_b[row] * kLog2e;
-    if (shared) {
-        float r = 0.f;
-        if (p.aK) {
-            const T *q = static_cast<const T *>(p.q) + (long long)t * p.q_stride + (long long)h * p.d;
-            const T *k0 = static_cast<const T *>(p.aK) + table;
-            for (int c = lane; c < p.d; c += 32) r = fmaf(to_f(q[c]), to_f(k0[c]), r);
+    const int t = (int)(row / p.H), h = (int)(row - (long long)t * p.H), kvh = h / p.g;
+    // where the row's parts are (everything that depends on nothing is on its way at once)
+    const int from = p.q_start[0], end = p.q_start[p.B], shared = p.first_key[t];
+    const int c0 = p.part[0].owner[(long long)t * p.Hkv + kvh], c1 = p.part[1].owner[(long long)t * p.Hkv + kvh];
+    float r = 0.f, v0[N];
+    {
+        const long long table = (long long)kvh * p.ths;
+        const T *q = static_cast<const T *>(p.q) + (long long)t * p.q_stride + (long long)h * p.d;
+        const T *k0 = static_cast<const T *>(p.aK) + table, *av = static_cast<const T *>(p.aV) + table;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        for (int i = 0; i < N; ++i) {
+            const int c = lane + 32 * i;
+            v0[i] = p.aV && c < p.d ? to_f(av[c]) : 0.f;
+            if (p.aK && c < p.d) r = fmaf(to_f(q[c]), to_f(k0[c]), r);
         }
-        a = fmaf(r, p.scale_log2, p.lse_a[row] * kLog2e);
     }
-    const float m = fmaxf(a, b), mu = m == -INFINITY ? 0.f : m;
-    const float wa = exp2f(a - mu), wb = exp2f(b - mu), l = wa + wb, inv = l > 0.f ? 1.f / l : 0.f;
-    const T *v0 = p.aV ? static_cast<const T *>(p.aV) + table : nullptr;
-    for (int c = lane; c < p.d; c += 32) {
-        float z = wb * p.o_b[row * p.d + c];
-        if (shared) z = fmaf(wa, p.o_a[row * p.d + c] + (v0 ? to_f(v0[c]) : 0.f), z);
-        static_cast<T *>(p.out)[row * p.d + c] = from_f<T>(z * inv);
+    if (t < from || t >= end) return;        // no request's
+    if (p.aK) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     }
-    if (p.lse && lane == 0) p.lse[row] = row_lse(mu, l);
+    float m = -INFINITY, l = 0.f, acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int x = shared > 0 ? 0 : 1; x < 2; ++x) {
+        const Part &a = p.part[x];
+        const int c = min(x ? c1 : c0, a.launched - 1);
+        const float add = x ? 0.f : r * p.scale_log2;
+        Desc d{};
+        int rr = 0, left = 1, e = c, G = a.launched;
+        if (c >= 0) {
+            d = a.desc[c];
+            if (a.ctas) G = min(max(*a.ctas, 1), G);
+            rr = (t - d.row0) * p.g + (h - kvh * p.g);
+            left = d.n;
+            // (offsets that do not ascend may leave a token without an owner: what follows stays within the arrays)
+            if (!d.valid || rr < 0 || rr >= min(d.cnt * p.g, a.rec_rows)) continue;
+        }
+        const bool listed = c < 0 || d.n > 0;   // the pieces are counted
+        bool more = true;
+        while (more) {
+            float mi[kBatch], li[kBatch], y[kBatch][N], mn = m;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                mi[u] = -INFINITY;
+                li[u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[u][i] = 0.f;
+                if (!more) continue;
+                if (listed) more = left-- > 0 && e < a.launched;   // in the CTAs c .. c + n - 1
+                else {                                             // short ranges: those whose range begins another tile
+                    while (e < G) {
+                        const int t0 = e == c ? 0 : tiles_before(range_begin(d.total, e, G) - d.x, d.c0, d.wt, d.nt);
+                        const int t1 = tiles_before(range_begin(d.total, e + 1, G) - d.x, d.c0, d.wt, d.nt);
+                        if (t0 >= d.nt) e = G;
+                        else if (t1 > t0) break;
+                        else ++e;
+                    }
+                    more = e < G;
+                }
+                if (!more) continue;
+                const float *o = a.o + row * p.d;
+                if (c < 0) {                     // all of it
+                    mi[u] = a.lse[row];
+                    li[u] = mi[u] == -INFINITY ? 0.f : 1.f;
+                    mi[u] *= kLog2e;
+                } else {
+                    const float *rec = a.rec + ((long long)e * 2 + (e == c ? 1 : 0)) * a.rec_rows * (p.d + 2);
+                    mi[u] = rec[rr];
+                    li[u] = rec[a.rec_rows + rr];
+                    o = rec + 2 * a.rec_rows + (long long)rr * p.d;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (lane + 32 * i < p.d) y[u][i] = o[lane + 32 * i];
+                ++e;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                mi[u] += add;
+                mn = fmaxf(mn, mi[u]);
+            }
+            const float mu = mn == -INFINITY ? 0.f : mn, f = exp2f(m - mu);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] *= f;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float w = exp2f(mi[u] - mu);
+                l = fmaf(w, li[u], l);
+                const float lv = x ? 0.f : li[u];
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = fmaf(w, fmaf(lv, v0[i], y[u][i]), acc[i]);
+            }
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane + 32 * i < p.d) static_cast<T *>(p.out)[row * p.d + lane + 32 * i] = from_f<T>(acc[i] * inv);
+    if (p.lse && lane == 0) p.lse[row] = row_lse(m == -INFINITY ? 0.f : m, l);
+}
+
+template <typename T>
+cudaError_t launch_join(const JoinParams &j, cudaStream_t s) {
+    const long long rows = (long long)j.tokens * j.H;
+    const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    if (j.d <= 32) return launch_early(shared_join_kernel<T, 1>, grid, kJoinThreads, 0, s, j);
+    if (j.d <= 64) return launch_early(shared_join_kernel<T, 2>, grid, kJoinThreads, 0, s, j);
+    return launch_early(shared_join_kernel<T, 4>, grid, kJoinThreads, 0, s, j);
 }
 
 // [d > 64] as measured: tiles of the kernel for chunks with one and two query tiles; tiles of the one for generated
 // tokens, which HBM bounds
-constexpr Costs kChunkCosts[2] = {{6400.f, 1900.f, 2550.f, 6400.f}, {8600.f, 2600.f, 3450.f, 8600.f}};
-constexpr Costs kTokenCosts[2] = {{1100.f, 1100.f, 1100.f, 2200.f}, {2200.f, 2200.f, 2200.f, 4400.f}};
+constexpr Costs kChunkCosts[2] = {{6400.f, 2900.f, 3900.f, 6400.f}, {8600.f, 4500.f, 6000.f, 8600.f}};
+constexpr Costs kTokenCosts[2] = {{1500.f, 1500.f, 1500.f, 3000.f}, {3000.f, 3000.f, 3000.f, 6000.f}};
 
 size_t round16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 }  // namespace
 }  // namespace paged
 
-// workspace: that of either part, their outputs and log-sum-exps, first keys, the shared parts' list, CTAs
+// workspace: that of either part, their outputs, log-sum-exps and owners, first keys, the shared parts' list, CTAs
 unsigned long long paged_shared_workspace_bytes(int tokens, int H, int d) {
     const size_t rows = (size_t)tokens * H;
-    return 2 * paged_workspace_bytes(d) + 16 + 2 * paged::round16(rows * d * 4) + 2 * paged::round16(rows * 4) +
+    return 2 * paged_workspace_bytes(d) + 16 + 2 * paged::round16(rows * d * 4) + 4 * paged::round16(rows * 4) +
            4 * paged::round16(((size_t)tokens + 2) * 4);
 }
 
@@ -246,6 +349,8 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     float *o_b = reinterpret_cast<float *>(take(round16(rows * a.d * 4)));
     float *lse_a = reinterpret_cast<float *>(take(round16(rows * 4)));
     float *lse_b = reinterpret_cast<float *>(take(round16(rows * 4)));
+    int *owner_a = reinterpret_cast<int *>(take(round16(rows * 4)));
+    int *owner_b = reinterpret_cast<int *>(take(round16(rows * 4)));
     SplitParams sp;
     std::memset(&sp, 0, sizeof(sp));
     fill_params(a, &sp.p);
@@ -268,6 +373,7 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     const bool few = paged_decode_covers(a);
     sp.own_tokens = few ? 16 / g : 2 * sp.tile_tokens;
     sp.own = few ? kTokenCosts[a.d > 64] : kChunkCosts[a.d > 64];
+    if (few && a.max_new * g > 8) sp.own = Costs{1.5f * sp.own.item, 1.5f * sp.own.tile, 1.5f * sp.own.tile2, 1.5f * sp.own.fixed};
     sp.own_per_sm = few && a.d <= 64 ? 2 : 1;
     cudaError_t e = launch_early(shared_split_kernel, dim3(1), kSplitThreads, 0, s, sp);
     if (e != cudaSuccess) return e;
@@ -280,34 +386,31 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     part.row_of = sp.row_of;
     part.B = sp.most;
     part.max_new = a.tokens;
-    part.flat = part.f32_out = 1;
-    part.out = o_a;
-    part.lse = lse_a;
-    PagedMerge merges[2];
-    part.merge = &merges[0];
+    part.flat = 1;
+    part.owner = owner_a;
     part.ctas = sp.ctas;
-    if ((e = launch_paged(part, s)) != cudaSuccess) return e;
-    part = a;                // each request's own
-    part.first_key = sp.first_key;
-    part.f32_out = 1;
-    part.out = o_b;
-    part.lse = lse_b;
-    part.workspace = static_cast<char *>(a.workspace) + paged_workspace_bytes(a.d);
-    part.merge = &merges[1];
-    part.ctas = sp.ctas + 1;
-    part.overlap = 1;
-    if ((e = launch_paged(part, s)) != cudaSuccess) return e;
-    if (merges[0].grid && merges[1].grid) {
-        if ((e = launch_merges(merges[0], merges[1], s)) != cudaSuccess) return e;
-    } else {   // (what ran on the SIMT units has been merged)
-        for (PagedMerge &m : merges)
-            if (m.grid) {
-                m.p.merge = nullptr;
-                if ((e = launch_merge(m.p, m.grid, true, s)) != cudaSuccess) return e;
-            }
-    }
     JoinParams j;
     std::memset(&j, 0, sizeof(j));
+    auto run = [&](PagedArgs &x, Part &r, float *o, float *lse) {
+        PagedLeft left{};
+        x.left = &left;
+        x.f32_out = 1;
+        x.out = o;
+        x.lse = lse;
+        const cudaError_t st = launch_paged(x, s);
+        const char *ws = static_cast<const char *>(x.workspace);
+        r = Part{o, lse, reinterpret_cast<const float *>(ws + desc_bytes()), x.owner, left.ctas,
+                 reinterpret_cast<const Desc *>(ws), left.rec_rows, left.grid};
+        return st;
+    };
+    if ((e = run(part, j.part[0], o_a, lse_a)) != cudaSuccess) return e;
+    part = a;                // each request's own
+    part.first_key = sp.first_key;
+    part.workspace = static_cast<char *>(a.workspace) + paged_workspace_bytes(a.d);
+    part.owner = owner_b;
+    part.ctas = sp.ctas + 1;
+    part.overlap = 1;
+    if ((e = run(part, j.part[1], o_b, lse_b)) != cudaSuccess) return e;
     j.q = a.q;
     j.aK = a.aK;
     j.aV = a.aV;
@@ -315,19 +418,16 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     j.ths = a.ths;
     j.tokens = a.tokens;
     j.H = a.H;
+    j.Hkv = a.Hkv;
     j.g = a.H / a.Hkv;
     j.d = a.d;
     j.scale_log2 = sp.p.scale_log2;
     j.first_key = sp.first_key;
-    j.o_a = o_a;
-    j.o_b = o_b;
-    j.lse_a = lse_a;
-    j.lse_b = lse_b;
+    j.q_start = a.q_start;
+    j.B = a.B;
     j.out = a.out;
     j.lse = a.lse;
-    const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-    return a.bf16 ? launch_early(shared_join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, j)
-                  : launch_early(shared_join_kernel<float>, grid, kJoinThreads, 0, s, j);
+    return a.bf16 ? launch_join<__nv_bfloat16>(j, s) : launch_join<float>(j, s);
 }
 
 }  // namespace relattn

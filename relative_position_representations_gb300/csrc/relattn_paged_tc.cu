@@ -304,6 +304,7 @@ __device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, 
         if (more && g.t1 > g.t0)   // (here, where nothing waits for it)
             for (int s = 0; s < 2; ++s)
                 if (slot_work(tp, pc, s).t_last >= pc.t0) pc.act |= 1 << s;
+        if (more) write_owner(p, g);
         if (lane == 0) ring[i] = pc;
         __syncwarp();
         ptx::mbar_arrive_w(bars + 8u * (B_PIECE_FULL + i));

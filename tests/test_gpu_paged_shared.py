@@ -107,6 +107,7 @@ def check(x, clip_k=0, window=0, sinks=0, scale=None, max_new=0, weight_step=2.0
     bad = ~(np.abs(got - z) <= tol)[:rows]
     assert not bad.any(), (int(bad.sum()), np.abs(got - z)[:rows][bad].max(), np.argwhere(bad)[:4])
     g_lse = f64(got_lse)
+    assert (got[rows:] == 5.0).all() and (g_lse[rows:] == 5.0).all()   # no request's
     tol = 4.0 * (d + 6) * u * size + 2.0 ** -20 + 2.0 * keys * u + 12.0 * u * known
     with np.errstate(invalid="ignore"):
         assert ((g_lse == lse) | (np.abs(g_lse - lse) <= tol))[:rows].all()
