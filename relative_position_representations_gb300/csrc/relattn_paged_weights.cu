@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
 // ======================================================================= SIMT
 // A unit is 32 keys of one head, staged in shared memory as fp32; the rows that see any of them come 32 at a
 // time, four to a warp, lane = key. A lane adds up its key's weights over the rows; the warps are joined
-// at the end, in order. Bound by shared memory, as the attention's SIMT kernel.
+// at the end, in order. The next rows are on their way into registers meanwhile. Bound by latency (a CTA takes
+// 2 us for 32 rows) and shared memory, as the attention's SIMT kernel.
 constexpr int kSimtThreads = 256;
 constexpr int kRun = 32;
 constexpr int kRunsPerTile = kTile / kRun;
@@ -153,14 +154,26 @@ struct SimtLayout {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __grid_constant__ WeightParams w) {
+__device__ __forceinline__ float4 load4(const T *row, int c, int d, bool vec) {
+    if (vec) {
+        if (sizeof(T) == 4) return *reinterpret_cast<const float4 *>(row + c);
+        const uint2 w = *reinterpret_cast<const uint2 *>(row + c);
+        return make_float4(ptx::bf16lo_to_f32(w.x), ptx::bf16hi_to_f32(w.x), ptx::bf16lo_to_f32(w.y), ptx::bf16hi_to_f32(w.y));
+    }
+    return make_float4(to_f(row[c]), c + 1 < d ? to_f(row[c + 1]) : 0.f, c + 2 < d ? to_f(row[c + 2]) : 0.f,
+                       c + 3 < d ? to_f(row[c + 3]) : 0.f);
+}
+
+// N4: 16-byte chunks of a row that a thread's share of 32 rows needs, ceil(d / 4 / 8)
+template <typename T, int N4>
+__global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __grid_constant__ WeightParams w, int vec) {
     extern __shared__ __align__(16) float smf[];
     __shared__ int entry_s;
     __shared__ long long unit_s, rest_s;
     const Params &p = w.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int d = p.d, k = p.clip_k, P = 1 << p.pshift;
-    const bool ak = p.aK != nullptr;
+    const bool ak = p.aK != nullptr, wide = vec != 0;
     const SimtLayout L(d, k, ak);
     float *qs = smf + L.q, *Ks = smf + L.k, *As = smf + L.a, *Rs = smf + L.R, *nls = smf + L.nl, *part = smf + L.part;
     grid_wait();
@@ -182,8 +195,20 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
             }
         }
     };
-    auto stage = [&](float *dst, int ld, const T *row) {   // eight threads to a row; null: zeros
-        for (int c = my_c; c < L.d4; c += 8) dst[my_row * ld + c] = row && c < d ? to_f(row[c]) : 0.f;
+    // eight threads to a row: chunks my_c, my_c + 8, ...; null: zeros
+    auto fetch = [&](float4 (&x)[N4], const T *row) {
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+            const int c = 4 * (my_c + 8 * i);
+            x[i] = row && c < L.d4 ? load4(row, c, d, wide) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    auto put = [&](float *dst, int ld, const float4 (&x)[N4]) {
+#pragma unroll
+        for (int i = 0; i < N4; ++i) {
+            const int c = 4 * (my_c + 8 * i);
+            if (c < L.d4) *reinterpret_cast<float4 *>(dst + my_row * ld + c) = x[i];
+        }
     };
     for (;;) {
         __syncthreads();
@@ -226,29 +251,38 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
                 if (pg >= 0) row = static_cast<const T *>(p.k) + (long long)pg * p.page_stride + at * d;
                 else if (my_c == 0) report_page(p);
             }
-            stage(Ks, L.ld, row);
+            float4 x[N4];
+            fetch(x, row);
+            put(Ks, L.ld, x);
         }
         const int t_lo = first_token(j0, s.pos0), t_hi = end_token(p, j0, kRun, s.pos0, s.n);
         const long long r_end = (long long)t_hi * p.g;
         float sum = 0.f;
+        float4 qx[N4];
+        float nx;
+        auto fetch_rows = [&](long long r0) {
+            const long long r = r0 + my_row;
+            const int tok = (int)(r / p.g), hh = (int)(r - (long long)tok * p.g);
+            const bool on = r < r_end;
+            fetch(qx, on ? static_cast<const T *>(p.q) + (long long)(s.q0 + tok) * p.q_stride + (long long)(kvh * p.g + hh) * d
+                         : nullptr);
+            nx = on ? w.nl[(long long)(s.q0 + tok) * p.H + kvh * p.g + hh] : -INFINITY;
+        };
+        fetch_rows((long long)t_lo * p.g);
         for (long long r0 = (long long)t_lo * p.g; r0 < r_end; r0 += kRun) {
             const int nr = (int)min((long long)kRun, r_end - r0);
             __syncthreads();                 // the previous rows are done
-            {
-                const long long r = r0 + my_row;
-                const int tok = (int)(r / p.g), hh = (int)(r - (long long)tok * p.g);
-                const bool on = my_row < nr;
-                const long long head = (long long)(s.q0 + tok) * p.H + kvh * p.g + hh;
-                stage(qs, L.d4, on ? static_cast<const T *>(p.q) + (long long)(s.q0 + tok) * p.q_stride +
-                                         (long long)(kvh * p.g + hh) * d : nullptr);
-                if (my_c == 0) nls[my_row] = on ? w.nl[head] : -INFINITY;
-            }
+            put(qs, L.d4, qx);
+            if (my_c == 0) nls[my_row] = nx;
+            fetch_rows(r0 + kRun);
             const bool band = ak && j0 + kRun - 1 > s.pos0 + (int)(r0 / p.g) - k;
             if (band)
                 for (int w0 = 0; w0 <= k; w0 += kRun) {
                     __syncthreads();
-                    stage(As, L.ld, w0 + my_row <= k ? static_cast<const T *>(p.aK) + (long long)kvh * p.ths +
-                                                           (long long)(w0 + my_row) * d : nullptr);
+                    float4 x4[N4];
+                    fetch(x4, w0 + my_row <= k ? static_cast<const T *>(p.aK) + (long long)kvh * p.ths + (long long)(w0 + my_row) * d
+                                               : nullptr);
+                    put(As, L.ld, x4);
                     __syncthreads();
                     float x[4];
                     scores(As, x);
@@ -285,17 +319,29 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
     }
 }
 
-template <typename T>
-cudaError_t launch_simt(WeightParams w, cudaStream_t s) {
+template <typename T, int N4>
+cudaError_t launch_simt_n(WeightParams w, cudaStream_t s) {
     w.per_tile = kRunsPerTile;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
     cudaError_t e = launch_weights_prep(w, sizeof(T) == 2, s);
     if (e != cudaSuccess) return e;
-    const SimtLayout L(w.p.d, w.p.clip_k, w.p.aK != nullptr);
-    e = opt_in_smem(reinterpret_cast<const void *>(weights_simt_kernel<T>), di);
+    const Params &p = w.p;
+    const SimtLayout L(p.d, p.clip_k, p.aK != nullptr);
+    // 16-byte (fp32) or 8-byte (bf16) loads where every row starts on such a boundary
+    const long long es = sizeof(T);
+    const uint64_t al = (uint64_t)(p.d * es) | (uint64_t)(p.q_stride * es) | (uint64_t)(p.page_stride * es) |
+                        (uint64_t)(p.ths * es) | reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
+                        reinterpret_cast<uintptr_t>(p.aK);
+    e = opt_in_smem(reinterpret_cast<const void *>(weights_simt_kernel<T, N4>), di);
     if (e != cudaSuccess) return e;
-    return launch_early(weights_simt_kernel<T>, dim3(2 * di.sms), kSimtThreads, L.words * sizeof(float), s, w);
+    return launch_early(weights_simt_kernel<T, N4>, dim3(2 * di.sms), kSimtThreads, L.words * sizeof(float), s, w,
+                        al % (4 * es) == 0 ? 1 : 0);
+}
+
+template <typename T>
+cudaError_t launch_simt(const WeightParams &w, cudaStream_t s) {
+    return w.p.d <= 32 ? launch_simt_n<T, 1>(w, s) : w.p.d <= 64 ? launch_simt_n<T, 2>(w, s) : launch_simt_n<T, 4>(w, s);
 }
 
 // ======================================================================= generated tokens

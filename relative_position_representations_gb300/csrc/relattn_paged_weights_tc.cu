@@ -42,7 +42,7 @@ constexpr int KB = 32;               // columns read from an accumulator at a ti
 constexpr int kUnits = 4;            // announced ahead
 constexpr int kMaxK = 4, kMaxQ = 4;  // stages
 constexpr int kAccs = 3;             // accumulators
-constexpr int kSides = 4;            // tiles whose page numbers and masses are held
+constexpr int kSides = 8;            // tiles whose page numbers and masses are held
 constexpr int kBatch = 4;            // query tiles whose constants come together ...
 constexpr int kBatches = 2;          // ... and how often
 constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
@@ -615,11 +615,23 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                             const float *row = Rs;
 #pragma unroll 1
                             for (int c = 0; c < kTile; c += KB) {
+                                // 32 columns, whose tokens stand at p0 .. p1
+                                const int p0 = t.pos_lo + c / p.g, p1 = t.pos_lo + (c + KB - 1) / p.g;
+                                const bool past = far || p0 - k >= j_hi;   // of the band for all of the warp's keys
+                                if (p1 < j_lo) {                            // none of them in sight yet
+                                    row += KB * tp.SR;
+                                    hh = (hh + KB) % p.g;
+                                    lab = j - t.pos_lo + k - (c + KB) / p.g;
+                                    continue;
+                                }
                                 float x[KB];
                                 ptx::tmem_ld32f(acc_at() + (uint32_t)c, x);
                                 ptx::tmem_ld_wait();
-                                if (far) {
+                                if (past) {
                                     weights(x, c);
+                                    row += KB * tp.SR;
+                                    hh = (hh + KB) % p.g;
+                                    lab = j - t.pos_lo + k - (c + KB) / p.g;
                                 } else {   // R of token i: its entry for key j, one further back with every token
 #pragma unroll
                                     for (int e = 0; e < KB; ++e) {
