@@ -271,6 +271,45 @@ def test_replayed_with_other_lengths_and_groups():
         assert torch.equal(out, want)
 
 
+def test_a_wait_that_runs_out():
+    """Queries that never come, in both parts: the call ends and says so, and the next one is right."""
+    rp = _rp()
+    x = make([(640, [(i * 11, 1) for i in range(20)])], 8, 2, 64, 16)
+    g = [x[k].to(DEV) for k in ("q", "k_pages", "v_pages")] + [i32(x[k]) for k in ("table", "q_start", "kv_len", "group_start",
+                                                                                 "prefix_len")]
+    try:
+        rp.relattn_set_wait_limit(2_000_000)
+        rp.relattn_debug_withhold_first_load(1)
+        rp.relattn_paged_shared_fwd(*g, max_new=1)
+        assert rp.relattn_get_device_error() == 4
+    finally:
+        rp.relattn_debug_withhold_first_load(0)
+        rp.relattn_set_wait_limit(2_000_000_000)
+    check(x, max_new=1)
+
+
+def test_a_step_that_is_cut_and_goes_on():
+    """A group's requests behind a shared prefix, cut by their weights (the prefix lies below `sinks`), attended again: the
+    prefix stays as it is for all of them."""
+    rp = _rp()
+    x = make([(256, [(150, 1), (90, 1), (200, 1)])], 4, 2, 64, 16, clip_k=5, key=True, value=True)
+    N = x["k_pages"].shape[0]
+    g = {k: x[k].to(DEV) for k in ("q", "k_pages", "v_pages", "aK", "aV")}
+    table, qs, kv, gs, pl = (i32(x[k]) for k in ("table", "q_start", "kv_len", "group_start", "prefix_len"))
+    lse = torch.empty((3, 4), device=DEV)
+    mass = torch.rand((N, 2, 16), device=DEV)
+    kw = dict(aK=g["aK"], aV=g["aV"], clip_k=5, max_new=1)
+    rp.relattn_paged_shared_fwd(g["q"], g["k_pages"], g["v_pages"], table, qs, kv, gs, pl, lse=lse, **kw)
+    # (the shared pages' masses hold no defined number afterwards; below `sinks` none is looked at)
+    rp.relattn_paged_weights(g["q"], g["k_pages"], table, qs, kv, lse, mass, aK=g["aK"], clip_k=5, max_new=1)
+    kv2, _ = rp.relattn_paged_evict(kv, table, g["k_pages"], g["v_pages"], mass, 320, limit=350, sinks=256, recent=16)
+    assert kv2.tolist() == [320, 346 + 1, 320]
+    shared = torch.from_numpy(x["table"][0, :16])
+    assert torch.equal(g["k_pages"][shared].cpu(), x["k_pages"][shared])
+    y = dict(x, k_pages=g["k_pages"].cpu(), v_pages=g["v_pages"].cpu(), kv_len=np.array(kv2.tolist()))
+    check(y, 5, max_new=1)
+
+
 def test_two_streams_at_once():
     rp = _rp()
     xs = [make([(4096, [(i * 11, 1) for i in range(20)])], 8, 2, 128, 16, seed=s) for s in range(2)]

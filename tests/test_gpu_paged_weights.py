@@ -227,10 +227,58 @@ def test_lse_of_the_forward(dtype, d, P, max_new, terms, window, sinks):
     assert (got[T:] == 5.0).all()
     u = 2.0 ** -24
     tol = 4.0 * (d + 6) * u * size + 2.0 ** -20 + 2.0 * max(kv) * u + 8.0 * u * np.abs(np.where(np.isinf(lse), 0, lse))
-    same = (got[:T] == lse[:T]) | (np.abs(got - lse)[:T] <= tol[:T])
+    with np.errstate(invalid="ignore"):
+        same = (got[:T] == lse[:T]) | (np.abs(got - lse)[:T] <= tol[:T])
     assert same.all()
     out2, lse2 = rp.relattn_paged_fwd_lse(*call, **kw)
     assert torch.equal(out2[:T], out[:T]) and np.array_equal(f64(lse2)[:T], got[:T])
+
+
+@pytest.mark.parametrize("offset,stride", [(1, 0), (0, 1), (2, 3)])
+@pytest.mark.parametrize("max_new,new", [(1, [1, 1, 1]), (0, [40, 1, 130])])
+def test_masses_on_any_boundary(offset, stride, max_new, new):
+    """Masses that no 16-byte copy may take."""
+    rp = _rp()
+    kv, d, k = [300, 129, 200], 64, 5
+    x = make(new, kv, 4, 2, d, 16, BF16, k, key=True)
+    N = x["k_pages"].shape[0]
+    a = args_of(x)
+    lse = op.log_sum(**a, clip_k=k, window=0, sinks=0, scale=0.125)[0].astype(np.float32)
+    mass = np.random.default_rng(1).random((N, 2, 16)).astype(np.float32)
+    want, bound = op.weights(**a, clip_k=k, window=0, sinks=0, scale=0.125, lse=lse.astype(np.float64),
+                             mass=mass.astype(np.float64), accumulate=True)
+    room = torch.full((offset + N * (32 + stride) + 8,), 7.0, device=DEV)
+    m = room[offset:offset + N * (32 + stride)].view(N, 32 + stride)[:, :32].unflatten(1, (2, 16))
+    m.copy_(torch.from_numpy(mass))
+    g = on_gpu(x)
+    rp.relattn_paged_weights(g["q"], g["k_pages"], g["table"], g["q_start"], g["kv_len"], torch.from_numpy(lse).to(DEV), m,
+                             aK=g["aK"], clip_k=k, scale=0.125, max_new=max_new)
+    assert rp.relattn_get_device_error() == 0
+    assert (np.abs(f64(m) - want) <= bound).all()
+    rest = room.clone()
+    rest[offset:offset + N * (32 + stride)].view(N, 32 + stride)[:, :32] = 7.0
+    assert bool((rest == 7.0).all())
+
+
+@pytest.mark.parametrize("max_new,new", [(1, 1), (0, 40)])
+@pytest.mark.parametrize("key", [False, True])
+def test_a_wait_that_runs_out(max_new, new, key):
+    """Loads that never come: the kernel gives up, says so, and the next call is right."""
+    rp = _rp()
+    x = make([new] * 3, [900, 500, 100], 4, 2, 64, 16, BF16, 4, key=key)
+    g = on_gpu(x)
+    m = torch.zeros(x["k_pages"].shape[:3], device=DEV)
+    lse = torch.zeros((3 * new, 4), device=DEV)
+    try:
+        rp.relattn_set_wait_limit(2_000_000)
+        rp.relattn_debug_withhold_first_load(1)
+        rp.relattn_paged_weights(g["q"], g["k_pages"], g["table"], g["q_start"], g["kv_len"], lse, m, aK=g["aK"], clip_k=4 * key,
+                                 max_new=max_new)
+        assert rp.relattn_get_device_error() == 4
+    finally:
+        rp.relattn_debug_withhold_first_load(0)
+        rp.relattn_set_wait_limit(2_000_000_000)
+    check(x, 4 * key, max_new=max_new)
 
 
 # ------------------------------------------------------------------------------------ together
