@@ -354,13 +354,15 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRowThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // keys of a warp per tile
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
 constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
 
 template <int D>
 constexpr int kStageBytes = kTile * D * 2;
+// A row warp's chain on a tile (products, exponentials, two shuffles) is latency, so several CTAs share an SM (with two and
+// one: 32 requests of 1K-2K keys, 16 heads of 64: 28.2 us in place of 26.5; 64 of 2K-16K, two key heads of 128: 55.2, 53.6)
 template <int D>
-constexpr int kCtasPerSm = D == 64 ? 2 : 1;
+constexpr int kCtasPerSm = D == 64 ? 3 : 2;
 
 enum : int { B_FULL = 0, B_EMPTY = kMaxStages, B_PIECE_FULL = 2 * kMaxStages, B_PIECE_EMPTY = B_PIECE_FULL + kPieces,
              kNumBars = B_PIECE_EMPTY + kPieces };
@@ -685,7 +687,7 @@ cudaError_t launch_decode(const PagedWeightsArgs &a, const WeightParams &w, cuda
     if (!make_page_map(&tm, a.a.k_pages, a.a, box)) return cudaErrorInvalidValue;
     const int share = (di.smem_optin + 1024) / kCtasPerSm<D> - 1024;
     int stages = kMaxStages;
-    while (stages > 2 && (int)Layout::make<D, NT>(w.p.clip_k, AK, stages).bytes > share) --stages;
+    while (stages > 1 && (int)Layout::make<D, NT>(w.p.clip_k, AK, stages).bytes > share) --stages;
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(di.sms * kCtasPerSm<D>), kThreads, Layout::make<D, NT>(w.p.clip_k, AK, stages).bytes, s,

@@ -614,7 +614,7 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                             int hh = 0, lab = j - t.pos_lo + k;
                             const float *row = Rs;
 #pragma unroll 1
-                            for (int c = 0; c < kTile; c += KB) {
+                            for (int c = 0; c < t.ntok * p.g; c += KB) {
                                 // 32 columns, whose tokens stand at p0 .. p1
                                 const int p0 = t.pos_lo + c / p.g, p1 = t.pos_lo + (c + KB - 1) / p.g;
                                 const bool past = far || p0 - k >= j_hi;   // of the band for all of the warp's keys
