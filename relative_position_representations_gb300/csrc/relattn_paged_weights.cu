@@ -210,11 +210,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
             if (c < L.d4) *reinterpret_cast<float4 *>(dst + my_row * ld + c) = x[i];
         }
     };
-    for (;;) {
+    for (bool begin = true;; begin = false) {
         __syncthreads();
         if (warp == 0) {
-            unsigned long long u = 0;
-            if (lane == 0) u = atomicAdd(w.ticket, 1ull);
+            unsigned long long u = blockIdx.x;   // the first ticket is the CTA's own
+            if (!begin && lane == 0) u = gridDim.x + atomicAdd(w.ticket, 1ull);
             u = __shfl_sync(0xffffffffu, u, 0);
             long long rest = 0;
             int e = 0;

@@ -132,9 +132,9 @@ __device__ void ticket_role(const TcParams &tp, const Shared &sh) {
     Unit *ring = reinterpret_cast<Unit *>(sh.ptr + tp.off_unit);
     const int count = *tp.w.count;
     const long long total = tp.w.start[count];
-    for (;;) {
-        unsigned long long t = 0;
-        if (lane == 0) t = atomicAdd(tp.w.ticket, 1ull);
+    for (bool begin = true;; begin = false) {
+        unsigned long long t = blockIdx.x;   // the first ticket is the CTA's own
+        if (!begin && lane == 0) t = gridDim.x + atomicAdd(tp.w.ticket, 1ull);
         t = __shfl_sync(0xffffffffu, t, 0);
         Unit u{};
         if ((long long)t < total) {
