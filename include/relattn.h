@@ -437,8 +437,10 @@ RELATTN_API relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_st
 
 /*
  * relattn_paged_shared_fwd — relattn_paged_fwd for requests that share long prefixes (one instruction
- * text, one document, samples of one prompt): the same results, with a group's shared keys read and
- * multiplied once for all of its rows.
+ * text, one document, samples of one prompt): the same function, with a group's shared keys read and
+ * multiplied once for all of its rows. On the tensor cores the weights of the shared keys are rounded to
+ * bf16 (as those of chunks are; a generated token's weights of its own keys keep 16 bits), since
+ * tiles of 128 rows meet them; sums, statistics and what the two parts leave for each other are fp32.
  *
  *   group_start       [groups + 1] int32, ascending: requests group_start[g] .. group_start[g + 1] - 1
  *                     are group g; requests in front of the first and behind the last share nothing.

@@ -1,6 +1,7 @@
 """relation-aware self-attention on GB300 (sm_103a): the Shaw forward, T5 / ALiBi /
 per-offset scalar biases, labelled edges, a decode step, a paged key/value cache with its
-attention, the Shaw gradients and those of labelled edges and the scalar biases.
+attention (prefixes shared by a batch included), the attention weights of its keys and eviction by
+them, the Shaw gradients and those of labelled edges and the scalar biases.
 
 The compute lives in librelattn.so (C ABI, include/relattn.h); this package holds its
 ctypes binding (`_lib`), the in-tree build script (`build`) and the named workloads with

@@ -960,8 +960,8 @@ def relattn_paged_shared_workspace_size(tokens, H, Hkv, d) -> int:
 def relattn_paged_shared_fwd(q, k_pages, v_pages, block_table, q_start, kv_len, group_start, prefix_len, aK=None,
                              aV=None, clip_k=0, window=0, sinks=0, scale=None, max_new=0, out=None,
                              workspace=None, table_head_stride=None, stream=None, lse=None):
-    """relattn_paged_fwd for requests that share long prefixes: the same results, with the shared keys of a
-    group read and multiplied once for all of its rows.
+    """relattn_paged_fwd for requests that share long prefixes: the same function, with the shared keys of a
+    group read and multiplied once for all of its rows (bf16: their weights are rounded to bf16).
 
     group_start: [groups + 1] int32, ascending: requests group_start[g] .. group_start[g + 1] - 1 are group g
     (the others share nothing). prefix_len: [groups] int32: the table rows of a group name the same pages

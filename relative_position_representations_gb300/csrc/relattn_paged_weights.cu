@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
 // ======================================================================= SIMT
 // A unit is 32 keys of one head, staged in shared memory as fp32; the rows that see any of them come 32 at a
 // time, four to a warp, lane = key. A lane adds up its key's weights over the rows; the warps are joined
-// at the end, in order. The next rows are on their way into registers meanwhile. Bound by latency (a CTA takes
+// at the end, in order (three chunks of 61 - 127 tokens over 100 - 700 keys, 8 heads of 64, fp32, key term: 29 us, 4 of them
+// the set-up). The next rows are on their way into registers meanwhile. Bound by latency (a CTA takes
 // 2 us for 32 rows) and shared memory, as the attention's SIMT kernel.
 constexpr int kSimtThreads = 256;
 constexpr int kRun = 32;
