@@ -342,6 +342,10 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     // Under a window a token sees little of a prefix; one token shares with nobody. The requests' own rows of
     // the table hold the prefix too.
     if (a.window > 0 || sa.groups == 0 || a.tokens < 2) return launch_paged(a, s);
+    // Requests that fill a tile of 128 rows by themselves share their reads in the L2 as it is, and two parts cost more
+    // than they save (32 requests behind 8192 keys, 16 / 4 heads of 128: 16 new tokens 75 us here, 103 without; 24 tokens
+    // 93 and 105; 32 tokens, 128 rows, 114 and 106).
+    if ((long long)a.tokens * (a.H / a.Hkv) >= 128LL * a.B) return launch_paged(a, s);
     const size_t rows = (size_t)a.tokens * a.H, ints = round16(((size_t)a.tokens + 2) * 4);
     char *w = static_cast<char *>(a.workspace) + 2 * paged_workspace_bytes(a.d);
     auto take = [&](size_t bytes) {

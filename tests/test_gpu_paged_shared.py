@@ -178,6 +178,16 @@ def test_chunks_and_prompts_behind_a_prefix():
         check(make(groups, H, Hkv, d, 32, clip_k=20, key=True, value=True, after=[(0, 77)]), 20)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_requests_that_fill_a_tile_run_as_without_groups(d):
+    rp = _rp()
+    x = make([(256, [(0, 150), (30, 120)])], 4, 2, d, 16, clip_k=7, key=True, value=True)
+    out = check(x, 7)
+    g = {k: x[k].to(DEV) for k in ("q", "k_pages", "v_pages", "aK", "aV")}
+    assert torch.equal(out, rp.relattn_paged_fwd(g["q"], g["k_pages"], g["v_pages"], i32(x["table"]), i32(x["q_start"]),
+                                                 i32(x["kv_len"]), aK=g["aK"], aV=g["aV"], clip_k=7))
+
+
 def test_long_prefixes_are_cut_into_pieces():
     x = make([(8192, [(i * 37 % 200, 1) for i in range(40)])], 8, 2, 128, 64, clip_k=8, key=True, value=True)
     check(x, 8, max_new=1)
