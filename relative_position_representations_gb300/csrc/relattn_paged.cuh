@@ -483,9 +483,19 @@ cudaError_t launch_early(void (*kern)(Args...), dim3 grid, int threads, size_t s
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
-// (with p.overlap a kernel starts when the one in front of it has passed this wait itself, so that what
-// stands in front of that one is over; it waits for it at its own end)
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A kernel's start. With p.overlap it begins when the one in front of it has passed grid_wait() itself, so that what
+// stands in front of that one is over, and waits for it at its own end. What those earlier kernels have written
+// is seen through the release and the acquire of p.ctas, which the last of them writes at its end.
+__device__ __forceinline__ void grid_start(const Params &p) {
+    if (!p.overlap) {
+        grid_wait();
+        return;
+    }
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p.ctas) : "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // (pages and queries are read by TMA too)
+}
 // Lets the dependent kernel's CTAs come up beside this one's. After grid_wait(): what stands in front
 // of this kernel is then over for the dependent too.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

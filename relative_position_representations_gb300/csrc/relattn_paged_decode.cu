@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
         ptx::tma_prefetch_desc(&tm_v);
     }
     __syncthreads();
-    if (!p.overlap) grid_wait();
+    grid_start(p);
     grid_release();
     if (!idle_cta(p)) {
         if (threadIdx.x >= kRowThreads)

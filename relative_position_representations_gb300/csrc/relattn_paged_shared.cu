@@ -165,9 +165,12 @@ __global__ void __launch_bounds__(kSplitThreads) shared_split_kernel(const __gri
             }
         }
         if (work == 0.f) at = 1;
-        if (lane == 0) {
-            sp.ctas[0] = at;
-            sp.ctas[1] = max(sp.sms - at, 1) * sp.own_per_sm;
+        if (lane == 0) {   // behind everything that this block has written (grid_start)
+            __threadfence();
+            const int n[2] = {at, max(sp.sms - at, 1) * sp.own_per_sm};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(sp.ctas + i), "r"(n[i]) : "memory");
         }
     }
 }

@@ -982,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Before the warpgroups trade registers (the scan needs more than a control warp keeps), and by
     // every warp alike: the compiler fails to allocate a branch of one warp here.
     Range *range = reinterpret_cast<Range *>(sh.ptr + tp.off_stat);
-    if (!p.overlap) grid_wait();
+    grid_start(p);
     grid_release();
     if (idle_cta(p)) {
         if (p.overlap) grid_wait();

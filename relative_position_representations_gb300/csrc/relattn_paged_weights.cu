@@ -84,10 +84,11 @@ __global__ void __launch_bounds__(kPrepThreads) weights_prep_kernel(const __grid
                 all += units_s[i];
                 some += count_s[i];
             }
-            // (offsets that do not ascend may give more requests rows than there are tokens)
-            if (one && busy + c - 1 < p.tokens) {
-                w.busy[busy + c - 1] = b;
-                w.start[busy + c - 1] = at + u - mine;
+            // (offsets that do not ascend may give more requests rows than there are tokens: the first ones count)
+            const int entry = busy + c - 1;
+            if (one && entry <= p.tokens) {
+                w.start[entry] = at + u - mine;
+                if (entry < p.tokens) w.busy[entry] = b;
             }
             at += all;
             busy += some;

@@ -194,6 +194,22 @@ def test_pages_outside_the_cache(max_new, dtype):
         assert (p in touched) or bool((m[p] == 1).all())
 
 
+@pytest.mark.parametrize("max_new,dtype", [(1, BF16), (0, BF16), (0, F32)])
+@pytest.mark.parametrize("q_start", [[0, 12, 3, 9, -4, 12], [12, 0, 12, 0, 12, 0], [5, 4, 3, 2, 1, 0], [0, 1, 0, 1, 0, 1],
+                                     [-9, 99, -9, 99, -9, 99]])
+def test_offsets_that_are_not_ascending_end_and_stay_within_the_arrays(max_new, dtype, q_start):
+    rp = _rp()
+    x = make([3, 2, 2, 4, 1], [30, 90, 40, 12, 70], 4, 2, 64, 16, dtype, 3, key=True)
+    g = on_gpu(x)
+    N = x["k_pages"].shape[0]
+    for T in (12, 2):
+        room = torch.full((N + 4, 2, 16), 3.0, device=DEV)
+        rp.relattn_paged_weights(g["q"][:T], g["k_pages"].nan_to_num(), g["table"].clamp(0, N - 1), i32(q_start), g["kv_len"],
+                                 torch.zeros((T, 4), device=DEV), room[2:-2], aK=g["aK"], clip_k=3, max_new=max_new)
+        assert rp.relattn_get_device_error() == 0
+        assert bool((room[:2] == 3).all()) and bool((room[-2:] == 3).all())
+
+
 def test_no_tokens():
     rp = _rp()
     x = make([1], [60], 2, 2, 64, 16, BF16)
