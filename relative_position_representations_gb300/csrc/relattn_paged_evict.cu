@@ -20,7 +20,8 @@
 // 21 of them the selection. 131071 keys cut to 32768, 4 heads: 86 - 117 us; 30 are the selection (four units, so 32 CTAs:
 // three passes of 5 us and the runs' list), the moving takes four rounds of 9 us, each a chain of the list's lookups, the
 // rows' latency and the flags. Tried and dropped: the next block's lookups while this one's rows arrive (101 -> 118
-// us), blocks of 64 places with three or four CTAs an SM (106, 112).
+// us), blocks of 64 places with three or four CTAs an SM (106, 112), clusters of 16 for few units (evict of one long
+// request 75 -> 84 us).
 #include <cstdint>
 #include <cstring>
 
