@@ -9,22 +9,23 @@
 // A row's constant nl (the table term of far keys less the log-sum-exp) is formed in front and
 // lies in shared memory beside its query tile, so a weight is one FMA and one exponential. Where some key of
 // a unit is less than clip_k back, R = Q aK^T is one product more of the query tile, its accumulator
-// drained into shared memory by the first tile's threads (a row each).
+// drained into shared memory by one group's threads (a row each).
 //
-// Roles (384 threads, one CTA per SM): warp 3 takes tickets and announces units, warp 0 loads keys, tables and
-// query tiles, warp 2 the rows' constants, warp 1 issues the MMAs, warps 4-7 and 8-11 sum a pair's first and
-// second tile. A warp takes all of its scores into registers and gives the accumulator back before it works on
-// them. (Sixteen warps with half of the columns each: the instructions around a tile count twice, 1.30 us a
-// pair of tiles and a query tile in place of 1.08.)
+// Roles (512 threads, one CTA per SM): warp 3 takes tickets and announces units, warp 0 loads keys, tables and
+// query tiles, warp 2 the rows' constants, warp 1 issues the MMAs; three groups of four warps, 4-7, 8-11 and 12-15, add up
+// the products in turn, each out of its own accumulator, 32 columns while the next come. What the groups have of a key meets
+// in shared memory, in the order of the unit's turns, so equal calls give equal bits. (Two groups, a tile of the pair each, with
+// all of a row's scores in registers: a query tile with a pair 1.10 us in place of 0.90, since two warps to a scheduler do not
+// hide each other's waits and loads; a single query tile 7 % faster, whose keys are the bound. Sixteen warps with half of the
+// columns each 1.30. A second R beside the first: 247 us in place of 242 on the prompts below, for a stage of queries less.)
 // TMEM: three accumulators of 128 columns, and the unit's keys, copied there where more than one query
 // tile passes by: a 128 x 128 product with both operands in shared memory reads as much as that can give.
 //
-// What bounds it. Many rows: the sums, 2200 cycles for a query tile with both key tiles where the tensor cores work 1024
-// and the exponentials take as long; a warp's wait, load, release and loop are 900 of them, and two warps to a scheduler
-// do not hide that. A chunk of 4096 tokens over 64K keys, 8 heads of 128: 450 us, 1150 TFLOP/s, 0.60 of the tensor rate.
-// Four prompts of 4096 tokens, 16 heads of 128: 165 us, with the key term 233: the rows' constants 17, R and its gathers
-// 46. One query tile to a request (32 tokens, 16 / 4 heads of 128, 4K - 32K keys): 42 us, of which 23 stream the keys at
-// 5.2 TB/s; the rest are the set-up's launch, the first ticket and loads, and the last units.
+// What bounds it. Many rows: the sums, 1800 cycles for a query tile with both key tiles where the tensor cores work 1024
+// and the exponentials (32 a cycle) take as long. A chunk of 4096 tokens over 64K keys, 8 heads of 128: 376 us, 1370
+// TFLOP/s, 0.71 of the tensor rate. Four prompts of 4096 tokens, 16 heads of 128: 152 us, with the key term 220: the rows'
+// constants 17, R and its gathers 50. One query tile to a request (32 tokens, 16 / 4 heads of 128, 4K - 32K keys): 45
+// us, of which 25 stream the keys at 4.9 TB/s; the rest are the set-up's launch, the first ticket and loads, and the last units.
 #include <cstdint>
 #include <cstring>
 
@@ -43,12 +44,14 @@ using tc::Shared;
 using tc::wait_bar;
 using tc::wait_bar_ctrl;
 
-constexpr int kSumWarps = 8;
+constexpr int kAccs = 3;             // accumulators, a group of four summing warps to each
+constexpr int kSumWarps = 4 * kAccs;
 constexpr int kThreads = 128 + 32 * kSumWarps;
 constexpr int KB = 32;               // columns read from an accumulator at a time
 constexpr int kUnits = 4;            // announced ahead
 constexpr int kMaxK = 4, kMaxQ = 4;  // stages
-constexpr int kAccs = 3;             // accumulators
+constexpr int kParts = 1;            // pairs of tiles whose sums are joined at once
+constexpr uint32_t kPartBytes = kAccs * 2 * kTile * 4;
 constexpr int kSides = 8;            // tiles whose page numbers and masses are held
 constexpr int kBatch = 4;            // query tiles whose constants come together ...
 constexpr int kBatches = 2;          // ... and how often
@@ -59,7 +62,8 @@ enum : int {
     B_AK_FULL = B_Q_EMPTY + kMaxQ, B_AK_EMPTY, B_UNIT_FULL, B_UNIT_EMPTY = B_UNIT_FULL + kUnits,
     B_ACC_FULL = B_UNIT_EMPTY + kUnits, B_ACC_EMPTY = B_ACC_FULL + kAccs, B_SIDE_FULL = B_ACC_EMPTY + kAccs,
     B_SIDE_EMPTY = B_SIDE_FULL + kSides, B_NL_FULL = B_SIDE_EMPTY + kSides, B_NL_EMPTY = B_NL_FULL + kBatches,
-    B_R_FULL = B_NL_EMPTY + kBatches, B_R_EMPTY, B_KEYS_FREE, B_DRAIN, kNumBars
+    B_R_FULL = B_NL_EMPTY + kBatches, B_R_EMPTY, B_PART_FULL, B_PART_EMPTY = B_PART_FULL + kParts,
+    B_KEYS_FREE = B_PART_EMPTY + kParts, B_DRAIN, kNumBars
 };
 
 struct Unit {
@@ -81,7 +85,7 @@ struct TcParams {
     int box;             // keys per TMA box
     int nk, nq;          // stages of keys and of query tiles
     int old_by_tma;      // masses are fetched with the keys
-    uint32_t tile_bytes, off_q, off_ak, off_r, off_nl, off_side, off_unit, off_bar;
+    uint32_t tile_bytes, off_q, off_ak, off_r, off_nl, off_side, off_part, off_unit, off_bar;
 };
 
 // what a query tile is to a unit, the same for every role
@@ -473,20 +477,19 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem) {
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 template <int D, bool AK>
-__device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
+__device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int group_in) {
     const Params &p = tp.w.p;
-    const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
+    const int group = __shfl_sync(0xffffffffu, group_in, 0);
     const int lane = threadIdx.x & 31;
     const int quad = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5) & 3, 0);
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + kAccCol + (uint32_t)group * kTile;
     const uint32_t bars = sh.base + tp.off_bar;
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     const float sl2 = p.scale_log2;
     const int k = p.clip_k;
     float *Rs = reinterpret_cast<float *>(sh.ptr + tp.off_r);
-    uint32_t r_it = 0;
-    int acc_i = 0;
-    uint32_t acc_ph = 0;
+    uint32_t r_it = 0, acc_ph = 0;
+    int turn = 0;                        // the group that the next product is for
     bool bad = false;
     // a wait that runs out marks the lane, whose warp leaves at the next unit (the flag that it has set ends
     // the others' waits; there is no barrier that they would miss it at)
@@ -498,113 +501,110 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
         __syncwarp();
         ptx::mbar_arrive_w(b);
     };
-    // the accumulators in turn: R's, the first tile's, the second's; a warp passes over those that are not its own
-    auto wait_acc = [&]() {
-        wait_own(bar(B_ACC_FULL + acc_i), acc_ph);
-        ptx::tc_fence_after();
+    auto my_turn = [&]() {
+        const bool mine = turn == group;
+        turn = turn == kAccs - 1 ? 0 : turn + 1;
+        return mine;
     };
-    auto next_acc = [&]() {
-        if (++acc_i == kAccs) {
-            acc_i = 0;
-            acc_ph ^= 1u;
-        }
+    auto wait_acc = [&]() {
+        wait_own(bar(B_ACC_FULL + group), acc_ph);
+        ptx::tc_fence_after();
+        acc_ph ^= 1u;
     };
     auto release_acc = [&]() {
         ptx::tc_fence_before();
-        arrive(bar(B_ACC_EMPTY + acc_i));
+        arrive(bar(B_ACC_EMPTY + group));
     };
-    auto acc_at = [&]() { return lanes + kAccCol + (uint32_t)acc_i * kTile; };
     Units units(tp, sh);
-    Ring nr(kBatches), sr(kSides);
+    Ring nr(kBatches), sr(kSides), pr(kParts);
     for (;; ++units.it) {
         wait_own(units.full(), units.parity());
         if (__any_sync(0xffffffffu, bad)) break;
         const Unit u = units.get();
         arrive(units.empty());
         if (!u.more) break;
+        // the group's place in the turns of this unit, in whose order the sums are joined
+        const int place = group >= turn ? group - turn : group - turn + kAccs;
         const int last = u.pos0 + u.n - 1, first = p.window > 0 ? max(0, max(u.pos0, 0) - p.window + 1) : 0;
         for (int t0 = u.t0; t0 < u.t1; t0 += 2) {
-            const bool two = t0 + 1 < u.t1, have = !slot || two;
-            const int j0 = u.key(t0 + slot);
-            const int j = j0 + quad * 32 + lane, j_lo = j0 + quad * 32, j_hi = j_lo + 31;
-            // Query tiles plain0 .. plain1 - 1 are whole, see all of the warp's keys and lie past the band (of either
-            // tile): no masks, no tables. They come after the first one or two, but for windows.
-            int plain0, plain1 = min(u.n / tp.TS, u.qb);
-            {
-                const int past = max(AK ? max(j_hi, max(j0, u.key(t0 + 1 - slot)) + kTile - 1) + k : j_hi, u.pos0);
-                plain0 = (past - u.pos0 + tp.TS - 1) / tp.TS;
-                if (p.window > 0 && j_hi >= p.sinks)
-                    plain1 = (int)max(0LL, min((long long)plain1, ((long long)j_lo + p.window - u.pos0) / tp.TS));
-                if (u.pos0 < 0) plain1 = 0;
-            }
-            float2 s01 = dup(0.f), s23 = dup(0.f);
+            const bool two = t0 + 1 < u.t1;
+            const int ja = u.key(t0), jb = u.key(t0 + 1);
+            // Query tiles from plain0 on lie past the band of either tile, those from there to plain1 - 1 are also whole and
+            // see all of the warp's keys: no masks, no tables. They come after the first one or two, but for windows.
+            const int plain0 = (max(max(ja, jb) + kTile - 1 + (AK ? k : 0), u.pos0) - u.pos0 + tp.TS - 1) / tp.TS;
+            auto plain_end = [&](int j_lo) {
+                int end = u.pos0 < 0 ? 0 : min(u.n / tp.TS, u.qb);
+                if (p.window > 0 && j_lo + 31 >= p.sinks)
+                    end = (int)max(0LL, min((long long)end, ((long long)j_lo + p.window - u.pos0) / tp.TS));
+                return end;
+            };
+            const int end_a = plain_end(ja + quad * 32), end_b = plain_end(jb + quad * 32);
+            float2 a01 = dup(0.f), a23 = dup(0.f), b01 = dup(0.f), b23 = dup(0.f);   // of the two tiles
+            int tile = -1;               // what this group has of the query tile
             for (int q = u.qa; q < u.qb; ++q) {
                 const int in = (q - u.qa) & (kBatch - 1);
                 if (in == 0 && t0 == u.t0) wait_own(bar(B_NL_FULL + nr.st), nr.ph);
                 const float *nl = reinterpret_cast<const float *>(sh.ptr + tp.off_nl + (nr.st * kBatch + in) * BM * 4);
-                auto weights = [&](float *x, int c) {   // of 32 columns, with their constants
-#pragma unroll
-                    for (int e = 0; e < KB; e += 4) {
-                        const float4 n = *reinterpret_cast<const float4 *>(nl + c + e);
-                        const float2 a = __ffma2_rn(pair(x, e), dup(sl2), make_float2(n.x, n.y));
-                        const float2 b = __ffma2_rn(pair(x, e + 2), dup(sl2), make_float2(n.z, n.w));
-                        x[e] = ptx::ex2(a.x);
-                        x[e + 1] = ptx::ex2(a.y);
-                        x[e + 2] = ptx::ex2(b.x);
-                        x[e + 3] = ptx::ex2(b.y);
-                    }
-                };
-                auto add = [&](const float *x) {
-#pragma unroll
-                    for (int e = 0; e < KB; e += 4) {
-                        s01 = __fadd2_rn(s01, make_float2(x[e], x[e + 1]));
-                        s23 = __fadd2_rn(s23, make_float2(x[e + 2], x[e + 3]));
-                    }
-                };
-                if (q >= plain0 && q < plain1) {
-                    if (slot) next_acc();
-                    if (have) {
+                const bool band = AK && q < plain0 && query_tile(tp, u, q, ja, jb).band;
+                if (AK && band) {
+                    if (my_turn()) {   // R, a row each
                         wait_acc();
-                        float x[kTile];
+                        wait_own(bar(B_R_EMPTY), (r_it & 1u) ^ 1u);   // the last one has been read
+                        float *row = Rs + (quad * 32 + lane) * tp.SR;
+                        float r0 = 0.f;
+                        for (int c0 = 0; c0 < tp.npad; c0 += 16) {
+                            uint32_t r[16];
+                            ptx::tmem_ld16(acc + (uint32_t)c0, r);
+                            ptx::tmem_ld_wait();
+                            if (c0 == 0) r0 = __uint_as_float(r[0]);
 #pragma unroll
-                        for (int c = 0; c < kTile; c += KB) ptx::tmem_ld32f(acc_at() + (uint32_t)c, x + c);
-                        ptx::tmem_ld_wait();
+                            for (int e = 0; e < 16; ++e)
+                                if (c0 + e <= k) row[c0 + e] = (__uint_as_float(r[e]) - r0) * sl2;
+                        }
                         release_acc();
-                        next_acc();
-#pragma unroll
-                        for (int c = 0; c < kTile; c += KB) {
-                            weights(x + c, c);
-                            add(x + c);
-                        }
+                        ptx::mbar_arrive_w(bar(B_R_FULL));
                     }
-                    if (!slot && two) next_acc();
-                } else {
-                    const QueryTile t = query_tile(tp, u, q, u.key(t0), u.key(t0 + 1));
-                    if (AK && t.band) {
-                        if (slot == 0) {   // R, a row each
-                            wait_acc();
-                            wait_own(bar(B_R_EMPTY), (r_it & 1u) ^ 1u);   // the last one has been read
-                            float *row = Rs + (quad * 32 + lane) * tp.SR;
-                            float r0 = 0.f;
-                            for (int c0 = 0; c0 < tp.npad; c0 += 16) {
-                                uint32_t r[16];
-                                ptx::tmem_ld16(acc_at() + (uint32_t)c0, r);
-                                ptx::tmem_ld_wait();
-                                if (c0 == 0) r0 = __uint_as_float(r[0]);
+                    wait_own(bar(B_R_FULL), r_it & 1u);
+                    ++r_it;
+                }
+                tile = my_turn() ? 0 : -1;
+                if (two && my_turn()) tile = 1;
+                if (tile >= 0) {
+                    float2 s01 = tile ? b01 : a01, s23 = tile ? b23 : a23;
+                    auto weights = [&](float *x, int c) {   // of 32 columns, with their constants
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (c0 + e <= k) row[c0 + e] = (__uint_as_float(r[e]) - r0) * sl2;
-                            }
-                            release_acc();
-                            ptx::mbar_arrive_w(bar(B_R_FULL));
+                        for (int e = 0; e < KB; e += 4) {
+                            const float4 n = *reinterpret_cast<const float4 *>(nl + c + e);
+                            const float2 v = __ffma2_rn(pair(x, e), dup(sl2), make_float2(n.x, n.y));
+                            const float2 w = __ffma2_rn(pair(x, e + 2), dup(sl2), make_float2(n.z, n.w));
+                            x[e] = ptx::ex2(v.x);
+                            x[e + 1] = ptx::ex2(v.y);
+                            x[e + 2] = ptx::ex2(w.x);
+                            x[e + 3] = ptx::ex2(w.y);
                         }
-                        next_acc();
-                        wait_own(bar(B_R_FULL), r_it & 1u);
-                        ++r_it;
-                    }
-                    if (slot) next_acc();
-                    if (have) {
-                        wait_acc();
+                    };
+                    auto add = [&](const float *x) {
+#pragma unroll
+                        for (int e = 0; e < KB; e += 4) {
+                            s01 = __fadd2_rn(s01, make_float2(x[e], x[e + 1]));
+                            s23 = __fadd2_rn(s23, make_float2(x[e + 2], x[e + 3]));
+                        }
+                    };
+                    wait_acc();
+                    if (q >= plain0 && q < (tile ? end_b : end_a)) {
+                        float x[2][KB];                     // 32 columns come while the last ones are added up
+                        ptx::tmem_ld32f(acc, x[0]);
+#pragma unroll
+                        for (int i = 0; i < kTile / KB; ++i) {
+                            ptx::tmem_ld_wait();
+                            if (i + 1 < kTile / KB) ptx::tmem_ld32f(acc + (uint32_t)((i + 1) * KB), x[(i + 1) & 1]);
+                            else release_acc();
+                            weights(x[i & 1], i * KB);
+                            add(x[i & 1]);
+                        }
+                    } else {
+                        const int j = (tile ? jb : ja) + quad * 32 + lane, j_lo = j - lane, j_hi = j_lo + 31;
+                        const QueryTile t = query_tile(tp, u, q, ja, jb);
                         const bool far = !AK || k == 0 || j_hi <= t.pos_lo - k;   // else R is there
                         const bool full = t.ntok == tp.TS && j_hi <= t.pos_lo &&
                                           (p.window == 0 || j_lo > t.pos_hi - p.window || j_hi < p.sinks);
@@ -632,14 +632,26 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                                     continue;
                                 }
                                 float x[KB];
-                                ptx::tmem_ld32f(acc_at() + (uint32_t)c, x);
+                                ptx::tmem_ld32f(acc + (uint32_t)c, x);
                                 ptx::tmem_ld_wait();
                                 if (past) {
                                     weights(x, c);
                                     row += KB * tp.SR;
                                     hh = (hh + KB) % p.g;
                                     lab = j - t.pos_lo + k - (c + KB) / p.g;
-                                } else {   // R of token i: its entry for key j, one further back with every token
+                                } else if (p.g == 1) {   // R of token i: its entry for key j, one further back with every token
+#pragma unroll
+                                    for (int e = 0; e < KB; e += 4) {
+                                        const float4 n = *reinterpret_cast<const float4 *>(nl + c + e);
+                                        const float ns[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            x[e + i] = ptx::ex2(fmaf(x[e + i], sl2, ns[i] + row[__viaddmin_s32_relu(lab, -(e + i), k)]));
+                                            row += tp.SR;
+                                        }
+                                    }
+                                    lab -= KB;
+                                } else {
 #pragma unroll
                                     for (int e = 0; e < KB; ++e) {
                                         x[e] = ptx::ex2(fmaf(x[e], sl2, nl[c + e] + row[min(max(lab, 0), k)]));
@@ -650,40 +662,67 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                                         }
                                     }
                                 }
-                                const uint32_t on = below(c_hi - c) & ~below(c_lo - c);
+                                // (masked where a row does not see a key of the warp's, or is none)
+                                if (!full && (p.window > 0 || p0 < j_hi || c + KB > t.ntok * p.g)) {
+                                    const uint32_t on = below(c_hi - c) & ~below(c_lo - c);
 #pragma unroll
-                                for (int e = 0; e < KB; ++e) x[e] = on >> e & 1 ? x[e] : 0.f;
+                                    for (int e = 0; e < KB; ++e) x[e] = on >> e & 1 ? x[e] : 0.f;
+                                }
                                 add(x);
                                 __syncwarp();
                             }
                         }
                         release_acc();
-                        next_acc();
                     }
-                    if (!slot && two) next_acc();
-                    if (AK && t.band) arrive(bar(B_R_EMPTY));
+                    if (tile) {
+                        b01 = s01;
+                        b23 = s23;
+                    } else {
+                        a01 = s01;
+                        a23 = s23;
+                    }
                 }
+                if (AK && band) arrive(bar(B_R_EMPTY));
                 if ((in == kBatch - 1 || q + 1 == u.qb) && t0 + 2 >= u.t1) {
                     arrive(bar(B_NL_EMPTY + nr.st));
                     nr.next();
                 }
             }
-            if (slot) sr.next();   // (the pair's first tile is the other warps')
-            if (have) {
+            // ---- the sums: of several query tiles joined by one group for either tile
+            int mine = tile;             // the tile that this group finishes
+            const float sum_a = (a01.x + a01.y) + (a23.x + a23.y), sum_b = (b01.x + b01.y) + (b23.x + b23.y);
+            float sum = tile > 0 ? sum_b : sum_a;
+            if (u.qb - u.qa != 1) {
+                float *part = reinterpret_cast<float *>(sh.ptr + tp.off_part + pr.st * kPartBytes) + quad * 32 + lane;
+                wait_own(bar(B_PART_EMPTY + pr.st), pr.ph ^ 1u);
+                part[place * 2 * kTile] = sum_a;
+                part[(place * 2 + 1) * kTile] = sum_b;
+                arrive(bar(B_PART_FULL + pr.st));
+                mine = group == 0 || (group == 1 && two) ? group : -1;
+                if (group < 2) {
+                    wait_own(bar(B_PART_FULL + pr.st), pr.ph);
+                    sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kAccs; ++i) sum += part[(i * 2 + group) * kTile];
+                    arrive(bar(B_PART_EMPTY + pr.st));
+                }
+                pr.next();
+            }
+            for (int i = 0; i < (two ? 2 : 1); ++i, sr.next()) {
+                if (mine != i) continue;
+                const int j0 = i ? jb : ja, j = j0 + quad * 32 + lane;
                 wait_own(bar(B_SIDE_FULL + sr.st), sr.ph);
                 const uint8_t *side = sh.ptr + tp.off_side + sr.st * kSideBytes;
                 const int pg = reinterpret_cast<const int *>(side)[(j - j0) / tp.box];
-                const bool mine = pg >= 0 && j <= last && (j >= first || j < p.sinks);
+                const bool seen = pg >= 0 && j <= last && (j >= first || j < p.sinks);
                 float *at = tp.w.mass + (long long)pg * tp.w.mass_stride +
                             (((long long)u.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
                 float old = 0.f;
-                if (tp.w.accumulate && mine && j < u.pos0)
+                if (tp.w.accumulate && seen && j < u.pos0)
                     old = tp.old_by_tma ? reinterpret_cast<const float *>(side + 64)[j - j0] : *at;
                 arrive(bar(B_SIDE_EMPTY + sr.st));
-                if (mine && !bad) *at = old + ((s01.x + s01.y) + (s23.x + s23.y));
-                sr.next();
+                if (seen && !bad) *at = old + sum;
             }
-            if (!slot && two) sr.next();
         }
     }
 }
@@ -707,11 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
             if (i >= B_UNIT_EMPTY && i < B_ACC_FULL) n = 3 + kSumWarps;
-            if (i >= B_ACC_EMPTY && i < B_SIDE_FULL) n = kSumWarps / 2;        // a tile's warps
-            if (i >= B_SIDE_EMPTY && i < B_NL_FULL) n = 4;                     // a tile's warps
+            if (i >= B_ACC_EMPTY && i < B_SIDE_FULL) n = 4;                    // a group
+            if (i >= B_SIDE_EMPTY && i < B_NL_FULL) n = 4;                     // a group
             if (i >= B_NL_EMPTY && i < B_R_FULL) n = kSumWarps;
-            if (i == B_R_FULL) n = kSumWarps / 2;
+            if (i == B_R_FULL) n = 4;
             if (i == B_R_EMPTY) n = kSumWarps;
+            if (i >= B_PART_FULL && i < B_PART_EMPTY) n = kSumWarps;
+            if (i >= B_PART_EMPTY && i < B_KEYS_FREE) n = 8;                   // two groups
             ptx::mbar_init(bars + 8u * (uint32_t)i, n);
         }
         *sh.abort_flag = 0;
@@ -772,20 +813,21 @@ cudaError_t launch_d(const PagedWeightsArgs &wa, const WeightParams &w, cudaStre
     tp.box = a.page_size < kTile ? a.page_size : kTile;
     tp.tile_bytes = (uint32_t)kTile * D * 2;
     const uint32_t ak_bytes = ak && p.clip_k ? (uint32_t)tp.npad * D * 2 : 0, r_bytes = ak && p.clip_k ? BM * tp.SR * 4 : 0;
-    const uint32_t rest = r_bytes + kBatches * kBatch * BM * 4 + kSides * kSideBytes + kUnits * sizeof(Unit) + kNumBars * 8 + 16;
+    const uint32_t rest = r_bytes + kBatches * kBatch * BM * 4 + kSides * kSideBytes + kParts * kPartBytes + kUnits * sizeof(Unit) + kNumBars * 8 + 16;
     int stages = (int)(((uint32_t)di.smem_optin - rest - ak_bytes) / tp.tile_bytes);
     if (stages > kMaxK + kMaxQ) stages = kMaxK + kMaxQ;
-    if (stages < 4) return cudaErrorNotSupported;
+    if (stages < 3) return cudaErrorNotSupported;
     // Two tiles of keys are enough where they move on to TMEM. One query tile to a request: the keys stream
     // by and the query tile stays, so more keys are on their way
     const long long rows = (long long)(a.max_new > 0 ? a.max_new : a.tokens / a.B) * p.g;
-    tp.nk = rows <= BM ? (stages - 2 < kMaxK ? stages - 2 : kMaxK) : 2;
+    tp.nk = rows <= BM && stages > 4 ? (stages - 2 < kMaxK ? stages - 2 : kMaxK) : 2;
     tp.nq = stages - tp.nk < kMaxQ ? stages - tp.nk : kMaxQ;
     tp.off_q = tp.nk * tp.tile_bytes;
     tp.off_ak = tp.off_q + tp.nq * tp.tile_bytes;
     tp.off_nl = tp.off_ak + ak_bytes;
     tp.off_side = tp.off_nl + kBatches * kBatch * BM * 4;
-    tp.off_unit = tp.off_side + kSides * kSideBytes;
+    tp.off_part = tp.off_side + kSides * kSideBytes;
+    tp.off_unit = tp.off_part + kParts * kPartBytes;
     tp.off_bar = tp.off_unit + kUnits * sizeof(Unit);
     tp.off_r = tp.off_bar + kNumBars * 8 + 16;
     uint32_t smem = tp.off_r + r_bytes;
