@@ -489,7 +489,7 @@ RELATTN_API relattn_status_t relattn_paged_shared_workspace_size(int tokens, int
  *   q_start, kv_len, aK, table_head_stride, clip_k, window, sinks, scale, B, tokens, max_new, H, Hkv,
  *   d, dtype          as in relattn_paged_fwd. The rows may also be only the last tokens of a prompt,
  *                     whose weights stand for those of what follows.
- *   lse               [tokens, H] fp32, contiguous.
+ *   lse               [tokens, H] fp32, contiguous. A row whose entry is -infinity counts nothing.
  *   mass              [num_pages, Hkv, page_size] fp32, mass_stride elements between pages. Written
  *                     are the entries of keys that some row of the request sees, no others.
  *   accumulate        1: keys in front of the new tokens keep what they have and get the sum added, the

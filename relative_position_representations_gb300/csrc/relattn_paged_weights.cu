@@ -538,8 +538,11 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
                 for (int e = 0; e < 2; ++e) {
                     const int r2 = g0 + 8 * n + 2 * c + e, t2 = r2 / p.g, h2 = r2 - t2 * p.g;
                     pos[n][e] = g.pos_lo + (r2 < rows ? t2 : 0);
-                    nl[n][e] = -INFINITY;
-                    if (r2 < rows) nl[n][e] = -kLog2e * __ldg(w.lse + (long long)(g.row0 + t2) * p.H + g.kvh * p.g + h2);
+                    nl[n][e] = -INFINITY;   // (of a row without keys, as its log-sum-exp says, too)
+                    if (r2 < rows) {
+                        const float lse = __ldg(w.lse + (long long)(g.row0 + t2) * p.H + g.kvh * p.g + h2);
+                        if (lse != -INFINITY) nl[n][e] = -kLog2e * lse;
+                    }
                 }
             }
             if (AK) {

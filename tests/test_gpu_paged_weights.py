@@ -421,3 +421,28 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for m, w in zip(ms, want):
         assert torch.equal(m, w)
+
+
+@pytest.mark.parametrize("max_new,new,dtype", [(1, 1, BF16), (1, 30, BF16), (0, 40, BF16), (0, 40, F32)])
+@pytest.mark.parametrize("key", [False, True])
+def test_rows_marked_as_without_keys_add_nothing(max_new, new, dtype, key):
+    """A log-sum-exp of -infinity is that of a row without keys, whatever the row sees."""
+    rp = _rp()
+    k = 5 * key
+    x = make([new, new, 1], [300, 129, 200], 4, 2, 64, 16, dtype, k, key=key)
+    N = x["k_pages"].shape[0]
+    a = args_of(x)
+    lse = op.log_sum(**a, clip_k=k, window=0, sinks=0, scale=0.125)[0].astype(np.float32)
+    none = np.random.default_rng(2).random(lse.shape) < 0.5
+    none[0], none[-1] = True, False
+    mass = np.random.default_rng(1).random((N, 2, 16)).astype(np.float32)
+    # (1e6: a weight of 0 in 64 bits as well)
+    want, bound = op.weights(**a, clip_k=k, window=0, sinks=0, scale=0.125, lse=np.where(none, 1e6, lse).astype(np.float64),
+                             mass=mass.astype(np.float64), accumulate=True)
+    m = torch.from_numpy(mass).to(DEV)
+    g = on_gpu(x)
+    marked = torch.from_numpy(np.where(none, np.float32(-np.inf), lse)).to(DEV)
+    rp.relattn_paged_weights(g["q"], g["k_pages"], g["table"], g["q_start"], g["kv_len"], marked, m, aK=g["aK"], clip_k=k,
+                             scale=0.125, max_new=max_new)
+    assert rp.relattn_get_device_error() == 0
+    assert (np.abs(f64(m) - want) <= bound).all()
