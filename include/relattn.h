@@ -543,7 +543,8 @@ RELATTN_API relattn_status_t relattn_paged_weights_workspace_size(int tokens, in
  *                     pages that become free, request after request, are written to
  *                     free_pages[free_head - n .. free_head - 1]; free_head_out = free_head - n (may
  *                     be the same address). With free_head < n or > num_free nothing is given back
- *                     and the status word becomes RELATTN_ERR_INVALID_ARG.
+ *                     and the status word becomes RELATTN_ERR_INVALID_ARG. Numbers outside the cache are
+ *                     no pages: they are not written and not counted.
  *   kv_len_out        [B] int32: budget where a request was cut, else kv_len (may be kv_len itself).
  *   workspace         caller-owned device scratch of relattn_paged_evict_workspace_size bytes (with
  *                     max_keys = max_pages * page_size), 16-byte aligned; calls that may overlap need

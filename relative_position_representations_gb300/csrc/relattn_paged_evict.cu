@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
 }
 
 // ------------------------------------------------------------------ lengths and free pages
-// One block: kv_len_out, and the pages behind the budget back onto the list, request by request.
+// One block: kv_len_out, and the pages behind the budget back onto the list, request by request. Entries outside
+// the cache are no pages and stay off it.
 __device__ void evict_lengths(const EvictParams &p) {
     const PagedEvictArgs &a = p.a;
     __shared__ int warp_sum[kMoveThreads / 32], count_s[kMoveThreads], to_s[kMoveThreads];
@@ -384,17 +385,15 @@ __device__ void evict_lengths(const EvictParams &p) {
     const int first = (int)(((long long)a.budget + a.page_size - 1) >> p.shift);
     const int requests = p.state[1];
     auto pages = [&](int i) { return (int)(((long long)p.list[i].y + a.page_size - 1) >> p.shift) - first; };
+    auto row_of = [&](int i) { return a.block_table + (long long)p.list[i].x * a.bt_stride + first; };
+    auto exists = [&](int page) { return (unsigned)page < (unsigned)a.num_pages; };
     // a request's length may be overwritten in place: only those in the list change
     if (a.kv_len_out != a.kv_len)
         for (int b = tid; b < a.B; b += kMoveThreads) {
             const int n = a.kv_len[b];
             if (min(max(n, 0), p.cap) <= a.limit) a.kv_len_out[b] = n;
         }
-    int total = 0;
-    for (int i = tid; i < requests; i += kMoveThreads) {
-        a.kv_len_out[p.list[i].x] = a.budget;
-        total += pages(i);
-    }
+    for (int i = tid; i < requests; i += kMoveThreads) a.kv_len_out[p.list[i].x] = a.budget;
     if (!a.free_pages) return;
     auto block_scan = [&](int v, int &all) {   // inclusive
 #pragma unroll
@@ -412,10 +411,41 @@ __device__ void evict_lengths(const EvictParams &p) {
         }
         return v;
     };
-    int all;
-    block_scan(total, all);
+    // f(number, place on the list) of every entry: a warp takes a request's, or the block where they are many
+    auto entries = [&](auto f) {
+        int at = 0;
+        for (int i0 = 0; i0 < requests; i0 += kMoveThreads) {
+            const int i = i0 + tid, n = i < requests ? pages(i) : 0;
+            int sum;
+            const int mine = at + block_scan(n, sum) - n;
+            at += sum;
+            __syncthreads();
+            count_s[tid] = n;
+            to_s[tid] = mine;
+            __syncthreads();
+            for (int q = warp; q < kMoveThreads; q += kMoveThreads / 32) {
+                const int nn = count_s[q];
+                if (nn == 0 || nn > kManyPages) continue;
+                const int *row = row_of(i0 + q);
+                for (int e = lane; e < nn; e += 32) f(row[e], to_s[q] + e);
+            }
+            for (int q = 0; q < min(kMoveThreads, requests - i0); ++q) {
+                const int nn = count_s[q];
+                if (nn <= kManyPages) continue;
+                const int *row = row_of(i0 + q);
+#pragma unroll 4
+                for (int e = tid; e < nn; e += kMoveThreads) f(row[e], to_s[q] + e);
+            }
+            __syncthreads();
+        }
+        return at;
+    };
+    int good = 0, all;
+    const int total = entries([&](int page, int) { good += exists(page); });
+    block_scan(good, all);
     const int head = *a.free_head;
     __syncthreads();
+    if (all < total && tid == 0) atomicCAS(a.err, 0, paged::kInvalidArg);
     if (head > a.num_free || head < all) {   // not the list that the pages came from
         if (tid == 0) {
             *a.free_head_out = head;
@@ -425,31 +455,21 @@ __device__ void evict_lengths(const EvictParams &p) {
     }
     if (tid == 0) *a.free_head_out = head - all;
     int *dst = a.free_pages + head - all;
-    int at = 0;
-    for (int i0 = 0; i0 < requests; i0 += kMoveThreads) {
-        const int i = i0 + tid, n = i < requests ? pages(i) : 0;
-        int sum;
-        const int mine = at + block_scan(n, sum) - n;
-        at += sum;
-        // a warp per request writes its pages, or the block where they are many
-        __syncthreads();
-        count_s[tid] = n;
-        to_s[tid] = mine;
-        __syncthreads();
-        for (int q = warp; q < kMoveThreads; q += kMoveThreads / 32) {
-            const int nn = count_s[q];
-            if (nn > kManyPages) continue;
-            const int *row = a.block_table + (long long)(nn ? p.list[i0 + q].x : 0) * a.bt_stride + first;
-            for (int e = lane; e < nn; e += 32) dst[to_s[q] + e] = row[e];
+    if (all == total) {
+        entries([&](int page, int to) { dst[to] = page; });
+        return;
+    }
+    int at = 0;                                // some are left out: the places are counted
+    for (int i = 0; i < requests; ++i) {
+        const int n = pages(i), *row = row_of(i);
+        for (int e0 = 0; e0 < n; e0 += kMoveThreads) {
+            const int page = e0 + tid < n ? row[e0 + tid] : -1;
+            int sum;
+            const int to = at + block_scan(exists(page), sum) - 1;
+            if (exists(page)) dst[to] = page;
+            at += sum;
+            __syncthreads();
         }
-        for (int q = 0; q < min(kMoveThreads, requests - i0); ++q) {
-            const int nn = count_s[q];
-            if (nn <= kManyPages) continue;
-            const int *row = a.block_table + (long long)p.list[i0 + q].x * a.bt_stride + first;
-#pragma unroll 4
-            for (int e = tid; e < nn; e += kMoveThreads) dst[to_s[q] + e] = row[e];
-        }
-        __syncthreads();
     }
 }
 

@@ -257,3 +257,28 @@ def test_on_another_stream_and_twice_at_once():
         assert n.tolist() == [1000, 1000]
         assert np.array_equal(f(o[0]), w[1]) and np.array_equal(f(o[1]), w[2]) and np.array_equal(f(o[2]), w[3])
     assert rp.relattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,budget,bad", [
+    ([100], 50, [(0, 4)]),                                          # the only page that a budget leaves: none of it
+    ([100, 90, 20, 97], 50, [(0, 6), (1, 4), (1, 5), (3, 5)]),      # all of a request's, some of the others'
+    ([100, 3000, 90], 50, [(1, 4), (1, 69), (1, 187), (2, 1)]),     # of hundreds; one in front of the budget too
+    ([5000], 40, [(0, i) for i in range(3, 313, 2)])])
+def test_numbers_of_no_page_do_not_get_onto_the_list(lens, budget, bad):
+    """Table entries outside the cache are reported and left out of what is given back."""
+    rp = _rp()
+    P = 16
+    x = make(lens, 2, 64, P, seed=4)
+    N = x["mass"].shape[0]
+    for i, (b, e) in enumerate(bad):
+        x["table"][b, e] = (-1, N, 2 ** 30, -2 ** 31)[i % 4]
+    gone = [int(p) for b, n in enumerate(lens) if n > budget for p in x["table"][b, -(-budget // P):-(-n // P)]]
+    gone = [p for p in gone if 0 <= p < N]
+    want, head = x["free"].copy(), x["head"] - len(gone)
+    want[head:head + len(gone)] = gone
+    free = i32(x["free"])
+    out, got = rp.relattn_paged_evict(i32(lens), i32(x["table"]), x["k"].to(DEV), x["v"].to(DEV), x["mass"].to(DEV), budget,
+                                      free_pages=free, free_head=i32([x["head"]]))
+    assert rp.relattn_get_device_error() == 1
+    assert out.tolist() == [min(n, budget) for n in lens]
+    assert int(got) == head and np.array_equal(free.cpu().numpy(), want)
