@@ -554,7 +554,9 @@ RELATTN_API relattn_status_t relattn_paged_weights_workspace_size(int tokens, in
  * all of its keys lie below `sinks`; no other page may be shared. A page number outside the cache
  * sets the status word to RELATTN_ERR_INVALID_ARG: its masses count least, and rows from or to it
  * are not copied. bf16 or fp32, d <= 128, B <= 16384, else RELATTN_ERR_UNSUPPORTED. Waits between
- * the CTAs (for a row to be read before it is overwritten) are bounded as in relattn_fwd.
+ * the CTAs (for a row to be read before it is overwritten) are bounded as in relattn_fwd. After one that runs
+ * out (RELATTN_ERR_TIMEOUT in the status word) the keys, values and masses of the requests that were cut are
+ * undefined; their lengths, the free list and every other request are as after any other call.
  */
 RELATTN_API relattn_status_t relattn_paged_evict(const int *kv_len, const int *block_table,
                                      long long table_stride, int max_pages, void *k_pages,
@@ -744,7 +746,8 @@ RELATTN_API relattn_status_t relattn_get_device_error(relattn_stream_t stream);
 /*
  * relattn_set_wait_limit — the bound of every device-side wait of the tensor-core forward
  * kernels (relattn_fwd, relattn_t5bias_fwd, relattn_alibi_fwd, relattn_offset_bias_fwd,
- * relattn_paged_fwd on bf16), in SM clock cycles; the default is 2e9 (about one second at 2 GHz). A wait that
+ * relattn_paged_fwd, relattn_paged_shared_fwd and relattn_paged_weights on bf16, and of relattn_paged_evict, which
+ * only stops moving rows where it had to wait), in SM clock cycles; the default is 2e9 (about one second at 2 GHz). A wait that
  * runs out makes every warp of the kernel stop, wait (again bounded) for its copies and
  * tensor-core operations in flight, release its tensor memory and exit; the call's output is
  * then undefined and relattn_get_device_error reports RELATTN_ERR_TIMEOUT. The setting is
@@ -757,7 +760,8 @@ RELATTN_API relattn_status_t relattn_set_wait_limit(long long cycles);
 /*
  * relattn_debug_withhold_first_load — test hook for the timeout path: with on = 1, each
  * producer warp of the tensor-core forward kernels announces the Q tiles of its first work
- * item to their barrier but never loads them (relattn_paged_fwd: the queries of each CTA's first piece), so the
+ * item to their barrier but never loads them (relattn_paged_fwd: the queries of each CTA's first piece;
+ * relattn_paged_evict: the word that a head's first block of rows has been read), so the
  * bounded wait for them runs out (no fault, no trap: the kernel exits through its abort path). on = 0
  * (the default) restores normal launches. Process-wide; never set it in production.
  */

@@ -1125,7 +1125,8 @@ def relattn_set_wait_limit(cycles: int) -> None:
 
 
 def relattn_debug_withhold_first_load(on: bool) -> None:
-    """Test hook: the tensor-core forward kernels withhold their first Q load (timeout test)."""
+    """Test hook: the tensor-core forward kernels withhold their first Q load, eviction the word that its first
+    rows have been read (timeout tests)."""
     st = int(_lib.relattn_debug_withhold_first_load(1 if on else 0))
     if st != OK:
         raise RelattnError(st, "relattn_debug_withhold_first_load")

@@ -878,6 +878,7 @@ relattn_status_t relattn_paged_evict(const int *kv_len, const int *block_table, 
     a.free_head_out = free_head_out;
     a.workspace = workspace;
     a.wait_limit = g_wait_limit.load();
+    a.withhold = g_withhold_q.load();
     const relattn_status_t st = paged_device(&a.err);
     if (st != RELATTN_OK) return st;
     return from_cuda(relattn::launch_paged_evict(a, reinterpret_cast<cudaStream_t>(stream)));

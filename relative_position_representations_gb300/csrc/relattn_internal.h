@@ -251,6 +251,7 @@ struct PagedEvictArgs {
     void *workspace;
     int *err;
     long long wait_limit;
+    int withhold;                     // test hook: a unit's first block is never said to have been read
 };
 unsigned long long paged_evict_workspace_bytes(int B, int Hkv, long long max_keys);
 cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s);

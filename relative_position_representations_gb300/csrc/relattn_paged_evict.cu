@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
         __threadfence();                     // the rows have been read
         __syncthreads();
         if (tid == 0) {
-            store_release(done + t, 1);
+            if (!a.withhold || t > 0) store_release(done + t, 1);
             int ok = 1;
             const long long t0 = clock64();
             for (int q = dep0; q <= dep1 && ok; ++q)

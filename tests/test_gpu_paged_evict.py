@@ -282,3 +282,32 @@ def test_numbers_of_no_page_do_not_get_onto_the_list(lens, budget, bad):
     assert rp.relattn_get_device_error() == 1
     assert out.tolist() == [min(n, budget) for n in lens]
     assert int(got) == head and np.array_equal(free.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 128), (BF16, 33)])
+def test_a_wait_that_runs_out(dtype, d):
+    """A block of rows that is never said to have been read: those that would overwrite them give up and say so; lengths, the
+    free list and the request that is not cut are as they should be, and the next call is right."""
+    rp = _rp()
+    lens, budget = [600, 100, 700], 256
+    x = make(lens, 2, d, 16, dtype=dtype, seed=d)
+    want = op.evict(lens, x["table"], *(x[n].double().numpy() for n in ("k", "v", "mass")), budget, budget, 0, 100, x["free"],
+                    x["head"])
+    k, v, mass, free = x["k"].to(DEV), x["v"].to(DEV), x["mass"].to(DEV), i32(x["free"])
+    try:
+        rp.relattn_set_wait_limit(2_000_000)
+        rp.relattn_debug_withhold_first_load(1)
+        out, head = rp.relattn_paged_evict(i32(lens), i32(x["table"]), k, v, mass, budget, recent=100, free_pages=free,
+                                           free_head=i32([x["head"]]))
+        assert rp.relattn_get_device_error() == 4
+    finally:
+        rp.relattn_debug_withhold_first_load(0)
+        rp.relattn_set_wait_limit(2_000_000_000)
+    assert out.tolist() == want[0].tolist() == [256, 100, 256]
+    assert int(head) == want[5] and np.array_equal(free.cpu().numpy(), want[4])
+    cut = torch.from_numpy(np.concatenate([x["table"][0], x["table"][2]]))
+    rest = torch.ones(len(x["k"]), dtype=torch.bool)
+    rest[cut[cut < len(rest)]] = False
+    for got, was in ((k, x["k"]), (v, x["v"]), (mass, x["mass"])):
+        assert torch.equal(got.cpu()[rest], was[rest])
+    run(x, lens, budget, budget, 0, 100)
