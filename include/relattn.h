@@ -493,12 +493,15 @@ RELATTN_API relattn_status_t relattn_paged_shared_workspace_size(int tokens, int
  *   mass              [num_pages, Hkv, page_size] fp32, mass_stride elements between pages. Written
  *                     are the entries of keys that some row of the request sees, no others.
  *   accumulate        1: keys in front of the new tokens keep what they have and get the sum added, the
- *                     new tokens' own entries are set; 0: every entry that is written is set.
+ *                     new tokens' own entries are set; 0: every entry that is written is set. A key in
+ *                     front of the new tokens of several requests that share its page (as prefixes for
+ *                     relattn_paged_shared_fwd are) gets the sums of all of them with 1, and holds one of them
+ *                     with 0.
  *   workspace         caller-owned device scratch of relattn_paged_weights_workspace_size bytes, 16-byte
  *                     aligned; calls that may overlap need one each.
  *
- * Each entry is summed in one place and in a fixed order, in fp32, so equal calls give equal bits. Entries of
- * a page that several requests of the call share hold no defined number afterwards. A page number
+ * A request's part of an entry is summed in one place and in a fixed order, in fp32, so equal calls give equal bits,
+ * but for pages that several requests of the call share, where the order of the requests' sums is open. A page number
  * outside the cache counts nothing and sets the status word to RELATTN_ERR_INVALID_ARG. bf16 with d =
  * 64 or 128, pages of at least 8 keys and rows that start on 16-byte boundaries runs on the tensor
  * cores (with at most 16 query rows, max_new times H / Hkv, per key/value head on a kernel for

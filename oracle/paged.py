@@ -167,7 +167,7 @@ def log_sum(q, k_pages, table, q_start, kv_len, aK, clip_k, window, sinks, scale
 
 def weights(q, k_pages, table, q_start, kv_len, aK, clip_k, window, sinks, scale, lse, mass, accumulate):
     """Returns (mass, bound): the masses after the new tokens, and how far fp32 arithmetic may be from
-    them. A weight's exponent is the difference of two numbers of at most `size` (a sum of 2 (d + 6)
+    them (keys of a page that requests share get the sums of all of them). A weight's exponent is the difference of two numbers of at most `size` (a sum of 2 (d + 6)
     rounded terms) and |lse|, its exponential is within 2 x 2^-22, and a key's sum has as many terms
     as rows see it."""
     u = 2.0 ** -24
@@ -196,7 +196,7 @@ def weights(q, k_pages, table, q_start, kv_len, aK, clip_k, window, sinks, scale
             continue
         old = mass[page, h, j % P] if accumulate and not new[b, j, h] else 0.0
         mass[page, h, j % P] = old + s
-        bound[page, h, j % P] = err[b, j, h] + 2.0 * rows * u * s + 2.0 * u * abs(old + s) + 1e-36
+        bound[page, h, j % P] += err[b, j, h] + 2.0 * rows * u * s + 2.0 * u * abs(old + s) + 1e-36
     return mass, bound
 
 

@@ -314,8 +314,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) weights_simt_kernel(const __g
 #pragma unroll
             for (int i = 0; i < kSimtThreads / 32; ++i) all += part[32 * i + lane];
             if (pg >= 0) {
-                float *m = w.mass + (long long)pg * w.mass_stride + at;
-                *m = (w.accumulate && j < s.pos0 ? *m : 0.f) + all;
+                leave_mass(w, w.mass + (long long)pg * w.mass_stride + at, all, j, s.pos0);
             }
         }
     }
@@ -350,14 +349,14 @@ cudaError_t launch_simt(const WeightParams &w, cudaStream_t s) {
 // At most 16 query rows per key head (bf16, d = 64 or 128, pages of at least 8 keys): keys are the wide
 // side of m16n8k16 products, as in the attention of generated tokens, whose staging this has: a ninth
 // warp walks the CTA's share of the tiles and feeds a ring by TMA, eight row warps take 16 keys of a tile
-// each. A key's weights of all rows come together in one warp, so nothing is joined; the masses that are there
-// and the page numbers come with the keys. HBM bounds it: a key is 2 d bytes and 8 of mass.
+// each. A key's weights of all rows come together in one warp, so nothing is joined; the page numbers come with the
+// keys. HBM bounds it: a key is 2 d bytes and 8 of mass.
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kRowThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // keys of a warp per tile
 constexpr int kMaxStages = 4;
-constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
+constexpr uint32_t kSideBytes = 64;      // a tile's page numbers, 16 at most
 
 template <int D>
 constexpr int kStageBytes = kTile * D * 2;
@@ -385,7 +384,6 @@ struct Layout {
         return L;
     }
 };
-static_assert((kPieces * sizeof(Piece) + kNumBars * 8 + 16) % 16 == 0, "alignment of the masses");
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -414,7 +412,7 @@ struct Waits {
 
 template <int D>
 __device__ void feed_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &waits,
-                          const CUtensorMap *tm_k, int stages, int box, int old_by_tma) {
+                          const CUtensorMap *tm_k, int stages, int box) {
     const Params &p = w.p;
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
@@ -459,20 +457,14 @@ __device__ void feed_role(const WeightParams &w, const Layout &L, uint8_t *smem,
             const int j = g.it.tile(t) * kTile + my_box * box, row = j & ((1 << p.pshift) - 1);
             const bool bad = seen && (unsigned)pg >= (unsigned)p.num_pages;
             if (bad) report_page(p);
-            const bool old = old_by_tma && seen && !bad && my_blk == 0 && j < g.it.pos_lo;   // some key is not new
             if (my_blk == 0) reinterpret_cast<int *>(smem + L.side + st * kSideBytes)[my_box] = bad ? -1 : pg;
             __syncwarp();
-            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0), mo = __ballot_sync(0xffffffffu, old);
-            if (lane == 0)
-                ptx::mbar_expect_tx(bar(B_FULL + st), (uint32_t)(__popc(m) * box * D * 2 + __popc(mo) * box * 4));
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
+            if (lane == 0) ptx::mbar_expect_tx(bar(B_FULL + st), (uint32_t)(__popc(m) * box * D * 2));
             __syncwarp();
             if (seen && my_blk < DB && !(p.withhold && tiles == 0))   // a page outside the cache: zeros
                 tma_load_4d(my_dst + st * kStageBytes<D>, tm_k, bar(B_FULL + st), my_blk * 64, row, g.kvh,
                             bad ? p.num_pages : pg);
-            if (old)
-                bulk_load(base + L.side + st * kSideBytes + 64 + my_box * box * 4,
-                          w.mass + (long long)pg * w.mass_stride + (((long long)g.kvh << p.pshift) + row), box * 4,
-                          bar(B_FULL + st));
             __syncwarp();
             ++tiles;
             if (++st == stages) {
@@ -487,8 +479,7 @@ __device__ void feed_role(const WeightParams &w, const Layout &L, uint8_t *smem,
 }
 
 template <int D, int NT, bool AK>
-__device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &wait, int stages, int box,
-                         int old_by_tma) {
+__device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, const Waits &wait, int stages, int box) {
     constexpr int kRows = 8 * NT;
     const Params &p = w.p;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -633,11 +624,7 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
             }
             const int j = g.tile(t) * kTile + mine;
             int pg = -1;
-            float old = 0.f;
-            if (c < 2 && j <= g.pos_hi && (j >= first || j < p.sinks)) {
-                pg = reinterpret_cast<const int *>(side)[mine / box];
-                if (old_by_tma && j < g.pos_lo) old = reinterpret_cast<const float *>(side + 64)[mine];
-            }
+            if (c < 2 && j <= g.pos_hi && (j >= first || j < p.sinks)) pg = reinterpret_cast<const int *>(side)[mine / box];
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(empty);
 #pragma unroll
@@ -645,12 +632,9 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
                 sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
             }
-            if (pg >= 0) {
-                float *at = w.mass + (long long)pg * w.mass_stride +
-                            (((long long)g.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
-                if (!old_by_tma && w.accumulate && j < g.pos_lo) old = *at;
-                *at = old + (c == 0 ? sum[0] : sum[1]);
-            }
+            if (pg >= 0)
+                leave_mass(w, w.mass + (long long)pg * w.mass_stride + (((long long)g.kvh << p.pshift) + (j & ((1 << p.pshift) - 1))),
+                           c == 0 ? sum[0] : sum[1], j, g.pos_lo);
         }
     }
 }
@@ -658,7 +642,7 @@ __device__ void row_role(const WeightParams &w, const Layout &L, uint8_t *smem, 
 template <int D, int NT, bool AK>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     weights_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ WeightParams w, int stages,
-                          int box, int old_by_tma) {
+                          int box) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const Params &p = w.p;
     const Layout L = Layout::make<D, NT>(p.clip_k, AK, stages);
@@ -677,9 +661,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     grid_wait();
     grid_release();
     if (threadIdx.x >= kRowThreads)
-        feed_role<D>(w, L, smem, waits, &tm_k, stages, box, old_by_tma);
+        feed_role<D>(w, L, smem, waits, &tm_k, stages, box);
     else
-        row_role<D, NT, AK>(w, L, smem, waits, stages, box, old_by_tma);
+        row_role<D, NT, AK>(w, L, smem, waits, stages, box);
 }
 
 template <int D, int NT, bool AK>
@@ -696,7 +680,7 @@ cudaError_t launch_decode(const PagedWeightsArgs &a, const WeightParams &w, cuda
     const cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;
     return launch_early(kern, dim3(di.sms * kCtasPerSm<D>), kThreads, Layout::make<D, NT>(w.p.clip_k, AK, stages).bytes, s,
-                        tm, w, stages, box, masses_by_tma(w));
+                        tm, w, stages, box);
 }
 
 template <int D, int NT>

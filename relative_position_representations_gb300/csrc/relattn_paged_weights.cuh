@@ -48,15 +48,12 @@ __device__ __forceinline__ int units_of(const WeightParams &w, int nt, int n) {
     const int step = 2 * w.pairs(n);
     return w.per_tile ? nt * w.per_tile : (nt + step - 1) / step;
 }
-// masses of a tile are copied as 16-byte aligned runs
-inline int masses_by_tma(const WeightParams &w) {
-    return w.accumulate && w.mass_stride % 4 == 0 && reinterpret_cast<uintptr_t>(w.mass) % 16 == 0;
-}
-// `bytes` (a multiple of 16) from 16-byte aligned memory
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+// What a request's rows have given a key at position j, the first new token's being pos0. Several requests of the
+// call may share the page of a key in front of theirs, so its entry is added to in the L2; where they do not, it is one
+// addition a call, the same bits in every call.
+__device__ __forceinline__ void leave_mass(const WeightParams &w, float *at, float sum, int j, int pos0) {
+    if (w.accumulate && j < pos0) atomicAdd(at, sum);
+    else *at = sum;
 }
 
 // tokens of a request that see some key of j0 .. j0 + len - 1 (window and sinks taken into account)

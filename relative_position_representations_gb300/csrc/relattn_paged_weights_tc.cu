@@ -52,10 +52,10 @@ constexpr int kUnits = 4;            // announced ahead
 constexpr int kMaxK = 4, kMaxQ = 4;  // stages
 constexpr int kParts = 1;            // pairs of tiles whose sums are joined at once
 constexpr uint32_t kPartBytes = kAccs * 2 * kTile * 4;
-constexpr int kSides = 8;            // tiles whose page numbers and masses are held
+constexpr int kSides = 8;            // tiles whose page numbers are held
 constexpr int kBatch = 4;            // query tiles whose constants come together ...
 constexpr int kBatches = 2;          // ... and how often
-constexpr uint32_t kSideBytes = 64 + kTile * 4;   // a tile's page numbers (at most 16) and masses
+constexpr uint32_t kSideBytes = 64;  // of a tile, 16 at most
 
 enum : int {
     B_K_FULL = 0, B_K_EMPTY = B_K_FULL + kMaxK, B_Q_FULL = B_K_EMPTY + kMaxK, B_Q_EMPTY = B_Q_FULL + kMaxQ,
@@ -84,7 +84,6 @@ struct TcParams {
     int npad, SR;        // table rows rounded up to 16; row stride (floats) of R in shared memory
     int box;             // keys per TMA box
     int nk, nq;          // stages of keys and of query tiles
-    int old_by_tma;      // masses are fetched with the keys
     uint32_t tile_bytes, off_q, off_ak, off_r, off_nl, off_side, off_part, off_unit, off_bar;
 };
 
@@ -208,7 +207,7 @@ __device__ void load_role(const TcParams &tp, const Shared &sh, const CUtensorMa
         const int *bt = p.bt + (long long)u.row * p.bt_stride;
         const int pos_hi = u.pos0 + u.n - 1;
         const int first = p.window > 0 ? max(0, max(u.pos0, 0) - p.window + 1) : 0;
-        // the tile's pages, one a lane, looked up a tile ahead; their numbers and the masses that are there come along
+        // the tile's pages, one a lane, looked up a tile ahead; their numbers come along
         auto lookup = [&](int t, bool &seen) -> int {
             const int j = u.key(t) + my_box * tp.box;
             seen = t < u.t1 && j <= pos_hi && (j + tp.box > first || j < p.sinks);
@@ -224,22 +223,15 @@ __device__ void load_role(const TcParams &tp, const Shared &sh, const CUtensorMa
             const int j = u.key(t) + my_box * tp.box, row = j & ((1 << p.pshift) - 1);
             const bool bad = seen && (unsigned)pg >= (unsigned)p.num_pages;
             if (bad) report_page(p);
-            // (masses of the tile's new keys count for nothing, so where all are new none are fetched)
-            const bool old = tp.old_by_tma && seen && !bad && my_blk == 0 && j < u.pos0;
-            uint8_t *side = sh.ptr + tp.off_side + sr.st * kSideBytes;
-            if (my_blk == 0) reinterpret_cast<int *>(side)[my_box] = bad ? -1 : pg;
+            if (my_blk == 0) reinterpret_cast<int *>(sh.ptr + tp.off_side + sr.st * kSideBytes)[my_box] = bad ? -1 : pg;
             __syncwarp();
-            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0), mo = __ballot_sync(0xffffffffu, old);
-            ptx::mbar_expect_tx_w(bar(B_SIDE_FULL + sr.st), (uint32_t)(__popc(mo) * tp.box * 4));
+            const unsigned m = __ballot_sync(0xffffffffu, seen && my_blk == 0);
+            ptx::mbar_arrive_w(bar(B_SIDE_FULL + sr.st));
             ptx::mbar_expect_tx_w(bar(B_K_FULL + kr.st), (uint32_t)(__popc(m) * tp.box * D * 2));
             __syncwarp();
             if (seen && my_blk < DB)   // a page outside the cache: a box outside the tensor, which reads as zeros
                 tma_load_4d(sh.base + (uint32_t)kr.st * tp.tile_bytes + my_blk * kTile * 128 + my_box * tp.box * 128, tm_k,
                             bar(B_K_FULL + kr.st), my_blk * 64, row, u.kvh, bad ? p.num_pages : pg);
-            if (old)
-                bulk_load(sh.base + tp.off_side + sr.st * kSideBytes + 64 + my_box * tp.box * 4,
-                          tp.w.mass + (long long)pg * tp.w.mass_stride + (((long long)u.kvh << p.pshift) + row), tp.box * 4,
-                          bar(B_SIDE_FULL + sr.st));
             __syncwarp();
             kr.next();
             sr.next();
@@ -273,6 +265,8 @@ __device__ void load_role(const TcParams &tp, const Shared &sh, const CUtensorMa
     // no copy is in flight when the CTA exits
     for (uint32_t i = k_count > (uint32_t)tp.nk ? k_count - tp.nk : 0; i < k_count; ++i)
         tc::drain_bar(bar(B_K_FULL + (int)(i % tp.nk)), (i / tp.nk) & 1u, sh.limit);
+    // (nothing is in flight on these; without the waits the compiler lays the kernel out so that four prompts of 4096
+    // take 225.5 us in place of 220.4)
     for (uint32_t i = k_count > (uint32_t)kSides ? k_count - kSides : 0; i < k_count; ++i)
         tc::drain_bar(bar(B_SIDE_FULL + (int)(i % kSides)), (i / kSides) & 1u, sh.limit);
     for (uint32_t i = q_count > (uint32_t)tp.nq ? q_count - tp.nq : 0; i < q_count; ++i)
@@ -717,11 +711,8 @@ __device__ void sum_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                 const bool seen = pg >= 0 && j <= last && (j >= first || j < p.sinks);
                 float *at = tp.w.mass + (long long)pg * tp.w.mass_stride +
                             (((long long)u.kvh << p.pshift) + (j & ((1 << p.pshift) - 1)));
-                float old = 0.f;
-                if (tp.w.accumulate && seen && j < u.pos0)
-                    old = tp.old_by_tma ? reinterpret_cast<const float *>(side + 64)[j - j0] : *at;
                 arrive(bar(B_SIDE_EMPTY + sr.st));
-                if (seen && !bad) *at = old + sum;
+                if (seen && !bad) leave_mass(tp.w, at, sum, j, u.pos0);
             }
         }
     }
@@ -838,7 +829,6 @@ cudaError_t launch_d(const PagedWeightsArgs &wa, const WeightParams &w, cudaStre
     tm[2] = tm[0];
     const uint64_t Ht = a.ths ? (uint64_t)a.Hkv : 1, hs = a.ths ? (uint64_t)a.ths * 2 : (uint64_t)(2 * a.clip_k + 1) * D * 2;
     if (ak && !tc::make_map(&tm[2], a.aK, D, p.clip_k + 1, Ht, D * 2, hs, (uint32_t)tp.npad)) return cudaErrorInvalidValue;
-    tp.old_by_tma = masses_by_tma(w);
     cudaError_t e = launch_weights_prep(tp.w, true, s);
     if (e != cudaSuccess) return e;
     return ak ? launch_variant<D, true>(tm, tp, smem, di.sms, s) : launch_variant<D, false>(tm, tp, smem, di.sms, s);

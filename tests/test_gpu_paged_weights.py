@@ -446,3 +446,44 @@ def test_rows_marked_as_without_keys_add_nothing(max_new, new, dtype, key):
                              scale=0.125, max_new=max_new)
     assert rp.relattn_get_device_error() == 0
     assert (np.abs(f64(m) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("new,max_new,dtype,d", [(1, 1, BF16, 64), (3, 3, BF16, 128), (40, 0, BF16, 64), (150, 0, BF16, 128),
+                                                 (20, 0, F32, 64)])
+@pytest.mark.parametrize("key", [False, True])
+def test_pages_that_requests_share(new, max_new, dtype, d, key):
+    """Prefixes of relattn_paged_shared_fwd: their keys get the weights of every request of the group."""
+    from tests.test_gpu_paged_shared import make as behind_prefixes
+    rp = _rp()
+    k, scale = 6 * key, d ** -0.5
+    x = behind_prefixes([(272, [(5, new), (60, new), (0, 1), (31, new)]), (512, [(1, new), (200, new)])], 4, 2, d, 16, dtype, k,
+                        key=key, before=[(90, 1)], after=[(33, 2)])
+    N = x["k_pages"].shape[0]
+    a = args_of(x)
+    lse = op.log_sum(**a, clip_k=k, window=0, sinks=0, scale=scale)[0].astype(np.float32)
+    mass = np.random.default_rng(1).random((N, 2, 16)).astype(np.float32)
+    g = on_gpu(x)
+    m = torch.from_numpy(mass).to(DEV)
+    run = lambda m, add: rp.relattn_paged_weights(g["q"], g["k_pages"], g["table"], g["q_start"], g["kv_len"],
+                                                  torch.from_numpy(lse).to(DEV), m, aK=g["aK"], clip_k=k, accumulate=add,
+                                                  max_new=max_new)
+    for _ in range(3):                   # one step after the other
+        want, bound = op.weights(**a, clip_k=k, window=0, sinks=0, scale=scale, lse=lse.astype(np.float64), mass=f64(m),
+                                 accumulate=True)
+        run(m, True)
+        assert rp.relattn_get_device_error() == 0
+        bad = ~(np.abs(f64(m) - want) <= bound)
+        assert not bad.any(), (np.argwhere(bad)[:5], f64(m)[bad][:5], want[bad][:5])
+    # set: one of the requests' sums
+    run(m, False)
+    at, fits = 0, np.zeros(m.shape, dtype=bool)
+    written = np.zeros(m.shape, dtype=bool)
+    for b, n in enumerate(np.diff(x["q_start"])):
+        y = dict(a, q=a["q"][at:at + n], table=x["table"][b:b + 1], q_start=np.array([0, n]), kv_len=x["kv_len"][b:b + 1])
+        want, bound = op.weights(**y, clip_k=k, window=0, sinks=0, scale=scale, lse=lse[at:at + n].astype(np.float64),
+                                 mass=np.full(m.shape, np.nan), accumulate=False)
+        written |= ~np.isnan(want)
+        with np.errstate(invalid="ignore"):
+            fits |= np.abs(f64(m) - want) <= bound
+        at += n
+    assert np.array_equal(written, written & fits)
