@@ -86,19 +86,23 @@ void fill_params(const PagedArgs &a, Params *p) {
     p->d = a.d;
     p->out = a.out;
     p->lse = a.lse;
-    p->step = a.flat ? 0 : 1;
-    p->f32_out = a.f32_out;
-    p->first_key = a.first_key;
-    p->row_of = a.row_of;
-    p->ctas = a.ctas;
-    p->overlap = a.overlap;
-    p->owner = a.owner;
-    p->left = a.left;
     p->desc = static_cast<Desc *>(a.workspace);
     p->part = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + desc_bytes());
     p->err = a.err;
     p->withhold = a.withhold;
     p->wait_limit = a.wait_limit > 0 ? a.wait_limit : 2000000000ll;
+}
+
+void fill_params(const PagedArgs &a, PartParams *p) {
+    fill_params(a, static_cast<Params *>(p));
+    p->step = a.flat ? 0 : 1;
+    p->f32_out = a.f32_out;
+    p->overlap = a.overlap;
+    p->first_key = a.first_key;
+    p->row_of = a.row_of;
+    p->ctas = a.ctas;
+    p->owner = a.owner;
+    p->left = a.left;
 }
 
 // ------------------------------------------------------------------ merge
@@ -224,11 +228,13 @@ cudaError_t launch_merge_t(const Params &p, int grid, cudaStream_t s) {
 }
 
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s) {
-    if (p.owner) {   // the caller joins the pieces
-        *p.left = PagedLeft{p.rec_rows, grid, p.ctas};
-        return cudaSuccess;
-    }
-    return bf16 && !p.f32_out ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
+    return bf16 ? launch_merge_t<__nv_bfloat16>(p, grid, s) : launch_merge_t<float>(p, grid, s);
+}
+
+cudaError_t launch_merge(const PartParams &p, int grid, bool bf16, cudaStream_t s) {
+    if (!p.owner) return launch_merge(static_cast<const Params &>(p), grid, bf16, s);
+    *p.left = PagedLeft{p.rec_rows, grid, p.ctas};
+    return cudaSuccess;
 }
 
 // ------------------------------------------------------------------ SIMT kernel
@@ -282,9 +288,10 @@ struct SimtLayout {
     }
 };
 
-// N4: 16-byte chunks of a row that a thread's share of 32 rows needs, ceil(d / 4 / 8)
+// N4: 16-byte chunks of a row that a thread's share of 32 rows needs, ceil(d / 4 / 8). One kernel for plain calls and parts:
+// the same time (chunk_f32 of the measured cases 47.3 us with and without what parts have).
 template <typename T, int N4>
-__global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __grid_constant__ Params p, int vec) {
+__global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __grid_constant__ PartParams p, int vec) {
     extern __shared__ __align__(16) float smf[];
     __shared__ Range rg_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const __gri
 
 template <typename T, int N4>
 cudaError_t launch_simt_t(const PagedArgs &a, cudaStream_t s) {
-    Params p;
+    PartParams p;
     fill_params(a, &p);
     p.T = p.g >= kSimtRows ? 1 : kSimtRows / p.g;
     p.T1 = p.T;

@@ -44,6 +44,9 @@ struct Desc {
 };
 static_assert(sizeof(Desc) == 64, "descriptor");
 
+// Params are those of a plain call, PartParams those of a part of a call whose requests share prefixes
+// (relattn_paged_shared.cu). The kernels are compiled for either: what only parts have costs plain calls registers and
+// cold code otherwise (four prompts of 4096, key term 284 -> 295 us, 128 windows of 1024 33.1 -> 34.8).
 struct Params {
     const void *q, *k, *v, *aK, *aV;
     long long q_stride, page_stride, bt_stride, ths;
@@ -60,21 +63,26 @@ struct Params {
     int rec_rows;                            // rows of a record
     void *out;
     float *lse;                              // [tokens][H] or null
-    // a call whose requests share prefixes (relattn_paged_shared.cu) runs in two parts
-    int step;                                // 1; 0: all tokens of a request stand at its last position
-    int f32_out;                             // out is fp32 whatever the inputs are
-    const int *first_key;                    // [tokens] or null: first key of the token's request (whole tiles)
-    const int *row_of;                       // [B] or null: the request's row of the block table
-    const int *ctas;                         // CTAs that share the work (the others have none); null: all
-    int overlap;                             // runs beside the kernel in front of it, and ends after it
     Desc *desc;                              // [gridDim.x]
     float *part;                             // [gridDim.x][2] records {m[rows], l[rows], O[rows][d]}
-    int *owner;                              // [tokens][Hkv] or null: the CTA that begins a token's item, where
-                                             // the item goes on behind its range; else -1 (out has its rows)
-    PagedLeft *left;                         // host
     int *err;
     long long wait_limit;
     int withhold;                            // test hook: a CTA's first queries are announced, not loaded
+    // what PartParams has, for code that knows either
+    static constexpr int step = 1, f32_out = 0, overlap = 0;
+    static constexpr const int *first_key = nullptr, *row_of = nullptr, *ctas = nullptr;
+    static constexpr int *owner = nullptr;
+};
+struct PartParams : Params {
+    int step;                                // 1; 0: all tokens of a request stand at its last position
+    int f32_out;                             // out is fp32 whatever the inputs are
+    int overlap;                             // runs beside the kernel in front of it, and ends after it
+    const int *first_key;                    // [tokens] or null: first key of the token's request (whole tiles)
+    const int *row_of;                       // [B] or null: the request's row of the block table
+    const int *ctas;                         // CTAs that share the work (the others have none); null: all
+    int *owner;                              // [tokens][Hkv] or null: the CTA that begins a token's item, where
+                                             // the item goes on behind its range; else -1 (out has its rows)
+    PagedLeft *left;                         // host
 };
 
 inline size_t desc_bytes() { return (size_t)kMaxGrid * sizeof(Desc); }
@@ -86,7 +94,8 @@ struct Seq {
     int lo;         // first tile of its keys
 };
 
-__device__ __forceinline__ Seq load_seq(const Params &p, int b) {
+template <typename PP>
+__device__ __forceinline__ Seq load_seq(const PP &p, int b) {
     Seq s;
     s.q0 = min(max(p.q_start[b], 0), p.tokens);
     const int q1 = min(max(p.q_start[b + 1], s.q0), p.tokens);
@@ -120,7 +129,8 @@ struct Item {
     }
 };
 
-__device__ __forceinline__ Item make_item(const Params &p, const Seq &s, int qt) {
+template <typename PP>
+__device__ __forceinline__ Item make_item(const PP &p, const Seq &s, int qt) {
     Item it;
     it.i0 = qt * p.T;
     it.cnt = min(p.T, s.n - it.i0);
@@ -148,7 +158,8 @@ __device__ __forceinline__ long long range_begin(long long total, int c, int G) 
     return total / G * c + total % G * c / G;
 }
 // CTAs of the launch that take part
-__device__ __forceinline__ int grid_of(const Params &p, int launched) {
+template <typename PP>
+__device__ __forceinline__ int grid_of(const PP &p, int launched) {
     return p.ctas ? min(max(*p.ctas, 1), launched) : launched;
 }
 
@@ -165,8 +176,8 @@ struct Range {
 // together. I: a type that holds the whole line (32 bits where the host has seen that they do: this
 // code runs once, cold, in front of everything else, so every instruction of it counts). Every CTA
 // looks at all requests, twice where a batch does not hold them: 13 to 17 us for each 1000 of them.
-template <typename I, int kBatch = 4>
-__device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
+template <typename I, int kBatch = 4, typename PP>
+__device__ __forceinline__ Range find_range_t(const PP &p, int c, int G) {
     constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     auto scan = [&](I v) {
@@ -273,7 +284,8 @@ __device__ __forceinline__ Range find_range_t(const Params &p, int c, int G) {
     return r;
 }
 
-__device__ __forceinline__ Range find_range(const Params &p) {
+template <typename PP>
+__device__ __forceinline__ Range find_range(const PP &p) {
     const int c = (int)blockIdx.x, G = grid_of(p, (int)gridDim.x);
     return p.long_line ? find_range_t<long long>(p, c, G) : find_range_t<int>(p, c, G);
 }
@@ -293,7 +305,8 @@ struct Segment {
 // at a time: a batch of fixed slots may have thousands of idle ones in a row, whose loads one after
 // the other would be the step's time (three busy slots of 4096 with 20000 keys each, d = 64: 312 us in
 // place of 66; of 16384: 1416 and 230, of which 214 are the scan in front).
-__device__ __forceinline__ int next_busy(const Params &p, int b) {
+template <typename PP>
+__device__ __forceinline__ int next_busy(const PP &p, int b) {
     const int lane = threadIdx.x & 31;
     for (; b < p.B; b += 128) {
         int n[4];
@@ -316,7 +329,8 @@ struct Walk {
     int b, kvh, qt, nq;
     long long x, x0, x1;
     Seq s;
-    __device__ __forceinline__ Walk(const Params &p, const Range &r)
+    template <typename PP>
+    __device__ __forceinline__ Walk(const PP &p, const Range &r)
         : b(r.b), kvh(r.kvh), qt(r.qt), nq(0), x(r.x), x0(r.x0), x1(r.x1), s{0, 0, 0, 0} {
         if (b < p.B) {
             s = load_seq(p, b);
@@ -325,7 +339,8 @@ struct Walk {
     }
     // the next piece of work of the range; an item without any key comes as one piece with no
     // tiles, in the range where it starts
-    __device__ __forceinline__ bool next(const Params &p, Segment &g) {
+    template <typename PP>
+    __device__ __forceinline__ bool next(const PP &p, Segment &g) {
         while (x < x1 && b < p.B) {
             if (qt >= nq) {
                 qt = 0;
@@ -377,23 +392,27 @@ struct Piece {
 static_assert(sizeof(Piece) == 48, "piece");
 constexpr int kPieces = 4;   // announced ahead
 
-__device__ __forceinline__ int table_row(const Params &p, int b) { return p.row_of && b < p.B ? p.row_of[b] : b; }
+template <typename PP>
+__device__ __forceinline__ int table_row(const PP &p, int b) { return p.row_of && b < p.B ? p.row_of[b] : b; }
 
-__device__ __forceinline__ Piece make_piece(const Params &p, const Segment &g, bool more) {
+template <typename PP>
+__device__ __forceinline__ Piece make_piece(const PP &p, const Segment &g, bool more) {
     return Piece{g.s.q0 + g.it.i0, more ? g.it.cnt : 0, g.it.pos_lo, g.it.pos_hi, g.it.ns, g.it.lo,
                  g.it.nt, g.t0, g.t1, g.kvh, table_row(p, g.b), 0};
 }
 
 // Says where the rows of the segment's item are, if it is the item's first (a warp calls it).
-__device__ __forceinline__ void write_owner(const Params &p, const Segment &g) {
-    if (!p.owner || g.t0 > 0) return;
-    for (int i = threadIdx.x & 31; i < g.it.cnt; i += 32)
-        p.owner[(long long)(g.s.q0 + g.it.i0 + i) * p.Hkv + g.kvh] = g.whole() ? -1 : (int)blockIdx.x;
+template <typename PP>
+__device__ __forceinline__ void write_owner(const PP &p, const Segment &g) {
+    if (p.owner && g.t0 == 0)
+        for (int i = threadIdx.x & 31; i < g.it.cnt; i += 32)
+            p.owner[(long long)(g.s.q0 + g.it.i0 + i) * p.Hkv + g.kvh] = g.whole() ? -1 : (int)blockIdx.x;
 }
 
 // Leaves the descriptor of the item that goes on behind the range (one thread per CTA calls it,
 // once, with the last segment of the range).
-__device__ __forceinline__ void write_desc(const Params &p, const Segment *g, long long total) {
+template <typename PP>
+__device__ __forceinline__ void write_desc(const PP &p, const Segment *g, long long total) {
     Desc d;
     d.valid = 0;
     d.row0 = d.cnt = d.kvh = d.nt = d.c0 = d.wt = d.n = 0;
@@ -420,7 +439,8 @@ __device__ __forceinline__ void write_desc(const Params &p, const Segment *g, lo
 }
 
 // a CTA of the launch without a part in the work
-__device__ __forceinline__ bool idle_cta(const Params &p) {
+template <typename PP>
+__device__ __forceinline__ bool idle_cta(const PP &p) {
     if (!p.ctas || (int)blockIdx.x < grid_of(p, (int)gridDim.x)) return false;
     if (threadIdx.x == 0) p.desc[blockIdx.x].valid = 0;
     return true;
@@ -487,7 +507,8 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // A kernel's start. With p.overlap it begins when the one in front of it has passed grid_wait() itself, so that what
 // stands in front of that one is over, and waits for it at its own end. What those earlier kernels have written
 // is seen through the release and the acquire of p.ctas, which the last of them writes at its end.
-__device__ __forceinline__ void grid_start(const Params &p) {
+template <typename PP>
+__device__ __forceinline__ void grid_start(const PP &p) {
     if (!p.overlap) {
         grid_wait();
         return;
@@ -502,8 +523,11 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 
 // Fills the parts of Params that do not depend on the kernel.
 void fill_params(const PagedArgs &a, Params *p);
+void fill_params(const PagedArgs &a, PartParams *p);
 // joins the pieces of split items; launched behind the attention kernel as its dependent
 cudaError_t launch_merge(const Params &p, int grid, bool bf16, cudaStream_t s);
+// leaves a part's pieces to the caller, and says where they are
+cudaError_t launch_merge(const PartParams &p, int grid, bool bf16, cudaStream_t s);
 
 }  // namespace paged
 

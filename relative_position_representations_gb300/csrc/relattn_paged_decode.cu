@@ -132,8 +132,8 @@ struct Waits {
 };
 
 // ======================================================================= the walking warp
-template <int D, int NT>
-__device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const Waits &waits, const CUtensorMap *tm_q,
+template <int D, int NT, typename PP>
+__device__ void feed_role(const PP &p, const Layout &L, uint8_t *smem, const Waits &waits, const CUtensorMap *tm_q,
                           const CUtensorMap *tm_k, const CUtensorMap *tm_v, int stages, int box) {
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
@@ -217,8 +217,8 @@ __device__ void feed_role(const Params &p, const Layout &L, uint8_t *smem, const
 }
 
 // ======================================================================= the row warps
-template <int D, int NT, bool AK, bool AV>
-__device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const Waits &wait, int stages) {
+template <int D, int NT, bool AK, bool AV, typename PP>
+__device__ void row_role(const PP &p, const Layout &L, uint8_t *smem, const Waits &wait, int stages) {
     constexpr int kRows = 8 * NT;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -578,10 +578,10 @@ __device__ void row_role(const Params &p, const Layout &L, uint8_t *smem, const 
     }
 }
 
-template <int D, int NT, bool AK, bool AV>
+template <int D, int NT, bool AK, bool AV, typename PP>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p, int stages, int box) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PP p, int stages, int box) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const Layout L = Layout::make<D, NT>(p.clip_k, AK || AV, stages);
     const uint32_t bars = ptx::smem_u32(smem) + L.bar;
@@ -609,9 +609,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D>)
     if (p.overlap) grid_wait();
 }
 
-template <int D, int NT, bool AK, bool AV>
-cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box, cudaStream_t s) {
-    auto kern = paged_decode_kernel<D, NT, AK, AV>;
+template <int D, int NT, bool AK, bool AV, typename PP>
+cudaError_t launch_variant(const CUtensorMap (&tm)[3], const PP &p, int box, cudaStream_t s) {
+    auto kern = paged_decode_kernel<D, NT, AK, AV, PP>;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
     // as many stages as the CTA's share of the SM's shared memory holds (1 KB per CTA is the
@@ -631,9 +631,9 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[3], const Params &p, int box,
     return launch_merge(p, grid, true, s);
 }
 
-template <int D, int NT>
+template <int D, int NT, typename PP>
 cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
-    Params p;
+    PP p;
     fill_params(a, &p);
     p.T = 8 * NT / p.g;
     p.T1 = p.T;
@@ -653,6 +653,13 @@ cudaError_t launch_rows(const PagedArgs &a, cudaStream_t s) {
     return launch_variant<D, NT, false, false>(tm, p, box, s);
 }
 
+template <typename PP>
+cudaError_t launch_for(const PagedArgs &a, cudaStream_t s) {
+    const bool eight = (long long)a.max_new * (a.H / a.Hkv) <= 8;
+    if (a.d == 64) return eight ? launch_rows<64, 1, PP>(a, s) : launch_rows<64, 2, PP>(a, s);
+    return eight ? launch_rows<128, 1, PP>(a, s) : launch_rows<128, 2, PP>(a, s);
+}
+
 constexpr int kMostRows = 16;
 
 }  // namespace
@@ -664,9 +671,7 @@ bool paged_decode_covers(const PagedArgs &a) {
 }
 
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t s) {
-    const bool eight = (long long)a.max_new * (a.H / a.Hkv) <= 8;
-    if (a.d == 64) return eight ? paged::launch_rows<64, 1>(a, s) : paged::launch_rows<64, 2>(a, s);
-    return eight ? paged::launch_rows<128, 1>(a, s) : paged::launch_rows<128, 2>(a, s);
+    return a.owner ? paged::launch_for<paged::PartParams>(a, s) : paged::launch_for<paged::Params>(a, s);
 }
 
 }  // namespace relattn

@@ -85,8 +85,9 @@ enum : int {
 };
 constexpr int kNumBars = B_KV0 + 2 * kMaxStages;
 
+template <typename PP>
 struct TcParams {
-    Params p;
+    PP p;
     int TS;              // tokens per slot
     int W, npad;         // table rows (clip_k + 1), rounded up to 16
     int SR;              // row stride (floats) of the R rows in shared memory
@@ -101,7 +102,8 @@ struct Pieces {
     uint32_t bars;
     const Piece *ring;
     uint32_t it;
-    __device__ __forceinline__ Pieces(const TcParams &tp, const Shared &sh)
+    template <typename PP>
+    __device__ __forceinline__ Pieces(const TcParams<PP> &tp, const Shared &sh)
         : bars(sh.base + tp.off_bar), ring(reinterpret_cast<const Piece *>(sh.ptr + tp.off_piece)), it(0) {}
     // false: the wait ran out, or there is no more
     template <typename Wait>
@@ -151,8 +153,9 @@ struct SlotWork {
     }
 };
 
-__device__ __forceinline__ SlotWork slot_work(const TcParams &tp, const Piece &g, int slot) {
-    const Params &p = tp.p;
+template <typename PP>
+__device__ __forceinline__ SlotWork slot_work(const TcParams<PP> &tp, const Piece &g, int slot) {
+    const PP &p = tp.p;
     SlotWork w;
     w.split = g.cnt <= tp.TS;
     w.tok0 = w.split ? 0 : slot * tp.TS;
@@ -187,10 +190,10 @@ __device__ __forceinline__ int v_lag(bool split) {
 }
 
 // ======================================================================= producers
-template <int D, bool AK, bool AV>
-__device__ void kv_role(const TcParams &tp, const Shared &sh, const CUtensorMap *tm_k,
+template <int D, bool AK, bool AV, typename PP>
+__device__ void kv_role(const TcParams<PP> &tp, const Shared &sh, const CUtensorMap *tm_k,
                         const CUtensorMap *tm_v, const CUtensorMap *tm_ak, const CUtensorMap *tm_av) {
-    const Params &p = tp.p;
+    const PP &p = tp.p;
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
     const uint32_t bars = sh.base + tp.off_bar, sKV = sh.base + tp.off_kv;
@@ -279,9 +282,9 @@ __device__ void kv_role(const TcParams &tp, const Shared &sh, const CUtensorMap 
 }
 
 // Walks the CTA's range, announces its pieces and loads their query tiles.
-template <int D>
-__device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, const CUtensorMap *tm_q) {
-    const Params &p = tp.p;
+template <int D, typename PP>
+__device__ void walk_role(const TcParams<PP> &tp, const Range rg, const Shared &sh, const CUtensorMap *tm_q) {
+    const PP &p = tp.p;
     constexpr int DB = D / 64;
     const int lane = threadIdx.x & 31;
     const uint32_t bars = sh.base + tp.off_bar;
@@ -333,10 +336,10 @@ __device__ void walk_role(const TcParams &tp, const Range rg, const Shared &sh, 
 // ======================================================================= MMA issuers
 // One warp per slot; both walk every ring entry and each releases it, so the release barriers
 // count two arrivals; an entry, or Q, is released only after it was waited for.
-template <int D, bool AK, bool AV>
-__device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
+template <int D, bool AK, bool AV, typename PP>
+__device__ void mma_role(const TcParams<PP> &tp, const Shared &sh, uint32_t tmem, int slot_in) {
     using T = Tm<D>;
-    const Params &p = tp.p;
+    const PP &p = tp.p;
     const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
     const int lane = threadIdx.x & 31;
     const uint32_t bars = sh.base + tp.off_bar;
@@ -514,10 +517,10 @@ __device__ void mma_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
 // the bits below n of 32
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-template <int D, bool AK, bool AV>
-__device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, int slot_in) {
+template <int D, bool AK, bool AV, typename PP>
+__device__ void row_role(const TcParams<PP> &tp, const Shared &sh, uint32_t tmem, int slot_in) {
     using T = Tm<D>;
-    const Params &p = tp.p;
+    const PP &p = tp.p;
     const int slot = __shfl_sync(0xffffffffu, slot_in, 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
@@ -924,7 +927,7 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
                         put64(v, 2 * c0);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(r[e] * inv);
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(p.f32_out ? r[e] * inv : r[e]);
                         put64(v, 4 * c0);
                         put64(v + 16, 4 * c0 + 64);
                     }
@@ -945,13 +948,13 @@ __device__ void row_role(const TcParams &tp, const Shared &sh, uint32_t tmem, in
 }
 
 // ======================================================================= kernel
-template <int D, bool AK, bool AV>
+template <int D, bool AK, bool AV, typename PP>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ak,
-                    const __grid_constant__ CUtensorMap tm_av, const __grid_constant__ TcParams tp) {
+                    const __grid_constant__ CUtensorMap tm_av, const __grid_constant__ TcParams<PP> tp) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const Params &p = tp.p;
+    const PP &p = tp.p;
     Shared sh;
     sh.base = ptx::smem_u32(smem_raw);
     sh.ptr = smem_raw;
@@ -1031,8 +1034,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ======================================================================= host
 // Shared memory for items of two tiles (wide) or one; false when fewer than `min_stages` stages
 // of the ring fit.
-template <int D>
-bool layout(TcParams *tp, bool wide, int smem_optin, int min_stages) {
+template <int D, typename PP>
+bool layout(TcParams<PP> *tp, bool wide, int smem_optin, int min_stages) {
     uint32_t off = 0;
     for (int s = 0; s < 2; ++s) {
         tp->off_q[s] = off;
@@ -1066,9 +1069,9 @@ bool layout(TcParams *tp, bool wide, int smem_optin, int min_stages) {
     return true;
 }
 
-template <int D, bool AK, bool AV>
-cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaStream_t s) {
-    auto kern = paged_tc_kernel<D, AK, AV>;
+template <int D, bool AK, bool AV, typename PP>
+cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams<PP> &tp, cudaStream_t s) {
+    auto kern = paged_tc_kernel<D, AK, AV, PP>;
     const DeviceInfo di = device_info();
     cudaError_t e = opt_in_smem(reinterpret_cast<const void *>(kern), di);
     if (e != cudaSuccess) return e;
@@ -1094,13 +1097,13 @@ cudaError_t launch_variant(const CUtensorMap (&tm)[5], const TcParams &tp, cudaS
     return launch_merge(tp.p, grid, true, s);
 }
 
-template <int D>
+template <int D, typename PP>
 cudaError_t launch_d(const PagedArgs &a, cudaStream_t s) {
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return cudaErrorInvalidDevice;
-    TcParams tp;
+    TcParams<PP> tp;
     std::memset(&tp, 0, sizeof(tp));
-    Params &p = tp.p;
+    PP &p = tp.p;
     fill_params(a, &p);
     tp.TS = BM / p.g;
     tp.W = a.clip_k + 1;
@@ -1145,7 +1148,8 @@ bool paged_tc_covers(const PagedArgs &a) {
 }
 
 cudaError_t launch_paged_tc(const PagedArgs &a, cudaStream_t s) {
-    return a.d == 64 ? paged::launch_d<64>(a, s) : paged::launch_d<128>(a, s);
+    if (a.owner) return a.d == 64 ? paged::launch_d<64, paged::PartParams>(a, s) : paged::launch_d<128, paged::PartParams>(a, s);
+    return a.d == 64 ? paged::launch_d<64, paged::Params>(a, s) : paged::launch_d<128, paged::Params>(a, s);
 }
 
 }  // namespace relattn
