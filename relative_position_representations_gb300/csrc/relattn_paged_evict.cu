@@ -411,25 +411,29 @@ __device__ void evict_lengths(const EvictParams &p) {
         }
         return v;
     };
-    // f(number, place on the list) of every entry: a warp takes a request's, or the block where they are many
-    auto entries = [&](auto f) {
+    // f(number, place on the list) of every entry: a warp takes a request's, or the block where they are many (again: their
+    // numbers and places are in shared memory from the last time, where all requests fit)
+    auto entries = [&](bool again, auto f) {
         int at = 0;
         for (int i0 = 0; i0 < requests; i0 += kMoveThreads) {
-            const int i = i0 + tid, n = i < requests ? pages(i) : 0;
-            int sum;
-            const int mine = at + block_scan(n, sum) - n;
-            at += sum;
-            __syncthreads();
-            count_s[tid] = n;
-            to_s[tid] = mine;
-            __syncthreads();
-            for (int q = warp; q < kMoveThreads; q += kMoveThreads / 32) {
+            if (!again || requests > kMoveThreads) {
+                const int i = i0 + tid, n = i < requests ? pages(i) : 0;
+                int sum;
+                const int mine = at + block_scan(n, sum) - n;
+                at += sum;
+                __syncthreads();
+                count_s[tid] = n;
+                to_s[tid] = mine;
+                __syncthreads();
+            }
+            const int here = min(kMoveThreads, requests - i0);
+            for (int q = warp; q < here; q += kMoveThreads / 32) {
                 const int nn = count_s[q];
-                if (nn == 0 || nn > kManyPages) continue;
+                if (nn > kManyPages) continue;
                 const int *row = row_of(i0 + q);
                 for (int e = lane; e < nn; e += 32) f(row[e], to_s[q] + e);
             }
-            for (int q = 0; q < min(kMoveThreads, requests - i0); ++q) {
+            for (int q = 0; q < here; ++q) {
                 const int nn = count_s[q];
                 if (nn <= kManyPages) continue;
                 const int *row = row_of(i0 + q);
@@ -440,10 +444,10 @@ __device__ void evict_lengths(const EvictParams &p) {
         }
         return at;
     };
-    int good = 0, all;
-    const int total = entries([&](int page, int) { good += exists(page); });
-    block_scan(good, all);
     const int head = *a.free_head;
+    int good = 0, all;
+    const int total = entries(false, [&](int page, int) { good += exists(page); });
+    block_scan(good, all);
     __syncthreads();
     if (all < total && tid == 0) atomicCAS(a.err, 0, paged::kInvalidArg);
     if (head > a.num_free || head < all) {   // not the list that the pages came from
@@ -456,7 +460,7 @@ __device__ void evict_lengths(const EvictParams &p) {
     if (tid == 0) *a.free_head_out = head - all;
     int *dst = a.free_pages + head - all;
     if (all == total) {
-        entries([&](int page, int to) { dst[to] = page; });
+        entries(true, [&](int page, int to) { dst[to] = page; });
         return;
     }
     int at = 0;                                // some are left out: the places are counted
