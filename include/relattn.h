@@ -453,10 +453,12 @@ RELATTN_API relattn_status_t relattn_paged_fwd_lse(const void *q, long long q_st
  *   All other arguments, limits and refusals as in relattn_paged_fwd.
  *
  * Which of a group's rows a shared key is read through is not defined, nor how much of the prefix is shared: up
- * to a multiple of 128, and up to clip_k - 1 keys less where new tokens follow closely. With window > 0, and
- * where the requests bring 128 query rows per key/value head each (tokens * (H / Hkv) >= 128 * B), the call
+ * to a multiple of 128, and up to clip_k - 1 keys less where new tokens follow closely (the request whose new tokens
+ * stand first decides for its group, so one that has just begun inside the prefix is better left out). With window > 0,
+ * and where the call's B requests, idle ones counted, bring 128 query rows per key/value head on average (tokens *
+ * (H / Hkv) >= 128 * B; a long chunk among generated tokens can do that for all), the call
  * does what relattn_paged_fwd does. It pays where many rows share long prefixes (64 generated tokens behind
- * 8192 keys, 16 / 4 heads of 128: 48 us in place of 166; behind 1024 keys 37 and 42); a handful of requests, or a few
+ * 8192 keys, 16 / 4 heads of 128: 48 us in place of 167; behind 1024 keys 38 and 41); a handful of requests, or a few
  * hundred shared keys, are served faster by relattn_paged_fwd. group_start and prefix_len are device memory like the
  * lengths, so a captured step can be replayed; other numbers than allowed stay within the arrays, but then any
  * row may hold anything. groups <= 2^24, else RELATTN_ERR_UNSUPPORTED.
@@ -506,7 +508,8 @@ RELATTN_API relattn_status_t relattn_paged_shared_workspace_size(int tokens, int
  * 64 or 128, pages of at least 8 keys and rows that start on 16-byte boundaries runs on the tensor
  * cores (with at most 16 query rows, max_new times H / Hkv, per key/value head on a kernel for
  * generated tokens, else up to clip_k = 127), everything else on the SIMT units. Limits and refusals as in
- * relattn_paged_fwd; tokens = 0 does nothing.
+ * relattn_paged_fwd; tokens = 0 does nothing. A request that relattn_paged_plan has left out takes part with its rows,
+ * as in relattn_paged_fwd, for its last cached tokens: the masses of its keys mean nothing afterwards.
  */
 RELATTN_API relattn_status_t relattn_paged_weights(const void *q, long long q_stride, const void *k_pages,
                                        long long page_stride, int num_pages, int page_size,

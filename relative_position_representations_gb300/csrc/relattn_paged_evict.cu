@@ -16,12 +16,13 @@
 // in place are neither read nor written. HBM bounds it: every moved row is read once, written once.
 // A block is as many places (128 at most) as a CTA's registers hold at once.
 //
-// 64 requests of 2000 - 2304 keys cut to 2048, 4 heads of 128: 77 - 101 us by how many keys move (448 MB: 4.4 - 5.8 TB/s),
-// 21 of them the selection. 131071 keys cut to 32768, 4 heads: 86 - 117 us; 30 are the selection (four units, so 32 CTAs:
-// three passes of 5 us and the runs' list), the moving takes four rounds of 9 us, each a chain of the list's lookups, the
-// rows' latency and the flags. Tried and dropped: the next block's lookups while this one's rows arrive (101 -> 118
-// us), blocks of 64 places with three or four CTAs an SM (106, 112), clusters of 16 for few units (evict of one long
-// request 75 -> 84 us).
+// Measured in a graph, each pass on a cache that no other has cut (what a cut leaves behind its budget are copies of what it
+// has kept, so a second cut of the same cache moves other rows, in the end few). 64 requests of 2000 - 2304 keys cut to 2048,
+// 4 heads of 128: 123 us, 441 MB read and written (3.6 TB/s), 21 us of them the selection. 131071 keys cut to 32768, 4 heads:
+// 66 us (135 MB), of which 30 are the selection (four units, so 32 CTAs: three passes of 5 us and the runs' list); the moving
+// takes four rounds of 9 us, each a chain of the list's lookups, the rows' latency and the flags. Tried and dropped, on caches
+// that had been cut before: the next block's lookups while this one's rows arrive (101 -> 118 us), blocks of 64 places with
+// three or four CTAs an SM (106, 112), clusters of 16 for few units (evict of one long request 75 -> 84 us).
 #include <cstdint>
 #include <cstring>
 

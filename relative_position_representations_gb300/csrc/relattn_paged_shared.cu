@@ -3,7 +3,7 @@
 // In two parts, whose softmaxes are joined: over the shared keys, where the rows of all requests of
 // a group go through the same products (so each shared key is read once for a group and meets full tiles of
 // rows), and over each request's own keys. With L the shared part's length, chosen on a tile's border and
-// so that every row of the group stands at least clip_k - 1 behind its last key, all of its keys have
+// so that every row of the group stands at least clip_k behind its last key, all of its keys have
 // the first table row in common:
 //   e_ij = scale q_i . (k_j + aK_0),  sum_j p_ij (v_j + aV_0) = sum_j p_ij v_j + aV_0 sum_j p_ij,
 // so the part needs neither positions nor masks nor tables: it is plain attention, and the two constants
@@ -347,7 +347,8 @@ cudaError_t launch_paged_shared(const PagedSharedArgs &sa, cudaStream_t s) {
     if (a.window > 0 || sa.groups == 0 || a.tokens < 2) return launch_paged(a, s);
     // Requests that fill a tile of 128 rows by themselves share their reads in the L2 as it is, and two parts cost more
     // than they save (32 requests behind 8192 keys, 16 / 4 heads of 128: 16 new tokens 75 us here, 103 without; 24 tokens
-    // 93 and 105; 32 tokens, 128 rows, 114 and 106).
+    // 95 and 105; 32 tokens, 128 rows, 115 and 106). The host knows the average alone: one long chunk among generated tokens
+    // turns the sharing off for all of them.
     if ((long long)a.tokens * (a.H / a.Hkv) >= 128LL * a.B) return launch_paged(a, s);
     const size_t rows = (size_t)a.tokens * a.H, ints = round16(((size_t)a.tokens + 2) * 4);
     char *w = static_cast<char *>(a.workspace) + 2 * paged_workspace_bytes(a.d);

@@ -361,7 +361,8 @@ constexpr uint32_t kSideBytes = 64;      // a tile's page numbers, 16 at most
 template <int D>
 constexpr int kStageBytes = kTile * D * 2;
 // A row warp's chain on a tile (products, exponentials, two shuffles) is latency, so several CTAs share an SM (with two and
-// one: 32 requests of 1K-2K keys, 16 heads of 64: 28.2 us in place of 26.5; 64 of 2K-16K, two key heads of 128: 55.2, 53.6)
+// one: 32 requests of 1K-2K keys, 16 heads of 64: 28.2 us in place of 26.5; 64 of 2K-16K, two key heads of 128: 55.2, 53.6;
+// 25.2 and 51.1 as the kernel is now)
 template <int D>
 constexpr int kCtasPerSm = D == 64 ? 3 : 2;
 

@@ -22,9 +22,9 @@
 // tile passes by: a 128 x 128 product with both operands in shared memory reads as much as that can give.
 //
 // What bounds it. Many rows: the sums, 1800 cycles for a query tile with both key tiles where the tensor cores work 1024
-// and the exponentials (32 a cycle) take as long. A chunk of 4096 tokens over 64K keys, 8 heads of 128: 376 us, 1370
-// TFLOP/s, 0.71 of the tensor rate. Four prompts of 4096 tokens, 16 heads of 128: 152 us, with the key term 220: the rows'
-// constants 17, R and its gathers 50. One query tile to a request (32 tokens, 16 / 4 heads of 128, 4K - 32K keys): 45
+// and the exponentials (32 a cycle) take as long. A chunk of 4096 tokens over 64K keys, 8 heads of 128: 380 us, 1400
+// TFLOP/s, 0.73 of the tensor rate. Four prompts of 4096 tokens, 16 heads of 128: 152 us, with the key term 220: the rows'
+// constants 17, R and its gathers 50. One query tile to a request (32 tokens, 16 / 4 heads of 128, 4K - 32K keys): 43
 // us, of which 25 stream the keys at 4.9 TB/s; the rest are the set-up's launch, the first ticket and loads, and the last units.
 #include <cstdint>
 #include <cstring>
