@@ -498,7 +498,8 @@ RELATTN_API relattn_status_t relattn_paged_shared_workspace_size(int tokens, int
  *                     new tokens' own entries are set; 0: every entry that is written is set. A key in
  *                     front of the new tokens of several requests that share its page (as prefixes for
  *                     relattn_paged_shared_fwd are) gets the sums of all of them with 1, and holds one of them
- *                     with 0.
+ *                     with 0. A key that is new to one request and in front of another's tokens holds no
+ *                     defined number.
  *   workspace         caller-owned device scratch of relattn_paged_weights_workspace_size bytes, 16-byte
  *                     aligned; calls that may overlap need one each.
  *

@@ -311,3 +311,30 @@ def test_a_wait_that_runs_out(dtype, d):
     for got, was in ((k, x["k"]), (v, x["v"]), (mass, x["mass"])):
         assert torch.equal(got.cpu()[rest], was[rest])
     run(x, lens, budget, budget, 0, 100)
+
+
+@pytest.mark.parametrize("bad", [False, True])
+def test_more_requests_are_cut_than_a_block_has_threads(bad):
+    """Their pages go back in several turns, in the requests' order."""
+    rp = _rp()
+    rng = np.random.default_rng(6)
+    P, budget = 4, 18
+    lens = rng.integers(10, 70, 1300).tolist()
+    x = make(lens, 1, 8, P, kind="ties", seed=6)
+    if not bad:
+        run(x, lens, budget, budget, 1, 3, in_place=True)
+        return
+    N, first = x["mass"].shape[0], -(-budget // P)
+    for b in range(0, 1300, 7):
+        if lens[b] > budget:
+            x["table"][b, int(rng.integers(first, -(-lens[b] // P) + 1)) - 1] = -3   # (some in front of the budget)
+    gone = [int(p) for b, n in enumerate(lens) if n > budget for p in x["table"][b, first:-(-n // P)]]
+    assert sum(n > budget for n in lens) > 1000 and min(gone) < 0
+    gone = [p for p in gone if 0 <= p < N]
+    want, head = x["free"].copy(), x["head"] - len(gone)
+    want[head:head + len(gone)] = gone
+    free = i32(x["free"])
+    _, got = rp.relattn_paged_evict(i32(lens), i32(x["table"]), x["k"].to(DEV), x["v"].to(DEV), x["mass"].to(DEV), budget,
+                                    sinks=1, recent=3, free_pages=free, free_head=i32([x["head"]]))
+    assert rp.relattn_get_device_error() == 1
+    assert int(got) == head and np.array_equal(free.cpu().numpy(), want)
